@@ -8,6 +8,10 @@ library's CUDA kernels, and a missing library is an error, never a fallback.
     out = decode_step(q, k, v, g, state)                         # one token, in place
     dq, dk, dv, dg, d_init = chunk_bwd(q, k, v, g, d_out, init_state=S0)   # training
 
+    y, state = conv_fwd(x, weight, activation="silu")            # a selective-scan layer
+    y, state = scan_fwd(u, dt, a, b, c, z=z)                     # (conv_bwd, scan_bwd; conv_step, scan_step)
+    children, used = fork_pages(pools, used, parents)            # pages of the state pools
+
 The recurrence (the "i14 Laplace 3B on AWS Trainium2" page, paragraph "GLA
 mixer"): ``S_t = diag(exp g_t) S_{t-1} + k_t^T v_t``, ``o_t = scale q_t S_t``.
 """
@@ -23,7 +27,9 @@ from ._binding import (GLA_FLAG_FP32_IO, GLA_FLAG_FP32_OUT, GLA_FLAG_VECTOR_GATE
 
 __all__ = ["chunk_fwd", "chunk_bwd", "decode_step", "status_sync", "set_wait_limit_ns", "GlaError",
            "lib", "version",
-           "GLA_FLAG_FP32_IO", "GLA_FLAG_FP32_OUT", "GLA_FLAG_VECTOR_GATE"]
+           "GLA_FLAG_FP32_IO", "GLA_FLAG_FP32_OUT", "GLA_FLAG_VECTOR_GATE",
+           "conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step",
+           "copy_pages", "fork_pages", "compact_pages", "free_pages", "PAGE_NEW"]
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -296,3 +302,8 @@ def status_sync(stream=None) -> int:
     if rc != 0:
         raise GlaError(rc, "gla_status_sync")
     return rc
+
+
+# The selective-scan layer and the state pools' pages live in files of their own.
+from .pages import PAGE_NEW, compact_pages, copy_pages, fork_pages, free_pages  # noqa: E402
+from .ssm import conv_bwd, conv_fwd, conv_step, scan_bwd, scan_fwd, scan_step  # noqa: E402

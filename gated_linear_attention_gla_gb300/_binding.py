@@ -23,12 +23,23 @@ GLA_ERR_TIMEOUT = 5
 GLA_FLAG_FP32_IO = 1 << 0
 GLA_FLAG_VECTOR_GATE = 1 << 1
 GLA_FLAG_FP32_OUT = 1 << 2
+GLA_FLAG_SILU = 1 << 3
+GLA_FLAG_SOFTPLUS = 1 << 4
+
+GLA_PAGE_NEW = -2
+GLA_MAX_PAGES = 524288
 
 _lock = threading.Lock()
 _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_i64 = ctypes.c_int64
+
+
+class PagePool(ctypes.Structure):
+    """gla_page_pool: page i is the page_bytes bytes at base + i * page_bytes."""
+    _fields_ = [("base", _vp), ("page_bytes", _i64)]
 
 
 class GlaError(RuntimeError):
@@ -83,6 +94,36 @@ def lib() -> ctypes.CDLL:
             L.gla_chunk_bwd_fixed_workspace.restype = _i
             L.gla_chunk_bwd_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i, ctypes.c_uint]
             L.gla_chunk_bwd_workspace_size.restype = ctypes.c_size_t
+            sz, un = ctypes.c_size_t, ctypes.c_uint
+            L.gla_conv_fwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                                       _vp, un]
+            L.gla_conv_fwd.restype = _i
+            L.gla_conv_bwd.argtypes = [_vp, _i64] + [_vp] * 10 + [_i] * 4 + [_vp, sz, _vp, un]
+            L.gla_conv_bwd.restype = _i
+            L.gla_conv_bwd_workspace_size.argtypes = [_i] * 5
+            L.gla_conv_bwd_workspace_size.restype = sz
+            L.gla_conv_step.argtypes = [_vp, _i64, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i,
+                                        _vp, un]
+            L.gla_conv_step.restype = _i
+            rows = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+            L.gla_scan_fwd.argtypes = rows + [_vp] * 4 + [_i] * 4 + [_vp, sz, _vp, un]
+            L.gla_scan_fwd.restype = _i
+            L.gla_scan_fwd_workspace_size.argtypes = [_i] * 5
+            L.gla_scan_fwd_workspace_size.restype = sz
+            L.gla_scan_bwd.argtypes = rows + [_vp] * 13 + [_i] * 4 + [_vp, sz, _vp, un]
+            L.gla_scan_bwd.restype = _i
+            L.gla_scan_bwd_workspace_size.argtypes = [_i] * 5
+            L.gla_scan_bwd_workspace_size.restype = sz
+            L.gla_scan_step.argtypes = rows + [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, un]
+            L.gla_scan_step.restype = _i
+            L.gla_pages_copy.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _i, _vp]
+            L.gla_pages_copy.restype = _i
+            L.gla_pages_fork.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp]
+            L.gla_pages_fork.restype = _i
+            L.gla_pages_compact.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp]
+            L.gla_pages_compact.restype = _i
+            L.gla_pages_free.argtypes = [_vp, _vp, _i, _vp, _i, _vp]
+            L.gla_pages_free.restype = _i
             L.gla_status_string.argtypes = [_i]
             L.gla_status_string.restype = ctypes.c_char_p
             L.gla_status_sync.argtypes = [_vp]

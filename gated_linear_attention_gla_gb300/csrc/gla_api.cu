@@ -86,6 +86,8 @@ uint64_t handoff_wait_limit_ns() {
   const uint64_t v = g_wait_limit_ns.load(std::memory_order_relaxed);
   return v != 0 ? v : kDefaultWaitLimitNs;
 }
+unsigned* device_status_word(cudaError_t* err) { return status_word(err); }
+int cuda_result(cudaError_t e) { return cuda_status(e); }
 }  // namespace gla
 
 extern "C" {

@@ -12,7 +12,8 @@ enum : unsigned {
   kDevBadSeqlens = 1u << 0,  // a cu_seqlens entry was out of order or out of range
   kDevTimeout = 1u << 1,     // a bounded mbarrier wait gave up
   kDevLayout = 1u << 2,      // a kernel's shared-memory window was not 1024-byte aligned
-  // (kDevBadSeqlens also flags a decode slot index outside the state pool)
+  // (kDevBadSeqlens also flags a decode slot index outside the state pool, and a
+  // page table's entry that names no page it could)
 };
 
 // Log-decays below -kGateClamp are raised to it before in-chunk cumulative
@@ -106,6 +107,112 @@ struct ChunkBwdArgs {
   unsigned* status;
 };
 
+// The short causal convolution (gla_conv_*): x [rows, D] with x_stride elements
+// between rows, weight [D, W], states [B, W - 1, D] in x's dtype.
+struct ConvArgs {
+  const void* x;
+  long long x_stride;
+  const float* weight;
+  const float* bias;        // [D] or null
+  const void* init_state;   // or null
+  void* out;                // [rows, D]
+  void* final_state;        // or null; may be init_state
+  const int32_t* cu_seqlens;
+  int B, T, D, W;
+  bool silu, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+struct ConvBwdArgs {
+  const void* x;
+  long long x_stride;
+  const float* weight;
+  const float* bias;
+  const void* init_state;
+  const void* d_out;           // [rows, D]
+  const float* d_final_state;  // [B, W - 1, D] fp32 or null
+  void* dx;                    // [rows, D]
+  float* d_weight;             // [D, W]
+  float* d_bias;               // [D] or null
+  float* d_init_state;         // [B, W - 1, D] fp32 or null
+  const int32_t* cu_seqlens;
+  int B, T, D, W;
+  bool silu, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+struct ConvStepArgs {
+  const void* x;
+  long long x_stride;
+  const float* weight;
+  const float* bias;
+  void* state;              // [N, W - 1, D], or a pool of num_slots pages
+  int num_slots;
+  const int32_t* slots;     // pages read, or null
+  const int32_t* out_slots; // pages written, or null: those read
+  void* out;
+  int N, D, W;
+  bool silu, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+// The selective scan (gla_scan_*): u, dt, z [rows, D], b, c [rows, NS], each
+// with its own row stride; a [D, NS]; states [B, D, NS] fp32.
+struct ScanArgs {
+  const void *u, *dt, *b, *c, *z;  // z may be null
+  long long u_stride, dt_stride, b_stride, c_stride, z_stride;
+  const float* a;
+  const float* skip;     // [D] or null
+  const float* dt_bias;  // [D] or null
+  const float* init_state;
+  void* out;
+  float* final_state;
+  const int32_t* cu_seqlens;
+  int B, T, D, NS;
+  bool softplus, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+struct ScanBwdArgs {
+  ScanArgs f;                  // the forward's inputs (out and final_state unused)
+  const void* d_out;           // [rows, D]
+  const float* d_final_state;  // [B, D, NS] or null
+  void *du, *ddt, *db, *dc, *dz;  // dz null without z
+  float *da, *dskip, *ddt_bias;   // dskip, ddt_bias may be null
+  float* d_init_state;            // or null
+};
+
+struct ScanStepArgs {
+  const void *u, *dt, *b, *c, *z;
+  long long u_stride, dt_stride, b_stride, c_stride, z_stride;
+  const float* a;
+  const float* skip;
+  const float* dt_bias;
+  float* state;
+  int num_slots;
+  const int32_t* slots;
+  const int32_t* out_slots;
+  void* out;
+  int N, D, NS;
+  bool softplus, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+// One pool of state pages: page i at base + i * page_bytes.
+struct PagePool {
+  void* base;
+  long long page_bytes;
+};
+constexpr int kMaxPools = 64;  // pools of one copy launch
+struct PagePools {
+  char* base[kMaxPools];
+  long long bytes[kMaxPools];
+  int first[kMaxPools];  // index of the pool's first slice
+  int count;
+};
+constexpr int kPageNew = -2;       // gla.h's GLA_PAGE_NEW
+constexpr int kMaxPages = 524288;  // pages of a pool (the copy plan keeps three bits a page)
+
 // Wall-time limit of the tensor-core prefill kernels' hand-off waits, read at
 // each launch (process-wide; set by gla_set_wait_limit_ns, default 2 s).  Their
 // teardown drains keep the default.
@@ -139,6 +246,32 @@ size_t chunk_bwd_tc_workspace(int B, int H, long long rows, int dk, int dv, bool
 cudaError_t launch_chunk_bwd_tc(const ChunkBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_tc_vec_dv(const ChunkBwdArgs& a, void* workspace,
                                        cudaStream_t stream);
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream);
+size_t conv_bwd_workspace(long long rows, int D, int W);
+cudaError_t launch_conv_bwd(const ConvBwdArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream);
+// workspace bytes of a scan (0: none) and the scan itself
+size_t scan_fwd_workspace(int B, long long rows, int D, int NS);
+cudaError_t launch_scan_fwd(const ScanArgs& a, void* workspace, cudaStream_t stream);
+size_t scan_bwd_workspace(int B, long long rows, int D, int NS);
+cudaError_t launch_scan_bwd(const ScanBwdArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagePool* pools, int count, int S, const int32_t* src,
+                              const int32_t* dst, int32_t* plan, int n, unsigned* status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagePool* pools, int count, int S, const int32_t* used,
+                              int32_t* used_out, const int32_t* parents, int32_t* children,
+                              int n, unsigned* status, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagePool* pools, int count, int S, const int32_t* used,
+                                 int32_t* used_out, const int32_t* slots, int32_t* slots_out,
+                                 int n, int32_t* forward, unsigned* status, cudaStream_t stream);
+cudaError_t launch_pages_free(int S, const int32_t* used, int32_t* used_out,
+                              const int32_t* slots, int n, unsigned* status,
+                              cudaStream_t stream);
+// what the entry points share (gla_api.cu): the current GPU's status word, a
+// CUDA result remembered for gla_last_error_string as a status, range checks
+unsigned* device_status_word(cudaError_t* err);
+int cuda_result(cudaError_t e);
 // the fixed device workspace of gla_chunk_bwd_fixed_workspace (a static array;
 // its address, or null with *err set)
 constexpr size_t kBwdFixedWorkspaceBytes = 384ull << 20;

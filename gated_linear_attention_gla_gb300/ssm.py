@@ -1,0 +1,256 @@
+"""The selective-scan layer's parts that carry state (argument marshalling only).
+
+A short causal convolution per channel, ``conv_*``, and a state space scan whose
+decay and drive depend on the token, ``scan_*``, each for prompts (dense, or
+packed with ``cu_seqlens``), for training (``*_bwd``: every gradient, from the
+forward's inputs alone) and for single tokens (``*_step``, on dense states or on
+a pool of pages).  Formulas, layouts and limits: ``include/gla.h``.
+
+``x``, ``u``, ``dt``, ``z``, ``b`` and ``c`` may be column slices of one
+projection's output (rows at one distance, 16-byte aligned except for b and c);
+everything else is contiguous.  Parameters and their gradients are fp32, the
+convolution's states have x's dtype, the scan's are fp32.  Call arguments given
+as ``stream`` run the call (and what it allocates) on that stream.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from ._binding import GLA_FLAG_SILU, GLA_FLAG_SOFTPLUS
+from ._marshal import (batch, check, done, io_flags, launch_on, lib, on_gpu, page_tables, ptr,
+                       row_stride, scratch, shaped)
+
+_F32 = torch.float32
+
+
+def _silu_flag(activation) -> int:
+    check(activation in (None, "silu"), 'activation is None or "silu"')
+    return GLA_FLAG_SILU if activation else 0
+
+
+def _conv_common(x, weight, bias):
+    check(x.is_cuda, "x must be a CUDA tensor")
+    on_gpu(_F32, x.device, weight=weight, bias=bias)
+    D = x.shape[-1]
+    check(weight.dim() == 2 and weight.shape[0] == D and weight.is_contiguous(),
+          f"weight must be contiguous [{D}, W]")
+    shaped((D,), bias=bias)
+    return D, weight.shape[1]
+
+
+def conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None,
+             activation: Optional[str] = None, out=None, final_state=None,
+             output_final_state: bool = True, stream=None, out_dtype=None):
+    """Causal convolution of a prompt; returns ``(out, final_state)``.
+
+    ``x`` [B, T, D], or packed [1, R, D] / [R, D] with ``cu_seqlens`` (int32
+    [B + 1] on the GPU); ``weight`` [D, W] (W = 2, 3, 4; column W - 1 meets the
+    token itself) and ``bias`` [D], fp32; ``activation`` None or "silu";
+    ``init_state`` and ``final_state`` [B, W - 1, D] in x's dtype, the last W - 1
+    inputs (oldest first).  ``out`` has x's dtype, or fp32
+    (``out_dtype=torch.float32``); ``final_state`` may be ``init_state``.
+    """
+    D, W = _conv_common(x, weight, bias)
+    lead, B, T = batch(x, cu_seqlens, "x")
+    stride = row_stride(x, "x", lead, D)
+    flags = io_flags(x.dtype, out.dtype if out is not None else out_dtype or x.dtype)
+    flags |= _silu_flag(activation)
+    on_gpu(x.dtype, x.device, init_state=init_state, final_state=final_state)
+    shaped((B, W - 1, D), init_state=init_state, final_state=final_state)
+    with launch_on(x.device, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        else:
+            check(out.shape == x.shape and out.is_contiguous() and out.device == x.device,
+                  "out must be contiguous, of x's shape, on x's GPU")
+        if final_state is None and output_final_state:
+            final_state = torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
+        done(lib().gla_conv_fwd(ptr(x), stride, ptr(weight), ptr(bias), ptr(init_state), ptr(out),
+                                ptr(final_state), ptr(cu_seqlens), B, T, D, W, s, flags),
+             "gla_conv_fwd")
+    return out, final_state
+
+
+def conv_bwd(x, weight, d_out, bias=None, init_state=None, d_final_state=None, cu_seqlens=None,
+             activation: Optional[str] = None, grad_dtype=None, need_d_init: bool = True,
+             workspace=None, stream=None):
+    """Gradient of ``conv_fwd``; returns ``(dx, d_weight, d_bias, d_init)``.
+
+    ``d_out`` (x's shape and dtype, contiguous) and ``d_final_state`` (fp32
+    [B, W - 1, D], or None for zero) are the gradients of the forward's outputs.
+    ``dx`` has x's dtype, or fp32 with ``grad_dtype=torch.float32``; ``d_bias`` is
+    None without a bias; ``d_init`` is fp32 (None when not requested).
+    """
+    D, W = _conv_common(x, weight, bias)
+    lead, B, T = batch(x, cu_seqlens, "x")
+    stride = row_stride(x, "x", lead, D)
+    grad_dtype = grad_dtype or x.dtype
+    flags = io_flags(x.dtype, grad_dtype) | _silu_flag(activation)
+    dev = x.device
+    on_gpu(x.dtype, dev, d_out=d_out, init_state=init_state)
+    on_gpu(_F32, dev, d_final_state=d_final_state)
+    shaped(x.shape, d_out=d_out)
+    shaped((B, W - 1, D), init_state=init_state, d_final_state=d_final_state)
+    with launch_on(dev, stream) as s:
+        size = lib().gla_conv_bwd_workspace_size(B, T, D, W, cu_seqlens is not None)
+        workspace = scratch(size, workspace, dev)
+        dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
+        dw = torch.empty((D, W), dtype=_F32, device=dev)
+        db = torch.empty(D, dtype=_F32, device=dev) if bias is not None else None
+        di = torch.empty((B, W - 1, D), dtype=_F32, device=dev) if need_d_init else None
+        done(lib().gla_conv_bwd(ptr(x), stride, ptr(weight), ptr(bias), ptr(init_state),
+                                ptr(d_out), ptr(d_final_state), ptr(dx), ptr(dw), ptr(db),
+                                ptr(di), ptr(cu_seqlens), B, T, D, W, ptr(workspace), size, s,
+                                flags), "gla_conv_bwd")
+    return dx, dw, db, di
+
+
+def conv_step(x, weight, state, bias=None, activation: Optional[str] = None, slots=None,
+              out_slots=None, out=None, stream=None, out_dtype=None):
+    """One token for N sequences: ``x`` [N, D]; returns ``out`` [N, D].
+
+    ``state`` [N, W - 1, D] in x's dtype is shifted by x in place.  With
+    ``slots`` (int32 [N] on the GPU) it is a pool [num_slots, W - 1, D]: row n
+    reads page ``slots[n]`` and writes it, or page ``out_slots[n]`` where that is
+    given (the page read stays as it was).  -1 in either marks a row that does
+    nothing.
+    """
+    D, W = _conv_common(x, weight, bias)
+    check(x.dim() == 2, "x is [N, D]")
+    N = x.shape[0]
+    stride = row_stride(x, "x", (N,), D)
+    on_gpu(x.dtype, x.device, state=state)
+    page_tables(N, x.device, slots, out_slots)
+    check(state.dim() == 3 and state.shape[1:] == (W - 1, D) and state.is_contiguous() and
+          (slots is not None or state.shape[0] == N),
+          f"state must be contiguous [{N if slots is None else 'num_slots'}, {W - 1}, {D}]")
+    flags = io_flags(x.dtype, out.dtype if out is not None else out_dtype or x.dtype)
+    flags |= _silu_flag(activation)
+    with launch_on(x.device, stream) as s:
+        if out is None:
+            out = torch.empty((N, D), dtype=out_dtype or x.dtype, device=x.device)
+        else:
+            check(out.shape == (N, D) and out.is_contiguous() and out.device == x.device,
+                  "out must be contiguous, of x's shape, on x's GPU")
+        done(lib().gla_conv_step(ptr(x), stride, ptr(weight), ptr(bias), ptr(state),
+                                 0 if slots is None else state.shape[0], ptr(slots),
+                                 ptr(out_slots), ptr(out), N, D, W, s, flags), "gla_conv_step")
+    return out
+
+
+def _scan_common(u, dt, a, b, c, skip, z, dt_bias, lead):
+    """Checks; returns (D, N, the row arguments shared by the scan's entry points)."""
+    check(u.is_cuda, "u must be a CUDA tensor")
+    dev = u.device
+    on_gpu(u.dtype, dev, dt=dt, b=b, c=c, z=z)
+    on_gpu(_F32, dev, a=a, skip=skip, dt_bias=dt_bias)
+    D, N = u.shape[-1], a.shape[-1]
+    shaped((D, N), a=a)
+    shaped((D,), skip=skip, dt_bias=dt_bias)
+    args = (ptr(u), row_stride(u, "u", lead, D), ptr(dt), row_stride(dt, "dt", lead, D), ptr(a),
+            ptr(b), row_stride(b, "b", lead, N), ptr(c), row_stride(c, "c", lead, N), ptr(skip),
+            ptr(z), 0 if z is None else row_stride(z, "z", lead, D), ptr(dt_bias))
+    return D, N, args
+
+
+def scan_fwd(u, dt, a, b, c, skip=None, z=None, dt_bias=None, softplus: bool = True,
+             init_state=None, cu_seqlens=None, out=None, final_state=None,
+             output_final_state: bool = True, workspace=None, stream=None, out_dtype=None):
+    """Selective scan of a prompt; returns ``(out, final_state)``.
+
+    ``u``, ``dt``, ``z`` [B, T, D] (packed: [1, R, D] or [R, D] with
+    ``cu_seqlens``), ``b``, ``c`` [.., N] with N = 8, 16, 32 or 64, all in u's
+    dtype; ``a`` [D, N], ``skip`` [D], ``dt_bias`` [D] fp32.  ``softplus``: the
+    step size is softplus(dt + dt_bias), else their sum.  States are fp32
+    [B, D, N]; ``final_state`` may be ``init_state``.  ``out`` has u's dtype, or
+    fp32 (``out_dtype=torch.float32``).  ``workspace``: a uint8 tensor of
+    gla_scan_fwd_workspace_size bytes, or None for a fresh one.
+    """
+    lead, B, T = batch(u, cu_seqlens, "u")
+    D, N, args = _scan_common(u, dt, a, b, c, skip, z, dt_bias, lead)
+    dev = u.device
+    flags = io_flags(u.dtype, out.dtype if out is not None else out_dtype or u.dtype)
+    flags |= GLA_FLAG_SOFTPLUS if softplus else 0
+    on_gpu(_F32, dev, init_state=init_state, final_state=final_state)
+    shaped((B, D, N), init_state=init_state, final_state=final_state)
+    with launch_on(dev, stream) as s:
+        size = lib().gla_scan_fwd_workspace_size(B, T, D, N, cu_seqlens is not None)
+        workspace = scratch(size, workspace, dev)
+        if out is None:
+            out = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=dev)
+        else:
+            check(out.shape == u.shape and out.is_contiguous() and out.device == dev,
+                  "out must be contiguous, of u's shape, on u's GPU")
+        if final_state is None and output_final_state:
+            final_state = torch.empty((B, D, N), dtype=_F32, device=dev)
+        done(lib().gla_scan_fwd(*args, ptr(init_state), ptr(out), ptr(final_state),
+                                ptr(cu_seqlens), B, T, D, N, ptr(workspace), size, s, flags),
+             "gla_scan_fwd")
+    return out, final_state
+
+
+def scan_bwd(u, dt, a, b, c, d_out, skip=None, z=None, dt_bias=None, softplus: bool = True,
+             init_state=None, d_final_state=None, cu_seqlens=None, grad_dtype=None,
+             need_d_init: bool = True, workspace=None, stream=None):
+    """Gradient of ``scan_fwd``; returns ``(du, ddt, da, db, dc, dskip, dz, ddt_bias, d_init)``.
+
+    ``d_out`` (u's shape and dtype, contiguous) and ``d_final_state`` (fp32 state,
+    or None for zero) are the gradients of the forward's outputs.  du, ddt, db,
+    dc, dz come in u's dtype, or fp32 with ``grad_dtype=torch.float32``; da, dskip,
+    ddt_bias and d_init are fp32; gradients of what was not given are None.
+    """
+    lead, B, T = batch(u, cu_seqlens, "u")
+    D, N, args = _scan_common(u, dt, a, b, c, skip, z, dt_bias, lead)
+    dev = u.device
+    grad_dtype = grad_dtype or u.dtype
+    flags = io_flags(u.dtype, grad_dtype) | (GLA_FLAG_SOFTPLUS if softplus else 0)
+    on_gpu(u.dtype, dev, d_out=d_out)
+    on_gpu(_F32, dev, init_state=init_state, d_final_state=d_final_state)
+    shaped(u.shape, d_out=d_out)
+    shaped((B, D, N), init_state=init_state, d_final_state=d_final_state)
+    with launch_on(dev, stream) as s:
+        size = lib().gla_scan_bwd_workspace_size(B, T, D, N, cu_seqlens is not None)
+        workspace = scratch(size, workspace, dev)
+        new = lambda shape, dtype=_F32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        du, ddt = new(u.shape, grad_dtype), new(u.shape, grad_dtype)
+        db, dc = new(b.shape, grad_dtype), new(c.shape, grad_dtype)
+        dz = new(u.shape, grad_dtype) if z is not None else None
+        da = new((D, N))
+        dskip = new(D) if skip is not None else None
+        dbias = new(D) if dt_bias is not None else None
+        di = new((B, D, N)) if need_d_init else None
+        done(lib().gla_scan_bwd(*args, ptr(init_state), ptr(d_out), ptr(d_final_state), ptr(du),
+                                ptr(ddt), ptr(da), ptr(db), ptr(dc), ptr(dskip), ptr(dz),
+                                ptr(dbias), ptr(di), ptr(cu_seqlens), B, T, D, N, ptr(workspace),
+                                size, s, flags), "gla_scan_bwd")
+    return du, ddt, da, db, dc, dskip, dz, dbias, di
+
+
+def scan_step(u, dt, a, b, c, state, skip=None, z=None, dt_bias=None, softplus: bool = True,
+              slots=None, out_slots=None, out=None, stream=None, out_dtype=None):
+    """One token for R sequences: ``u``, ``dt``, ``z`` [R, D], ``b``, ``c`` [R, N]; returns
+    ``out`` [R, D].  ``state`` (fp32 [R, D, N]) is updated in place; with ``slots``
+    and ``out_slots`` it is a pool [num_slots, D, N], as for ``conv_step``."""
+    check(u.dim() == 2, "u is [R, D]")
+    R = u.shape[0]
+    D, N, args = _scan_common(u, dt, a, b, c, skip, z, dt_bias, (R,))
+    dev = u.device
+    on_gpu(_F32, dev, state=state)
+    page_tables(R, dev, slots, out_slots)
+    check(state.dim() == 3 and state.shape[1:] == (D, N) and state.is_contiguous() and
+          (slots is not None or state.shape[0] == R),
+          f"state must be contiguous [{R if slots is None else 'num_slots'}, {D}, {N}]")
+    flags = io_flags(u.dtype, out.dtype if out is not None else out_dtype or u.dtype)
+    flags |= GLA_FLAG_SOFTPLUS if softplus else 0
+    with launch_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((R, D), dtype=out_dtype or u.dtype, device=dev)
+        else:
+            check(out.shape == (R, D) and out.is_contiguous() and out.device == dev,
+                  "out must be contiguous, of u's shape, on u's GPU")
+        done(lib().gla_scan_step(*args, ptr(state), 0 if slots is None else state.shape[0],
+                                 ptr(slots), ptr(out_slots), ptr(out), R, D, N, s, flags),
+             "gla_scan_step")
+    return out

@@ -34,6 +34,14 @@
  *                    gla_chunk_bwd_workspace_size sizes its tensor-core path's
  *                    workspace, gla_chunk_bwd_fixed_workspace runs it on a
  *                    buffer of the library's own.
+ *   gla_conv_fwd, gla_conv_bwd, gla_conv_step
+ *                    the short causal convolution in front of a selective scan:
+ *                    prompts, gradients, one token over a pool of states.
+ *   gla_scan_fwd, gla_scan_bwd, gla_scan_step
+ *                    the selective state space scan, whose decay differs for
+ *                    every channel, state and token: likewise.
+ *   gla_pages_copy, gla_pages_fork, gla_pages_compact, gla_pages_free
+ *                    the pages of state pools, managed on the device.
  *   gla_status_sync, gla_status_string, gla_last_error_string, gla_version,
  *   gla_chunk_fwd_kernel, gla_set_wait_limit_ns
  *                    diagnostics.
@@ -84,6 +92,9 @@ typedef enum gla_status {
 #define GLA_FLAG_FP32_OUT (1u << 2)    /* out is fp32 while q, k, v stay bf16; the bf16 output of
                                           the same call is exactly this result rounded to
                                           nearest-even (same kernels, only the store differs) */
+#define GLA_FLAG_SILU (1u << 3)        /* gla_conv_*: silu after the convolution */
+#define GLA_FLAG_SOFTPLUS (1u << 4)    /* gla_scan_*: the step size is softplus(dt + dt_bias)
+                                          (default dt + dt_bias) */
 
 /*
  * gla_chunk_fwd -- chunked prefill over a batch of sequences.
@@ -370,6 +381,191 @@ size_t gla_chunk_bwd_workspace_size(int B, int H, int T, int dk, int dv, int pac
  * launches nothing.
  */
 const char *gla_chunk_fwd_kernel(int dk, int dv, int chunk, unsigned flags);
+
+/*
+ * The selective-scan layer.  Its parts that carry state: a short causal
+ * convolution per channel, and a state space scan whose decay and drive depend
+ * on the token.  (Projections before, between and after them are matrix
+ * products.)  The pages the recurrence above comes from have no counterpart;
+ * these entry points stand beside it for layers whose decay is one value per
+ * (channel, state, token), which no matrix product over a chunk covers.
+ *
+ * Shared by the six entry points below
+ *   - Tokens are rows: row b * T + t of a dense batch, or packed rows with
+ *     cu_seqlens as for gla_chunk_fwd (a malformed cu_seqlens is reported by
+ *     gla_status_sync as GLA_ERR_INVALID_ARG; the call's outputs are then
+ *     unspecified, nothing outside them is written).
+ *   - x, u, dt, z, b and c take the distance between rows in elements
+ *     (x_stride, ...), so that they may be column slices of one projection's
+ *     output.  Every other tensor is contiguous.
+ *   - D, the channels, is a multiple of 8.  Rows of x, u, dt, z start on 16
+ *     bytes (pointer and stride); b and c rows on an element.
+ *   - Parameters (weight, bias, a, skip, dt_bias) and their gradients are fp32.
+ *   - Gradients come in the inputs' dtype, or fp32 with GLA_FLAG_FP32_OUT; they
+ *     are summed in a fixed order (the same inputs give the same bits).
+ *   - Outputs and workspaces must not overlap one another or any input.
+ */
+
+/*
+ * gla_conv_fwd -- p[t][d] = bias[d] + sum_j weight[d][W-1-j] x[t-j][d],
+ * out = p, or p / (1 + exp(-p)) with GLA_FLAG_SILU.
+ *
+ *   x            [rows, D], bf16 or fp32 (GLA_FLAG_FP32_IO)
+ *   weight       [D, W], W = 2, 3 or 4; bias [D] or NULL
+ *   init_state   [B, W-1, D] in x's dtype: the W-1 rows before each sequence,
+ *                oldest first, or NULL (zeros)
+ *   out          [rows, D], x's dtype (fp32 with GLA_FLAG_FP32_OUT)
+ *   final_state  [B, W-1, D] in x's dtype: the last W-1 rows (of init_state
+ *                and x), or NULL.  May be init_state itself.
+ */
+gla_status gla_conv_fwd(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                        const void *init_state, void *out, void *final_state,
+                        const int32_t *cu_seqlens, int B, int T, int D, int W,
+                        gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_conv_bwd -- the gradient of gla_conv_fwd.  d_out [rows, D] in x's dtype;
+ * d_final_state and d_init_state [B, W-1, D] fp32, or NULL (zero; not
+ * written); dx [rows, D]; d_weight [D, W]; d_bias [D] or NULL.  workspace:
+ * gla_conv_bwd_workspace_size(...) bytes of device memory, 256-byte aligned.
+ */
+gla_status gla_conv_bwd(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                        const void *init_state, const void *d_out, const float *d_final_state,
+                        void *dx, float *d_weight, float *d_bias, float *d_init_state,
+                        const int32_t *cu_seqlens, int B, int T, int D, int W, void *workspace,
+                        size_t workspace_bytes, gla_stream_t stream, unsigned flags);
+size_t gla_conv_bwd_workspace_size(int B, int T, int D, int W, int packed);
+
+/*
+ * gla_conv_step -- one token for each of N sequences.  x, out [N, D];
+ * state [N, W-1, D] in x's dtype, shifted by x in place; with slots (DEVICE
+ * int32 [N]) a pool of num_slots pages, as for gla_decode_step_slots.
+ * out_slots (DEVICE int32 [N], or NULL for slots): the page that receives row
+ * n's new state; page slots[n] is then left as it was, and several rows may
+ * read the same page (a fork during the step).  The pages written by one call
+ * must be distinct, and none may be read by another row.  A row with -1 in
+ * either table does nothing.
+ */
+gla_status gla_conv_step(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                         void *state, int num_slots, const int32_t *slots,
+                         const int32_t *out_slots, void *out, int N, int D, int W,
+                         gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_scan_fwd -- for every sequence, channel d and state n = 0 .. N-1
+ *     delta  = dt + dt_bias[d], or softplus of it with GLA_FLAG_SOFTPLUS
+ *     h[t][d][n] = exp(delta a[d][n]) h[t-1][d][n] + delta u[t][d] b[t][n]
+ *     out[t][d]  = (sum_n c[t][n] h[t][d][n] + skip[d] u[t][d]) z / (1 + exp(-z))
+ *
+ *   u, dt        [rows, D]; b, c [rows, N]: bf16, or fp32 with GLA_FLAG_FP32_IO
+ *   a            [D, N], finite; N = 8, 16, 32 or 64 (16-byte aligned)
+ *   skip, dt_bias  [D] or NULL (zero)
+ *   z            [rows, D] or NULL (no gate); z_stride is then ignored
+ *   init_state   fp32 [B, D, N] or NULL (zeros); final_state likewise or NULL
+ *                (not written), may be init_state itself
+ *   out          [rows, D], u's dtype (fp32 with GLA_FLAG_FP32_OUT)
+ *   workspace    gla_scan_fwd_workspace_size(...) bytes (256-byte aligned; NULL
+ *                where that is 0)
+ */
+gla_status gla_scan_fwd(const void *u, int64_t u_stride, const void *dt, int64_t dt_stride,
+                        const float *a, const void *b, int64_t b_stride, const void *c,
+                        int64_t c_stride, const float *skip, const void *z, int64_t z_stride,
+                        const float *dt_bias, const float *init_state, void *out,
+                        float *final_state, const int32_t *cu_seqlens, int B, int T, int D,
+                        int N, void *workspace, size_t workspace_bytes, gla_stream_t stream,
+                        unsigned flags);
+size_t gla_scan_fwd_workspace_size(int B, int T, int D, int N, int packed);
+
+/*
+ * gla_scan_bwd -- the gradient of gla_scan_fwd.  d_out [rows, D] in u's dtype;
+ * d_final_state, d_init_state fp32 [B, D, N] or NULL; du, ddt, dz [rows, D]
+ * (dz NULL exactly without z); db, dc [rows, N]; da [D, N]; dskip, ddt_bias [D]
+ * or NULL.  Nothing of the forward call is needed but its inputs.
+ */
+gla_status gla_scan_bwd(const void *u, int64_t u_stride, const void *dt, int64_t dt_stride,
+                        const float *a, const void *b, int64_t b_stride, const void *c,
+                        int64_t c_stride, const float *skip, const void *z, int64_t z_stride,
+                        const float *dt_bias, const float *init_state, const void *d_out,
+                        const float *d_final_state, void *du, void *ddt, float *da, void *db,
+                        void *dc, float *dskip, void *dz, float *ddt_bias, float *d_init_state,
+                        const int32_t *cu_seqlens, int B, int T, int D, int N, void *workspace,
+                        size_t workspace_bytes, gla_stream_t stream, unsigned flags);
+size_t gla_scan_bwd_workspace_size(int B, int T, int D, int N, int packed);
+
+/*
+ * gla_scan_step -- one token for each of `rows` sequences: u, dt, z, out
+ * [rows, D], b, c [rows, N]; state fp32 [rows, D, N] updated in place, or a
+ * pool with slots and out_slots as for gla_conv_step.
+ */
+gla_status gla_scan_step(const void *u, int64_t u_stride, const void *dt, int64_t dt_stride,
+                         const float *a, const void *b, int64_t b_stride, const void *c,
+                         int64_t c_stride, const float *skip, const void *z, int64_t z_stride,
+                         const float *dt_bias, float *state, int num_slots,
+                         const int32_t *slots, const int32_t *out_slots, void *out, int rows,
+                         int D, int N, gla_stream_t stream, unsigned flags);
+
+/*
+ * The pages of state pools.  A sequence's state is page i of every pool (one
+ * pool per layer and kind of state: the pools of gla_decode_step_slots,
+ * gla_conv_step, gla_scan_step), and `used` (DEVICE int32 [num_pages]) is 0 for
+ * a free page.  The operators below read and write the tables on the device,
+ * in page order, and move the pages of all pools; the host waits for nothing.
+ *
+ *   pools        HOST array of num_pools pools (read before the call returns):
+ *                page i is the page_bytes bytes at base + i * page_bytes;
+ *                page_bytes a multiple of 16, at most 2^32
+ *   num_pages    pages of every pool, at most GLA_MAX_PAGES
+ *   used, used_out   [num_pages]; used_out may be used (in place)
+ * An entry of a table that names no page it could (out of range; a free page
+ * where a used one is meant) is skipped and reported by gla_status_sync as
+ * GLA_ERR_INVALID_ARG.  -1 entries are skipped silently.
+ */
+#define GLA_MAX_PAGES 524288
+#define GLA_PAGE_NEW (-2)
+typedef struct gla_page_pool {
+    void *base;         /* DEVICE, 16-byte aligned */
+    int64_t page_bytes;
+} gla_page_pool;
+
+/*
+ * gla_pages_copy -- page dst[i] = page src[i] (DEVICE int32 [n] each) for all
+ * pairs at once.  A pair whose dst another pair writes, or whose dst another
+ * pair reads, is skipped and reported.  copied [n] receives dst[i] for the
+ * pairs that were copied and -1 for the others.
+ */
+gla_status gla_pages_copy(const gla_page_pool *pools, int num_pools, int num_pages,
+                          const int32_t *src, const int32_t *dst, int32_t *copied, int n,
+                          gla_stream_t stream);
+
+/*
+ * gla_pages_fork -- a new page for every entry of parents: a copy of page
+ * parents[i] (used; several entries may name it), or, where it is
+ * GLA_PAGE_NEW, zeros.  children[i] receives its number: the free pages in
+ * ascending order go to the entries in order.  When no page is left an entry
+ * gets -1 and the call is reported as GLA_ERR_INVALID_ARG.
+ */
+gla_status gla_pages_fork(const gla_page_pool *pools, int num_pools, int num_pages,
+                          const int32_t *used, int32_t *used_out, const int32_t *parents,
+                          int32_t *children, int n, gla_stream_t stream);
+
+/*
+ * gla_pages_compact -- with L pages used, moves the used pages at or behind L
+ * to the free pages in front of L (the k-th of the ones, in ascending order,
+ * to the k-th of the others), so that pages 0 .. L-1 are the used ones; the
+ * rest keep their bytes.  forward [num_pages] receives every used page's new
+ * number (-1 for the free pages); slots_out[i] = forward[slots[i]] (-1 for -1,
+ * and for an entry that names no used page); slots_out may be slots.
+ */
+gla_status gla_pages_compact(const gla_page_pool *pools, int num_pools, int num_pages,
+                             const int32_t *used, int32_t *used_out, const int32_t *slots,
+                             int32_t *slots_out, int n, int32_t *forward, gla_stream_t stream);
+
+/*
+ * gla_pages_free -- marks the pages slots[0 .. n) free; their bytes stay.  A
+ * page that was free already, or is named twice, is reported.
+ */
+gla_status gla_pages_free(const int32_t *used, int32_t *used_out, int num_pages,
+                          const int32_t *slots, int n, gla_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char *gla_status_string(gla_status status);
