@@ -57,15 +57,15 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const long long t = hi - K + i;
-      if (t >= lo) r[i] = *reinterpret_cast<const Raw<IO, V>*>(x + t * a.x_stride);
+      if (t >= lo) r[i] = load_raw<IO, V>(x + t * a.x_stride);
       else if (init)  // before the sequence: row K - (lo - t) of the initial state
-        r[i] = *reinterpret_cast<const Raw<IO, V>*>(
+        r[i] = load_raw<IO, V>(
             init + ((long long)s * K + K - (lo - t)) * a.D + c);
       else r[i] = zero_raw<IO, V>();
     }
     IO* fin = (IO*)a.final_state + (long long)s * K * a.D + c;
 #pragma unroll
-    for (int i = 0; i < K; ++i) *reinterpret_cast<Raw<IO, V>*>(fin + (long long)i * a.D) = r[i];
+    for (int i = 0; i < K; ++i) store_raw<IO, V>(fin + (long long)i * a.D, r[i]);
     return;
   }
 
@@ -89,13 +89,13 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
       for (int i = 0; i < K; ++i) {
         const long long t = r - K + i;
         Raw<IO, V> v = zero_raw<IO, V>();
-        if (t >= lo) v = *reinterpret_cast<const Raw<IO, V>*>(x + t * a.x_stride);
+        if (t >= lo) v = load_raw<IO, V>(x + t * a.x_stride);
         else if (init)
-          v = *reinterpret_cast<const Raw<IO, V>*>(
+          v = load_raw<IO, V>(
               init + ((long long)s * K + K - (lo - t)) * a.D + c);
         unpack_as<IO, V>(v, win[i]);
       }
-      auto step = [&](const Raw<IO, V>& raw, long long row) {
+      auto step = [&](const Raw<IO, V>& raw, long long row, bool in) {
         float xv[V], y[V];
         unpack_as<IO, V>(raw, xv);
 #pragma unroll
@@ -109,25 +109,28 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
           for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
           win[K - 1][i] = xv[i];
         }
+        if (!in) return;
         if constexpr (sizeof(OUT) * V > 16) {  // fp32 results of 8 bf16 channels
           float lo4[4], hi4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) { lo4[i] = y[i]; hi4[i] = y[i + V / 2]; }
-          *reinterpret_cast<uint4*>(out + row * a.D) = pack_as<float, 4>(lo4);
-          *reinterpret_cast<uint4*>(out + row * a.D + 4) = pack_as<float, 4>(hi4);
+          store_raw<OUT, 4>(out + row * a.D, pack_as<OUT, 4>(lo4));
+          store_raw<OUT, 4>(out + row * a.D + 4, pack_as<OUT, 4>(hi4));
         } else {
-          *reinterpret_cast<Raw<OUT, V>*>(out + row * a.D) = pack_as<OUT, V>(y);
+          store_raw<OUT, V>(out + row * a.D, pack_as<OUT, V>(y));
         }
       };
-      for (; r + kUnroll <= end; r += kUnroll) {
+      // (one loop for whole and partial groups: rows behind the sequence load
+      // zeros and store nothing)
+      for (; r < end; r += kUnroll) {
         Raw<IO, V> v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          v[u] = *reinterpret_cast<const Raw<IO, V>*>(x + (r + u) * a.x_stride);
+          v[u] = r + u < end ? load_raw<IO, V>(x + (r + u) * a.x_stride) : zero_raw<IO, V>();
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) step(v[u], r + u);
+        for (int u = 0; u < kUnroll; ++u) step(v[u], r + u, r + u < end);
       }
-      for (; r < end; ++r) step(*reinterpret_cast<const Raw<IO, V>*>(x + r * a.x_stride), r);
+      r = end;
     }
     if (++s >= a.B) {  // no sequence holds the rows that are left
       if (r < r1 && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
@@ -158,11 +161,11 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvStepArgs a) {
     to = t;
   }
   IO* pool = (IO*)a.state + c;
-  const Raw<IO, V> xr = *reinterpret_cast<const Raw<IO, V>*>((const IO*)a.x + n * a.x_stride + c);
+  const Raw<IO, V> xr = load_raw<IO, V>((const IO*)a.x + n * a.x_stride + c);
   Raw<IO, V> old[K];
 #pragma unroll
   for (int i = 0; i < K; ++i)
-    old[i] = *reinterpret_cast<const Raw<IO, V>*>(pool + (from * K + i) * a.D);
+    old[i] = load_raw<IO, V>(pool + (from * K + i) * a.D);
   float w[V][W], p[V];
   load_filter<W, V>(a.weight, a.bias, c, w, p);
   float xv[V];
@@ -183,8 +186,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvStepArgs a) {
   for (int i = 0; i < V; ++i) out[i] = from_f32<OUT>(p[i]);
 #pragma unroll
   for (int i = 0; i + 1 < K; ++i)
-    *reinterpret_cast<Raw<IO, V>*>(pool + (to * K + i) * a.D) = old[i + 1];
-  *reinterpret_cast<Raw<IO, V>*>(pool + (to * K + K - 1) * a.D) = xr;
+    store_raw<IO, V>(pool + (to * K + i) * a.D, old[i + 1]);
+  store_raw<IO, V>(pool + (to * K + K - 1) * a.D, xr);
 }
 
 template <typename IO, typename OUT, int W, bool SILU>

@@ -30,7 +30,7 @@ template <bool SILU> __device__ __forceinline__ float d_act(float p) {
 }
 
 template <typename OUT> __device__ __forceinline__ void store4(OUT* p, const float (&x)[kV]) {
-  *reinterpret_cast<Raw<OUT, kV>*>(p) = pack_as<OUT, kV>(x);
+  store_raw<OUT, kV>(p, pack_as<OUT, kV>(x));
 }
 
 // Rows t0 - K .. t0 - 1 of sequence s (from row lo on; its initial state before).
@@ -42,9 +42,9 @@ __device__ __forceinline__ void load_window(const ConvBwdArgs& a, int s, long lo
     const long long t = t0 - K + i;
     Raw<IO, kV> v = zero_raw<IO, kV>();
     if (t >= lo)
-      v = *reinterpret_cast<const Raw<IO, kV>*>((const IO*)a.x + t * a.x_stride + c);
+      v = load_raw<IO, kV>((const IO*)a.x + t * a.x_stride + c);
     else if (a.init_state)
-      v = *reinterpret_cast<const Raw<IO, kV>*>(
+      v = load_raw<IO, kV>(
           (const IO*)a.init_state + ((long long)s * K + K - (lo - t)) * a.D + c);
     unpack_as<IO, kV>(v, win[i]);
   }
@@ -87,7 +87,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
       for (int e = 0; e < kV; ++e) g[i][e] = 0.f;
       // a sequence shorter than the filter leaves rows of its initial state in the final one
       if (a.d_final_state && i >= hi - lo)
-        unpack_as<float, kV>(*reinterpret_cast<const Raw<float, kV>*>(
+        unpack_as<float, kV>(load_raw<float, kV>(
                                  a.d_final_state + (s * K + i - (hi - lo)) * a.D + c),
                              g[i]);
     }
@@ -95,8 +95,8 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
     for (int t = 0; t < K; ++t) {
       if (lo + t < hi) {
         float xv[kV], dv[kV];
-        unpack_as<IO, kV>(*reinterpret_cast<const Raw<IO, kV>*>(x + (lo + t) * a.x_stride), xv);
-        unpack_as<IO, kV>(*reinterpret_cast<const Raw<IO, kV>*>(dy + (lo + t) * a.D), dv);
+        unpack_as<IO, kV>(load_raw<IO, kV>(x + (lo + t) * a.x_stride), xv);
+        unpack_as<IO, kV>(load_raw<IO, kV>(dy + (lo + t) * a.D), dv);
 #pragma unroll
         for (int e = 0; e < kV; ++e) {
           float p = bias[e];
@@ -149,9 +149,9 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           const bool in = t + u < min(hi, end + K);
-          xr[u] = in ? *reinterpret_cast<const Raw<IO, kV>*>(x + (t + u) * a.x_stride)
+          xr[u] = in ? load_raw<IO, kV>(x + (t + u) * a.x_stride)
                      : zero_raw<IO, kV>();
-          dr[u] = in ? *reinterpret_cast<const Raw<IO, kV>*>(dy + (t + u) * a.D)
+          dr[u] = in ? load_raw<IO, kV>(dy + (t + u) * a.D)
                      : zero_raw<IO, kV>();
         }
 #pragma unroll
@@ -192,7 +192,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
             if (a.d_final_state && q >= hi - K) {
               float f[kV];
               unpack_as<float, kV>(
-                  *reinterpret_cast<const Raw<float, kV>*>(
+                  load_raw<float, kV>(
                       a.d_final_state + ((long long)s * K + q - (hi - K)) * a.D + c),
                   f);
 #pragma unroll

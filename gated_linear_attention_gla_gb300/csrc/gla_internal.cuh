@@ -251,7 +251,7 @@ size_t conv_bwd_workspace(long long rows, int D, int W);
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream);
 // workspace bytes of a scan (0: none) and the scan itself
-size_t scan_fwd_workspace(int B, long long rows, int D, int NS);
+size_t scan_fwd_workspace(int B, long long rows, int D, int NS, bool packed);
 cudaError_t launch_scan_fwd(const ScanArgs& a, void* workspace, cudaStream_t stream);
 size_t scan_bwd_workspace(int B, long long rows, int D, int NS);
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, void* workspace, cudaStream_t stream);

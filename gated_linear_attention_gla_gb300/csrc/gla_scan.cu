@@ -6,200 +6,484 @@
 //
 // Every (channel, n) has a decay of its own at every token, so no product of
 // matrices forms the in-chunk part (as it does in chunk_fwd): the work is NS
-// exponentials and 4 NS multiply-adds per token and channel, on the CUDA cores.
+// exponentials and 4 NS multiplies and adds per token and channel, on the CUDA
+// cores; instruction issue and the exponential unit bound it, not HBM.
 //
-// NS / 4 adjacent lanes own a channel, four states each in registers; a block
-// of 8 warps owns a tile of 1024 / NS channels of one sequence and walks its tokens
-// in tiles of 1024 (token, channel) pairs.  Per tile every thread turns four
-// pairs into (delta, delta u) in shared memory, loaded a tile ahead; the
-// lanes then run the recurrence, the sum over n is reduced over the lanes of
-// a channel for four tokens at once, and the thread that holds u and z of a
-// pair finishes and stores it.  One barrier per tile (double-buffered).
+// A block owns 1024 / NS channels of one run of tokens.  Four compute warps: NS / 8
+// lanes a channel, eight states each in four register pairs (f32x2 instructions
+// work on two states); the next two tokens are in registers before the current
+// ones are used.  Four helper warps turn (dt, u) of the next 1024 (token,
+// channel) pairs into (delta, delta u) in shared memory, and finish and store
+// the outputs of the previous ones, so the recurrence never waits for loads,
+// the softplus or the gate.  Two stages, handed over by named barriers.  Lanes
+// that differ in the state sit in different quarters of a warp, so that the
+// reads of b and c are broadcasts within a quarter (2 cycles instead of 4 for 16
+// bytes a lane); the sums over n go through shared memory, up to two terms per
+// pair, and the helpers add them.
+//
+// One run is a whole sequence, or, where sequences times channel tiles leave
+// SMs idle, a chunk of it (three launches): what every chunk adds to the state
+// and the sum of its step sizes (the same kernel without c, y and z; the last
+// chunks are left out), the states between the chunks, and the chunks
+// themselves from those.
 #include "gla_scan.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPairs = 1024;  // (token, channel) pairs of a tile
-constexpr int kV = 4;         // pairs per thread: adjacent channels of a token
+constexpr int kCompute = 128;  // threads of the recurrence
+constexpr int kHelp = 128;     // threads of a helper group; group g serves stage g
+constexpr int kGroups = 2;     // stages: tiles g, g + kGroups, ... pass through stage g
+constexpr int kThreads = kCompute + kGroups * kHelp;
+constexpr int kPairs = 1024;   // (token, channel) pairs of a tile
+constexpr int kV = 8;          // adjacent channels of a token: a helper's pairs of a tile
 
-template <typename IO, typename OUT, int NS>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs p) {
-  constexpr int LPC = NS / 4;             // lanes per channel
-  constexpr int CT = kThreads / LPC;      // channels per block
-  constexpr int TT = kPairs / CT;         // tokens per tile
-  constexpr int VPT = CT / kV;            // threads per token of a tile
-  constexpr int BC = (TT * NS + kThreads - 1) / kThreads;  // b (and c) elements per thread
+// Named barriers 1, 2: stage 0, 1 prepared; 3, 4: stage 0, 1 used.  Each joins the
+// compute warps and one helper group.
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCompute + kHelp) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kCompute + kHelp) : "memory");
+}
 
+// What a chunked call keeps between its launches.
+struct FwdSpace {
+  float* h;    // [slots][D][NS]: what a chunk adds, then the state in front of it
+  float* sum;  // [slots][D]: its step sizes
+};
+
+// The layout of a tile's shared memory.
+template <typename IO, int NS> struct Tile {
+  static constexpr int LPC = NS / 8;              // lanes per channel
+  static constexpr int CPW = 32 / LPC;            // channels per warp
+  static constexpr int CT = kCompute / LPC;       // channels per block
+  static constexpr int TT = kPairs / CT;          // tokens per tile
+  static constexpr int NP = LPC > 1 ? 2 : 1;      // terms of a pair's sum over n
+  static constexpr int HELD = 4 * NP / LPC;       // tokens (of 4) whose term a lane holds
+  float2 d[kGroups][TT * CT];                     // (delta, delta u); see dd_at
+  float b[kGroups][TT][NS], c[kGroups][TT][NS];
+  float y[kGroups][NP][TT][CT];
+  // rows as they come, each thread its own: of the tile in the stage, of the next
+  // one of the group, and of those whose copies are in flight
+  static constexpr int AHEAD = sizeof(IO) == 2 ? 2 : 1, RING = AHEAD + 2;
+  Raw<IO, kV> u[kGroups][RING][kHelp], dt[kGroups][RING][kHelp], z[kGroups][RING][kHelp];
+  // Place of channel ch in a row of d: its 16-byte unit (two channels) is moved
+  // within its 128 bytes so that the helpers' stores, 64 bytes apart, spread
+  // over the banks.
+  static __device__ __forceinline__ int dd_at(int ch) {
+    const int unit = ch >> 1;
+    return (unit ^ ((unit >> 3) & 3)) * 2 + (ch & 1);
+  }
+};
+
+// Sums y[0 .. 4) over the lanes of a channel but one pair: afterwards a lane
+// holds HELD of the four, from *first on, as one of NP terms.
+template <int LPC, int CPW>
+__device__ __forceinline__ void reduce_states(float (&y)[4], int q, int* first) {
+  constexpr unsigned full = 0xffffffffu;
+  *first = 0;
+  if constexpr (LPC >= 4) {
+    const bool up = (q & (LPC / 2)) != 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float give = up ? y[k] : y[k + 2], keep = up ? y[k + 2] : y[k];
+      y[k] = keep + __shfl_xor_sync(full, give, CPW * LPC / 2);
+    }
+    *first = up ? 2 : 0;
+  }
+  if constexpr (LPC >= 8) {
+    const bool up = (q & (LPC / 4)) != 0;
+    const float give = up ? y[0] : y[1], keep = up ? y[1] : y[0];
+    y[0] = keep + __shfl_xor_sync(full, give, CPW * LPC / 4);
+    *first += up ? 1 : 0;
+  }
+}
+
+// SUMS: the first of the three launches; else the scan itself, from init_state
+// (chunk 0: one run per sequence) or from w.h.
+template <typename IO, typename OUT, int NS, bool SUMS>
+__global__ void __launch_bounds__(kThreads)
+scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
+  using L = Tile<IO, NS>;
+  constexpr int LPC = L::LPC, CT = L::CT, TT = L::TT;
   extern __shared__ __align__(16) unsigned char smem[];
-  auto s_d = reinterpret_cast<float2 (*)[TT][CT]>(smem);  // [2]: delta, delta u
-  auto s_b = reinterpret_cast<float (*)[TT][NS]>(smem + 2 * kPairs * 8);
-  auto s_c = s_b + 2;
-  auto s_y = reinterpret_cast<float (*)[TT][CT]>(s_c + 2);
+  L& s = *reinterpret_cast<L*>(smem);
 
-  const int tid = threadIdx.x;
-  const int q = tid % LPC, lc = tid / LPC;        // the recurrence's role
   const int tiles = (p.D + CT - 1) / CT;
   const int d0 = (int)(blockIdx.x % tiles) * CT;
-  const int ch = min(d0 + lc, p.D - 1);
-  const int vt = tid / VPT, vc = (tid % VPT) * kV;  // the pairs' role
-  const bool von = d0 + vc < p.D;
-  const int s = (int)(blockIdx.x / tiles);
-  const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
+  const long long slot = blockIdx.x / tiles;
+  Chunk k;
+  if (chunk) {
+    k = chunk_of_slot(p, slot, chunk);
+    if (!k.ok || (SUMS && k.last)) return;
+  } else {
+    k.s = (int)slot;
+    if (!seq_ok(p, k.s, threadIdx.x == 0, &k.t0, &k.t1)) return;
+    k.last = true;
+  }
+  const int tiles_t = (int)((k.t1 - k.t0 + TT - 1) / TT);
 
-  long long lo, hi;
-  seq_rows(p.cu_seqlens, s, p.T, &lo, &hi);
-  if (lo < 0 || hi < lo || hi > rows || (p.cu_seqlens && (__ldg(p.cu_seqlens) != 0 ||
-                                                         __ldg(p.cu_seqlens + p.B) != rows))) {
-    if (tid == 0) atomicOr(p.status, kDevBadSeqlens);
+  if (threadIdx.x < kCompute) {
+    const int lane = threadIdx.x & 31, q = lane / L::CPW;
+    const int lc = (threadIdx.x >> 5) * L::CPW + lane % L::CPW;
+    const int ch = min(d0 + lc, p.D - 1);
+    auto load8 = [&](const float* from, f32x2 (&v)[4], float scale) {
+      const float4* r = reinterpret_cast<const float4*>(from + (long long)ch * NS) + q * 2;
+      const float4 x = r[0], y = r[1];
+      v[0] = pack2(x.x * scale, x.y * scale);
+      v[1] = pack2(x.z * scale, x.w * scale);
+      v[2] = pack2(y.x * scale, y.y * scale);
+      v[3] = pack2(y.z * scale, y.w * scale);
+    };
+    f32x2 a[4], h[4] = {0, 0, 0, 0};
+    load8(p.a, a, kLog2e);
+    if (!SUMS) {
+      const float* from = chunk ? w.h + slot * p.D * NS
+                                : p.init_state ? p.init_state + (long long)k.s * p.D * NS : nullptr;
+      if (from) load8(from, h, 1.f);
+    }
+    const int at = L::dd_at(lc);
+    float sum = 0.f;
+    for (int i = 0; i < tiles_t; ++i) {
+      const int buf = i & 1;
+      bar_sync(1 + buf);
+      const float2* sd = &s.d[buf][at];
+      const float* sb = &s.b[buf][0][q * 8];
+      const float* sc = &s.c[buf][0][q * 8];
+      // Token t's row of d, b, c, in registers from two tokens before its use;
+      // its decays from one token before.  (The two rows read behind the tile's
+      // last lie in the arrays behind; nothing comes of them.)
+      struct Row {
+        float2 d;
+        f32x2 b[4], c[4];
+      };
+      auto fetch = [&](int t, Row& r) {
+        r.d = sd[t * CT];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float4 v = reinterpret_cast<const float4*>(sb + t * NS)[m];
+          r.b[2 * m] = pack2(v.x, v.y);
+          r.b[2 * m + 1] = pack2(v.z, v.w);
+          if (!SUMS) {
+            const float4 x = reinterpret_cast<const float4*>(sc + t * NS)[m];
+            r.c[2 * m] = pack2(x.x, x.y);
+            r.c[2 * m + 1] = pack2(x.z, x.w);
+          }
+        }
+      };
+      Row r[4];  // token t in r[t % 4]
+      f32x2 e[4];
+      fetch(0, r[0]);
+      fetch(1, r[1]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) e[m] = ex2x2(mul2(both(r[0].d.x), a[m]));
+#pragma unroll 1
+      for (int t4 = 0; t4 < TT; t4 += 4) {
+        float y[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          fetch(t4 + x + 2, r[(x + 2) % 4]);
+          const Row& cur = r[x];
+          const f32x2 dl = both(r[(x + 1) % 4].d.x), du = both(cur.d.y);
+          f32x2 ys = 0;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const f32x2 en = ex2x2(mul2(dl, a[m]));
+            h[m] = fma2(e[m], h[m], mul2(du, cur.b[m]));
+            if (!SUMS) ys = m == 0 ? mul2(cur.c[0], h[0]) : fma2(cur.c[m], h[m], ys);
+            e[m] = en;
+          }
+          if (SUMS) {
+            sum += cur.d.x;
+          } else {
+            float y0, y1;
+            unpack2(ys, &y0, &y1);
+            y[x] = y0 + y1;
+          }
+        }
+        if constexpr (!SUMS) {
+          int first;
+          reduce_states<LPC, L::CPW>(y, q, &first);
+#pragma unroll
+          for (int m = 0; m < L::HELD; ++m) s.y[buf][q & (L::NP - 1)][t4 + first + m][lc] = y[m];
+        }
+      }
+      bar_arrive(3 + buf);
+    }
+    if (d0 + lc < p.D) {
+      float* to = SUMS ? w.h + slot * p.D * NS
+                       : k.last && p.final_state ? p.final_state + (long long)k.s * p.D * NS : nullptr;
+      if (to) {
+        float4* r = reinterpret_cast<float4*>(to + (long long)ch * NS) + q * 2;
+        float4 x, y;
+        unpack2(h[0], &x.x, &x.y);
+        unpack2(h[1], &x.z, &x.w);
+        unpack2(h[2], &y.x, &y.y);
+        unpack2(h[3], &y.z, &y.w);
+        r[0] = x;
+        r[1] = y;
+      }
+      if (SUMS && q == 0) w.sum[slot * p.D + ch] = sum;
+    }
     return;
   }
 
-  float a2[4], h[4];
-  {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.a + (long long)ch * NS) + q);
-    a2[0] = a.x * kLog2e; a2[1] = a.y * kLog2e; a2[2] = a.z * kLog2e; a2[3] = a.w * kLog2e;
-    float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.init_state)
-      h0 = *(reinterpret_cast<const float4*>(p.init_state + ((long long)s * p.D + ch) * NS) + q);
-    h[0] = h0.x; h[1] = h0.y; h[2] = h0.z; h[3] = h0.w;
-  }
-  float bias[kV], skip[kV];
+  // the helper groups: a thread owns kV channels of one token of its tiles
+  const int tid = (threadIdx.x - kCompute) % kHelp, g = (threadIdx.x - kCompute) / kHelp;
+  constexpr int VPT = CT / kV;            // threads per token
+  const int vt = tid / VPT, vc = (tid % VPT) * kV;
+  const bool von = d0 + vc < p.D;
+  f32x2 bias[kV / 2], skip[kV / 2];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    bias[i] = von && p.dt_bias ? __ldg(p.dt_bias + d0 + vc + i) : 0.f;
-    skip[i] = von && p.skip ? __ldg(p.skip + d0 + vc + i) : 0.f;
+  for (int i = 0; i < kV / 2; ++i) {
+    const int ch = d0 + vc + 2 * i;
+    bias[i] = von && p.dt_bias ? pack2(__ldg(p.dt_bias + ch), __ldg(p.dt_bias + ch + 1)) : 0;
+    skip[i] = !SUMS && von && p.skip ? pack2(__ldg(p.skip + ch), __ldg(p.skip + ch + 1)) : 0;
   }
-
   using R = Raw<IO, kV>;
-  R ru = zero_raw<IO, kV>(), rdt = ru, rz = ru, fu = ru, fz = ru;  // next tile; tile to finish
-  IO rb[BC], rc[BC];
-  auto load = [&](long long t0) {
-    const long long t = t0 + vt;
-    ru = rdt = rz = zero_raw<IO, kV>();
-    if (t < hi && von) {
-      ru = *reinterpret_cast<const R*>((const IO*)p.u + t * p.u_stride + d0 + vc);
-      rdt = *reinterpret_cast<const R*>((const IO*)p.dt + t * p.dt_stride + d0 + vc);
-      if (p.z) rz = *reinterpret_cast<const R*>((const IO*)p.z + t * p.z_stride + d0 + vc);
-    }
+  constexpr int BC = (TT * NS + kHelp - 1) / kHelp;  // b (and c) elements per thread and tile
+  constexpr bool AHEAD = BC <= 4;                    // ... kept in registers a group's tile ahead
+  constexpr int STEP = kGroups * TT;                 // tokens from a group's tile to its next
+  IO rb[AHEAD ? BC : 1], rc[AHEAD ? BC : 1];
+  const long long row = k.t0 + g * TT + vt;
+  const IO* pu = (const IO*)p.u + row * p.u_stride + d0 + vc;
+  const IO* pd = (const IO*)p.dt + row * p.dt_stride + d0 + vc;
+  const IO* pz = !SUMS && p.z ? (const IO*)p.z + row * p.z_stride + d0 + vc : nullptr;
+  OUT* po = (OUT*)p.out + row * p.D + d0 + vc;
+  const int left = (int)(k.t1 - k.t0);               // tokens of the run
+  const IO* pb = (const IO*)p.b + k.t0 * p.b_stride;
+  const IO* pc = (const IO*)p.c + k.t0 * p.c_stride;
+  auto copy = [](R* to, const IO* from) {
 #pragma unroll
-    for (int k = 0; k < BC; ++k) {
-      const int i = tid + k * kThreads;
-      const long long tb = t0 + i / NS;
-      rb[k] = rc[k] = from_f32<IO>(0.f);
-      if (i < TT * NS && tb < hi) {
-        rb[k] = ((const IO*)p.b)[tb * p.b_stride + i % NS];
-        rc[k] = ((const IO*)p.c)[tb * p.c_stride + i % NS];
-      }
-    }
+    for (int i = 0; i < (int)sizeof(R) / 16; ++i)
+      cp_async16(reinterpret_cast<char*>(to) + 16 * i, reinterpret_cast<const char*>(from) + 16 * i);
   };
-  auto finish = [&](long long t0, int buf) {  // y of the pairs whose u and z are in fu, fz
-    const long long t = t0 + vt;
-    if (t >= hi || !von) return;
-    float u[kV], z[kV], y[kV];
-    unpack_as<IO, kV>(fu, u);
-    unpack_as<IO, kV>(fz, z);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      y[i] = fmaf(skip[i], u[i], s_y[buf][vt][vc + i]);
-      if (p.z) y[i] *= silu(z[i]);
+  int put = 0, get = 0;           // ring places of the next tile to load and to prepare
+  auto next = [](int i) { return i + 1 == L::RING ? 0 : i + 1; };
+  int t_load = g * TT + vt;       // this thread's token in the next tile to load
+  auto load = [&]() {             // always one group of copies, even of nothing
+    if (t_load < left && von) {
+      copy(&s.u[g][put][tid], pu);
+      copy(&s.dt[g][put][tid], pd);
+      if (!SUMS && p.z) copy(&s.z[g][put][tid], pz);
     }
-    *reinterpret_cast<Raw<OUT, kV>*>((OUT*)p.out + t * p.D + d0 + vc) = pack_as<OUT, kV>(y);
+    cp_commit();
+    put = next(put);
+    t_load += STEP;
+    pu += STEP * p.u_stride;
+    pd += STEP * p.dt_stride;
+    if (!SUMS && p.z) pz += STEP * p.z_stride;
   };
-
-  load(lo);
-  int buf = 0;
-  for (long long t0 = lo; t0 < hi; t0 += TT, buf ^= 1) {
-    {
-      float u[kV], x[kV];
-      unpack_as<IO, kV>(ru, u);
-      unpack_as<IO, kV>(rdt, x);
-      const bool in = t0 + vt < hi;
+  auto load_bc = [&](int t0) {
+    if constexpr (AHEAD) {
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        float delta = x[i] + bias[i];
-        if (p.softplus) delta = softplus(delta);
-        // tokens behind the sequence: decay 1, no drive
-        s_d[buf][vt][vc + i] = in ? make_float2(delta, delta * u[i]) : make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int k = 0; k < BC; ++k) {
-        const int i = tid + k * kThreads;
-        if (i < TT * NS) {
-          (&s_b[buf][0][0])[i] = to_f32(rb[k]);
-          (&s_c[buf][0][0])[i] = to_f32(rc[k]);
+      for (int e = 0; e < BC; ++e) {
+        const int x = tid + e * kHelp, t = t0 + x / NS;
+        rb[e] = rc[e] = from_f32<IO>(0.f);
+        if (t < left && x < TT * NS) {
+          rb[e] = pb[t * p.b_stride + x % NS];
+          if (!SUMS) rc[e] = pc[t * p.c_stride + x % NS];
         }
       }
     }
-    __syncthreads();
-    if (t0 > lo) finish(t0 - TT, buf ^ 1);
-    fu = ru;
-    fz = rz;
-    if (t0 + TT < hi) load(t0 + TT);
-#pragma unroll 2
-    for (int t4 = 0; t4 < TT; t4 += 4) {
-      float y[4];
+  };
+  auto store_bc = [&](int t0) {
+    float* sb = &s.b[g][0][0];
+    float* sc = &s.c[g][0][0];
+    if constexpr (AHEAD) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 dd = s_d[buf][t4 + k][lc];
-        const float4 b = *reinterpret_cast<const float4*>(&s_b[buf][t4 + k][q * 4]);
-        const float4 c = *reinterpret_cast<const float4*>(&s_c[buf][t4 + k][q * 4]);
-        h[0] = fmaf(ex2(dd.x * a2[0]), h[0], dd.y * b.x);
-        h[1] = fmaf(ex2(dd.x * a2[1]), h[1], dd.y * b.y);
-        h[2] = fmaf(ex2(dd.x * a2[2]), h[2], dd.y * b.z);
-        h[3] = fmaf(ex2(dd.x * a2[3]), h[3], dd.y * b.w);
-        y[k] = fmaf(c.x, h[0], fmaf(c.y, h[1], fmaf(c.z, h[2], c.w * h[3])));
+      for (int e = 0; e < BC; ++e) {
+        const int x = tid + e * kHelp;
+        if (TT * NS % kHelp != 0 && x >= TT * NS) break;
+        sb[x] = to_f32(rb[e]);
+        if (!SUMS) sc[x] = to_f32(rc[e]);
       }
-      int first;
-      reduce4<LPC>(y, q, &first);
-      if constexpr (LPC == 2) {
-        s_y[buf][t4 + first][lc] = y[0];
-        s_y[buf][t4 + first + 1][lc] = y[1];
-      } else {
-        if (q % (LPC / 4) == 0) s_y[buf][t4 + first][lc] = y[0];
+    } else {
+#pragma unroll 8
+      for (int e = 0; e < BC; ++e) {
+        const int x = tid + e * kHelp, t = t0 + x / NS;
+        sb[x] = t < left ? to_f32(pb[t * p.b_stride + x % NS]) : 0.f;
+        if (!SUMS) sc[x] = t < left ? to_f32(pc[t * p.c_stride + x % NS]) : 0.f;
       }
     }
+  };
+
+  load_bc(g * TT);
+#pragma unroll
+  for (int i = 0; i <= L::AHEAD; ++i) load();
+  int last = 0;                   // ring place of the tile in the stage
+  // one pass per tile of the group, and one to finish the last
+  for (int tile = g; tile < tiles_t + kGroups; tile += kGroups) {
+    const bool more = tile < tiles_t, prior = tile >= kGroups;
+    const int t = tile * TT + vt;
+    // (delta, delta u) of the tile, before its stage is free
+    f32x2 u[kV / 2], x[kV / 2];
+#pragma unroll
+    for (int j = 0; j < kV / 2; ++j) x[j] = u[j] = 0;  // behind the run: decay 1, no drive
+    if (more) {
+      cp_wait<L::AHEAD>();
+      if (t < left && von) {
+        unpack_pairs<IO, kV>(s.u[g][get][tid], u);
+        unpack_pairs<IO, kV>(s.dt[g][get][tid], x);
+#pragma unroll
+        for (int j = 0; j < kV / 2; ++j) {
+          x[j] = add2(x[j], bias[j]);
+          if (p.softplus) x[j] = softplus2(x[j]);
+          u[j] = mul2(x[j], u[j]);
+        }
+      }
+    }
+    f32x2 y[kV / 2];
+    if (prior) {
+      bar_sync(3 + g);
+      if (!SUMS) {
+#pragma unroll
+        for (int m = 0; m < kV / 4; ++m) {
+          const float4 v = *reinterpret_cast<const float4*>(&s.y[g][0][vt][vc + 4 * m]);
+          y[2 * m] = pack2(v.x, v.y);
+          y[2 * m + 1] = pack2(v.z, v.w);
+          if (L::NP == 2) {
+            const float4 v2 = *reinterpret_cast<const float4*>(&s.y[g][L::NP - 1][vt][vc + 4 * m]);
+            y[2 * m] = add2(y[2 * m], pack2(v2.x, v2.y));
+            y[2 * m + 1] = add2(y[2 * m + 1], pack2(v2.z, v2.w));
+          }
+        }
+      }
+    }
+    if (more) {
+      store_bc(tile * TT);
+#pragma unroll
+      for (int j = 0; j < kV / 2; ++j) {
+        float d0v, d1v, u0, u1;
+        unpack2(x[j], &d0v, &d1v);
+        unpack2(u[j], &u0, &u1);
+        *reinterpret_cast<float4*>(&s.d[g][vt * CT + L::dd_at(vc + 2 * j)]) =
+            make_float4(d0v, u0, d1v, u1);
+      }
+      bar_arrive(1 + g);
+      load_bc((tile + kGroups) * TT);
+    }
+    if (!SUMS && prior && t - STEP < left && von) {
+      f32x2 z[kV / 2];
+      float o[kV];
+      unpack_pairs<IO, kV>(s.u[g][last][tid], u);
+      if (p.z) unpack_pairs<IO, kV>(s.z[g][last][tid], z);
+#pragma unroll
+      for (int j = 0; j < kV / 2; ++j) {
+        f32x2 v = fma2(skip[j], u[j], y[j]);
+        if (p.z) v = mul2(v, mul2(z[j], sigmoid2(z[j])));
+        unpack2(v, &o[2 * j], &o[2 * j + 1]);
+      }
+      store_raw<OUT, kV>(po, pack_as<OUT, kV>(o));
+    }
+    if (prior) po += STEP * (long long)p.D;
+    last = get;
+    get = next(get);
+    if (more) load();
   }
-  __syncthreads();
-  if (hi > lo) finish(lo + (hi - lo - 1) / TT * TT, buf ^ 1);
-  if (p.final_state && d0 + lc < p.D)
-    *(reinterpret_cast<float4*>(p.final_state + ((long long)s * p.D + d0 + lc) * NS) + q) =
-        make_float4(h[0], h[1], h[2], h[3]);
+  cp_wait<0>();
 }
 
-template <typename IO, typename OUT, int NS>
-cudaError_t launch_typed(const ScanArgs& a, cudaStream_t stream) {
-  constexpr int CT = kThreads / (NS / 4), TT = kPairs / CT;
-  constexpr int smem = 2 * (kPairs * 12 + 2 * TT * NS * 4);
-  auto kernel = scan_fwd_kernel<IO, OUT, NS>;
+// The states in front of the chunks, and the final states of empty sequences.
+__global__ void __launch_bounds__(128)
+scan_fwd_chunks_kernel(ScanArgs p, FwdSpace w, long long chunk) {
+  const int quads = p.NS / 4;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long per = (long long)p.D * quads;
+  if (i >= per * p.B) return;
+  const int s = (int)(i / per);
+  const long long in = i % per;
+  long long lo, hi;
+  if (!seq_ok(p, s, in == 0, &lo, &hi)) return;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.init_state) run = reinterpret_cast<const float4*>(p.init_state)[(long long)s * per + in];
+  if (lo == hi) {
+    if (p.final_state) reinterpret_cast<float4*>(p.final_state)[(long long)s * per + in] = run;
+    return;
+  }
+  float4 x = __ldg(reinterpret_cast<const float4*>(p.a) + in);
+  x.x *= kLog2e; x.y *= kLog2e; x.z *= kLog2e; x.w *= kLog2e;
+  // the last chunk's own sums were left out: its slot only receives a state
+  const long long f = first_slot(p, s, chunk), n = (hi - lo + chunk - 1) / chunk;
+  scan_chunks(reinterpret_cast<float4*>(w.h), w.sum, x, f, n - 1, per, in, p.D, (int)(in / quads),
+              false, &run);
+  reinterpret_cast<float4*>(w.h)[(f + n - 1) * per + in] = run;
+}
+
+template <typename IO, typename OUT, int NS, bool SUMS>
+cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk, long long runs,
+                          cudaStream_t stream) {
+  constexpr int CT = Tile<IO, NS>::CT, smem = (int)sizeof(Tile<IO, NS>);
+  auto kernel = scan_fwd_kernel<IO, OUT, NS, SUMS>;
   if constexpr (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * a.B), kThreads, smem, stream>>>(a);
+  kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * runs), kThreads, smem, stream>>>(a, w,
+                                                                                        chunk);
   return cudaGetLastError();
 }
 
+// The chunk length of a call, 0 for whole sequences.  In units of a block's time
+// for one token (about 0.06 us at NS = 16, one or two blocks a SM): whole
+// sequences take the longest one times the waves of blocks; chunks take 1.7
+// times the work (the extra pass) spread over all SMs, and about 100 for two more
+// launches.  A packed call's longest sequence is not known here: 2.5 times the
+// mean.  Measured, D = 2048 and NS = 16, whole against best chunk: 4 x 2048
+// tokens 122 and 187 us, 1 x 2048 121 and 58 (512), 1 x 512 33 and 21 (128),
+// three packed sequences of 20001 tokens 830 and 415 (1024).
+long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
+  constexpr long long kSMs = 152;
+  const long long tiles = ((long long)D * NS + 1023) / 1024, work = rows * tiles / kSMs;
+  long long longest = (rows + B - 1) / B;
+  if (packed) longest = longest * 5 / 2 < rows ? longest * 5 / 2 : rows;
+  const long long whole = (B * tiles + kSMs - 1) / kSMs * longest;
+  if (work * 17 / 10 + 100 >= whole) return 0;
+  long long chunk = 64;
+  while (chunk < work && chunk < 1024) chunk *= 2;
+  return chunk;
+}
+
+template <typename IO, typename OUT, int NS>
+cudaError_t launch_typed(const ScanArgs& a, void* workspace, cudaStream_t stream) {
+  const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
+  const long long chunk = rows > 0 ? chunk_rule(a.B, rows, a.D, NS, a.cu_seqlens != nullptr) : 0;
+  if (chunk == 0) return launch_kernel<IO, OUT, NS, false>(a, FwdSpace{}, 0, a.B, stream);
+  const long long slots = slots_of(a.B, rows, chunk);
+  FwdSpace w;
+  w.h = static_cast<float*>(workspace);
+  w.sum = w.h + slots * a.D * NS;
+  cudaError_t e = launch_kernel<IO, OUT, NS, true>(a, w, chunk, slots, stream);
+  if (e != cudaSuccess) return e;
+  const long long per = (long long)a.B * a.D * (NS / 4);
+  scan_fwd_chunks_kernel<<<(unsigned)((per + 127) / 128), 128, 0, stream>>>(a, w, chunk);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_kernel<IO, OUT, NS, false>(a, w, chunk, slots, stream);
+}
+
 template <typename IO, typename OUT>
-cudaError_t launch_io(const ScanArgs& a, cudaStream_t stream) {
+cudaError_t launch_io(const ScanArgs& a, void* workspace, cudaStream_t stream) {
   switch (a.NS) {
-    case 8: return launch_typed<IO, OUT, 8>(a, stream);
-    case 16: return launch_typed<IO, OUT, 16>(a, stream);
-    case 32: return launch_typed<IO, OUT, 32>(a, stream);
-    default: return launch_typed<IO, OUT, 64>(a, stream);
+    case 8: return launch_typed<IO, OUT, 8>(a, workspace, stream);
+    case 16: return launch_typed<IO, OUT, 16>(a, workspace, stream);
+    case 32: return launch_typed<IO, OUT, 32>(a, workspace, stream);
+    default: return launch_typed<IO, OUT, 64>(a, workspace, stream);
   }
 }
 
 }  // namespace
 
-size_t scan_fwd_workspace(int, long long, int, int) { return 0; }
+size_t scan_fwd_workspace(int B, long long rows, int D, int NS, bool packed) {
+  const long long chunk = chunk_rule(B, rows, D, NS, packed);
+  return chunk ? (size_t)slots_of(B, rows, chunk) * D * (NS + 1) * 4 : 0;
+}
 
-cudaError_t launch_scan_fwd(const ScanArgs& a, void*, cudaStream_t stream) {
-  if (a.fp32_io) return launch_io<float, float>(a, stream);
-  if (a.fp32_out) return launch_io<__nv_bfloat16, float>(a, stream);
-  return launch_io<__nv_bfloat16, __nv_bfloat16>(a, stream);
+cudaError_t launch_scan_fwd(const ScanArgs& a, void* workspace, cudaStream_t stream) {
+  if (a.fp32_io) return launch_io<float, float>(a, workspace, stream);
+  if (a.fp32_out) return launch_io<__nv_bfloat16, float>(a, workspace, stream);
+  return launch_io<__nv_bfloat16, __nv_bfloat16>(a, workspace, stream);
 }
 
 }  // namespace gla

@@ -38,49 +38,14 @@ constexpr int kCH = 64;    // tokens per chunk
 constexpr int kSub = 8;    // tokens per recomputed group
 constexpr int kV = 4;      // adjacent channels per load
 
-// The tile a block works on: chunk `c` of sequence `s` lies in rows [t0, t1);
-// slot is its place in the chunk arrays.
-struct Chunk {
-  long long t0, t1;
-  int s;
-  bool ok;
-};
-
-// Chunk slots: sequence s owns the slots from cu[s] / kCH + s on, which leaves
-// room for ceil(length / kCH) of them for any lengths.
-__device__ __forceinline__ long long first_slot(const ScanArgs& p, int s) {
-  const long long lo = p.cu_seqlens ? __ldg(p.cu_seqlens + s) : (long long)s * p.T;
-  return lo / kCH + s;
-}
-
-__device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& p, long long slot) {
-  int lo = 0, hi = p.B - 1;  // the last s with first_slot(s) <= slot
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_slot(p, mid) <= slot) lo = mid;
-    else hi = mid - 1;
-  }
-  const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
-  long long a, b;
-  seq_rows(p.cu_seqlens, lo, p.T, &a, &b);
-  const long long c = slot - first_slot(p, lo);
-  Chunk k;
-  k.s = lo;
-  k.ok = a >= 0 && b >= a && b <= rows && c >= 0 && a + c * kCH < b;
-  k.t0 = a + c * kCH;
-  k.t1 = min(k.t0 + kCH, b);
-  return k;
-}
-
 // Workspace, in floats: h and e [slots][D][NS], sums [slots][D] x 2, partials
 // of db and dc [channel tiles][rows][2 NS].
 struct Space {
   float *h, *e, *sum, *sum2, *part;
   size_t floats;
 };
-__host__ __device__ inline long long slots_of(int B, long long rows) { return rows / kCH + B; }
 inline Space space_of(float* base, int B, long long rows, int D, int NS) {
-  const size_t slots = (size_t)slots_of(B, rows);
+  const size_t slots = (size_t)slots_of(B, rows, kCH);
   const size_t tiles = ((size_t)D * NS + 1023) / 1024;
   Space w;
   size_t at = 0;
@@ -102,7 +67,7 @@ template <typename IO>
 __device__ __forceinline__ void load4(const void* base, long long row, long long stride, int ch,
                                       float (&x)[kV]) {
   unpack_as<IO, kV>(
-      *reinterpret_cast<const Raw<IO, kV>*>((const IO*)base + row * stride + ch), x);
+      load_raw<IO, kV>((const IO*)base + row * stride + ch), x);
 }
 
 // delta, u and g of the chunk's pairs, and b, c, into shared memory (zeros for
@@ -174,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) chunk_sums_kernel(ScanBwdArgs a, Spa
   const int tiles = (p.D + CT - 1) / CT;
   const long long slot = blockIdx.x / tiles;
   const int d0 = (int)(blockIdx.x % tiles) * CT;
-  const Chunk k = chunk_of_slot(p, slot);
+  const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) return;
   const int q = threadIdx.x % LPC, lc = threadIdx.x / LPC, ch = d0 + lc;
   stage<IO, NS, CT, false>(a, k, d0, s_delta, s_u, s_g, nullptr, s_b, s_c);
@@ -221,14 +186,8 @@ chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
   const long long in = i % per;  // channel * quads + quad
   const int ch = (int)(in / quads);
   long long lo, hi;
-  seq_rows(p.cu_seqlens, s, p.T, &lo, &hi);
-  const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
-  if (lo < 0 || hi < lo || hi > rows ||
-      (p.cu_seqlens && (__ldg(p.cu_seqlens) != 0 || __ldg(p.cu_seqlens + p.B) != rows))) {
-    if (in == 0) atomicOr(p.status, kDevBadSeqlens);
-    return;
-  }
-  const long long f = first_slot(p, s);
+  if (!seq_ok(p, s, in == 0, &lo, &hi)) return;
+  const long long f = first_slot(p, s, kCH);
   const long long n = min((hi - lo + kCH - 1) / kCH, slots - f);
   float4 x = __ldg(reinterpret_cast<const float4*>(p.a) + in);
   x.x *= kLog2e; x.y *= kLog2e; x.z *= kLog2e; x.w *= kLog2e;
@@ -236,30 +195,8 @@ chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
   const bool back = blockIdx.y != 0;
   const float* start = back ? a.d_final_state : p.init_state;
   if (start) run = reinterpret_cast<const float4*>(start)[(long long)s * per + in];
-  float4* v = reinterpret_cast<float4*>(back ? w.e : w.h);
-  constexpr int U = 4;
-  for (long long c0 = 0; c0 < n; c0 += U) {
-    float4 y[U];
-    float sum[U];
-    long long at[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long c = min(c0 + u, n - 1);
-      at[u] = f + (back ? n - 1 - c : c);
-      y[u] = v[at[u] * per + in];
-      sum[u] = w.sum[at[u] * p.D + ch];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c0 + u < n) {
-        v[at[u] * per + in] = run;
-        run.x = fmaf(ex2(x.x * sum[u]), run.x, y[u].x);
-        run.y = fmaf(ex2(x.y * sum[u]), run.y, y[u].y);
-        run.z = fmaf(ex2(x.z * sum[u]), run.z, y[u].z);
-        run.w = fmaf(ex2(x.w * sum[u]), run.w, y[u].w);
-      }
-    }
-  }
+  scan_chunks(reinterpret_cast<float4*>(back ? w.e : w.h), w.sum, x, f, n, per, in, p.D, ch, back,
+              &run);
   if (back && a.d_init_state) reinterpret_cast<float4*>(a.d_init_state)[(long long)s * per + in] = run;
 }
 
@@ -310,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
   const int q = tid % LPC, lc = tid / LPC, ch = d0 + lc;
   const bool on = ch < p.D;
   const long long at = (slot * p.D + ch) * NS + q * 4;
-  const Chunk k = chunk_of_slot(p, slot);
+  const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) {  // no chunk: its partials count as zero
     if (on) {
       *reinterpret_cast<float4*>(w.h + at) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -459,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       auto put = [&](void* to, const float* from) {
         const float4 x = *reinterpret_cast<const float4*>(from);
         const float y[kV] = {x.x, x.y, x.z, x.w};
-        *reinterpret_cast<Raw<OUT, kV>*>((OUT*)to + o) = pack_as<OUT, kV>(y);
+        store_raw<OUT, kV>((OUT*)to + o, pack_as<OUT, kV>(y));
       };
       put(a.du, &s_u[t][vc]);
       put(a.ddt, &s_delta[t][vc]);
@@ -525,7 +462,7 @@ cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t str
   constexpr int CT = channel_tile<NS>();
   const ScanArgs& p = a.f;
   const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
-  const long long slots = slots_of(p.B, rows);
+  const long long slots = slots_of(p.B, rows, kCH);
   const int tiles = (p.D + CT - 1) / CT;
   const Space w = space_of(static_cast<float*>(workspace), p.B, rows, p.D, NS);
   constexpr int staged = 2 * kCH * NS * 4;

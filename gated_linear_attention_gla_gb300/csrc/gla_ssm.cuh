@@ -8,7 +8,6 @@
 namespace gla {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eLo = 1.9259629891e-8f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^x by the hardware's approximation (flushes subnormal results to zero).
@@ -18,86 +17,177 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x by the hardware's approximation (1 / inf = 0).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // x / (1 + e^-x)
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + ex2(-kLog2e * x)); }
-__device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.f, 1.f + ex2(-kLog2e * x));
-}
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// e^-|x| with a relative error of a few 2^-24 (|x| up to 100; beyond that it
-// is zero in fp32 anyway): the product with log2(e) is split, and what its
-// rounding loses multiplies the result.
-__device__ __forceinline__ float exp_neg_abs(float x) {
-  const float m = -fminf(fabsf(x), 100.f);
-  const float t = m * kLog2e;
-  const float r = fmaf(m, kLog2e, -t) + m * kLog2eLo;
-  const float e = ex2(t);
-  return fmaf(e, r * kLn2, e);
+// Two fp32 values in one register pair: one instruction works on both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
+__device__ __forceinline__ void unpack2(f32x2 v, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// a * b as a * b - 0: the same value, and one instruction where mul.f32x2 measured two
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  return fma2(a, b, 0x8000000080000000ull);
+}
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {  // 2^x of both
+  float x, y;
+  unpack2(v, &x, &y);
+  return pack2(ex2(x), ex2(y));
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
 
-// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].  log1p(e) =
-// 2 atanh(s) with s = e / (2 + e) <= 1/3: the series 2 s (1 + s^2/3 + s^4/5 +
-// ...) up to s^12/13 leaves a relative remainder below s^14/15 < 2e-8, and
-// keeps the relative accuracy for the small values (1e-4 .. 1e-1) that step
-// sizes have.  *sig receives 1 / (1 + e^-x), its derivative.  A NaN stays one.
+// log(1 + e^x) of two values = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].
+// log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, and atanh(s) / s is a
+// polynomial in s^2 <= 1/9: the degree-4 one below (fitted for the least
+// relative error there) is off by 4e-9.  So the small step sizes (1e-4 ..
+// 1e-1) keep their relative accuracy: below 1e-6 for |x| <= 12, 1e-7 on
+// average, from the rounding of x log2(e).  A NaN stays one.
+__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+  float a, b;
+  unpack2(v, &a, &b);
+  const f32x2 e = ex2x2(mul2(pack2(fabsf(a), fabsf(b)), both(-kLog2e)));
+  float d0, d1;
+  unpack2(add2(e, both(2.f)), &d0, &d1);
+  const f32x2 s = mul2(e, pack2(rcp(d0), rcp(d1)));
+  const f32x2 z = mul2(s, s);
+  f32x2 p = fma2(both(0.14089167f), z, both(0.13980301f));
+  p = fma2(p, z, both(0.20012455f));
+  p = fma2(p, z, both(0.33333158f));
+  p = fma2(p, z, both(1.f));
+  // (a < 0 ? 0 : a keeps a NaN)
+  return fma2(mul2(s, p), both(2.f), pack2(a < 0.f ? 0.f : a, b < 0.f ? 0.f : b));
+}
+// the sigmoids of two values
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+  float a, b;
+  unpack2(add2(ex2x2(mul2(x, both(-kLog2e))), both(1.f)), &a, &b);
+  return pack2(rcp(a), rcp(b));
+}
 __device__ __forceinline__ float softplus(float x) {
-  const float e = exp_neg_abs(x);
-  const float s = __fdividef(e, 2.f + e), z = s * s;
-  float p = 1.f / 13;
-  p = fmaf(p, z, 1.f / 11);
-  p = fmaf(p, z, 1.f / 9);
-  p = fmaf(p, z, 1.f / 7);
-  p = fmaf(p, z, 1.f / 5);
-  p = fmaf(p, z, 1.f / 3);
-  p = fmaf(p, z, 1.f);
-  return fmaf(2.f * s, p, x < 0.f ? 0.f : x);
+  float y;
+  unpack2(softplus2(both(x)), &x, &y);
+  return x;
 }
 
-// V consecutive elements as they lie in memory (V * sizeof(T) = 4, 8 or 16 bytes).
-template <int BYTES> struct RawOf;
-template <> struct RawOf<4> { using type = uint32_t; };
-template <> struct RawOf<8> { using type = uint2; };
-template <> struct RawOf<16> { using type = uint4; };
-template <typename T, int V> using Raw = typename RawOf<V * (int)sizeof(T)>::type;
+// V consecutive elements as they lie in memory (4, 8, 16 or 32 bytes), as words.
+template <int WORDS> struct alignas(WORDS >= 4 ? 16 : WORDS * 4) Words {
+  uint32_t w[WORDS];
+};
+template <typename T, int V> using Raw = Words<V * (int)sizeof(T) / 4>;
 
-template <int V> __device__ __forceinline__ void unpack(const Raw<float, V>& r, float (&x)[V],
-                                                        float) {
-  const float* p = reinterpret_cast<const float*>(&r);
+template <int N> __device__ __forceinline__ Words<N> load_words(const void* p) {
+  Words<N> r;
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = p[i];
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = static_cast<const uint4*>(p)[i / 4];
+      r.w[i] = v.x; r.w[i + 1] = v.y; r.w[i + 2] = v.z; r.w[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
+    r.w[0] = *static_cast<const uint32_t*>(p);
+  }
+  return r;
 }
-template <int V> __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, V>& r,
-                                                        float (&x)[V], __nv_bfloat16) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(&r);
+template <int N> __device__ __forceinline__ void store_words(void* p, const Words<N>& r) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    x[2 * i] = __uint_as_float(p[i] << 16);
-    x[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+    for (int i = 0; i < N; i += 4)
+      static_cast<uint4*>(p)[i / 4] = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+  } else if constexpr (N == 2) {
+    *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+  } else {
+    *static_cast<uint32_t*>(p) = r.w[0];
   }
 }
-template <typename T, int V> __device__ __forceinline__ void unpack_as(const Raw<T, V>& r,
-                                                                       float (&x)[V]) {
-  unpack<V>(r, x, T());
+template <typename T, int V> __device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
+  return load_words<V * (int)sizeof(T) / 4>(p);
+}
+template <typename T, int V> __device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
+  store_words(p, r);
+}
+
+// the same as pairs: x[i] = elements 2 i, 2 i + 1
+template <typename T, int V>
+__device__ __forceinline__ void unpack_pairs(const Raw<T, V>& r, f32x2 (&x)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    if constexpr (sizeof(T) == 4)
+      x[i] = pack2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    else
+      x[i] = pack2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack_as(const Raw<T, V>& r, float (&x)[V]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      x[2 * i] = __uint_as_float(r.w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
+  }
 }
 template <typename T, int V> __device__ __forceinline__ Raw<T, V> pack_as(const float (&x)[V]) {
   Raw<T, V> r;
   if constexpr (sizeof(T) == 4) {
-    float* p = reinterpret_cast<float*>(&r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = x[i];
+    for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(x[i]);
   } else {
-    __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(&r);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) p[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < V / 2; ++i)  // two conversions, round to nearest even; x[2 i] low
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
   }
   return r;
 }
 template <typename T, int V> __device__ __forceinline__ Raw<T, V> zero_raw() {
   Raw<T, V> r;
-  uint32_t* p = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-  for (int i = 0; i < V * (int)sizeof(T) / 4; ++i) p[i] = 0u;
+  for (int i = 0; i < V * (int)sizeof(T) / 4; ++i) r.w[i] = 0u;
   return r;
+}
+
+// 16 bytes global -> shared without registers; a thread's copies form groups, and
+// cp_wait<N> waits until at most its N newest groups are outstanding.
+__device__ __forceinline__ void cp_async16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+               "l"(global)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Bounds [a, b) of sequence s in packed rows (dense batches: s * T ..).

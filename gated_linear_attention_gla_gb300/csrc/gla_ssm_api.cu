@@ -255,7 +255,7 @@ extern "C" {
 
 size_t gla_scan_fwd_workspace_size(int B, int T, int D, int N, int packed) {
   if (B <= 0 || T <= 0 || D <= 0 || !ns_ok(N)) return 0;
-  return gla::scan_fwd_workspace(B, packed ? (long long)T : (long long)B * T, D, N);
+  return gla::scan_fwd_workspace(B, packed ? (long long)T : (long long)B * T, D, N, packed != 0);
 }
 
 gla_status gla_scan_fwd(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride,
@@ -279,7 +279,7 @@ gla_status gla_scan_fwd(const void* u, int64_t u_stride, const void* dt, int64_t
   if (rows == 0 && !final_state) return GLA_OK;
   if (!aligned(out, 16) || !aligned(final_state, 16) || !aligned(workspace, 256))
     return GLA_ERR_MISALIGNED;
-  const size_t need = rows > 0 ? gla::scan_fwd_workspace(B, rows, D, N) : 0;
+  const size_t need = rows > 0 ? gla::scan_fwd_workspace(B, rows, D, N, cu_seqlens) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return GLA_ERR_INVALID_ARG;
   const size_t st = (size_t)((long long)B * D * N) * 4;
   const Range in[] = {GLA_SCAN_INPUTS(s, rows, esz),

@@ -443,3 +443,44 @@ def test_captured_and_on_another_stream(gla):
     assert all(torch.equal(p, q) for p, q in zip(held, fresh))
     assert not torch.equal(first[1], fresh[1])
     gla.status_sync()
+
+
+def test_large_ragged_calls_are_exact_and_repeatable(gla):
+    """Full-size packed calls (thousands of blocks in flight): every convolution output
+    equals the one computed sequence by sequence, and all operators give the
+    same bits five times over."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    lens = [1, 0, 7894, 1556, 1186, 571, 11851, 1755, 963, 4023, 38, 3141, 494, 2, 3, 33]
+    R, D, N, W = sum(lens), 2048, 16, 4
+    cu = cu_of(lens)
+    cu_gpu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    x, dy, bc = r(R, 2 * D)[:, :D], r(R, D), r(R, 2 * N)
+    w, bias = torch.randn(D, W, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda")
+    init = r(len(lens), W - 1, D)
+    a = -torch.rand(D, N, generator=g, device="cuda") * 8 - 0.1
+    dt = (r(R, D) - 4).contiguous()
+
+    def everything():
+        y, f = gla.conv_fwd(x, w, bias, init_state=init, cu_seqlens=cu_gpu, activation="silu")
+        dx = gla.conv_bwd(x, w, dy, bias, init_state=init, cu_seqlens=cu_gpu, activation="silu")
+        o, h = gla.scan_fwd(y, dt, a, bc[:, :N], bc[:, N:], z=x, cu_seqlens=cu_gpu)
+        grads = gla.scan_bwd(y, dt, a, bc[:, :N], bc[:, N:], dy, z=x, cu_seqlens=cu_gpu)
+        return [y, f, *dx, o, h, *[t for t in grads if t is not None]]
+
+    first = everything()
+    for _ in range(4):
+        assert all(torch.equal(p, q) for p, q in zip(first, everything()))
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        y, f = gla.conv_fwd(x[lo:hi][None], w, bias, init_state=init[i:i + 1], activation="silu")
+        assert torch.equal(y[0], first[0][lo:hi]) and torch.equal(f[0], first[1][i])
+    # and the last rows of every sequence against the definition
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        seq = torch.cat([init[i], x[lo:hi]]).double()[-(W + 7):]
+        k = seq.shape[0] - W + 1
+        p = bias.double() + sum(w[:, j].double() * seq[j:j + k] for j in range(W))
+        if hi > lo:
+            n = min(k, hi - lo)
+            err = (first[0][hi - n:hi].double() - (p / (1 + torch.exp(-p)))[-n:]).abs()
+            assert float((err - (2 ** -8 + 2 ** -18) * p[-n:].abs()).max()) < 1e-5
+    gla.status_sync()
