@@ -8,7 +8,18 @@ from . import _binding
 from ._binding import GLA_FLAG_FP32_IO, GLA_FLAG_FP32_OUT, GlaError
 
 
+# The current device and stream as plain ints, without building objects (the
+# decode paths are a few microseconds of kernel).
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
+    torch.cuda.current_device
+_stream = torch._C._cuda_getCurrentRawStream \
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
 def check(cond: bool, msg: str):
+    """For constant messages; a message that has to be formed is raised in place, so
+    that calls which are fine do not pay for it."""
     if not cond:
         raise ValueError(msg)
 
@@ -28,15 +39,19 @@ class launch_on:
         self.device, self.stream, self.guards = device, stream, ()
 
     def __enter__(self) -> int:
-        if self.device.index != torch.cuda.current_device():
+        index = self.device.index
+        if index != _device():
             self.guards = (torch.cuda.device(self.device),)
             self.guards[0].__enter__()
         if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            return _stream(index)
         s = self.stream
         if not isinstance(s, torch.cuda.Stream):
             s = torch.cuda.ExternalStream(int(s), device=self.device) if int(s) else \
                 torch.cuda.default_stream(self.device)
+        if s.device != self.device:
+            self.__exit__()
+            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
         ctx = torch.cuda.stream(s)
         ctx.__enter__()
         self.guards += (ctx,)
@@ -44,77 +59,93 @@ class launch_on:
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
-            g.__exit__(*exc)
+            g.__exit__(*exc or (None, None, None))
 
 
 def row_stride(t, name: str, lead, cols: int) -> int:
     """Elements between the rows of ``t`` [*lead, cols], whose rows lie at a uniform
     distance (a contiguous tensor, or columns of one)."""
-    check(t.dim() == len(lead) + 1 and t.shape[-1] == cols and tuple(t.shape[:-1]) == tuple(lead),
-          f"{name} must be {[*lead, cols]}")
+    shape = t.shape
+    if shape[-1] != cols or shape[:-1] != lead:
+        raise ValueError(f"{name} must be {[*lead, cols]}")
     if t.is_contiguous():
         return cols
-    check(t.stride(-1) == 1 or cols == 1, f"{name}'s last dimension must be contiguous")
+    if t.stride(-1) != 1 and cols != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
     step = want = None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if step is None:
             step, want = stride, stride * size
-        else:
-            check(stride == want, f"{name}'s rows must lie at one distance")
+        elif stride == want:
             want *= size
+        else:
+            raise ValueError(f"{name}'s rows must lie at one distance")
     if step is None or t.numel() == 0:
         return cols
-    check(step >= cols, f"{name}'s rows must not overlap")
+    if step < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
     return step
 
 
 def on_gpu(dtype, device, **tensors):
     """Every given tensor on ``device`` with ``dtype``."""
     for name, t in tensors.items():
-        if t is not None:
-            check(t.dtype == dtype and t.device == device, f"{name} must be {dtype} on {device}")
+        if t is not None and (t.dtype is not dtype or t.device != device):
+            raise ValueError(f"{name} must be {dtype} on {device}")
 
 
 def shaped(shape, **tensors):
     """Every given tensor contiguous and of ``shape``."""
     for name, t in tensors.items():
-        if t is not None:
-            check(t.shape == shape and t.is_contiguous(),
-                  f"{name} must be contiguous {list(shape)}")
+        if t is not None and (t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {list(shape)}")
 
 
 def io_flags(dtype, out_dtype) -> int:
-    if dtype == torch.float32:
-        check(out_dtype == torch.float32, "fp32 inputs give fp32 results")
+    if dtype is torch.float32:
+        check(out_dtype is torch.float32, "fp32 inputs give fp32 results")
         return GLA_FLAG_FP32_IO
-    check(dtype == torch.bfloat16, "inputs must be bf16 or fp32")
-    if out_dtype == torch.float32:
+    check(dtype is torch.bfloat16, "inputs must be bf16 or fp32")
+    if out_dtype is torch.float32:
         return GLA_FLAG_FP32_OUT
-    check(out_dtype == torch.bfloat16, "results come in the inputs' dtype, or fp32")
+    check(out_dtype is torch.bfloat16, "results come in the inputs' dtype, or fp32")
     return 0
 
 
 def batch(x, cu_seqlens, name: str):
     """(lead, B, T) of a dense [B, T, cols] or packed [1, R, cols] / [R, cols] tensor."""
     if cu_seqlens is None:
-        check(x.dim() == 3, f"a dense {name} is [B, T, D]")
-        return x.shape[:2], x.shape[0], x.shape[1]
-    check(x.dim() == 2 or (x.dim() == 3 and x.shape[0] == 1),
-          f"a packed {name} is [1, R, D] or [R, D]")
-    check(cu_seqlens.dtype == torch.int32 and cu_seqlens.device == x.device and
+        if x.dim() != 3:
+            raise ValueError(f"a dense {name} is [B, T, D]")
+        lead = x.shape[:2]
+        return lead, lead[0], lead[1]
+    if x.dim() != 2 and not (x.dim() == 3 and x.shape[0] == 1):
+        raise ValueError(f"a packed {name} is [1, R, D] or [R, D]")
+    check(cu_seqlens.dtype is torch.int32 and cu_seqlens.device == x.device and
           cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
           "cu_seqlens must be contiguous int32 [B + 1] on the inputs' GPU")
     return x.shape[:-1], cu_seqlens.numel() - 1, x.shape[-2]
 
 
+def output(out, shape, dtype, device):
+    """The given output, checked, or a fresh one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be contiguous {list(shape)} on {device}")
+    return out
+
+
 def page_tables(n, device, slots, out_slots):
+    if slots is None:
+        check(out_slots is None, "out_slots needs slots")
+        return
     for name, t in (("slots", slots), ("out_slots", out_slots)):
-        if t is not None:
-            check(t.dtype == torch.int32 and t.device == device and t.shape == (n,) and
-                  t.is_contiguous(), f"{name} must be contiguous int32 [{n}] on the inputs' GPU")
-    check(slots is not None or out_slots is None, "out_slots needs slots")
+        if t is not None and (t.dtype is not torch.int32 or t.device != device or
+                              t.shape != (n,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 [{n}] on {device}")
 
 
 def scratch(size: int, workspace, device):

@@ -21,9 +21,10 @@ PAGE_NEW = GLA_PAGE_NEW  # a parent for fork_pages: a page of zeros
 
 
 def _table(t, name: str, device=None, n=None):
-    check(t.is_cuda and t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and
-          (device is None or t.device == device) and (n is None or t.shape[0] == n),
-          f"{name} must be contiguous int32 [{'n' if n is None else n}] on the pools' GPU")
+    if not t.is_cuda or t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+            (device is not None and t.device != device) or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be contiguous int32 [{'n' if n is None else n}] on the "
+                         "pools' GPU")
     return t
 
 
@@ -33,12 +34,12 @@ def _pools(pools: Sequence[torch.Tensor], device, pages=None):
         pools = (pools,)
     arr = (PagePool * max(1, len(pools)))()
     for i, p in enumerate(pools):
-        check(p.is_cuda and p.device == device and p.is_contiguous() and p.dim() >= 2,
+        check(p.device == device and p.is_contiguous() and p.dim() >= 2,
               "a pool must be a contiguous tensor [num_pages, ...] on the tables' GPU")
-        pages = p.shape[0] if pages is None else pages
-        check(p.shape[0] == pages, "the pools and the table have one number of pages")
-        arr[i].base = p.data_ptr()
-        arr[i].page_bytes = p.numel() // max(1, pages) * p.element_size()
+        n = p.shape[0]
+        pages = n if pages is None else pages
+        check(n == pages, "the pools and the table have one number of pages")
+        arr[i] = PagePool(p.data_ptr(), p.numel() // max(1, n) * p.element_size())
     return arr, len(pools) if pages else 0, pages or 0
 
 

@@ -19,8 +19,8 @@ from typing import Optional
 import torch
 
 from ._binding import GLA_FLAG_SILU, GLA_FLAG_SOFTPLUS
-from ._marshal import (batch, check, done, io_flags, launch_on, lib, on_gpu, page_tables, ptr,
-                       row_stride, scratch, shaped)
+from ._marshal import (batch, check, done, io_flags, launch_on, lib, on_gpu, output, page_tables,
+                       ptr, row_stride, scratch, shaped)
 
 _F32 = torch.float32
 
@@ -30,12 +30,20 @@ def _silu_flag(activation) -> int:
     return GLA_FLAG_SILU if activation else 0
 
 
+def _state(state, rows, a, b, slots):
+    shape = state.shape
+    if len(shape) != 3 or shape[1] != a or shape[2] != b or not state.is_contiguous() or \
+            (slots is None and shape[0] != rows):
+        raise ValueError(f"state must be contiguous "
+                         f"[{rows if slots is None else 'num_slots'}, {a}, {b}]")
+
+
 def _conv_common(x, weight, bias):
     check(x.is_cuda, "x must be a CUDA tensor")
     on_gpu(_F32, x.device, weight=weight, bias=bias)
     D = x.shape[-1]
-    check(weight.dim() == 2 and weight.shape[0] == D and weight.is_contiguous(),
-          f"weight must be contiguous [{D}, W]")
+    if weight.dim() != 2 or weight.shape[0] != D or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous [{D}, W]")
     shaped((D,), bias=bias)
     return D, weight.shape[1]
 
@@ -60,11 +68,7 @@ def conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None,
     on_gpu(x.dtype, x.device, init_state=init_state, final_state=final_state)
     shaped((B, W - 1, D), init_state=init_state, final_state=final_state)
     with launch_on(x.device, stream) as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        else:
-            check(out.shape == x.shape and out.is_contiguous() and out.device == x.device,
-                  "out must be contiguous, of x's shape, on x's GPU")
+        out = output(out, x.shape, out_dtype or x.dtype, x.device)
         if final_state is None and output_final_state:
             final_state = torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
         done(lib().gla_conv_fwd(ptr(x), stride, ptr(weight), ptr(bias), ptr(init_state), ptr(out),
@@ -123,17 +127,11 @@ def conv_step(x, weight, state, bias=None, activation: Optional[str] = None, slo
     stride = row_stride(x, "x", (N,), D)
     on_gpu(x.dtype, x.device, state=state)
     page_tables(N, x.device, slots, out_slots)
-    check(state.dim() == 3 and state.shape[1:] == (W - 1, D) and state.is_contiguous() and
-          (slots is not None or state.shape[0] == N),
-          f"state must be contiguous [{N if slots is None else 'num_slots'}, {W - 1}, {D}]")
+    _state(state, N, W - 1, D, slots)
     flags = io_flags(x.dtype, out.dtype if out is not None else out_dtype or x.dtype)
     flags |= _silu_flag(activation)
     with launch_on(x.device, stream) as s:
-        if out is None:
-            out = torch.empty((N, D), dtype=out_dtype or x.dtype, device=x.device)
-        else:
-            check(out.shape == (N, D) and out.is_contiguous() and out.device == x.device,
-                  "out must be contiguous, of x's shape, on x's GPU")
+        out = output(out, (N, D), out_dtype or x.dtype, x.device)
         done(lib().gla_conv_step(ptr(x), stride, ptr(weight), ptr(bias), ptr(state),
                                  0 if slots is None else state.shape[0], ptr(slots),
                                  ptr(out_slots), ptr(out), N, D, W, s, flags), "gla_conv_step")
@@ -178,11 +176,7 @@ def scan_fwd(u, dt, a, b, c, skip=None, z=None, dt_bias=None, softplus: bool = T
     with launch_on(dev, stream) as s:
         size = lib().gla_scan_fwd_workspace_size(B, T, D, N, cu_seqlens is not None)
         workspace = scratch(size, workspace, dev)
-        if out is None:
-            out = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=dev)
-        else:
-            check(out.shape == u.shape and out.is_contiguous() and out.device == dev,
-                  "out must be contiguous, of u's shape, on u's GPU")
+        out = output(out, u.shape, out_dtype or u.dtype, dev)
         if final_state is None and output_final_state:
             final_state = torch.empty((B, D, N), dtype=_F32, device=dev)
         done(lib().gla_scan_fwd(*args, ptr(init_state), ptr(out), ptr(final_state),
@@ -239,17 +233,11 @@ def scan_step(u, dt, a, b, c, state, skip=None, z=None, dt_bias=None, softplus: 
     dev = u.device
     on_gpu(_F32, dev, state=state)
     page_tables(R, dev, slots, out_slots)
-    check(state.dim() == 3 and state.shape[1:] == (D, N) and state.is_contiguous() and
-          (slots is not None or state.shape[0] == R),
-          f"state must be contiguous [{R if slots is None else 'num_slots'}, {D}, {N}]")
+    _state(state, R, D, N, slots)
     flags = io_flags(u.dtype, out.dtype if out is not None else out_dtype or u.dtype)
     flags |= GLA_FLAG_SOFTPLUS if softplus else 0
     with launch_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((R, D), dtype=out_dtype or u.dtype, device=dev)
-        else:
-            check(out.shape == (R, D) and out.is_contiguous() and out.device == dev,
-                  "out must be contiguous, of u's shape, on u's GPU")
+        out = output(out, (R, D), out_dtype or u.dtype, dev)
         done(lib().gla_scan_step(*args, ptr(state), 0 if slots is None else state.shape[0],
                                  ptr(slots), ptr(out_slots), ptr(out), R, D, N, s, flags),
              "gla_scan_step")
