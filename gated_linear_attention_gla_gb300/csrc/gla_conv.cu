@@ -10,13 +10,17 @@
 // bf16 against ~10 instructions): HBM bounds it.  A thread owns 16 bytes of
 // adjacent channels and walks a run of rows with the last W - 1 rows in
 // registers, so that a row is read once but for the W - 1 rows in front of a
-// run; four rows' loads are in flight before the first is used.
+// run.  Its rows come through a ring of its own in shared memory, eight rows
+// ahead: the bytes in flight that HBM needs (about 45 KB a SM) without registers
+// or barriers.  65536 x 2048 bf16 rows: four rows ahead in registers 170 us.
 #include "gla_ssm.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kUnroll = 4;  // rows in flight per thread
+constexpr int kGroup = 4;   // rows of a group of copies
+constexpr int kAhead = 2;   // groups in flight
+constexpr int kRing = kAhead + 1;
 
 template <typename IO> constexpr int conv_vec() { return 16 / (int)sizeof(IO); }
 
@@ -69,74 +73,89 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
     return;
   }
 
-  float w[V][W], bias[V];
-  load_filter<W, V>(a.weight, a.bias, c, w, bias);
-  OUT* out = (OUT*)a.out + c;
-  long long r = (long long)blockIdx.x * run;
-  const long long r1 = min(r + run, rows);
-  int s = seq_of_row(a.cu_seqlens, a.B, a.T, r);
-  while (r < r1) {
-    long long lo, hi;
-    seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
-    if (lo > r || hi > rows) {  // malformed offsets: this run stops
-      if (threadIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
-      return;
-    }
-    const long long end = min(hi, r1);
-    if (end > r) {
-      float win[K][V];
+  // two adjacent channels a register pair
+  constexpr int P = V / 2;
+  f32x2 w[P][W], bias[P], win[K][P];
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const long long t = r - K + i;
-        Raw<IO, V> v = zero_raw<IO, V>();
-        if (t >= lo) v = load_raw<IO, V>(x + t * a.x_stride);
-        else if (init)
-          v = load_raw<IO, V>(
-              init + ((long long)s * K + K - (lo - t)) * a.D + c);
-        unpack_as<IO, V>(v, win[i]);
-      }
-      auto step = [&](const Raw<IO, V>& raw, long long row, bool in) {
-        float xv[V], y[V];
-        unpack_as<IO, V>(raw, xv);
+  for (int i = 0; i < P; ++i) {
+    const float* f = a.weight + (long long)(c + 2 * i) * W;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float p = bias[i];
-#pragma unroll
-          for (int k = 0; k < K; ++k) p = fmaf(w[i][k], win[k][i], p);
-          p = fmaf(w[i][K], xv[i], p);
-          y[i] = SILU ? silu(p) : p;
-#pragma unroll
-          for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
-          win[K - 1][i] = xv[i];
-        }
-        if (!in) return;
-        if constexpr (sizeof(OUT) * V > 16) {  // fp32 results of 8 bf16 channels
-          float lo4[4], hi4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { lo4[i] = y[i]; hi4[i] = y[i + V / 2]; }
-          store_raw<OUT, 4>(out + row * a.D, pack_as<OUT, 4>(lo4));
-          store_raw<OUT, 4>(out + row * a.D + 4, pack_as<OUT, 4>(hi4));
-        } else {
-          store_raw<OUT, V>(out + row * a.D, pack_as<OUT, V>(y));
-        }
-      };
-      // (one loop for whole and partial groups: rows behind the sequence load
-      // zeros and store nothing)
-      for (; r < end; r += kUnroll) {
-        Raw<IO, V> v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          v[u] = r + u < end ? load_raw<IO, V>(x + (r + u) * a.x_stride) : zero_raw<IO, V>();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) step(v[u], r + u, r + u < end);
-      }
-      r = end;
-    }
-    if (++s >= a.B) {  // no sequence holds the rows that are left
-      if (r < r1 && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
-      break;
-    }
+    for (int k = 0; k < W; ++k) w[i][k] = pack2(__ldg(f + k), __ldg(f + W + k));
+    bias[i] = a.bias ? pack2(__ldg(a.bias + c + 2 * i), __ldg(a.bias + c + 2 * i + 1)) : 0;
   }
+  __shared__ __align__(16) uint4 ring[kRing][kGroup][128];
+  const long long r0 = (long long)blockIdx.x * run, r1 = min(r0 + run, rows);
+  const IO* px = x + r0 * a.x_stride;  // the next row to copy
+  long long ahead = r0;
+  int put = 0;
+  auto copy_group = [&]() {
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      if (ahead < r1) cp_async16(&ring[put][u][threadIdx.x], px);
+      ++ahead;
+      px += a.x_stride;
+    }
+    cp_commit();
+    put = put + 1 == kRing ? 0 : put + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) copy_group();
+  OUT* out = (OUT*)a.out + r0 * a.D + c;
+  // the sequence of row r0, and its window there
+  int s = seq_of_row(a.cu_seqlens, a.B, a.T, r0);
+  long long lo = 0, hi = 0;
+  auto enter = [&](long long r) {  // false: malformed offsets
+    seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
+    if (lo > r || hi > rows) return false;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const long long t = r - K + i;
+      Raw<IO, V> v = zero_raw<IO, V>();
+      if (t >= lo) v = load_raw<IO, V>(x + t * a.x_stride);
+      else if (init) v = load_raw<IO, V>(init + ((long long)s * K + K - (lo - t)) * a.D + c);
+      unpack_pairs<IO, V>(v, win[i]);
+    }
+    return true;
+  };
+  bool ok = enter(r0);
+  int get = 0;
+  for (long long r = r0; r < r1 && ok; r += kGroup) {
+    copy_group();
+    cp_wait<kAhead>();
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const long long row = r + u;
+      if (row < r1 && ok) {
+        while (row >= hi && ok) {  // the next sequence that has a row (empty ones have none)
+          ++s;
+          ok = s < a.B && enter(row);
+        }
+        if (ok) {
+          f32x2 xv[P];
+          unpack_pairs<IO, V>(load_raw<IO, V>(reinterpret_cast<const IO*>(
+                                  &ring[get][u][threadIdx.x])), xv);
+          float y[V];
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            f32x2 p = bias[i];
+#pragma unroll
+            for (int k = 0; k < K; ++k) p = fma2(w[i][k], win[k][i], p);
+            p = fma2(w[i][K], xv[i], p);
+            if (SILU) p = mul2(p, sigmoid2(p));
+            unpack2(p, &y[2 * i], &y[2 * i + 1]);
+#pragma unroll
+            for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
+            win[K - 1][i] = xv[i];
+          }
+          store_raw<OUT, V>(out, pack_as<OUT, V>(y));
+        }
+      }
+      out += a.D;
+    }
+    get = get + 1 == kRing ? 0 : get + 1;
+  }
+  if (!ok && threadIdx.x == 0) atomicOr(a.status, kDevBadSeqlens);
+  cp_wait<0>();
 }
 
 // One token: the window is the page's W - 1 rows and x; the page written gets
@@ -197,7 +216,10 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
   const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
   const unsigned gy = (unsigned)((vecs + threads - 1) / threads);
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
-  const int run = 32;
+  // runs of 64 rows (5 % of the rows in front of them read twice), shorter where
+  // that leaves SMs without blocks
+  int run = 64;
+  while (run > 8 && (rows + run - 1) / run * gy < 2 * 152) run /= 2;
   const long long blocks = (rows + run - 1) / run;
   const long long states = a.final_state ? a.B : 0;
   // an in-place state is written by a launch of its own: its initial rows are
