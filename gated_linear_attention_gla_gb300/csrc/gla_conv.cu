@@ -24,18 +24,6 @@ constexpr int kRing = kAhead + 1;
 
 template <typename IO> constexpr int conv_vec() { return 16 / (int)sizeof(IO); }
 
-// The V channels' filters and biases.
-template <int W, int V>
-__device__ __forceinline__ void load_filter(const float* weight, const float* bias, int c,
-                                            float (&w)[V][W], float (&b)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[i][k] = __ldg(weight + (long long)(c + i) * W + k);
-    b[i] = bias ? __ldg(bias + c + i) : 0.f;
-  }
-}
-
 template <typename IO, typename OUT, int W, bool SILU>
 __global__ void __launch_bounds__(128)
 conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
@@ -73,16 +61,7 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
     return;
   }
 
-  // two adjacent channels a register pair
   constexpr int P = V / 2;
-  f32x2 w[P][W], bias[P], win[K][P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const float* f = a.weight + (long long)(c + 2 * i) * W;
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[i][k] = pack2(__ldg(f + k), __ldg(f + W + k));
-    bias[i] = a.bias ? pack2(__ldg(a.bias + c + 2 * i), __ldg(a.bias + c + 2 * i + 1)) : 0;
-  }
   __shared__ __align__(16) uint4 ring[kRing][kGroup][128];
   const long long r0 = (long long)blockIdx.x * run, r1 = min(r0 + run, rows);
   const IO* px = x + r0 * a.x_stride;  // the next row to copy
@@ -100,6 +79,25 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) copy_group();
+  // (behind the first copies, which take longest)
+  // two adjacent channels a register pair
+  f32x2 w[P][W], bias[P], win[K][P];
+  {
+    float f[V][W], b[V];
+    load_filters<W, V>(a.weight + (long long)c * W, f);
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 v = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c + i))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+      b[i] = v.x; b[i + 1] = v.y; b[i + 2] = v.z; b[i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[i][k] = pack2(f[2 * i][k], f[2 * i + 1][k]);
+      bias[i] = pack2(b[2 * i], b[2 * i + 1]);
+    }
+  }
   OUT* out = (OUT*)a.out + r0 * a.D + c;
   // the sequence of row r0, and its window there
   int s = seq_of_row(a.cu_seqlens, a.B, a.T, r0);
@@ -186,7 +184,13 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvStepArgs a) {
   for (int i = 0; i < K; ++i)
     old[i] = load_raw<IO, V>(pool + (from * K + i) * a.D);
   float w[V][W], p[V];
-  load_filter<W, V>(a.weight, a.bias, c, w, p);
+  load_filters<W, V>(a.weight + (long long)c * W, w);
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const float4 v = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c + i))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    p[i] = v.x; p[i + 1] = v.y; p[i + 2] = v.z; p[i + 3] = v.w;
+  }
   float xv[V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -200,9 +204,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvStepArgs a) {
     p[i] = fmaf(w[i][K], xv[i], p[i]);
     if (SILU) p[i] = silu(p[i]);
   }
-  OUT* out = (OUT*)a.out + n * a.D + c;
-#pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = from_f32<OUT>(p[i]);
+  store_raw<OUT, V>((OUT*)a.out + n * a.D + c, pack_as<OUT, V>(p));
 #pragma unroll
   for (int i = 0; i + 1 < K; ++i)
     store_raw<IO, V>(pool + (to * K + i) * a.D, old[i + 1]);
@@ -216,10 +218,11 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
   const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
   const unsigned gy = (unsigned)((vecs + threads - 1) / threads);
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
-  // runs of 64 rows (5 % of the rows in front of them read twice), shorter where
-  // that leaves SMs without blocks
-  int run = 64;
-  while (run > 8 && (rows + run - 1) / run * gy < 2 * 152) run /= 2;
+  // one wave of blocks (five a SM by registers), so that filters and windows are
+  // loaded once: 65536 x 2048 bf16 rows in runs of 64 111 us, this rule 94 us; at least
+  // 8 rows a run (its first W - 1 rows are read twice)
+  const long long share = (rows * gy + 5 * 152 - 1) / (5 * 152);
+  const int run = share < 8 ? 8 : (int)((share + kGroup - 1) / kGroup * kGroup);
   const long long blocks = (rows + run - 1) / run;
   const long long states = a.final_state ? a.B : 0;
   // an in-place state is written by a launch of its own: its initial rows are

@@ -6,22 +6,25 @@
 // The final state is a copy of the last W - 1 rows, so its gradient adds to
 // theirs; the initial state's rows are rows in front of the sequence.
 //
-// One pass over x and dy: a thread owns 4 adjacent channels and a run of 32
-// rows, with the last W - 1 rows of x and of dp in registers; dx of a row
-// leaves W - 1 rows later, so a run reads W - 1 rows past its end (their dp
-// only).  The weight's gradient is summed in registers over the run, in shared
+// One pass over x and dy: a thread owns 4 adjacent channels and a run of rows,
+// with the last W - 1 rows of x and of dp in registers; dx of a row leaves W - 1
+// rows later, so a run reads W - 1 rows past its end (for their dp only).  The
+// rows come through a ring of the thread's own in shared memory, eight rows
+// ahead.  The weight's gradient is summed in registers over the run, in shared
 // memory over a block's 8 runs, and written as one fp32 partial per block; a
 // second launch sums the partials in block order.  No atomics: the same inputs
-// give the same bits.
+// give the same bits.  Bound: HBM (6 bytes an element in bf16).
 #include "gla_ssm.cuh"
 
 namespace gla {
 namespace {
 
 constexpr int kV = 4;         // channels per thread
-constexpr int kRun = 32;      // rows per thread
 constexpr int kGroups = 8;    // runs per block
-constexpr int kUnroll = 4;    // rows in flight
+constexpr int kThreads = 32 * kGroups;
+constexpr int kGroup = 4;     // rows of a group of copies
+constexpr int kAhead = 2;     // groups in flight
+constexpr int kRing = kAhead + 1;
 
 template <bool SILU> __device__ __forceinline__ float d_act(float p) {
   if (!SILU) return 1.f;
@@ -50,9 +53,18 @@ __device__ __forceinline__ void load_window(const ConvBwdArgs& a, int s, long lo
   }
 }
 
+// dp = dy act'(p) of two channels
+template <bool SILU> __device__ __forceinline__ f32x2 d_pre(f32x2 dy, f32x2 p) {
+  if (!SILU) return dy;
+  const f32x2 s = sigmoid2(p);
+  // s (1 + p (1 - s)) = s + s p (1 - s)
+  const f32x2 sp = mul2(s, p);
+  return mul2(dy, fma2(sp, fma2(s, both(-1.f), both(1.f)), s));
+}
+
 template <typename IO, typename OUT, int W, bool SILU>
-__global__ void __launch_bounds__(32 * kGroups)
-conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
+__global__ void __launch_bounds__(kThreads, 2)
+conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
   constexpr int K = W - 1;
   const int lane = threadIdx.x, group = threadIdx.y;
   const int c = ((int)blockIdx.y * 32 + lane) * kV;
@@ -61,12 +73,13 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
   const IO* x = (const IO*)a.x + c;
   const IO* dy = (const IO*)a.d_out + c;
 
-  float w[kV][W], bias[kV];
-#pragma unroll
-  for (int i = 0; i < kV; ++i) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[i][k] = on ? __ldg(a.weight + (long long)(c + i) * W + k) : 0.f;
-    bias[i] = on && a.bias ? __ldg(a.bias + c + i) : 0.f;
+  float w[kV][W] = {}, bias[kV] = {};
+  if (on) {
+    load_filters<W, kV>(a.weight + (long long)c * W, w);
+    if (a.bias) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + c));
+      bias[0] = v.x; bias[1] = v.y; bias[2] = v.z; bias[3] = v.w;
+    }
   }
 
   if ((long long)blockIdx.x >= row_blocks) {
@@ -119,107 +132,165 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, long long row_blocks) {
     return;
   }
 
-  float dw[kV][W], db[kV];
+  constexpr int P = kV / 2;  // two adjacent channels a register pair
+  f32x2 w2[P][W], bias2[P], dw[P][W], db[P];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    db[i] = 0.f;
+  for (int i = 0; i < P; ++i) {
+    bias2[i] = pack2(bias[2 * i], bias[2 * i + 1]);
+    db[i] = 0;
 #pragma unroll
-    for (int k = 0; k < W; ++k) dw[i][k] = 0.f;
-  }
-  long long r = ((long long)blockIdx.x * kGroups + group) * kRun;
-  const long long r1 = min(r + kRun, rows);
-  int s = r < r1 ? seq_of_row(a.cu_seqlens, a.B, a.T, r) : 0;
-  while (on && r < r1) {
-    long long lo, hi;
-    seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
-    if (lo > r || hi > rows) {
-      atomicOr(a.status, kDevBadSeqlens);
-      break;
+    for (int k = 0; k < W; ++k) {
+      w2[i][k] = pack2(w[2 * i][k], w[2 * i + 1][k]);
+      dw[i][k] = 0;
     }
-    const long long end = min(hi, r1);
-    if (end > r) {
-      float win[K][kV], dpw[K][kV];
-      load_window<IO, K>(a, s, lo, r, c, win);
+  }
+  extern __shared__ __align__(16) unsigned char smem[];
+  using R = Raw<IO, kV>;
+  constexpr int kBytes = kV * (int)sizeof(IO);
+  auto ring = reinterpret_cast<R (*)[kGroup][2][kThreads]>(smem);  // [kRing]: x, dy
+  const int tid = group * 32 + lane;
+  const long long r0 = ((long long)blockIdx.x * kGroups + group) * run;
+  const long long r1 = min(r0 + run, rows), stop = min(r1 + K, rows);  // rows own, rows read
+  if (on && r0 < r1) {
+    const IO* px = x + r0 * a.x_stride;
+    const IO* pd = dy + r0 * a.D;
+    long long ahead = r0;
+    int put = 0, get = 0;
+    auto copy_group = [&]() {
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) {
+        if (ahead < stop) {
+          cp_async<kBytes>(&ring[put][u][0][tid], px);
+          cp_async<kBytes>(&ring[put][u][1][tid], pd);
+        }
+        ++ahead;
+        px += a.x_stride;
+        pd += a.D;
+      }
+      cp_commit();
+      put = put + 1 == kRing ? 0 : put + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy_group();
+
+    f32x2 win[K][P], dpw[K][P];  // the K rows before the current one
+    int s = seq_of_row(a.cu_seqlens, a.B, a.T, r0);
+    long long lo = 0, hi = 0, first = r0;  // the sequence's rows; the first of them in this run
+    auto enter = [&](long long r) {        // false: malformed offsets
+      seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
+      if (lo > r || hi > rows) return false;
+      first = r;
+      float w0[K][kV];
+      load_window<IO, K>(a, s, lo, r, c, w0);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < kV; ++e) dpw[k][e] = 0.f;
-      for (long long t = r; t < end + K; t += kUnroll) {
-        Raw<IO, kV> xr[kUnroll], dr[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const bool in = t + u < min(hi, end + K);
-          xr[u] = in ? load_raw<IO, kV>(x + (t + u) * a.x_stride)
-                     : zero_raw<IO, kV>();
-          dr[u] = in ? load_raw<IO, kV>(dy + (t + u) * a.D)
-                     : zero_raw<IO, kV>();
+        for (int i = 0; i < P; ++i) {
+          win[k][i] = pack2(w0[k][2 * i], w0[k][2 * i + 1]);
+          dpw[k][i] = 0;
         }
+      return true;
+    };
+    // dx of row q = (row of dp) - K from the K dp before and dp itself
+    auto emit = [&](long long q, const f32x2 (&dp)[P]) {
+      f32x2 d[P];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const long long row = t + u, q = row - K;
-          float xv[kV], dv[kV], dx[kV];
-          unpack_as<IO, kV>(xr[u], xv);
-          unpack_as<IO, kV>(dr[u], dv);
-          const bool mine = row < end;
+      for (int i = 0; i < P; ++i) {
+        d[i] = mul2(w2[i][0], dp[i]);
 #pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            float p = bias[e];
+        for (int k = 0; k < K; ++k) d[i] = fma2(w2[i][K - k], dpw[k][i], d[i]);
 #pragma unroll
-            for (int k = 0; k < K; ++k) p = fmaf(w[e][k], win[k][e], p);
-            p = fmaf(w[e][K], xv[e], p);
-            // rows behind the sequence have dy = 0; what they would multiply
-            // must not turn a neighbour's infinity into a NaN
-            const float dp = row < hi ? dv[e] * d_act<SILU>(p) : 0.f;
-            if (mine) {
-              db[e] += dp;
+        for (int k = 0; k + 1 < K; ++k) dpw[k][i] = dpw[k + 1][i];
+        dpw[K - 1][i] = dp[i];
+      }
+      if (q < first || q >= r1) return;
+      if (a.d_final_state && q >= hi - K) {
+        f32x2 f[P];
+        unpack_pairs<float, kV>(
+            load_raw<float, kV>(a.d_final_state + ((long long)s * K + q - (hi - K)) * a.D + c), f);
 #pragma unroll
-              for (int k = 0; k < K; ++k) dw[e][k] = fmaf(dp, win[k][e], dw[e][k]);
-              dw[e][K] = fmaf(dp, xv[e], dw[e][K]);
-            }
-            float d = w[e][0] * dp;  // dp_{q+K}
+        for (int i = 0; i < P; ++i) d[i] = add2(d[i], f[i]);
+      }
+      float o[kV];
 #pragma unroll
-            for (int k = 0; k < K; ++k) d = fmaf(w[e][K - k], dpw[k][e], d);  // dp_{q+k}
-            dx[e] = d;
+      for (int i = 0; i < P; ++i) unpack2(d[i], &o[2 * i], &o[2 * i + 1]);
+      store4<OUT>((OUT*)a.dx + q * a.D + c, o);
+    };
+    // the last rows before `row`, which no dp follows
+    auto flush = [&](long long row) {
+      const f32x2 none[P] = {};
+#pragma unroll 1
+      for (int k = 0; k < K; ++k) emit(row + k - K, none);
+    };
+
+    bool ok = enter(r0), more = ok;
+    long long row = r0;
+    while (more) {
+      copy_group();
+      cp_wait<kAhead>();
 #pragma unroll
-            for (int k = 0; k + 1 < K; ++k) {
-              win[k][e] = win[k + 1][e];
-              dpw[k][e] = dpw[k + 1][e];
-            }
-            win[K - 1][e] = xv[e];
-            dpw[K - 1][e] = dp;
+      for (int u = 0; u < kGroup; ++u) {
+        while (more && row >= hi) {  // the sequence ends here
+          flush(row);
+          ++s;
+          more = hi < r1;
+          ok = !more || s < a.B;
+          if (more) more = ok = ok && enter(row);
+        }
+        more = more && row < stop;
+        if (more) {
+          f32x2 xv[P], dv[P], dp[P];
+          unpack_pairs<IO, kV>(ring[get][u][0][tid], xv);
+          unpack_pairs<IO, kV>(ring[get][u][1][tid], dv);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            f32x2 p = bias2[i];
+#pragma unroll
+            for (int k = 0; k < K; ++k) p = fma2(w2[i][k], win[k][i], p);
+            p = fma2(w2[i][K], xv[i], p);
+            dp[i] = d_pre<SILU>(dv[i], p);
           }
-          if (q >= r && q < end) {
-            if (a.d_final_state && q >= hi - K) {
-              float f[kV];
-              unpack_as<float, kV>(
-                  load_raw<float, kV>(
-                      a.d_final_state + ((long long)s * K + q - (hi - K)) * a.D + c),
-                  f);
+          if (row < r1) {
 #pragma unroll
-              for (int e = 0; e < kV; ++e) dx[e] += f[e];
+            for (int i = 0; i < P; ++i) {
+              db[i] = add2(db[i], dp[i]);
+#pragma unroll
+              for (int k = 0; k < K; ++k) dw[i][k] = fma2(dp[i], win[k][i], dw[i][k]);
+              dw[i][K] = fma2(dp[i], xv[i], dw[i][K]);
             }
-            store4<OUT>((OUT*)a.dx + q * a.D + c, dx);
           }
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+#pragma unroll
+            for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
+            win[K - 1][i] = xv[i];
+          }
+          emit(row - K, dp);
+          ++row;
         }
       }
-      r = end;
+      get = get + 1 == kRing ? 0 : get + 1;
     }
-    if (++s >= a.B) {
-      if (r < r1) atomicOr(a.status, kDevBadSeqlens);
-      break;
-    }
+    // (a run that ends inside a sequence has read K rows more: all its rows are out)
+    if (!ok) atomicOr(a.status, kDevBadSeqlens);
+    cp_wait<0>();
   }
+  __syncthreads();  // the rings become the block's sums
 
   // the block's sums: [W + 1][128 channels] from the 8 groups
-  __shared__ float red[kGroups][W + 1][32 * kV];
+  auto red = reinterpret_cast<float (*)[W + 1][32 * kV]>(smem);  // [kGroups]
 #pragma unroll
-  for (int e = 0; e < kV; ++e) {
+  for (int i = 0; i < P; ++i) {
+    float2 v;
 #pragma unroll
-    for (int k = 0; k < W; ++k) red[group][k][lane * kV + e] = dw[e][k];
-    red[group][W][lane * kV + e] = db[e];
+    for (int k = 0; k < W; ++k) {
+      unpack2(dw[i][k], &v.x, &v.y);
+      *reinterpret_cast<float2*>(&red[group][k][lane * kV + 2 * i]) = v;
+    }
+    unpack2(db[i], &v.x, &v.y);
+    *reinterpret_cast<float2*>(&red[group][W][lane * kV + 2 * i]) = v;
   }
   __syncthreads();
-  const int tid = group * 32 + lane;
   for (int i = tid; i < (W + 1) * 32 * kV; i += 32 * kGroups) {
     const int k = i / (32 * kV), ch = i % (32 * kV);
     const int d = (int)blockIdx.y * 32 * kV + ch;
@@ -238,28 +309,47 @@ conv_bwd_sum_kernel(const float* partial, long long blocks, int D, int W, float*
   if (i >= (long long)(W + 1) * D) return;
   const int k = (int)(i / D), d = (int)(i % D);
   const long long step = (long long)(W + 1) * D;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  float s[8] = {};
   long long b = 0;
-  for (; b + 4 <= blocks; b += 4)
+  for (; b + 8 <= blocks; b += 8)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s[u] += partial[(b + u) * step + i];
-  for (; b < blocks; ++b) s[0] += partial[b * step + i];
-  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    for (int u = 0; u < 8; ++u) s[u] += partial[(b + u) * step + i];
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (b + u < blocks) s[u] += partial[(b + u) * step + i];
+  const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   if (k < W) dw[(long long)d * W + k] = sum;
   else if (db) db[d] = sum;
 }
 
-long long bwd_blocks(long long rows) { return (rows + kRun * kGroups - 1) / (kRun * kGroups); }
+// Rows per run: one wave of blocks (two a SM), at least 8 (W - 1 more are read).
+int bwd_run(long long rows, int D) {
+  const long long tiles = (D + 32 * kV - 1) / (32 * kV);
+  const long long run = (rows * tiles + 2 * 152 * kGroups - 1) / (2 * 152 * kGroups);
+  return run < 8 ? 8 : (int)run;
+}
+long long bwd_blocks(long long rows, int D) {
+  const long long per = (long long)bwd_run(rows, D) * kGroups;
+  return (rows + per - 1) / per;
+}
 
 template <typename IO, typename OUT, int W, bool SILU>
 cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream) {
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
-  const long long blocks = bwd_blocks(rows);
+  const long long blocks = bwd_blocks(rows, a.D);
   const long long states = a.d_init_state ? ((long long)a.B + kGroups - 1) / kGroups : 0;
+  constexpr int rings = kRing * kGroup * 2 * kThreads * kV * (int)sizeof(IO);
+  constexpr int sums = kGroups * (W + 1) * 32 * kV * 4;
+  constexpr int smem = rings > sums ? rings : sums;
+  auto kernel = conv_bwd_kernel<IO, OUT, W, SILU>;
+  if constexpr (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   if (blocks + states > 0)
-    conv_bwd_kernel<IO, OUT, W, SILU>
-        <<<dim3((unsigned)(blocks + states), (unsigned)((a.D + 32 * kV - 1) / (32 * kV))),
-           dim3(32, kGroups), 0, stream>>>(a, partial, blocks);
+    kernel<<<dim3((unsigned)(blocks + states), (unsigned)((a.D + 32 * kV - 1) / (32 * kV))),
+             dim3(32, kGroups), smem, stream>>>(a, partial, bwd_run(rows, a.D), blocks);
   const long long n = (long long)(W + 1) * a.D;
   conv_bwd_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
       partial, blocks, a.D, W, a.d_weight, a.d_bias);
@@ -284,7 +374,7 @@ cudaError_t bwd_io(const ConvBwdArgs& a, float* partial, cudaStream_t stream) {
 }  // namespace
 
 size_t conv_bwd_workspace(long long rows, int D, int W) {
-  return (size_t)bwd_blocks(rows) * (size_t)(W + 1) * (size_t)D * 4;
+  return (size_t)bwd_blocks(rows, D) * (size_t)(W + 1) * (size_t)D * 4;
 }
 
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, void* workspace, cudaStream_t stream) {

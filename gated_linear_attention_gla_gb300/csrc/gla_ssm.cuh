@@ -183,11 +183,38 @@ __device__ __forceinline__ void cp_async16(void* shared, const void* global) {
                "l"(global)
                : "memory");
 }
+// 8 or 16 bytes
+template <int BYTES> __device__ __forceinline__ void cp_async(void* shared, const void* global) {
+  static_assert(BYTES == 8 || BYTES == 16, "sizes of an asynchronous copy");
+  if constexpr (BYTES == 16) {
+    cp_async16(shared, global);
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+                 "l"(global)
+                 : "memory");
+  }
+}
 __device__ __forceinline__ void cp_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The filters [V][W] of V adjacent channels (16-byte aligned: V is a multiple of
+// 4), as 16-byte loads: neighbouring lanes' filters lie V * W * 4 bytes apart, and every
+// load instruction costs the cache a pass per lane, so few wide ones are cheap.
+template <int W, int V>
+__device__ __forceinline__ void load_filters(const float* weight, float (&w)[V][W]) {
+#pragma unroll
+  for (int i = 0; i < V * W / 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(weight) + i);
+    w[(4 * i) / W][(4 * i) % W] = v.x;
+    w[(4 * i + 1) / W][(4 * i + 1) % W] = v.y;
+    w[(4 * i + 2) / W][(4 * i + 2) % W] = v.z;
+    w[(4 * i + 3) / W][(4 * i + 3) % W] = v.w;
+  }
 }
 
 // Bounds [a, b) of sequence s in packed rows (dense batches: s * T ..).

@@ -78,7 +78,7 @@ gla_status gla_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
   if (!weight || (rows > 0 && (!x || !out))) return GLA_ERR_INVALID_ARG;
   if (rows == 0 && !final_state) return GLA_OK;
   if (!aligned(x, 16) || stride_misaligned(x_stride, esz) || !aligned(init_state, 16) ||
-      !aligned(out, 16) || !aligned(final_state, 16) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(out, 16) || !aligned(final_state, 16) || !aligned(weight, 16) || !aligned(bias, 16) ||
       !aligned(cu_seqlens, 4))
     return GLA_ERR_MISALIGNED;
   const size_t st = (size_t)((long long)B * (W - 1) * D * esz);
@@ -127,7 +127,7 @@ gla_status gla_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
     return GLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || stride_misaligned(x_stride, esz) || !aligned(init_state, 16) ||
       !aligned(d_out, 16) || !aligned(d_final_state, 16) || !aligned(dx, 16) ||
-      !aligned(d_init_state, 16) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(d_init_state, 16) || !aligned(weight, 16) || !aligned(bias, 16) ||
       !aligned(d_weight, 4) || !aligned(d_bias, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(workspace, 256))
     return GLA_ERR_MISALIGNED;
@@ -178,7 +178,7 @@ gla_status gla_conv_step(const void* x, int64_t x_stride, const float* weight, c
     return GLA_ERR_INVALID_ARG;
   if (!x || !weight || (!state && pages > 0) || !out) return GLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || stride_misaligned(x_stride, esz) || !aligned(state, 16) ||
-      !aligned(out, 16) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(slots, 4) ||
+      !aligned(out, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(slots, 4) ||
       !aligned(out_slots, 4))
     return GLA_ERR_MISALIGNED;
   const Range in[] = {{x, span(N, x_stride, D, esz)},
@@ -363,7 +363,8 @@ gla_status gla_scan_step(const void* u, int64_t u_stride, const void* dt, int64_
   if (bad != GLA_OK) return bad;
   const long long esz = s.fp32_io ? 4 : 2, osz = s.fp32_out ? 4 : 2;
   const long long pages = slots ? num_slots : rows;
-  if (pages * D * N > kMaxElems || (!state && pages > 0) || !out) return GLA_ERR_INVALID_ARG;
+  if (pages * D * N > kMaxElems || rows > 65535 * 1024 || (!state && pages > 0) || !out)
+    return GLA_ERR_INVALID_ARG;
   if (!aligned(state, 16) || !aligned(out, 16) || !aligned(slots, 4) || !aligned(out_slots, 4))
     return GLA_ERR_MISALIGNED;
   const Range in[] = {GLA_SCAN_INPUTS(s, rows, esz),
