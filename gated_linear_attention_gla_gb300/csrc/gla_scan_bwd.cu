@@ -24,15 +24,20 @@
 //      over d over the warp's channels, then over the warps in shared memory,
 //      then written as one fp32 partial per channel tile;
 //   4. the partials' sums (b, c over channel tiles; a, skip, dt_bias over chunks).
-// No atomics: the same inputs give the same bits.  Bound: the CUDA cores and
-// the exponential unit (three exponentials and ~17 multiply-adds per state and
-// token), not HBM.
+// No atomics: the same inputs give the same bits.
+//
+// Bound: instruction issue on the CUDA cores (three exponentials and ~17
+// multiply-adds per state and token), not HBM.  A lane owns four states of two
+// adjacent channels, one register pair per state (f32x2 instructions work on
+// both channels): the sums over d that every lane takes part in are halved, and
+// per-channel factors are pairs as they lie in shared memory.  The quarters of a
+// warp hold different states, so that reads of b and c are broadcasts.
 #include "gla_scan.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCH = 64;    // tokens per chunk
 constexpr int kSub = 8;    // tokens per recomputed group
@@ -63,113 +68,206 @@ inline Space space_of(float* base, int B, long long rows, int D, int NS) {
   return w;
 }
 
+// The lanes' roles: four states 4 q .. of the channels 2 pair, 2 pair + 1 of the
+// block's tile.
+template <int NS> struct Roles {
+  static constexpr int LPC = NS / 4;          // lanes per channel pair
+  static constexpr int PPW = 32 / LPC;        // pairs per warp
+  static constexpr int CT = kWarps * PPW * 2; // channels per block: 1024 / NS
+  static constexpr int PT = CT / 2;
+  static constexpr int VPT = CT / kV, STEP = kThreads / VPT;  // threads per token of a load
+};
+
+// A chunk's inputs in shared memory.
+template <int NS> struct Staged {
+  static constexpr int PT = Roles<NS>::PT;
+  float4 d[kCH][PT];            // delta, delta u of a channel pair; later s1, s2
+  float2 g[kCH][PT];            // g; later y
+  float2 b[kCH][NS], c[kCH][NS];  // each value twice
+};
+
+// u, dt, dy and z of four channels of a token, as they lie in memory, and as
+// values with delta and x = dt + bias.
+template <typename IO> struct RawRow {
+  Raw<IO, kV> u, dt, g, z;
+};
+struct Row {
+  float u[kV], dl[kV], g[kV], z[kV], x[kV];
+};
 template <typename IO>
-__device__ __forceinline__ void load4(const void* base, long long row, long long stride, int ch,
-                                      float (&x)[kV]) {
-  unpack_as<IO, kV>(
-      load_raw<IO, kV>((const IO*)base + row * stride + ch), x);
+__device__ __forceinline__ RawRow<IO> load_row(const ScanBwdArgs& a, long long row, int ch, bool on) {
+  const ScanArgs& p = a.f;
+  RawRow<IO> r;
+  r.u = r.dt = r.g = r.z = zero_raw<IO, kV>();
+  if (on) {
+    r.u = load_raw<IO, kV>((const IO*)p.u + row * p.u_stride + ch);
+    r.dt = load_raw<IO, kV>((const IO*)p.dt + row * p.dt_stride + ch);
+    r.g = load_raw<IO, kV>((const IO*)a.d_out + row * p.D + ch);
+    if (p.z) r.z = load_raw<IO, kV>((const IO*)p.z + row * p.z_stride + ch);
+  }
+  return r;
+}
+template <typename IO>
+__device__ __forceinline__ void unpack_row(const ScanArgs& p, const RawRow<IO>& raw,
+                                           const float (&bias)[kV], Row& r) {
+  unpack_as<IO, kV>(raw.u, r.u);
+  unpack_as<IO, kV>(raw.dt, r.x);
+  unpack_as<IO, kV>(raw.g, r.g);
+  unpack_as<IO, kV>(raw.z, r.z);
+#pragma unroll
+  for (int i = 0; i < kV; ++i) r.dl[i] = r.x[i] = r.x[i] + bias[i];
+  if (p.softplus) {
+#pragma unroll
+    for (int i = 0; i < kV; i += 2)
+      unpack2(softplus2(pack2(r.x[i], r.x[i + 1])), &r.dl[i], &r.dl[i + 1]);
+  }
 }
 
-// delta, u and g of the chunk's pairs, and b, c, into shared memory (zeros for
-// rows and channels that are not there); with kz, dy silu'(z) as well.
-template <typename IO, int NS, int CT, bool KZ>
-__device__ __forceinline__ void stage(const ScanBwdArgs& a, const Chunk& k, int d0,
-                                      float (*s_delta)[CT], float (*s_u)[CT], float (*s_g)[CT],
-                                      float (*s_k)[CT], float (*s_b)[NS], float (*s_c)[NS]) {
+__device__ __forceinline__ void load_bias(const ScanArgs& p, int ch, bool on, float (&bias)[kV]) {
+#pragma unroll
+  for (int i = 0; i < kV; ++i) bias[i] = on && p.dt_bias ? __ldg(p.dt_bias + ch + i) : 0.f;
+}
+
+// Zeros stand for rows and channels that are not there: decay 1, no drive.  The
+// loads of eight rows a thread (and of its share of b and c) are in flight
+// together.
+template <typename IO, int NS>
+__device__ __forceinline__ void stage(const ScanBwdArgs& a, const Chunk& k, int d0, Staged<NS>& s) {
+  using L = Roles<NS>;
   const ScanArgs& p = a.f;
-  constexpr int VPT = CT / kV, STEP = kThreads / VPT;
-  const int vt = (int)threadIdx.x / VPT, vc = ((int)threadIdx.x % VPT) * kV;
+  const int vt = (int)threadIdx.x / L::VPT, vc = ((int)threadIdx.x % L::VPT) * kV;
   const bool von = d0 + vc < p.D;
+  constexpr int N = kCH / L::STEP < 8 ? kCH / L::STEP : 8;         // rows at once
+  constexpr int BC = kCH * NS / kThreads < 8 ? kCH * NS / kThreads : 8;  // b, c elements at once
   float bias[kV];
+  load_bias(p, d0 + vc, von, bias);
+#pragma unroll 1
+  for (int r = 0; r < kCH; r += N * L::STEP) {
+    RawRow<IO> raw[N];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) bias[i] = von && p.dt_bias ? __ldg(p.dt_bias + d0 + vc + i) : 0.f;
+    for (int i = 0; i < N; ++i) {
+      const long long row = k.t0 + r + i * L::STEP + vt;
+      raw[i] = load_row<IO>(a, row, d0 + vc, row < k.t1 && von);
+    }
 #pragma unroll
-  for (int r = 0; r < kCH; r += STEP) {
-    const int t = r + vt;
-    if (t >= kCH) break;
-    const long long row = k.t0 + t;
-    float u[kV] = {}, dl[kV] = {}, g[kV] = {}, kz[kV] = {};
-    if (row < k.t1 && von) {
-      load4<IO>(p.u, row, p.u_stride, d0 + vc, u);
-      load4<IO>(p.dt, row, p.dt_stride, d0 + vc, dl);
-      load4<IO>(a.d_out, row, p.D, d0 + vc, g);
-      float z[kV];
-      if (p.z) load4<IO>(p.z, row, p.z_stride, d0 + vc, z);
+    for (int i = 0; i < N; ++i) {
+      const int t = r + i * L::STEP + vt;
+      const bool in = k.t0 + t < k.t1 && von;
+      Row v;
+      unpack_row<IO>(p, raw[i], bias, v);
+      if (p.z) {
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        dl[i] += bias[i];
-        if (p.softplus) dl[i] = softplus(dl[i]);
-        if (p.z) {
-          const float sg = sigmoid(z[i]);
-          if (KZ) kz[i] = g[i] * sg * fmaf(z[i], 1.f - sg, 1.f);
-          g[i] *= z[i] * sg;
+        for (int j = 0; j < kV; j += 2) {
+          const f32x2 z = pack2(v.z[j], v.z[j + 1]);
+          unpack2(mul2(pack2(v.g[j], v.g[j + 1]), mul2(z, sigmoid2(z))), &v.g[j], &v.g[j + 1]);
         }
       }
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v.dl[j] = in ? v.dl[j] : 0.f;
+      s.d[t][vc / 2] = make_float4(v.dl[0], v.dl[1], v.dl[0] * v.u[0], v.dl[1] * v.u[1]);
+      s.d[t][vc / 2 + 1] = make_float4(v.dl[2], v.dl[3], v.dl[2] * v.u[2], v.dl[3] * v.u[3]);
+      *reinterpret_cast<float4*>(&s.g[t][vc / 2]) = make_float4(v.g[0], v.g[1], v.g[2], v.g[3]);
     }
-    *reinterpret_cast<float4*>(&s_delta[t][vc]) = make_float4(dl[0], dl[1], dl[2], dl[3]);
-    *reinterpret_cast<float4*>(&s_u[t][vc]) = make_float4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<float4*>(&s_g[t][vc]) = make_float4(g[0], g[1], g[2], g[3]);
-    if (KZ) *reinterpret_cast<float4*>(&s_k[t][vc]) = make_float4(kz[0], kz[1], kz[2], kz[3]);
   }
-  for (int i = threadIdx.x; i < kCH * NS; i += kThreads) {
-    const long long row = k.t0 + i / NS;
-    float b = 0.f, c = 0.f;
-    if (row < k.t1) {
-      b = to_f32(((const IO*)p.b)[row * p.b_stride + i % NS]);
-      c = to_f32(((const IO*)p.c)[row * p.c_stride + i % NS]);
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < kCH * NS; i0 += BC * kThreads) {
+    IO rb[BC], rc[BC];
+#pragma unroll
+    for (int x = 0; x < BC; ++x) {
+      const int i = i0 + x * kThreads;
+      const long long row = k.t0 + i / NS;
+      rb[x] = rc[x] = from_f32<IO>(0.f);
+      if (row < k.t1) {
+        rb[x] = ((const IO*)p.b)[row * p.b_stride + i % NS];
+        rc[x] = ((const IO*)p.c)[row * p.c_stride + i % NS];
+      }
     }
-    s_b[i / NS][i % NS] = b;
-    s_c[i / NS][i % NS] = c;
+#pragma unroll
+    for (int x = 0; x < BC; ++x) {
+      const int i = i0 + x * kThreads;
+      const float b = to_f32(rb[x]), c = to_f32(rc[x]);
+      s.b[i / NS][i % NS] = make_float2(b, b);
+      s.c[i / NS][i % NS] = make_float2(c, c);
+    }
   }
 }
 
-template <int NS> __host__ __device__ constexpr int channel_tile() { return 1024 / NS; }
+// Four states of a channel pair from [channel][NS] (base at the pair's first
+// channel and the lane's first state), scaled; and back.
+__device__ __forceinline__ void load_states(const float* base, int NS, bool two, float scale,
+                                            f32x2 (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(base);
+  const float4 y = two ? *reinterpret_cast<const float4*>(base + NS) : make_float4(0.f, 0.f, 0.f, 0.f);
+  v[0] = pack2(x.x * scale, y.x * scale);
+  v[1] = pack2(x.y * scale, y.y * scale);
+  v[2] = pack2(x.z * scale, y.z * scale);
+  v[3] = pack2(x.w * scale, y.w * scale);
+}
+__device__ __forceinline__ void store_states(float* base, int NS, const f32x2 (&v)[4]) {
+  float4 x, y;
+  unpack2(v[0], &x.x, &y.x);
+  unpack2(v[1], &x.y, &y.y);
+  unpack2(v[2], &x.z, &y.z);
+  unpack2(v[3], &x.w, &y.w);
+  *reinterpret_cast<float4*>(base) = x;
+  *reinterpret_cast<float4*>(base + NS) = y;
+}
+// The lane's four values of a row of b or c, each twice.
+__device__ __forceinline__ void load_dup(const float2* row, f32x2 (&v)[4]) {
+  const float4 x = reinterpret_cast<const float4*>(row)[0], y = reinterpret_cast<const float4*>(row)[1];
+  v[0] = pack2(x.x, x.y);
+  v[1] = pack2(x.z, x.w);
+  v[2] = pack2(y.x, y.y);
+  v[3] = pack2(y.z, y.w);
+}
 
 // 1. What each chunk adds to the state and to the gradient before it.
 template <typename IO, int NS>
-__global__ void __launch_bounds__(kThreads) chunk_sums_kernel(ScanBwdArgs a, Space w) {
-  constexpr int LPC = NS / 4, CT = channel_tile<NS>();
+__global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, Space w) {
+  using L = Roles<NS>;
   const ScanArgs& p = a.f;
   extern __shared__ __align__(16) unsigned char smem[];
-  auto s_delta = reinterpret_cast<float (*)[CT]>(smem);
-  auto s_u = s_delta + kCH;
-  auto s_g = s_u + kCH;
-  auto s_b = reinterpret_cast<float (*)[NS]>(s_g + kCH);
-  auto s_c = s_b + kCH;
-  const int tiles = (p.D + CT - 1) / CT;
+  Staged<NS>& s = *reinterpret_cast<Staged<NS>*>(smem);
+  const int tiles = (p.D + L::CT - 1) / L::CT;
   const long long slot = blockIdx.x / tiles;
-  const int d0 = (int)(blockIdx.x % tiles) * CT;
+  const int d0 = (int)(blockIdx.x % tiles) * L::CT;
   const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) return;
-  const int q = threadIdx.x % LPC, lc = threadIdx.x / LPC, ch = d0 + lc;
-  stage<IO, NS, CT, false>(a, k, d0, s_delta, s_u, s_g, nullptr, s_b, s_c);
-  float a2[4] = {}, h[4] = {}, e[4] = {}, run[4] = {1.f, 1.f, 1.f, 1.f}, sum = 0.f;
-  if (ch < p.D) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p.a + (long long)ch * NS) + q);
-    a2[0] = x.x * kLog2e; a2[1] = x.y * kLog2e; a2[2] = x.z * kLog2e; a2[3] = x.w * kLog2e;
-  }
+  const int lane = threadIdx.x & 31, q = lane / L::PPW;
+  const int pair = (threadIdx.x >> 5) * L::PPW + lane % L::PPW, ch = d0 + 2 * pair;
+  const bool on = ch < p.D;  // (D is even: both channels or none)
+  stage<IO, NS>(a, k, d0, s);
+  f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, run[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) run[j] = both(1.f);
+  if (on) load_states(p.a + (long long)ch * NS + q * 4, NS, true, kLog2e, a2);
   __syncthreads();
-  const int len = (int)(k.t1 - k.t0);
 #pragma unroll 4
-  for (int t = 0; t < len; ++t) {
-    const float dl = s_delta[t][lc], du = dl * s_u[t][lc], g = s_g[t][lc];
-    const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][q * 4]);
-    const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][q * 4]);
-    const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
-    sum += dl;
+  for (int t = 0; t < kCH; ++t) {
+    const float4 d = s.d[t][pair];
+    const float2 gg = s.g[t][pair];
+    const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w), g = pack2(gg.x, gg.y);
+    f32x2 b[4], c[4];
+    load_dup(&s.b[t][q * 4], b);
+    load_dup(&s.c[t][q * 4], c);
+    sum = add2(sum, dl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float decay = ex2(dl * a2[j]);
-      h[j] = fmaf(decay, h[j], du * b[j]);
-      run[j] *= decay;
-      e[j] = fmaf(run[j] * c[j], g, e[j]);
+      const f32x2 decay = ex2x2(mul2(dl, a2[j]));
+      h[j] = fma2(decay, h[j], mul2(du, b[j]));
+      run[j] = mul2(run[j], decay);
+      e[j] = fma2(mul2(run[j], c[j]), g, e[j]);
     }
   }
-  if (ch < p.D) {
+  if (on) {
     const long long at = (slot * p.D + ch) * NS + q * 4;
-    *reinterpret_cast<float4*>(w.h + at) = make_float4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<float4*>(w.e + at) = make_float4(e[0], e[1], e[2], e[3]);
-    if (q == 0) w.sum[slot * p.D + ch] = sum;
+    store_states(w.h + at, NS, h);
+    store_states(w.e + at, NS, e);
+    if (q == 0) {
+      float2 v;
+      unpack2(sum, &v.x, &v.y);
+      *reinterpret_cast<float2*>(w.sum + slot * p.D + ch) = v;
+    }
   }
 }
 
@@ -200,11 +298,11 @@ chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
   if (back && a.d_init_state) reinterpret_cast<float4*>(a.d_init_state)[(long long)s * per + in] = run;
 }
 
-// The sums of v[0 .. 8) over the lanes that differ in the bits LPC .. 16,
+// The sums of v[0 .. 8) over the lanes that differ in the bits OFF, OFF / 2 .. 1,
 // scattered: afterwards a lane holds N of them, v[0 .. N), from index *first.
-template <int OFF, int LPC, int N>
+template <int OFF, int N>
 __device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int* first) {
-  if constexpr (OFF >= LPC) {
+  if constexpr (OFF >= 1) {
     if constexpr (N > 1) {
       const bool up = (lane & OFF) != 0;
 #pragma unroll
@@ -214,152 +312,189 @@ __device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int* fi
         v[k] = keep + __shfl_xor_sync(0xffffffffu, give, OFF);
       }
       if (up) *first += N / 2;
-      reduce_channels<OFF / 2, LPC, N / 2>(v, lane, first);
+      reduce_channels<OFF / 2, N / 2>(v, lane, first);
     } else {
       v[0] += __shfl_xor_sync(0xffffffffu, v[0], OFF);
-      reduce_channels<OFF / 2, LPC, 1>(v, lane, first);
+      reduce_channels<OFF / 2, 1>(v, lane, first);
     }
   }
 }
 
+// The sums of v[0 .. 4) over a channel pair's lanes (bits PPW and up),
+// scattered: a lane holds 4 / LPC of them, or one that lanes share.
+template <int LPC, int PPW>
+__device__ __forceinline__ void reduce_states(f32x2 (&v)[4], int q, int* first) {
+  constexpr unsigned full = 0xffffffffu;
+  const bool up = (q & (LPC / 2)) != 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const f32x2 give = up ? v[k] : v[k + 2], keep = up ? v[k + 2] : v[k];
+    v[k] = add2(keep, __shfl_xor_sync(full, give, PPW * LPC / 2));
+  }
+  *first = up ? 2 : 0;
+  if constexpr (LPC >= 4) {
+    const bool up2 = (q & (LPC / 4)) != 0;
+    const f32x2 give = up2 ? v[0] : v[1], keep = up2 ? v[1] : v[0];
+    v[0] = add2(keep, __shfl_xor_sync(full, give, PPW * LPC / 4));
+    *first += up2 ? 1 : 0;
+#pragma unroll
+    for (int off = LPC / 8; off > 0; off >>= 1)
+      v[0] = add2(v[0], __shfl_xor_sync(full, v[0], PPW * off));
+  }
+}
+
+template <int NS> struct GradSmem {
+  Staged<NS> in;
+  float4 h[kCH / kSub][2][kThreads];  // the state in front of every group, by thread
+  float red[kWarps][kSub][2 * NS];    // the warps' sums over d
+  float tail[2][Roles<NS>::STEP][Roles<NS>::CT];
+};
+
 // 3. The chunk's gradients.
 template <typename IO, typename OUT, int NS>
 __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a, Space w) {
-  constexpr int LPC = NS / 4, CT = channel_tile<NS>(), G = 32 / LPC;
-  constexpr int HELD = G >= 8 ? 1 : 8 / G;    // sums over d that a lane ends up with
+  using L = Roles<NS>;
+  constexpr int LPC = L::LPC, PPW = L::PPW, CT = L::CT;
+  constexpr int HELD = PPW >= 8 ? 1 : 8 / PPW;   // sums over d that a lane ends up with
   constexpr int kShare = LPC > 4 ? LPC / 4 : 1;  // lanes that share a sum over n
   const ScanArgs& p = a.f;
   extern __shared__ __align__(16) unsigned char smem[];
-  auto s_delta = reinterpret_cast<float (*)[CT]>(smem);  // later ddt
-  auto s_u = s_delta + kCH;                               // later du
-  auto s_g = s_u + kCH;
-  auto s_k = s_g + kCH;                                   // later dz
-  auto s_b = reinterpret_cast<float (*)[NS]>(s_k + kCH);
-  auto s_c = s_b + kCH;
-  auto s_h = reinterpret_cast<float4*>(s_c + kCH);        // [kCH / kSub][kThreads]
-  auto s_red = reinterpret_cast<float (*)[kSub][2 * NS]>(s_h + kCH / kSub * kThreads);  // [kWarps]
+  GradSmem<NS>& m = *reinterpret_cast<GradSmem<NS>*>(smem);
+  Staged<NS>& s = m.in;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane / PPW;
   const int tiles = (p.D + CT - 1) / CT, tile = (int)(blockIdx.x % tiles);
-  const long long slot = blockIdx.x / tiles;
-  const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
-  const int d0 = tile * CT;
-  const int q = tid % LPC, lc = tid / LPC, ch = d0 + lc;
+  const long long slot = blockIdx.x / tiles, rows = rows_of(p);
+  const int d0 = tile * CT, pair = warp * PPW + lane % PPW, ch = d0 + 2 * pair;
   const bool on = ch < p.D;
   const long long at = (slot * p.D + ch) * NS + q * 4;
   const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) {  // no chunk: its partials count as zero
     if (on) {
-      *reinterpret_cast<float4*>(w.h + at) = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (q == 0) w.sum[slot * p.D + ch] = w.sum2[slot * p.D + ch] = 0.f;
+      const f32x2 none[4] = {};
+      store_states(w.h + at, NS, none);
+      if (q == 0) {
+        const float2 zero = make_float2(0.f, 0.f);
+        *reinterpret_cast<float2*>(w.sum + slot * p.D + ch) = zero;
+        *reinterpret_cast<float2*>(w.sum2 + slot * p.D + ch) = zero;
+      }
     }
     return;
   }
-  stage<IO, NS, CT, true>(a, k, d0, s_delta, s_u, s_g, s_k, s_b, s_c);
-  float a2[4] = {}, h[4] = {}, e[4] = {}, da[4] = {};
-  float skip = 0.f, dskip = 0.f, dbias = 0.f;
+  f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, da[4] = {};
   if (on) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p.a + (long long)ch * NS) + q);
-    a2[0] = x.x * kLog2e; a2[1] = x.y * kLog2e; a2[2] = x.z * kLog2e; a2[3] = x.w * kLog2e;
-    const float4 y = *reinterpret_cast<const float4*>(w.h + at);
-    h[0] = y.x; h[1] = y.y; h[2] = y.z; h[3] = y.w;
-    const float4 v = *reinterpret_cast<const float4*>(w.e + at);
-    e[0] = v.x; e[1] = v.y; e[2] = v.z; e[3] = v.w;
-    if (p.skip) skip = __ldg(p.skip + ch);
+    load_states(p.a + (long long)ch * NS + q * 4, NS, true, kLog2e, a2);
+    load_states(w.h + at, NS, true, 1.f, h);
+    load_states(w.e + at, NS, true, 1.f, e);
   }
+  stage<IO, NS>(a, k, d0, s);
   __syncthreads();
   const int len = (int)(k.t1 - k.t0);
   const int groups = (len + kSub - 1) / kSub;
 
-  // forwards, keeping the state in front of every group (rows behind the
-  // sequence have delta = 0: decay 1, no drive)
+  // forwards, keeping the state in front of every group
   for (int gr = 0; gr < groups; ++gr) {
-    s_h[gr * kThreads + tid] = make_float4(h[0], h[1], h[2], h[3]);
+    float4 x, y;
+    unpack2(h[0], &x.x, &x.y);
+    unpack2(h[1], &x.z, &x.w);
+    unpack2(h[2], &y.x, &y.y);
+    unpack2(h[3], &y.z, &y.w);
+    m.h[gr][0][tid] = x;
+    m.h[gr][1][tid] = y;
     if (gr + 1 == groups) break;
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
       const int t = gr * kSub + i;
-      const float dl = s_delta[t][lc], du = dl * s_u[t][lc];
-      const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][q * 4]);
-      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+      const float4 d = s.d[t][pair];
+      const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w);
+      f32x2 b[4];
+      load_dup(&s.b[t][q * 4], b);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = fmaf(ex2(dl * a2[j]), h[j], du * b[j]);
+      for (int j = 0; j < 4; ++j)
+        h[j] = fma2(ex2x2(mul2(dl, a2[j])), h[j], mul2(du, b[j]));
     }
   }
   // backwards
+#pragma unroll 1
   for (int gr = groups - 1; gr >= 0; --gr) {
-    float hs[kSub + 1][4], ds[kSub][4];
+    f32x2 hs[kSub + 1][4], ds[kSub][4];
     {
-      const float4 x = s_h[gr * kThreads + tid];
-      hs[0][0] = x.x; hs[0][1] = x.y; hs[0][2] = x.z; hs[0][3] = x.w;
+      const float4 x = m.h[gr][0][tid], y = m.h[gr][1][tid];
+      hs[0][0] = pack2(x.x, x.y);
+      hs[0][1] = pack2(x.z, x.w);
+      hs[0][2] = pack2(y.x, y.y);
+      hs[0][3] = pack2(y.z, y.w);
     }
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
       const int t = gr * kSub + i;
-      const float dl = s_delta[t][lc], du = dl * s_u[t][lc];
-      const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][q * 4]);
-      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+      const float4 d = s.d[t][pair];
+      const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w);
+      f32x2 b[4];
+      load_dup(&s.b[t][q * 4], b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        ds[i][j] = ex2(dl * a2[j]);
-        hs[i + 1][j] = fmaf(ds[i][j], hs[i][j], du * b[j]);
+        ds[i][j] = ex2x2(mul2(dl, a2[j]));
+        hs[i + 1][j] = fma2(ds[i][j], hs[i][j], mul2(du, b[j]));
       }
     }
 #pragma unroll
     for (int half = kSub / 4 - 1; half >= 0; --half) {
-      float s1[4], s2[4], y[4];
+      f32x2 s1[4], s2[4], y[4];
       float vb[8], vc[8];
 #pragma unroll
       for (int x = 3; x >= 0; --x) {
         const int i = half * 4 + x, t = gr * kSub + i;
-        const float dl = s_delta[t][lc], du = dl * s_u[t][lc], g = s_g[t][lc];
-        const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][q * 4]);
-        const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][q * 4]);
-        const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
-        s1[x] = s2[x] = y[x] = 0.f;
+        const float4 d = s.d[t][pair];
+        const float2 gg = s.g[t][pair];
+        const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w), g = pack2(gg.x, gg.y);
+        f32x2 b[4], c[4];
+        load_dup(&s.b[t][q * 4], b);
+        load_dup(&s.c[t][q * 4], c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          e[j] = fmaf(c[j], g, e[j]);
-          vc[(x & 1) * 4 + j] = g * hs[i + 1][j];
-          vb[(x & 1) * 4 + j] = du * e[j];
-          s1[x] = fmaf(e[j], b[j], s1[x]);
-          y[x] = fmaf(c[j], hs[i + 1][j], y[x]);
-          e[j] *= ds[i][j];
-          const float wj = e[j] * hs[i][j];
-          da[j] = fmaf(dl, wj, da[j]);
-          s2[x] = fmaf(a2[j], wj, s2[x]);
+          float lo, hi;
+          e[j] = fma2(c[j], g, e[j]);
+          unpack2(mul2(g, hs[i + 1][j]), &lo, &hi);
+          vc[(x & 1) * 4 + j] = lo + hi;
+          unpack2(mul2(du, e[j]), &lo, &hi);
+          vb[(x & 1) * 4 + j] = lo + hi;
+          s1[x] = j == 0 ? mul2(e[0], b[0]) : fma2(e[j], b[j], s1[x]);
+          y[x] = j == 0 ? mul2(c[0], hs[i + 1][0]) : fma2(c[j], hs[i + 1][j], y[x]);
+          e[j] = mul2(e[j], ds[i][j]);
+          const f32x2 wj = mul2(e[j], hs[i][j]);
+          da[j] = fma2(dl, wj, da[j]);
+          s2[x] = j == 0 ? mul2(a2[0], wj) : fma2(a2[j], wj, s2[x]);
         }
         if ((x & 1) == 0) {  // tokens i and i + 1
           int fb = 0, fc = 0;
-          reduce_channels<16, LPC, 8>(vb, lane, &fb);
-          reduce_channels<16, LPC, 8>(vc, lane, &fc);
-          if (G <= 8 || (lane & LPC) == 0) {
+          reduce_channels<PPW / 2, 8>(vb, lane, &fb);
+          reduce_channels<PPW / 2, 8>(vc, lane, &fc);
+          if (PPW <= 8 || (lane & 1) == 0) {
 #pragma unroll
-            for (int m = 0; m < HELD; ++m) {
-              s_red[warp][i + (fb + m) / 4][q * 4 + (fb + m) % 4] = vb[m];
-              s_red[warp][i + (fc + m) / 4][NS + q * 4 + (fc + m) % 4] = vc[m];
+            for (int v = 0; v < HELD; ++v) {
+              m.red[warp][i + (fb + v) / 4][q * 4 + (fb + v) % 4] = vb[v];
+              m.red[warp][i + (fc + v) / 4][NS + q * 4 + (fc + v) % 4] = vc[v];
             }
           }
         }
       }
       int first;
-      reduce4<LPC>(s1, q, &first);
-      reduce4<LPC>(s2, q, &first);
-      reduce4<LPC>(y, q, &first);
-      __syncwarp();  // the channel's lanes have read delta, u and g
+      reduce_states<LPC, PPW>(s1, q, &first);
+      reduce_states<LPC, PPW>(s2, q, &first);
+      reduce_states<LPC, PPW>(y, q, &first);
+      __syncwarp();  // the pair's lanes have read these tokens' d and g
+      if (q % kShare == 0) {
 #pragma unroll
-      for (int m = 0; m < (LPC == 2 ? 2 : 1); ++m) {
-        const int t = gr * kSub + half * 4 + first + m;
-        if (t < len && q % kShare == 0) {
-          const float dl = s_delta[t][lc], u = s_u[t][lc], g = s_g[t][lc];
-          float ddt = fmaf(kLn2, s2[m], u * s1[m]);
-          // softplus'(x) = 1 - e^-softplus(x)
-          if (p.softplus) ddt *= -expm1f(-dl);
-          dskip = fmaf(g, u, dskip);
-          dbias += ddt;
-          s_delta[t][lc] = ddt;
-          s_u[t][lc] = fmaf(dl, s1[m], skip * g);
-          s_k[t][lc] *= fmaf(skip, u, y[m]);
+        for (int v = 0; v < (LPC == 2 ? 2 : 1); ++v) {
+          const int t = gr * kSub + half * 4 + first + v;
+          float4 o;
+          unpack2(s1[v], &o.x, &o.y);
+          unpack2(s2[v], &o.z, &o.w);
+          s.d[t][pair] = o;
+          float2 yy;
+          unpack2(y[v], &yy.x, &yy.y);
+          s.g[t][pair] = yy;
         }
       }
     }
@@ -368,40 +503,72 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       const int t = i / (2 * NS), col = i % (2 * NS);
       float sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) sum += s_red[v][t][col];
+      for (int v = 0; v < kWarps; ++v) sum += m.red[v][t][col];
       const long long row = k.t0 + gr * kSub + t;
       if (row < k.t1) w.part[((long long)tile * rows + row) * 2 * NS + col] = sum;
     }
     __syncthreads();
   }
-  // this chunk's share of da, dskip, ddt_bias over the inputs it has consumed
+  if (on) store_states(w.h + at, NS, da);  // over the state that has been read
+
+  // du, ddt, dz: the inputs once more (from L2), rows of adjacent channels
+  const int vt = tid / L::VPT, vc = (tid % L::VPT) * kV;
+  const bool von = d0 + vc < p.D;
+  float bias[kV], skip[kV], dskip[kV] = {}, dbias[kV] = {};
+  load_bias(p, d0 + vc, von, bias);
 #pragma unroll
-  for (int off = LPC / 2; off > 0; off >>= 1) {
-    dskip += __shfl_xor_sync(0xffffffffu, dskip, off);
-    dbias += __shfl_xor_sync(0xffffffffu, dbias, off);
-  }
-  if (on) {
-    *reinterpret_cast<float4*>(w.h + at) = make_float4(da[0], da[1], da[2], da[3]);
-    if (q == 0) {
-      w.sum[slot * p.D + ch] = dskip;
-      w.sum2[slot * p.D + ch] = dbias;
-    }
-  }
-  // du, ddt, dz in rows of adjacent channels (the last group's barrier precedes)
-  constexpr int VPT = CT / kV, STEP = kThreads / VPT;
-  const int vt = tid / VPT, vc = (tid % VPT) * kV;
-  if (d0 + vc < p.D) {
-    for (int t = vt; t < len; t += STEP) {
+  for (int i = 0; i < kV; ++i) skip[i] = von && p.skip ? __ldg(p.skip + d0 + vc + i) : 0.f;
+  constexpr int N = kCH / L::STEP < 8 ? kCH / L::STEP : 8;
+#pragma unroll 1
+  for (int r = vt; r < len && von; r += N * L::STEP) {
+    RawRow<IO> raw[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      raw[i] = load_row<IO>(a, k.t0 + r + i * L::STEP, d0 + vc, r + i * L::STEP < len);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int t = r + n * L::STEP;
+      if (t >= len) break;
+      Row v;
+      unpack_row<IO>(p, raw[n], bias, v);
+      const float4 o0 = s.d[t][vc / 2], o1 = s.d[t][vc / 2 + 1];
+      const float4 yy = *reinterpret_cast<const float4*>(&s.g[t][vc / 2]);
+      const float s1[kV] = {o0.x, o0.y, o1.x, o1.y}, s2[kV] = {o0.z, o0.w, o1.z, o1.w};
+      const float y[kV] = {yy.x, yy.y, yy.z, yy.w};
+      float du[kV], ddt[kV], dz[kV];
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        float g = v.g[i];
+        if (p.z) {
+          const float sg = sigmoid(v.z[i]);
+          dz[i] = g * sg * fmaf(v.z[i], 1.f - sg, 1.f) * fmaf(skip[i], v.u[i], y[i]);
+          g *= v.z[i] * sg;
+        }
+        ddt[i] = fmaf(kLn2, s2[i], v.u[i] * s1[i]);
+        if (p.softplus) ddt[i] *= sigmoid(v.x[i]);
+        du[i] = fmaf(v.dl[i], s1[i], skip[i] * g);
+        dskip[i] = fmaf(g, v.u[i], dskip[i]);
+        dbias[i] += ddt[i];
+      }
       const long long o = (k.t0 + t) * p.D + d0 + vc;
-      auto put = [&](void* to, const float* from) {
-        const float4 x = *reinterpret_cast<const float4*>(from);
-        const float y[kV] = {x.x, x.y, x.z, x.w};
-        store_raw<OUT, kV>((OUT*)to + o, pack_as<OUT, kV>(y));
-      };
-      put(a.du, &s_u[t][vc]);
-      put(a.ddt, &s_delta[t][vc]);
-      if (a.dz) put(a.dz, &s_k[t][vc]);
+      store_raw<OUT, kV>((OUT*)a.du + o, pack_as<OUT, kV>(du));
+      store_raw<OUT, kV>((OUT*)a.ddt + o, pack_as<OUT, kV>(ddt));
+      if (a.dz) store_raw<OUT, kV>((OUT*)a.dz + o, pack_as<OUT, kV>(dz));
     }
+  }
+  // this chunk's share of dskip and ddt_bias
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    m.tail[0][vt][vc + i] = dskip[i];
+    m.tail[1][vt][vc + i] = dbias[i];
+  }
+  __syncthreads();
+  for (int i = tid; i < 2 * CT; i += kThreads) {
+    const int which = i / CT, c = i % CT;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int t = 0; t < L::STEP; ++t) sum += m.tail[which][t][c];
+    if (d0 + c < p.D) (which ? w.sum2 : w.sum)[slot * p.D + d0 + c] = sum;
   }
 }
 
@@ -459,16 +626,13 @@ template <typename K> cudaError_t opt_in(K kernel, int bytes) {
 
 template <typename IO, typename OUT, int NS>
 cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t stream) {
-  constexpr int CT = channel_tile<NS>();
+  constexpr int CT = Roles<NS>::CT;
   const ScanArgs& p = a.f;
   const long long rows = p.cu_seqlens ? (long long)p.T : (long long)p.B * p.T;
   const long long slots = slots_of(p.B, rows, kCH);
   const int tiles = (p.D + CT - 1) / CT;
   const Space w = space_of(static_cast<float*>(workspace), p.B, rows, p.D, NS);
-  constexpr int staged = 2 * kCH * NS * 4;
-  constexpr int smem1 = 3 * kCH * CT * 4 + staged;
-  constexpr int smem3 = 4 * kCH * CT * 4 + staged + kCH / kSub * kThreads * 16 +
-                        kWarps * kSub * 2 * NS * 4;
+  constexpr int smem1 = (int)sizeof(Staged<NS>), smem3 = (int)sizeof(GradSmem<NS>);
   static_assert(smem3 <= 227 * 1024, "shared memory of a block");
   cudaError_t e = opt_in(chunk_sums_kernel<IO, NS>, smem1);
   if (e == cudaSuccess) e = opt_in(chunk_grads_kernel<IO, OUT, NS>, smem3);
