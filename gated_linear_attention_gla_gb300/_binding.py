@@ -56,6 +56,8 @@ class GlaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libgla.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

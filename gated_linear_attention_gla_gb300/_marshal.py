@@ -62,45 +62,38 @@ class launch_on:
             g.__exit__(*exc or (None, None, None))
 
 
-def row_stride(t, name: str, lead, cols: int) -> int:
-    """Elements between the rows of ``t`` [*lead, cols], whose rows lie at a uniform
-    distance (a contiguous tensor, or columns of one)."""
-    shape = t.shape
-    if shape[-1] != cols or shape[:-1] != lead:
-        raise ValueError(f"{name} must be {[*lead, cols]}")
-    if t.is_contiguous():
-        return cols
-    if t.stride(-1) != 1 and cols != 1:
+def rows(t, name: str, shape, dtype, device):
+    """(address, elements between rows) of ``t``, of ``shape`` [*lead, cols], whose rows lie
+    at a uniform distance (a contiguous tensor, or columns of one)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}")
+    st, n, cols = t.stride(), len(shape), shape[-1]
+    if st[-1] != 1 and cols != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    step = want = None
-    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
-            continue
-        if step is None:
-            step, want = stride, stride * size
-        elif stride == want:
-            want *= size
-        else:
+    if n == 2:
+        step = st[0] if shape[0] > 1 else None
+    elif n == 3 and shape[1] > 1:
+        step = st[1]
+        if shape[0] > 1 and st[0] != step * shape[1]:
             raise ValueError(f"{name}'s rows must lie at one distance")
+    elif n == 3:
+        step = st[0] if shape[0] > 1 else None
+    else:
+        raise ValueError(f"{name} must have two or three dimensions")
     if step is None or t.numel() == 0:
-        return cols
+        return t.data_ptr(), cols
     if step < cols:
         raise ValueError(f"{name}'s rows must not overlap")
-    return step
+    return t.data_ptr(), step
 
 
-def on_gpu(dtype, device, **tensors):
-    """Every given tensor on ``device`` with ``dtype``."""
-    for name, t in tensors.items():
-        if t is not None and (t.dtype is not dtype or t.device != device):
-            raise ValueError(f"{name} must be {dtype} on {device}")
-
-
-def shaped(shape, **tensors):
-    """Every given tensor contiguous and of ``shape``."""
-    for name, t in tensors.items():
-        if t is not None and (t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous {list(shape)}")
+def whole(t, name: str, shape, dtype, device):
+    """The address of ``t`` (None: 0), contiguous and of ``shape``."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
+    return t.data_ptr()
 
 
 def io_flags(dtype, out_dtype) -> int:
@@ -139,13 +132,12 @@ def output(out, shape, dtype, device):
 
 
 def page_tables(n, device, slots, out_slots):
+    """The addresses of the tables of pages read and written."""
     if slots is None:
         check(out_slots is None, "out_slots needs slots")
-        return
-    for name, t in (("slots", slots), ("out_slots", out_slots)):
-        if t is not None and (t.dtype is not torch.int32 or t.device != device or
-                              t.shape != (n,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 [{n}] on {device}")
+        return None, None
+    return (whole(slots, "slots", (n,), torch.int32, device),
+            whole(out_slots, "out_slots", (n,), torch.int32, device))
 
 
 def scratch(size: int, workspace, device):

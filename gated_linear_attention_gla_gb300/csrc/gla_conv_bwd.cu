@@ -342,11 +342,9 @@ cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream)
   constexpr int sums = kGroups * (W + 1) * 32 * kV * 4;
   constexpr int smem = rings > sums ? rings : sums;
   auto kernel = conv_bwd_kernel<IO, OUT, W, SILU>;
-  if constexpr (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, smem, done);
+  if (e != cudaSuccess) return e;
   if (blocks + states > 0)
     kernel<<<dim3((unsigned)(blocks + states), (unsigned)((a.D + 32 * kV - 1) / (32 * kV))),
              dim3(32, kGroups), smem, stream>>>(a, partial, bwd_run(rows, a.D), blocks);

@@ -249,7 +249,7 @@ cudaError_t launch_pages_copy(const PagePool* pools, int count, int S, const int
                               const int32_t* dst, int32_t* plan, int n, unsigned* status,
                               cudaStream_t stream) {
   const int smem = 3 * ((S + 31) / 32) * 4;
-  if (smem > 48 * 1024) {
+  if (smem > 48 * 1024) {  // (as many bytes as the call needs: set every time)
     const cudaError_t e = cudaFuncSetAttribute(
         copy_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -416,11 +416,9 @@ cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk,
                           cudaStream_t stream) {
   constexpr int CT = Tile<IO, NS>::CT, smem = (int)sizeof(Tile<IO, NS>);
   auto kernel = scan_fwd_kernel<IO, OUT, NS, SUMS>;
-  if constexpr (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, smem, done);
+  if (e != cudaSuccess) return e;
   kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * runs), kThreads, smem, stream>>>(a, w,
                                                                                         chunk);
   return cudaGetLastError();

@@ -618,12 +618,6 @@ sum_chunks_kernel(ScanBwdArgs a, Space w, long long slots) {
   *to = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-template <typename K> cudaError_t opt_in(K kernel, int bytes) {
-  return bytes > 48 * 1024
-             ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)
-             : cudaSuccess;
-}
-
 template <typename IO, typename OUT, int NS>
 cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t stream) {
   constexpr int CT = Roles<NS>::CT;
@@ -634,8 +628,9 @@ cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t str
   const Space w = space_of(static_cast<float*>(workspace), p.B, rows, p.D, NS);
   constexpr int smem1 = (int)sizeof(Staged<NS>), smem3 = (int)sizeof(GradSmem<NS>);
   static_assert(smem3 <= 227 * 1024, "shared memory of a block");
-  cudaError_t e = opt_in(chunk_sums_kernel<IO, NS>, smem1);
-  if (e == cudaSuccess) e = opt_in(chunk_grads_kernel<IO, OUT, NS>, smem3);
+  static std::atomic<uint64_t> done1{0}, done3{0};
+  cudaError_t e = allow_shared(chunk_sums_kernel<IO, NS>, smem1, done1);
+  if (e == cudaSuccess) e = allow_shared(chunk_grads_kernel<IO, OUT, NS>, smem3, done3);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(slots * tiles);
   if (rows > 0) chunk_sums_kernel<IO, NS><<<grid, kThreads, smem1, stream>>>(a, w);

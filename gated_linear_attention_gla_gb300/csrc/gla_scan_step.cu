@@ -193,8 +193,8 @@ cudaError_t launch_typed(const ScanStepArgs& a, cudaStream_t stream) {
   if (groups * kMostGroups < quads) groups = (quads + kMostGroups - 1) / kMostGroups;
   if (groups > quads) groups = quads;
   auto kernel = scan_step_kernel<IO, OUT, NS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(kernel, smem, done);
   if (e != cudaSuccess) return e;
   kernel<<<dim3((unsigned)tiles, (unsigned)groups), kThreads, smem, stream>>>(a);
   return cudaGetLastError();

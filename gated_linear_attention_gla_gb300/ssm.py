@@ -19,8 +19,8 @@ from typing import Optional
 import torch
 
 from ._binding import GLA_FLAG_SILU, GLA_FLAG_SOFTPLUS
-from ._marshal import (batch, check, done, io_flags, launch_on, lib, on_gpu, output, page_tables,
-                       ptr, row_stride, scratch, shaped)
+from ._marshal import (batch, check, done, io_flags, launch_on, lib, output, page_tables, ptr,
+                       rows, scratch, whole)
 
 _F32 = torch.float32
 
@@ -30,22 +30,25 @@ def _silu_flag(activation) -> int:
     return GLA_FLAG_SILU if activation else 0
 
 
-def _state(state, rows, a, b, slots):
+def _state(state, n, a, b, dtype, device, slots):
+    """The address of a state, dense or a pool, and the pool's pages."""
     shape = state.shape
-    if len(shape) != 3 or shape[1] != a or shape[2] != b or not state.is_contiguous() or \
-            (slots is None and shape[0] != rows):
-        raise ValueError(f"state must be contiguous "
-                         f"[{rows if slots is None else 'num_slots'}, {a}, {b}]")
+    if len(shape) != 3 or shape[1] != a or shape[2] != b or state.dtype is not dtype or \
+            state.device != device or not state.is_contiguous() or \
+            (slots is None and shape[0] != n):
+        raise ValueError(f"state must be contiguous {dtype} "
+                         f"[{n if slots is None else 'num_slots'}, {a}, {b}] on {device}")
+    return state.data_ptr(), 0 if slots is None else shape[0]
 
 
-def _conv_common(x, weight, bias):
+def _filter(x, weight, bias):
+    """(D, W, the filter's and the bias's addresses)."""
     check(x.is_cuda, "x must be a CUDA tensor")
-    on_gpu(_F32, x.device, weight=weight, bias=bias)
-    D = x.shape[-1]
-    if weight.dim() != 2 or weight.shape[0] != D or not weight.is_contiguous():
-        raise ValueError(f"weight must be contiguous [{D}, W]")
-    shaped((D,), bias=bias)
-    return D, weight.shape[1]
+    D, dev = x.shape[-1], x.device
+    check(weight.dim() == 2, "weight is [D, W]")
+    W = weight.shape[1]
+    return (D, W, whole(weight, "weight", (D, W), _F32, dev),
+            whole(bias, "bias", (D,), _F32, dev))
 
 
 def conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None,
@@ -60,20 +63,20 @@ def conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None,
     inputs (oldest first).  ``out`` has x's dtype, or fp32
     (``out_dtype=torch.float32``); ``final_state`` may be ``init_state``.
     """
-    D, W = _conv_common(x, weight, bias)
+    D, W, w, b = _filter(x, weight, bias)
     lead, B, T = batch(x, cu_seqlens, "x")
-    stride = row_stride(x, "x", lead, D)
-    flags = io_flags(x.dtype, out.dtype if out is not None else out_dtype or x.dtype)
+    dev, dt, st = x.device, x.dtype, (B, W - 1, D)
+    px, stride = rows(x, "x", x.shape, dt, dev)
+    flags = io_flags(dt, out.dtype if out is not None else out_dtype or dt)
     flags |= _silu_flag(activation)
-    on_gpu(x.dtype, x.device, init_state=init_state, final_state=final_state)
-    shaped((B, W - 1, D), init_state=init_state, final_state=final_state)
-    with launch_on(x.device, stream) as s:
-        out = output(out, x.shape, out_dtype or x.dtype, x.device)
+    init = whole(init_state, "init_state", st, dt, dev)
+    whole(final_state, "final_state", st, dt, dev)
+    with launch_on(dev, stream) as s:
+        out = output(out, x.shape, out_dtype or dt, dev)
         if final_state is None and output_final_state:
-            final_state = torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
-        done(lib().gla_conv_fwd(ptr(x), stride, ptr(weight), ptr(bias), ptr(init_state), ptr(out),
-                                ptr(final_state), ptr(cu_seqlens), B, T, D, W, s, flags),
-             "gla_conv_fwd")
+            final_state = torch.empty(st, dtype=dt, device=dev)
+        done(lib().gla_conv_fwd(px, stride, w, b, init, out.data_ptr(), ptr(final_state),
+                                ptr(cu_seqlens), B, T, D, W, s, flags), "gla_conv_fwd")
     return out, final_state
 
 
@@ -87,27 +90,25 @@ def conv_bwd(x, weight, d_out, bias=None, init_state=None, d_final_state=None, c
     ``dx`` has x's dtype, or fp32 with ``grad_dtype=torch.float32``; ``d_bias`` is
     None without a bias; ``d_init`` is fp32 (None when not requested).
     """
-    D, W = _conv_common(x, weight, bias)
+    D, W, w, b = _filter(x, weight, bias)
     lead, B, T = batch(x, cu_seqlens, "x")
-    stride = row_stride(x, "x", lead, D)
-    grad_dtype = grad_dtype or x.dtype
-    flags = io_flags(x.dtype, grad_dtype) | _silu_flag(activation)
-    dev = x.device
-    on_gpu(x.dtype, dev, d_out=d_out, init_state=init_state)
-    on_gpu(_F32, dev, d_final_state=d_final_state)
-    shaped(x.shape, d_out=d_out)
-    shaped((B, W - 1, D), init_state=init_state, d_final_state=d_final_state)
+    dev, dt, st = x.device, x.dtype, (B, W - 1, D)
+    px, stride = rows(x, "x", x.shape, dt, dev)
+    grad_dtype = grad_dtype or dt
+    flags = io_flags(dt, grad_dtype) | _silu_flag(activation)
+    init = whole(init_state, "init_state", st, dt, dev)
+    dy = whole(d_out, "d_out", x.shape, dt, dev)
+    df = whole(d_final_state, "d_final_state", st, _F32, dev)
     with launch_on(dev, stream) as s:
         size = lib().gla_conv_bwd_workspace_size(B, T, D, W, cu_seqlens is not None)
         workspace = scratch(size, workspace, dev)
         dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
         dw = torch.empty((D, W), dtype=_F32, device=dev)
         db = torch.empty(D, dtype=_F32, device=dev) if bias is not None else None
-        di = torch.empty((B, W - 1, D), dtype=_F32, device=dev) if need_d_init else None
-        done(lib().gla_conv_bwd(ptr(x), stride, ptr(weight), ptr(bias), ptr(init_state),
-                                ptr(d_out), ptr(d_final_state), ptr(dx), ptr(dw), ptr(db),
-                                ptr(di), ptr(cu_seqlens), B, T, D, W, ptr(workspace), size, s,
-                                flags), "gla_conv_bwd")
+        di = torch.empty(st, dtype=_F32, device=dev) if need_d_init else None
+        done(lib().gla_conv_bwd(px, stride, w, b, init, dy, df, dx.data_ptr(), dw.data_ptr(),
+                                ptr(db), ptr(di), ptr(cu_seqlens), B, T, D, W, ptr(workspace),
+                                size, s, flags), "gla_conv_bwd")
     return dx, dw, db, di
 
 
@@ -121,36 +122,32 @@ def conv_step(x, weight, state, bias=None, activation: Optional[str] = None, slo
     given (the page read stays as it was).  -1 in either marks a row that does
     nothing.
     """
-    D, W = _conv_common(x, weight, bias)
+    D, W, w, b = _filter(x, weight, bias)
     check(x.dim() == 2, "x is [N, D]")
-    N = x.shape[0]
-    stride = row_stride(x, "x", (N,), D)
-    on_gpu(x.dtype, x.device, state=state)
-    page_tables(N, x.device, slots, out_slots)
-    _state(state, N, W - 1, D, slots)
-    flags = io_flags(x.dtype, out.dtype if out is not None else out_dtype or x.dtype)
+    N, dev, dt = x.shape[0], x.device, x.dtype
+    px, stride = rows(x, "x", x.shape, dt, dev)
+    ps, pages = _state(state, N, W - 1, D, dt, dev, slots)
+    pi, po = page_tables(N, dev, slots, out_slots)
+    flags = io_flags(dt, out.dtype if out is not None else out_dtype or dt)
     flags |= _silu_flag(activation)
-    with launch_on(x.device, stream) as s:
-        out = output(out, (N, D), out_dtype or x.dtype, x.device)
-        done(lib().gla_conv_step(ptr(x), stride, ptr(weight), ptr(bias), ptr(state),
-                                 0 if slots is None else state.shape[0], ptr(slots),
-                                 ptr(out_slots), ptr(out), N, D, W, s, flags), "gla_conv_step")
+    with launch_on(dev, stream) as s:
+        out = output(out, (N, D), out_dtype or dt, dev)
+        done(lib().gla_conv_step(px, stride, w, b, ps, pages, pi, po, out.data_ptr(), N, D, W, s,
+                                 flags), "gla_conv_step")
     return out
 
 
 def _scan_common(u, dt, a, b, c, skip, z, dt_bias, lead):
     """Checks; returns (D, N, the row arguments shared by the scan's entry points)."""
     check(u.is_cuda, "u must be a CUDA tensor")
-    dev = u.device
-    on_gpu(u.dtype, dev, dt=dt, b=b, c=c, z=z)
-    on_gpu(_F32, dev, a=a, skip=skip, dt_bias=dt_bias)
-    D, N = u.shape[-1], a.shape[-1]
-    shaped((D, N), a=a)
-    shaped((D,), skip=skip, dt_bias=dt_bias)
-    args = (ptr(u), row_stride(u, "u", lead, D), ptr(dt), row_stride(dt, "dt", lead, D), ptr(a),
-            ptr(b), row_stride(b, "b", lead, N), ptr(c), row_stride(c, "c", lead, N), ptr(skip),
-            ptr(z), 0 if z is None else row_stride(z, "z", lead, D), ptr(dt_bias))
-    return D, N, args
+    dev, ty, wide = u.device, u.dtype, u.shape
+    D, N = wide[-1], a.shape[-1]
+    narrow = (*lead, N)
+    pz, sz = (None, 0) if z is None else rows(z, "z", wide, ty, dev)
+    return D, N, (*rows(u, "u", wide, ty, dev), *rows(dt, "dt", wide, ty, dev),
+                  whole(a, "a", (D, N), _F32, dev), *rows(b, "b", narrow, ty, dev),
+                  *rows(c, "c", narrow, ty, dev), whole(skip, "skip", (D,), _F32, dev), pz, sz,
+                  whole(dt_bias, "dt_bias", (D,), _F32, dev))
 
 
 def scan_fwd(u, dt, a, b, c, skip=None, z=None, dt_bias=None, softplus: bool = True,
@@ -171,17 +168,16 @@ def scan_fwd(u, dt, a, b, c, skip=None, z=None, dt_bias=None, softplus: bool = T
     dev = u.device
     flags = io_flags(u.dtype, out.dtype if out is not None else out_dtype or u.dtype)
     flags |= GLA_FLAG_SOFTPLUS if softplus else 0
-    on_gpu(_F32, dev, init_state=init_state, final_state=final_state)
-    shaped((B, D, N), init_state=init_state, final_state=final_state)
+    init = whole(init_state, "init_state", (B, D, N), _F32, dev)
+    whole(final_state, "final_state", (B, D, N), _F32, dev)
     with launch_on(dev, stream) as s:
         size = lib().gla_scan_fwd_workspace_size(B, T, D, N, cu_seqlens is not None)
         workspace = scratch(size, workspace, dev)
         out = output(out, u.shape, out_dtype or u.dtype, dev)
         if final_state is None and output_final_state:
             final_state = torch.empty((B, D, N), dtype=_F32, device=dev)
-        done(lib().gla_scan_fwd(*args, ptr(init_state), ptr(out), ptr(final_state),
-                                ptr(cu_seqlens), B, T, D, N, ptr(workspace), size, s, flags),
-             "gla_scan_fwd")
+        done(lib().gla_scan_fwd(*args, init, out.data_ptr(), ptr(final_state), ptr(cu_seqlens),
+                                B, T, D, N, ptr(workspace), size, s, flags), "gla_scan_fwd")
     return out, final_state
 
 
@@ -200,10 +196,9 @@ def scan_bwd(u, dt, a, b, c, d_out, skip=None, z=None, dt_bias=None, softplus: b
     dev = u.device
     grad_dtype = grad_dtype or u.dtype
     flags = io_flags(u.dtype, grad_dtype) | (GLA_FLAG_SOFTPLUS if softplus else 0)
-    on_gpu(u.dtype, dev, d_out=d_out)
-    on_gpu(_F32, dev, init_state=init_state, d_final_state=d_final_state)
-    shaped(u.shape, d_out=d_out)
-    shaped((B, D, N), init_state=init_state, d_final_state=d_final_state)
+    init = whole(init_state, "init_state", (B, D, N), _F32, dev)
+    dy = whole(d_out, "d_out", u.shape, u.dtype, dev)
+    df = whole(d_final_state, "d_final_state", (B, D, N), _F32, dev)
     with launch_on(dev, stream) as s:
         size = lib().gla_scan_bwd_workspace_size(B, T, D, N, cu_seqlens is not None)
         workspace = scratch(size, workspace, dev)
@@ -215,8 +210,8 @@ def scan_bwd(u, dt, a, b, c, d_out, skip=None, z=None, dt_bias=None, softplus: b
         dskip = new(D) if skip is not None else None
         dbias = new(D) if dt_bias is not None else None
         di = new((B, D, N)) if need_d_init else None
-        done(lib().gla_scan_bwd(*args, ptr(init_state), ptr(d_out), ptr(d_final_state), ptr(du),
-                                ptr(ddt), ptr(da), ptr(db), ptr(dc), ptr(dskip), ptr(dz),
+        done(lib().gla_scan_bwd(*args, init, dy, df, du.data_ptr(), ddt.data_ptr(),
+                                da.data_ptr(), db.data_ptr(), dc.data_ptr(), ptr(dskip), ptr(dz),
                                 ptr(dbias), ptr(di), ptr(cu_seqlens), B, T, D, N, ptr(workspace),
                                 size, s, flags), "gla_scan_bwd")
     return du, ddt, da, db, dc, dskip, dz, dbias, di
@@ -231,14 +226,12 @@ def scan_step(u, dt, a, b, c, state, skip=None, z=None, dt_bias=None, softplus: 
     R = u.shape[0]
     D, N, args = _scan_common(u, dt, a, b, c, skip, z, dt_bias, (R,))
     dev = u.device
-    on_gpu(_F32, dev, state=state)
-    page_tables(R, dev, slots, out_slots)
-    _state(state, R, D, N, slots)
+    ps, pages = _state(state, R, D, N, _F32, dev, slots)
+    pi, po = page_tables(R, dev, slots, out_slots)
     flags = io_flags(u.dtype, out.dtype if out is not None else out_dtype or u.dtype)
     flags |= GLA_FLAG_SOFTPLUS if softplus else 0
     with launch_on(dev, stream) as s:
         out = output(out, (R, D), out_dtype or u.dtype, dev)
-        done(lib().gla_scan_step(*args, ptr(state), 0 if slots is None else state.shape[0],
-                                 ptr(slots), ptr(out_slots), ptr(out), R, D, N, s, flags),
+        done(lib().gla_scan_step(*args, ps, pages, pi, po, out.data_ptr(), R, D, N, s, flags),
              "gla_scan_step")
     return out

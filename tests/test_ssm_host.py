@@ -237,18 +237,24 @@ def test_python_wrappers_refuse_cpu_tensors_and_bad_options():
 
 
 def test_row_strides():
-    from gated_linear_attention_gla_gb300._marshal import row_stride
+    from gated_linear_attention_gla_gb300._marshal import rows
     t = torch.zeros(3, 5, 32)
-    assert row_stride(t, "t", (3, 5), 32) == 32
-    assert row_stride(t[..., 8:16], "t", (3, 5), 8) == 32
-    assert row_stride(t[:, :1, :8], "t", (3, 1), 8) == 160    # one token a sequence
-    assert row_stride(t[:1, :1, :8], "t", (1, 1), 8) == 8
-    for bad, lead, cols in ((t[:, :4, :8], (3, 4), 8),         # rows at two distances
-                            (t[..., ::2], (3, 5), 16),         # columns apart
-                            (t[:, :1].expand(3, 5, 32), (3, 5), 32),  # one row five times
-                            (t.transpose(0, 1), (5, 3), 32)):
+    step = lambda v, dtype=torch.float32: rows(v, "t", v.shape, dtype, v.device)[1]  # noqa: E731
+    assert step(t) == 32 and step(t[..., 8:16]) == 32 and step(t[0, :, 8:16]) == 32
+    assert step(t[:, :1, :8]) == 160                            # one token a sequence
+    assert step(t[:1, :1, :8]) == 8 and step(t[0, :1, :8]) == 8  # one row
+    assert step(t[:0]) == 32
+    assert rows(t[..., 8:16], "t", (3, 5, 8), torch.float32, t.device)[0] == t.data_ptr() + 32
+    for bad in (t[:, :4, :8],                                  # rows at two distances
+                t[..., ::2],                                   # columns apart
+                t[:, :1].expand(3, 5, 32),                     # one row five times
+                t.transpose(0, 1), t[None]):
         with pytest.raises(ValueError):
-            row_stride(bad, "t", lead, cols)
+            step(bad)
+    with pytest.raises(ValueError):
+        step(t, torch.bfloat16)
+    with pytest.raises(ValueError):
+        rows(t, "t", (3, 5, 31), torch.float32, t.device)
 
 
 def _differences(f, t, idx, eps=1e-6):
