@@ -137,11 +137,11 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     bias2[i] = pack2(bias[2 * i], bias[2 * i + 1]);
-    db[i] = 0;
+    db[i] = f32x2{};
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       w2[i][k] = pack2(w[2 * i][k], w[2 * i + 1][k]);
-      dw[i][k] = 0;
+      dw[i][k] = f32x2{};
     }
   }
   extern __shared__ __align__(16) unsigned char smem[];
@@ -187,7 +187,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           win[k][i] = pack2(w0[k][2 * i], w0[k][2 * i + 1]);
-          dpw[k][i] = 0;
+          dpw[k][i] = f32x2{};
         }
       return true;
     };

@@ -136,7 +136,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
       v[2] = pack2(y.x * scale, y.y * scale);
       v[3] = pack2(y.z * scale, y.w * scale);
     };
-    f32x2 a[4], h[4] = {0, 0, 0, 0};
+    f32x2 a[4], h[4] = {};
     load8(p.a, a, kLog2e);
     if (!SUMS) {
       const float* from = chunk ? w.h + slot * p.D * NS
@@ -186,7 +186,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
           fetch(t4 + x + 2, r[(x + 2) % 4]);
           const Row& cur = r[x];
           const f32x2 dl = both(r[(x + 1) % 4].d.x), du = both(cur.d.y);
-          f32x2 ys = 0;
+          f32x2 ys = {};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const f32x2 en = ex2x2(mul2(dl, a[m]));
@@ -238,8 +238,8 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
 #pragma unroll
   for (int i = 0; i < kV / 2; ++i) {
     const int ch = d0 + vc + 2 * i;
-    bias[i] = von && p.dt_bias ? pack2(__ldg(p.dt_bias + ch), __ldg(p.dt_bias + ch + 1)) : 0;
-    skip[i] = !SUMS && von && p.skip ? pack2(__ldg(p.skip + ch), __ldg(p.skip + ch + 1)) : 0;
+    bias[i] = von && p.dt_bias ? pack2(__ldg(p.dt_bias + ch), __ldg(p.dt_bias + ch + 1)) : f32x2{};
+    skip[i] = !SUMS && von && p.skip ? pack2(__ldg(p.skip + ch), __ldg(p.skip + ch + 1)) : f32x2{};
   }
   using R = Raw<IO, kV>;
   constexpr int BC = (TT * NS + kHelp - 1) / kHelp;  // b (and c) elements per thread and tile
@@ -320,7 +320,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
     // (delta, delta u) of the tile, before its stage is free
     f32x2 u[kV / 2], x[kV / 2];
 #pragma unroll
-    for (int j = 0; j < kV / 2; ++j) x[j] = u[j] = 0;  // behind the run: decay 1, no drive
+    for (int j = 0; j < kV / 2; ++j) x[j] = u[j] = f32x2{};  // behind the run: decay 1, no drive
     if (more) {
       cp_wait<L::AHEAD>();
       if (t < left && von) {

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
   const int pair = (threadIdx.x >> 5) * L::PPW + lane % L::PPW, ch = d0 + 2 * pair;
   const bool on = ch < p.D;  // (D is even: both channels or none)
   stage<IO, NS>(a, k, d0, s);
-  f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, run[4], sum = 0;
+  f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, run[4], sum = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j) run[j] = both(1.f);
   if (on) load_states(p.a + (long long)ch * NS + q * 4, NS, true, kLog2e, a2);
@@ -324,22 +324,21 @@ __device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int* fi
 // scattered: a lane holds 4 / LPC of them, or one that lanes share.
 template <int LPC, int PPW>
 __device__ __forceinline__ void reduce_states(f32x2 (&v)[4], int q, int* first) {
-  constexpr unsigned full = 0xffffffffu;
   const bool up = (q & (LPC / 2)) != 0;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const f32x2 give = up ? v[k] : v[k + 2], keep = up ? v[k + 2] : v[k];
-    v[k] = add2(keep, __shfl_xor_sync(full, give, PPW * LPC / 2));
+    v[k] = add2(keep, shfl_xor2(give, PPW * LPC / 2));
   }
   *first = up ? 2 : 0;
   if constexpr (LPC >= 4) {
     const bool up2 = (q & (LPC / 4)) != 0;
     const f32x2 give = up2 ? v[0] : v[1], keep = up2 ? v[1] : v[0];
-    v[0] = add2(keep, __shfl_xor_sync(full, give, PPW * LPC / 4));
+    v[0] = add2(keep, shfl_xor2(give, PPW * LPC / 4));
     *first += up2 ? 1 : 0;
 #pragma unroll
     for (int off = LPC / 8; off > 0; off >>= 1)
-      v[0] = add2(v[0], __shfl_xor_sync(full, v[0], PPW * off));
+      v[0] = add2(v[0], shfl_xor2(v[0], PPW * off));
   }
 }
 

@@ -28,36 +28,25 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// Two fp32 values in one register pair: one instruction works on both.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float x, float y) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
+// Two fp32 values in one register pair: one instruction works on both.  (Of the
+// pair's type the compiler allocates pairs throughout; with 64-bit integers and
+// inline instructions it moved every exponential's result into place first, ten
+// instructions a token in the scan's recurrence.)
+using f32x2 = float2;
+__device__ __forceinline__ f32x2 pack2(float x, float y) { return make_float2(x, y); }
 __device__ __forceinline__ void unpack2(f32x2 v, float* x, float* y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
+  *x = v.x;
+  *y = v.y;
 }
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+__device__ __forceinline__ f32x2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ f32x2 shfl_xor2(f32x2 v, int lanes) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, v.x, lanes),
+                     __shfl_xor_sync(0xffffffffu, v.y, lanes));
 }
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// a * b as a * b - 0: the same value, and one instruction where mul.f32x2 measured two
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  return fma2(a, b, 0x8000000080000000ull);
-}
-__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {  // 2^x of both
-  float x, y;
-  unpack2(v, &x, &y);
-  return pack2(ex2(x), ex2(y));
-}
-__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
 
 // log(1 + e^x) of two values = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].
 // log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, and atanh(s) / s is a
