@@ -12,14 +12,14 @@
 // A block owns 1024 / NS channels of one run of tokens.  Four compute warps: NS / 8
 // lanes a channel, eight states each in four register pairs (f32x2 instructions
 // work on two states); the next two tokens are in registers before the current
-// ones are used.  Four helper warps turn (dt, u) of the next 1024 (token,
-// channel) pairs into (delta, delta u) in shared memory, and finish and store
-// the outputs of the previous ones, so the recurrence never waits for loads,
-// the softplus or the gate.  Two stages, handed over by named barriers.  Lanes
-// that differ in the state sit in different quarters of a warp, so that the
-// reads of b and c are broadcasts within a quarter (2 cycles instead of 4 for 16
-// bytes a lane); the sums over n go through shared memory, up to two terms per
-// pair, and the helpers add them.
+// ones are used.  Two or three helper groups of four warps take turns: one turns
+// (dt, u) of a tile of 1024 (token, channel) pairs into (delta, delta u) in shared
+// memory, and finishes and stores the outputs of its tile before, so that the
+// recurrence does not wait for loads, the softplus or the gate; named barriers
+// hand the stages over.  Lanes that differ in the state sit in different
+// quarters of a warp, so that the reads of b and c are broadcasts within a quarter
+// (2 cycles instead of 4 for 16 bytes a lane); the sums over n go through
+// shared memory, up to two terms per pair, and the helpers add them.
 //
 // One run is a whole sequence, or, where sequences times channel tiles leave
 // SMs idle, a chunk of it (three launches): what every chunk adds to the state
@@ -32,13 +32,22 @@ namespace gla {
 namespace {
 
 constexpr int kCompute = 128;  // threads of the recurrence
-constexpr int kHelp = 128;     // threads of a helper group; group g serves stage g
-constexpr int kGroups = 2;     // stages: tiles g, g + kGroups, ... pass through stage g
-constexpr int kThreads = kCompute + kGroups * kHelp;
+constexpr int kHelp = 128;     // threads of a helper group; group g of G serves stage g,
+                               // through which the tiles g, g + G, ... pass
+constexpr int threads_of(int groups) { return kCompute + groups * kHelp; }
+// A whole sequence a block leaves one or two blocks a SM: a third helper group
+// keeps the recurrence fed (8192 x 2048 x 16: 117 us with two, 109 with three, 114 with
+// four).  Chunks fill the SMs: two groups leave room for more blocks (20001 packed
+// tokens: 398 us with two, 409 with three).
+// (Three groups' stages of fp32 rows do not fit at NS = 64.)
+constexpr int kChunkGroups = 2;
+template <typename IO, int NS> constexpr int whole_groups() {
+  return sizeof(IO) == 4 && NS == 64 ? 2 : 3;
+}
 constexpr int kPairs = 1024;   // (token, channel) pairs of a tile
 constexpr int kV = 8;          // adjacent channels of a token: a helper's pairs of a tile
 
-// Named barriers 1, 2: stage 0, 1 prepared; 3, 4: stage 0, 1 used.  Each joins the
+// Named barriers 1 + g: stage g prepared; 1 + G + g: stage g used.  Each joins the
 // compute warps and one helper group.
 __device__ __forceinline__ void bar_sync(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCompute + kHelp) : "memory");
@@ -54,20 +63,20 @@ struct FwdSpace {
 };
 
 // The layout of a tile's shared memory.
-template <typename IO, int NS> struct Tile {
+template <typename IO, int NS, int G> struct Tile {
   static constexpr int LPC = NS / 8;              // lanes per channel
   static constexpr int CPW = 32 / LPC;            // channels per warp
   static constexpr int CT = kCompute / LPC;       // channels per block
   static constexpr int TT = kPairs / CT;          // tokens per tile
   static constexpr int NP = LPC > 1 ? 2 : 1;      // terms of a pair's sum over n
   static constexpr int HELD = 4 * NP / LPC;       // tokens (of 4) whose term a lane holds
-  float2 d[kGroups][TT * CT];                     // (delta, delta u); see dd_at
-  float b[kGroups][TT][NS], c[kGroups][TT][NS];
-  float y[kGroups][NP][TT][CT];
+  float2 d[G][TT * CT];                     // (delta, delta u); see dd_at
+  float b[G][TT][NS], c[G][TT][NS];
+  float y[G][NP][TT][CT];
   // rows as they come, each thread its own: of the tile in the stage, of the next
   // one of the group, and of those whose copies are in flight
   static constexpr int AHEAD = sizeof(IO) == 2 ? 2 : 1, RING = AHEAD + 2;
-  Raw<IO, kV> u[kGroups][RING][kHelp], dt[kGroups][RING][kHelp], z[kGroups][RING][kHelp];
+  Raw<IO, kV> u[G][RING][kHelp], dt[G][RING][kHelp], z[G][RING][kHelp];
   // Place of channel ch in a row of d: its 16-byte unit (two channels) is moved
   // within its 128 bytes so that the helpers' stores, 64 bytes apart, spread
   // over the banks.
@@ -102,10 +111,10 @@ __device__ __forceinline__ void reduce_states(float (&y)[4], int q, int* first) 
 
 // SUMS: the first of the three launches; else the scan itself, from init_state
 // (chunk 0: one run per sequence) or from w.h.
-template <typename IO, typename OUT, int NS, bool SUMS>
-__global__ void __launch_bounds__(kThreads)
+template <typename IO, typename OUT, int NS, bool SUMS, int G>
+__global__ void __launch_bounds__(threads_of(G))
 scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
-  using L = Tile<IO, NS>;
+  using L = Tile<IO, NS, G>;
   constexpr int LPC = L::LPC, CT = L::CT, TT = L::TT;
   extern __shared__ __align__(16) unsigned char smem[];
   L& s = *reinterpret_cast<L*>(smem);
@@ -145,8 +154,8 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
     }
     const int at = L::dd_at(lc);
     float sum = 0.f;
+    int buf = 0;
     for (int i = 0; i < tiles_t; ++i) {
-      const int buf = i & 1;
       bar_sync(1 + buf);
       const float2* sd = &s.d[buf][at];
       const float* sb = &s.b[buf][0][q * 8];
@@ -209,7 +218,8 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
           for (int m = 0; m < L::HELD; ++m) s.y[buf][q & (L::NP - 1)][t4 + first + m][lc] = y[m];
         }
       }
-      bar_arrive(3 + buf);
+      bar_arrive(1 + G + buf);
+      buf = buf + 1 == G ? 0 : buf + 1;
     }
     if (d0 + lc < p.D) {
       float* to = SUMS ? w.h + slot * p.D * NS
@@ -244,7 +254,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
   using R = Raw<IO, kV>;
   constexpr int BC = (TT * NS + kHelp - 1) / kHelp;  // b (and c) elements per thread and tile
   constexpr bool AHEAD = BC <= 4;                    // ... kept in registers a group's tile ahead
-  constexpr int STEP = kGroups * TT;                 // tokens from a group's tile to its next
+  constexpr int STEP = G * TT;                 // tokens from a group's tile to its next
   IO rb[AHEAD ? BC : 1], rc[AHEAD ? BC : 1];
   const long long row = k.t0 + g * TT + vt;
   const IO* pu = (const IO*)p.u + row * p.u_stride + d0 + vc;
@@ -252,8 +262,12 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
   const IO* pz = !SUMS && p.z ? (const IO*)p.z + row * p.z_stride + d0 + vc : nullptr;
   OUT* po = (OUT*)p.out + row * p.D + d0 + vc;
   const int left = (int)(k.t1 - k.t0);               // tokens of the run
-  const IO* pb = (const IO*)p.b + k.t0 * p.b_stride;
-  const IO* pc = (const IO*)p.c + k.t0 * p.c_stride;
+  // this thread's elements of b and c: column tid % NS of the rows tid / NS, tid /
+  // NS + kHelp / NS, ... of a tile
+  constexpr int BROWS = kHelp / NS;
+  const IO* pb = (const IO*)p.b + (k.t0 + g * TT + tid / NS) * p.b_stride + tid % NS;
+  const IO* pc = (const IO*)p.c + (k.t0 + g * TT + tid / NS) * p.c_stride + tid % NS;
+  int t_bc = g * TT + tid / NS;   // the first one's token
   auto copy = [](R* to, const IO* from) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(R) / 16; ++i)
@@ -275,20 +289,25 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
     pd += STEP * p.dt_stride;
     if (!SUMS && p.z) pz += STEP * p.z_stride;
   };
-  auto load_bc = [&](int t0) {
+  auto next_bc = [&]() {
+    t_bc += STEP;
+    pb += STEP * p.b_stride;
+    pc += STEP * p.c_stride;
+  };
+  auto load_bc = [&]() {
     if constexpr (AHEAD) {
 #pragma unroll
       for (int e = 0; e < BC; ++e) {
-        const int x = tid + e * kHelp, t = t0 + x / NS;
         rb[e] = rc[e] = from_f32<IO>(0.f);
-        if (t < left && x < TT * NS) {
-          rb[e] = pb[t * p.b_stride + x % NS];
-          if (!SUMS) rc[e] = pc[t * p.c_stride + x % NS];
+        if (t_bc + e * BROWS < left) {
+          rb[e] = pb[e * BROWS * p.b_stride];
+          if (!SUMS) rc[e] = pc[e * BROWS * p.c_stride];
         }
       }
+      next_bc();
     }
   };
-  auto store_bc = [&](int t0) {
+  auto store_bc = [&]() {
     float* sb = &s.b[g][0][0];
     float* sc = &s.c[g][0][0];
     if constexpr (AHEAD) {
@@ -302,20 +321,22 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
     } else {
 #pragma unroll 8
       for (int e = 0; e < BC; ++e) {
-        const int x = tid + e * kHelp, t = t0 + x / NS;
-        sb[x] = t < left ? to_f32(pb[t * p.b_stride + x % NS]) : 0.f;
-        if (!SUMS) sc[x] = t < left ? to_f32(pc[t * p.c_stride + x % NS]) : 0.f;
+        const int x = tid + e * kHelp;
+        const bool in = t_bc + e * BROWS < left;
+        sb[x] = in ? to_f32(pb[e * BROWS * p.b_stride]) : 0.f;
+        if (!SUMS) sc[x] = in ? to_f32(pc[e * BROWS * p.c_stride]) : 0.f;
       }
+      next_bc();
     }
   };
 
-  load_bc(g * TT);
+  load_bc();
 #pragma unroll
   for (int i = 0; i <= L::AHEAD; ++i) load();
   int last = 0;                   // ring place of the tile in the stage
   // one pass per tile of the group, and one to finish the last
-  for (int tile = g; tile < tiles_t + kGroups; tile += kGroups) {
-    const bool more = tile < tiles_t, prior = tile >= kGroups;
+  for (int tile = g; tile < tiles_t + G; tile += G) {
+    const bool more = tile < tiles_t, prior = tile >= G;
     const int t = tile * TT + vt;
     // (delta, delta u) of the tile, before its stage is free
     f32x2 u[kV / 2], x[kV / 2];
@@ -336,7 +357,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
     }
     f32x2 y[kV / 2];
     if (prior) {
-      bar_sync(3 + g);
+      bar_sync(1 + G + g);
       if (!SUMS) {
 #pragma unroll
         for (int m = 0; m < kV / 4; ++m) {
@@ -352,7 +373,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
       }
     }
     if (more) {
-      store_bc(tile * TT);
+      store_bc();
 #pragma unroll
       for (int j = 0; j < kV / 2; ++j) {
         float d0v, d1v, u0, u1;
@@ -362,7 +383,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
             make_float4(d0v, u0, d1v, u1);
       }
       bar_arrive(1 + g);
-      load_bc((tile + kGroups) * TT);
+      load_bc();
     }
     if (!SUMS && prior && t - STEP < left && von) {
       f32x2 z[kV / 2];
@@ -411,16 +432,17 @@ scan_fwd_chunks_kernel(ScanArgs p, FwdSpace w, long long chunk) {
   reinterpret_cast<float4*>(w.h)[(f + n - 1) * per + in] = run;
 }
 
-template <typename IO, typename OUT, int NS, bool SUMS>
+template <typename IO, typename OUT, int NS, bool SUMS, int G>
 cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk, long long runs,
                           cudaStream_t stream) {
-  constexpr int CT = Tile<IO, NS>::CT, smem = (int)sizeof(Tile<IO, NS>);
-  auto kernel = scan_fwd_kernel<IO, OUT, NS, SUMS>;
+  constexpr int CT = Tile<IO, NS, G>::CT, smem = (int)sizeof(Tile<IO, NS, G>);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
+  auto kernel = scan_fwd_kernel<IO, OUT, NS, SUMS, G>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * runs), kThreads, smem, stream>>>(a, w,
-                                                                                        chunk);
+  kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * runs), threads_of(G), smem, stream>>>(
+      a, w, chunk);
   return cudaGetLastError();
 }
 
@@ -448,17 +470,21 @@ template <typename IO, typename OUT, int NS>
 cudaError_t launch_typed(const ScanArgs& a, void* workspace, cudaStream_t stream) {
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
   const long long chunk = rows > 0 ? chunk_rule(a.B, rows, a.D, NS, a.cu_seqlens != nullptr) : 0;
-  if (chunk == 0) return launch_kernel<IO, OUT, NS, false>(a, FwdSpace{}, 0, a.B, stream);
+  if (chunk == 0)
+    return launch_kernel<IO, OUT, NS, false, whole_groups<IO, NS>()>(a, FwdSpace{}, 0, a.B,
+                                                                     stream);
   const long long slots = slots_of(a.B, rows, chunk);
   FwdSpace w;
   w.h = static_cast<float*>(workspace);
   w.sum = w.h + slots * a.D * NS;
-  cudaError_t e = launch_kernel<IO, OUT, NS, true>(a, w, chunk, slots, stream);
+  cudaError_t e = launch_kernel<IO, OUT, NS, true, kChunkGroups>(a, w, chunk, slots, stream);
   if (e != cudaSuccess) return e;
   const long long per = (long long)a.B * a.D * (NS / 4);
   scan_fwd_chunks_kernel<<<(unsigned)((per + 127) / 128), 128, 0, stream>>>(a, w, chunk);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_kernel<IO, OUT, NS, false>(a, w, chunk, slots, stream);
+  return e != cudaSuccess
+             ? e
+             : launch_kernel<IO, OUT, NS, false, kChunkGroups>(a, w, chunk, slots, stream);
 }
 
 template <typename IO, typename OUT>
