@@ -65,7 +65,7 @@ __device__ __forceinline__ bool seq_ok(const ScanArgs& p, int s, bool report, lo
 __device__ __forceinline__ void scan_chunks(float4* v, const float* sum, float4 x, long long f,
                                             long long n, long long per, long long in, int D,
                                             int ch, bool back, float4* run) {
-  constexpr int U = 8;
+  constexpr int U = 16;
   for (long long c0 = 0; c0 < n; c0 += U) {
     float4 y[U];
     float w[U];

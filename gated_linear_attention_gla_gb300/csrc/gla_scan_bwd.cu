@@ -592,29 +592,39 @@ sum_tiles_kernel(ScanBwdArgs a, Space w, int tiles, long long rows) {
   else ((OUT*)a.dc)[row * NS + col - NS] = from_f32<OUT>(sum);
 }
 
-// 4b. da, dskip and ddt_bias: the chunks' partials.
+// 4b. da, dskip and ddt_bias: the chunks' partials, 32 columns a block, eight
+// threads a column.
 __global__ void __launch_bounds__(256)
 sum_chunks_kernel(ScanBwdArgs a, Space w, long long slots) {
+  __shared__ float part[8][32];
   const long long D = a.f.D, DN = D * a.f.NS;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const float* from;
-  float* to;
-  long long step;
+  const int col = threadIdx.x % 32, row = threadIdx.x / 32;
+  const long long i = (long long)blockIdx.x * 32 + col;
+  const float* from = nullptr;
+  float* to = nullptr;
+  long long step = D;
   if (i < DN) { from = w.h + i; to = a.da + i; step = DN; }
-  else if (i < DN + D) { from = w.sum + i - DN; to = a.dskip ? a.dskip + i - DN : nullptr; step = D; }
+  else if (i < DN + D) { from = w.sum + i - DN; to = a.dskip ? a.dskip + i - DN : nullptr; }
   else if (i < DN + 2 * D) {
     from = w.sum2 + i - DN - D;
     to = a.ddt_bias ? a.ddt_bias + i - DN - D : nullptr;
-    step = D;
-  } else return;
-  if (!to) return;
+  }
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  long long t = 0;
-  for (; t + 4 <= slots; t += 4)
+  if (to) {
+    long long t = row;
+    for (; t + 24 < slots; t += 32)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s[u] += from[(t + u) * step];
-  for (; t < slots; ++t) s[0] += from[t * step];
-  *to = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int u = 0; u < 4; ++u) s[u] += from[(t + 8 * u) * step];
+    for (; t < slots; t += 8) s[0] += from[t * step];
+  }
+  part[row][col] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (row == 0 && to) {
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) sum += part[r][col];
+    *to = sum;
+  }
 }
 
 template <typename IO, typename OUT, int NS>
@@ -642,7 +652,7 @@ cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t str
     sum_tiles_kernel<OUT><<<(unsigned)((rows * 2 * NS + 255) / 256), 256, 0, stream>>>(a, w, tiles,
                                                                                       rows);
   const long long n = (long long)p.D * (NS + 2);
-  sum_chunks_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a, w, slots);
+  sum_chunks_kernel<<<(unsigned)((n + 31) / 32), 256, 0, stream>>>(a, w, slots);
   return cudaGetLastError();
 }
 
