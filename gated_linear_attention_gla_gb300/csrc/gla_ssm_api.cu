@@ -49,6 +49,7 @@ size_t span(long long rows, long long stride, long long cols, long long esz) {
 gla_status finish(cudaError_t e) { return static_cast<gla_status>(gla::cuda_result(e)); }
 
 bool ns_ok(int n) { return n == 8 || n == 16 || n == 32 || n == 64; }
+bool channels_ok(int D) { return D % 8 == 0 && D <= 1 << 24; }
 
 // Rows, channel count and row strides shared by the entry points below.
 // stride rows must hold the columns and keep every row 16-byte aligned.
@@ -66,7 +67,7 @@ gla_status gla_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
   if ((flags & ~(GLA_FLAG_FP32_IO | GLA_FLAG_FP32_OUT | GLA_FLAG_SILU)) != 0u || B < 0 || T < 0 ||
       D < 0)
     return GLA_ERR_INVALID_ARG;
-  if (W < 2 || W > 4 || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (W < 2 || W > 4 || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (B == 0 || D == 0) return GLA_OK;
   const bool fp32 = (flags & GLA_FLAG_FP32_IO) != 0;
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
@@ -114,7 +115,7 @@ gla_status gla_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
   if ((flags & ~(GLA_FLAG_FP32_IO | GLA_FLAG_FP32_OUT | GLA_FLAG_SILU)) != 0u || B < 0 || T < 0 ||
       D < 0)
     return GLA_ERR_INVALID_ARG;
-  if (W < 2 || W > 4 || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (W < 2 || W > 4 || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (D == 0) return GLA_OK;
   const bool fp32 = (flags & GLA_FLAG_FP32_IO) != 0;
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
@@ -167,7 +168,7 @@ gla_status gla_conv_step(const void* x, int64_t x_stride, const float* weight, c
   if ((flags & ~(GLA_FLAG_FP32_IO | GLA_FLAG_FP32_OUT | GLA_FLAG_SILU)) != 0u || N < 0 || D < 0 ||
       num_slots < 0 || (!slots && (num_slots != 0 || out_slots)))
     return GLA_ERR_INVALID_ARG;
-  if (W < 2 || W > 4 || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (W < 2 || W > 4 || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (N == 0 || D == 0) return GLA_OK;
   const bool fp32 = (flags & GLA_FLAG_FP32_IO) != 0;
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
@@ -266,7 +267,7 @@ gla_status gla_scan_fwd(const void* u, int64_t u_stride, const void* dt, int64_t
                         void* workspace, size_t workspace_bytes, gla_stream_t stream,
                         unsigned flags) {
   if ((flags & ~kScanFlags) != 0u || B < 0 || T < 0 || D < 0) return GLA_ERR_INVALID_ARG;
-  if (!ns_ok(N) || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (!ns_ok(N) || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (B == 0 || D == 0) return GLA_OK;
   gla::ScanArgs s{};
   const gla_status bad = scan_args(u, u_stride, dt, dt_stride, a, b, b_stride, c, c_stride, skip,
@@ -307,7 +308,7 @@ gla_status gla_scan_bwd(const void* u, int64_t u_stride, const void* dt, int64_t
                         const int32_t* cu_seqlens, int B, int T, int D, int N, void* workspace,
                         size_t workspace_bytes, gla_stream_t stream, unsigned flags) {
   if ((flags & ~kScanFlags) != 0u || B < 0 || T < 0 || D < 0) return GLA_ERR_INVALID_ARG;
-  if (!ns_ok(N) || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (!ns_ok(N) || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (D == 0) return GLA_OK;
   gla::ScanBwdArgs g{};
   const gla_status bad = scan_args(u, u_stride, dt, dt_stride, a, b, b_stride, c, c_stride, skip,
@@ -354,7 +355,7 @@ gla_status gla_scan_step(const void* u, int64_t u_stride, const void* dt, int64_
   if ((flags & ~kScanFlags) != 0u || rows < 0 || D < 0 || num_slots < 0 ||
       (!slots && (num_slots != 0 || out_slots)))
     return GLA_ERR_INVALID_ARG;
-  if (!ns_ok(N) || D % 8 != 0) return GLA_ERR_UNSUPPORTED;
+  if (!ns_ok(N) || !channels_ok(D)) return GLA_ERR_UNSUPPORTED;
   if (rows == 0 || D == 0) return GLA_OK;
   gla::ScanArgs s{};
   const gla_status bad = scan_args(u, u_stride, dt, dt_stride, a, b, b_stride, c, c_stride, skip,

@@ -398,8 +398,8 @@ const char *gla_chunk_fwd_kernel(int dk, int dv, int chunk, unsigned flags);
  *   - x, u, dt, z, b and c take the distance between rows in elements
  *     (x_stride, ...), so that they may be column slices of one projection's
  *     output.  Every other tensor is contiguous.
- *   - D, the channels, is a multiple of 8.  Rows of x, u, dt, z start on 16
- *     bytes (pointer and stride); b and c rows on an element.
+ *   - D, the channels, is a multiple of 8, at most 2^24.  Rows of x, u, dt, z
+ *     start on 16 bytes (pointer and stride); b and c rows on an element.
  *   - Parameters (weight, bias, a, skip, dt_bias) and their gradients are fp32;
  *     weight, bias and a start on 16 bytes.
  *   - Gradients come in the inputs' dtype, or fp32 with GLA_FLAG_FP32_OUT; they

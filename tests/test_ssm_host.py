@@ -45,7 +45,7 @@ def conv_fwd(L, **kw):
     (dict(flags=E.GLA_FLAG_SOFTPLUS), E.GLA_ERR_INVALID_ARG),
     (dict(B=-1), E.GLA_ERR_INVALID_ARG), (dict(T=-1), E.GLA_ERR_INVALID_ARG),
     (dict(W=1), E.GLA_ERR_UNSUPPORTED), (dict(W=5), E.GLA_ERR_UNSUPPORTED),
-    (dict(D=60), E.GLA_ERR_UNSUPPORTED),
+    (dict(D=60), E.GLA_ERR_UNSUPPORTED), (dict(D=1 << 25, xs=1 << 25), E.GLA_ERR_UNSUPPORTED),
     (dict(xs=56), E.GLA_ERR_INVALID_ARG),                    # rows overlap
     (dict(xs=68), E.GLA_ERR_MISALIGNED),                     # rows not 16-byte aligned (bf16)
     (dict(x=None), E.GLA_ERR_INVALID_ARG), (dict(w=None), E.GLA_ERR_INVALID_ARG),
