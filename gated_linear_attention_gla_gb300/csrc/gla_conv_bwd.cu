@@ -305,6 +305,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
 // d_weight[d][k] and d_bias[d] from the blocks' partials.
 __global__ void __launch_bounds__(256)
 conv_bwd_sum_kernel(const float* partial, long long blocks, int D, int W, float* dw, float* db) {
+  after_previous();
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (long long)(W + 1) * D) return;
   const int k = (int)(i / D), d = (int)(i % D);
@@ -349,9 +350,10 @@ cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream)
     kernel<<<dim3((unsigned)(blocks + states), (unsigned)((a.D + 32 * kV - 1) / (32 * kV))),
              dim3(32, kGroups), smem, stream>>>(a, partial, bwd_run(rows, a.D), blocks);
   const long long n = (long long)(W + 1) * a.D;
-  conv_bwd_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-      partial, blocks, a.D, W, a.d_weight, a.d_bias);
-  return cudaGetLastError();
+  const cudaError_t main = cudaGetLastError();
+  if (main != cudaSuccess) return main;
+  return launch_after(conv_bwd_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                      partial, blocks, a.D, W, a.d_weight, a.d_bias);
 }
 
 template <typename IO, typename OUT>

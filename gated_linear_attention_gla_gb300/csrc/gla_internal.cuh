@@ -307,6 +307,34 @@ inline cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done
   return e;
 }
 
+// A launch that may overlap its own start with the end of the launch before it on
+// the stream (programmatic dependent launch).  The kernel calls after_previous()
+// before it touches memory, so it sees everything the launch before has
+// written; what a chain of such launches wrote is complete when its last one is.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, int smem,
+                                cudaStream_t stream, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next launch of such a chain start (its blocks then wait for this
+// launch's end): for kernels of one block, which leave the GPU empty.
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Sequence bounds for sequence s: dense batches own rows [s*T, s*T+T); packed
 // batches read cu_seqlens.  Returns false (and flags the status word) for a
 // malformed entry.

@@ -42,6 +42,7 @@ __device__ __forceinline__ int block_rank(bool flag, int* total) {
 __global__ void __launch_bounds__(kPlan)
 fork_plan_kernel(const int32_t* used, int32_t* used_out, int S, const int32_t* parents,
                  int32_t* children, int n, unsigned* status) {
+  start_next();
   const int tid = threadIdx.x;
   auto wants = [&](int i) {
     const int p = parents[i];
@@ -97,6 +98,7 @@ fork_plan_kernel(const int32_t* used, int32_t* used_out, int S, const int32_t* p
 __global__ void __launch_bounds__(kPlan)
 compact_plan_kernel(const int32_t* used, int32_t* used_out, int S, const int32_t* slots,
                     int32_t* slots_out, int n, int32_t* forward, unsigned* status) {
+  start_next();
   const int tid = threadIdx.x;
   int L = 0;
   for (int base = 0; base < S; base += kPlan)
@@ -144,6 +146,7 @@ compact_plan_kernel(const int32_t* used, int32_t* used_out, int S, const int32_t
 __global__ void __launch_bounds__(kPlan)
 copy_plan_kernel(const int32_t* src, const int32_t* dst, int n, int S, int32_t* plan,
                  unsigned* status) {
+  start_next();
   extern __shared__ unsigned bits[];  // three maps of S bits: written, written twice, read
   const int words = (S + 31) / 32, tid = threadIdx.x;
   for (int i = tid; i < 3 * words; i += kPlan) bits[i] = 0u;
@@ -193,6 +196,7 @@ free_kernel(const int32_t* used, int32_t* used_out, int S, const int32_t* slots,
 // flight before its first store.
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const PagePools pools, const int32_t* src, const int32_t* dst, int n) {
+  after_previous();
   int q = 0;
   while (q + 1 < pools.count && (int)blockIdx.x >= pools.first[q + 1]) ++q;
   const long long off = ((long long)blockIdx.x - pools.first[q]) * kSlice;
@@ -236,11 +240,16 @@ cudaError_t copy_pages(const PagePool* list, int count, const int32_t* src, cons
       p.first[i] = slices;
       slices += (int)((p.bytes[i] + kSlice - 1) / kSlice);
     }
-    if (slices > 0)
-      copy_pages_kernel<<<dim3((unsigned)slices, (unsigned)(n < 65535 ? n : 65535)), kCopyThreads,
-                          0, stream>>>(p, src, dst, n);
+    if (slices > 0) {
+      // (pairs beyond 256 in turn: a compaction's list has every page, most of
+      // which stay)
+      const cudaError_t e =
+          launch_after(copy_pages_kernel, dim3((unsigned)slices, (unsigned)(n < 256 ? n : 256)),
+                       dim3(kCopyThreads), 0, stream, p, src, dst, n);
+      if (e != cudaSuccess) return e;
+    }
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -114,6 +114,7 @@ __device__ __forceinline__ void reduce_states(float (&y)[4], int q, int* first) 
 template <typename IO, typename OUT, int NS, bool SUMS, int G>
 __global__ void __launch_bounds__(threads_of(G))
 scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
+  if (!SUMS) after_previous();
   using L = Tile<IO, NS, G>;
   constexpr int LPC = L::LPC, CT = L::CT, TT = L::TT;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -409,6 +410,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
 // The states in front of the chunks, and the final states of empty sequences.
 __global__ void __launch_bounds__(128)
 scan_fwd_chunks_kernel(ScanArgs p, FwdSpace w, long long chunk) {
+  after_previous();
   const int quads = p.NS / 4;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long per = (long long)p.D * quads;
@@ -441,8 +443,10 @@ cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((long long)((a.D + CT - 1) / CT) * runs), threads_of(G), smem, stream>>>(
-      a, w, chunk);
+  const dim3 grid((unsigned)((long long)((a.D + CT - 1) / CT) * runs));
+  if (!SUMS && chunk)
+    return launch_after(kernel, grid, dim3(threads_of(G)), smem, stream, a, w, chunk);
+  kernel<<<grid, threads_of(G), smem, stream>>>(a, w, chunk);
   return cudaGetLastError();
 }
 
@@ -480,8 +484,8 @@ cudaError_t launch_typed(const ScanArgs& a, void* workspace, cudaStream_t stream
   cudaError_t e = launch_kernel<IO, OUT, NS, true, kChunkGroups>(a, w, chunk, slots, stream);
   if (e != cudaSuccess) return e;
   const long long per = (long long)a.B * a.D * (NS / 4);
-  scan_fwd_chunks_kernel<<<(unsigned)((per + 127) / 128), 128, 0, stream>>>(a, w, chunk);
-  e = cudaGetLastError();
+  e = launch_after(scan_fwd_chunks_kernel, dim3((unsigned)((per + 127) / 128)), dim3(128), 0,
+                   stream, a, w, chunk);
   return e != cudaSuccess
              ? e
              : launch_kernel<IO, OUT, NS, false, kChunkGroups>(a, w, chunk, slots, stream);

@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
 // last token from behind (blockIdx.y 1), in place; d_init.
 __global__ void __launch_bounds__(128)
 chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
+  after_previous();
   const ScanArgs& p = a.f;
   const int quads = p.NS / 4;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -352,6 +353,7 @@ template <int NS> struct GradSmem {
 // 3. The chunk's gradients.
 template <typename IO, typename OUT, int NS>
 __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a, Space w) {
+  after_previous();
   using L = Roles<NS>;
   constexpr int LPC = L::LPC, PPW = L::PPW, CT = L::CT;
   constexpr int HELD = PPW >= 8 ? 1 : 8 / PPW;   // sums over d that a lane ends up with
@@ -571,35 +573,36 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
   }
 }
 
-// 4a. db and dc: the channel tiles' partials.
+// 4. The partials' sums.  The first blocks: db and dc over the channel tiles, a
+// value a thread; the others: da, dskip and ddt_bias over the chunks, 32 columns
+// a block, eight threads a column.
 template <typename OUT>
 __global__ void __launch_bounds__(256)
-sum_tiles_kernel(ScanBwdArgs a, Space w, int tiles, long long rows) {
+sum_partials_kernel(ScanBwdArgs a, Space w, int tiles, long long rows, long long slots,
+                    long long row_blocks) {
+  after_previous();
   const int NS = a.f.NS;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long n = rows * 2 * NS;
-  if (i >= n) return;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  int t = 0;
-  for (; t + 4 <= tiles; t += 4)
+  if ((long long)blockIdx.x < row_blocks) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long n = rows * 2 * NS;
+    if (i >= n) return;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    int t = 0;
+    for (; t + 4 <= tiles; t += 4)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s[u] += w.part[(t + u) * n + i];
-  for (; t < tiles; ++t) s[0] += w.part[t * n + i];
-  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-  const long long row = i / (2 * NS);
-  const int col = (int)(i % (2 * NS));
-  if (col < NS) ((OUT*)a.db)[row * NS + col] = from_f32<OUT>(sum);
-  else ((OUT*)a.dc)[row * NS + col - NS] = from_f32<OUT>(sum);
-}
-
-// 4b. da, dskip and ddt_bias: the chunks' partials, 32 columns a block, eight
-// threads a column.
-__global__ void __launch_bounds__(256)
-sum_chunks_kernel(ScanBwdArgs a, Space w, long long slots) {
+      for (int u = 0; u < 4; ++u) s[u] += w.part[(t + u) * n + i];
+    for (; t < tiles; ++t) s[0] += w.part[t * n + i];
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    const long long row = i / (2 * NS);
+    const int col = (int)(i % (2 * NS));
+    if (col < NS) ((OUT*)a.db)[row * NS + col] = from_f32<OUT>(sum);
+    else ((OUT*)a.dc)[row * NS + col - NS] = from_f32<OUT>(sum);
+    return;
+  }
   __shared__ float part[8][32];
   const long long D = a.f.D, DN = D * a.f.NS;
   const int col = threadIdx.x % 32, row = threadIdx.x / 32;
-  const long long i = (long long)blockIdx.x * 32 + col;
+  const long long i = ((long long)blockIdx.x - row_blocks) * 32 + col;
   const float* from = nullptr;
   float* to = nullptr;
   long long step = D;
@@ -644,16 +647,18 @@ cudaError_t launch_typed(const ScanBwdArgs& a, void* workspace, cudaStream_t str
   const unsigned grid = (unsigned)(slots * tiles);
   if (rows > 0) chunk_sums_kernel<IO, NS><<<grid, kThreads, smem1, stream>>>(a, w);
   const long long per = (long long)p.B * p.D * (NS / 4);
-  if (p.B > 0) {
-    chunk_scan_kernel<<<dim3((unsigned)((per + 127) / 128), 2), 128, 0, stream>>>(a, w, slots);
-    chunk_grads_kernel<IO, OUT, NS><<<grid, kThreads, smem3, stream>>>(a, w);
-  }
-  if (rows > 0)
-    sum_tiles_kernel<OUT><<<(unsigned)((rows * 2 * NS + 255) / 256), 256, 0, stream>>>(a, w, tiles,
-                                                                                      rows);
-  const long long n = (long long)p.D * (NS + 2);
-  sum_chunks_kernel<<<(unsigned)((n + 31) / 32), 256, 0, stream>>>(a, w, slots);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (p.B > 0 && e == cudaSuccess)
+    e = launch_after(chunk_scan_kernel, dim3((unsigned)((per + 127) / 128), 2), dim3(128), 0,
+                     stream, a, w, slots);
+  if (p.B > 0 && e == cudaSuccess)
+    e = launch_after(chunk_grads_kernel<IO, OUT, NS>, dim3(grid), dim3(kThreads), smem3, stream, a,
+                     w);
+  if (e != cudaSuccess) return e;
+  const long long row_blocks = (rows * 2 * NS + 255) / 256;
+  const long long col_blocks = ((long long)p.D * (NS + 2) + 31) / 32;
+  return launch_after(sum_partials_kernel<OUT>, dim3((unsigned)(row_blocks + col_blocks)),
+                      dim3(256), 0, stream, a, w, tiles, rows, slots, row_blocks);
 }
 
 template <typename IO, typename OUT>
