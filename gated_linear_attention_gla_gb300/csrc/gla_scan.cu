@@ -351,7 +351,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
 #pragma unroll
         for (int j = 0; j < kV / 2; ++j) {
           x[j] = add2(x[j], bias[j]);
-          if (p.softplus) x[j] = softplus2(x[j]);
+          if (p.softplus) x[j] = softplus2<sizeof(IO) == 4>(x[j]);
           u[j] = mul2(x[j], u[j]);
         }
       }

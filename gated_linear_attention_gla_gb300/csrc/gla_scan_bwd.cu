@@ -119,7 +119,7 @@ __device__ __forceinline__ void unpack_row(const ScanArgs& p, const RawRow<IO>& 
   if (p.softplus) {
 #pragma unroll
     for (int i = 0; i < kV; i += 2)
-      unpack2(softplus2(pack2(r.x[i], r.x[i + 1])), &r.dl[i], &r.dl[i + 1]);
+      unpack2(softplus2<sizeof(IO) == 4>(pack2(r.x[i], r.x[i + 1])), &r.dl[i], &r.dl[i + 1]);
   }
 }
 
@@ -536,7 +536,13 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       const float4 yy = *reinterpret_cast<const float4*>(&s.g[t][vc / 2]);
       const float s1[kV] = {o0.x, o0.y, o1.x, o1.y}, s2[kV] = {o0.z, o0.w, o1.z, o1.w};
       const float y[kV] = {yy.x, yy.y, yy.z, yy.w};
-      float du[kV], ddt[kV], dz[kV];
+      float du[kV], ddt[kV], dz[kV], slope[kV];
+      if (p.softplus) {
+#pragma unroll
+        for (int i = 0; i < kV; i += 2)
+          unpack2(softplus_slope2<sizeof(IO) == 4>(pack2(v.x[i], v.x[i + 1])), &slope[i],
+                  &slope[i + 1]);
+      }
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         float g = v.g[i];
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
           g *= v.z[i] * sg;
         }
         ddt[i] = fmaf(kLn2, s2[i], v.u[i] * s1[i]);
-        if (p.softplus) ddt[i] *= sigmoid(v.x[i]);
+        if (p.softplus) ddt[i] *= slope[i];
         du[i] = fmaf(v.dl[i], s1[i], skip[i] * g);
         dskip[i] = fmaf(g, v.u[i], dskip[i]);
         dbias[i] += ddt[i];

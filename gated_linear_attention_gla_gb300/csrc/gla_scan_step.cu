@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStepArgs p) {
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       e[k] = to_f32(s.rows[buf][mine + k][1][lc]) + bias;
-      if (p.softplus) e[k] = softplus(e[k]);
+      if (p.softplus) e[k] = softplus<sizeof(IO) == 4>(e[k]);
       w[k] = e[k] * to_f32(s.rows[buf][mine + k][0][lc]);
     }
 #pragma unroll

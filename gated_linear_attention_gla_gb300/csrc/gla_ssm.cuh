@@ -8,6 +8,7 @@
 namespace gla {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLo = 1.9259630e-8f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^x by the hardware's approximation (flushes subnormal results to zero).
@@ -48,37 +49,56 @@ __device__ __forceinline__ f32x2 shfl_xor2(f32x2 v, int lanes) {
                      __shfl_xor_sync(0xffffffffu, v.y, lanes));
 }
 
+// e^-|x| of two values.  The rounding of the product with log2(e) costs up to
+// |x| 2^-24 of the result; EXACT multiplies what it lost back in.
+template <bool EXACT> __device__ __forceinline__ f32x2 exp_neg_abs2(f32x2 v) {
+  const f32x2 m = make_float2(-fabsf(v.x), -fabsf(v.y));
+  const f32x2 t = mul2(m, both(kLog2e));
+  f32x2 e = ex2x2(t);
+  if (EXACT) {
+    // (beyond 2^-126 the result is zero, and infinite arguments must not give NaN)
+    const f32x2 c = make_float2(fmaxf(m.x, -100.f), fmaxf(m.y, -100.f));
+    const f32x2 lost = fma2(c, both(kLog2eLo),
+                            fma2(c, both(kLog2e), mul2(c, both(-kLog2e))));
+    e = fma2(e, mul2(lost, both(kLn2)), e);
+  }
+  return e;
+}
+
 // log(1 + e^x) of two values = max(x, 0) + log1p(e), e = e^-|x| in (0, 1].
 // log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3, and atanh(s) / s is a
 // polynomial in s^2 <= 1/9: the degree-4 one below (fitted for the least
 // relative error there) is off by 4e-9.  So the small step sizes (1e-4 ..
 // 1e-1) keep their relative accuracy: below 1e-6 for |x| <= 12, 1e-7 on
-// average, from the rounding of x log2(e).  A NaN stays one.
-__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
-  float a, b;
-  unpack2(v, &a, &b);
-  const f32x2 e = ex2x2(mul2(pack2(fabsf(a), fabsf(b)), both(-kLog2e)));
-  float d0, d1;
-  unpack2(add2(e, both(2.f)), &d0, &d1);
-  const f32x2 s = mul2(e, pack2(rcp(d0), rcp(d1)));
+// average, all but 2e-7 of it from the rounding that EXACT takes back (for fp32
+// rows; in bf16 ones dt itself is known to 2^-9).  A NaN stays one.
+template <bool EXACT> __device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+  const f32x2 e = exp_neg_abs2<EXACT>(v);
+  const f32x2 d = add2(e, both(2.f));
+  const f32x2 s = mul2(e, make_float2(rcp(d.x), rcp(d.y)));
   const f32x2 z = mul2(s, s);
   f32x2 p = fma2(both(0.14089167f), z, both(0.13980301f));
   p = fma2(p, z, both(0.20012455f));
   p = fma2(p, z, both(0.33333158f));
   p = fma2(p, z, both(1.f));
-  // (a < 0 ? 0 : a keeps a NaN)
-  return fma2(mul2(s, p), both(2.f), pack2(a < 0.f ? 0.f : a, b < 0.f ? 0.f : b));
+  // (x < 0 ? 0 : x keeps a NaN)
+  return fma2(mul2(s, p), both(2.f), make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y));
 }
+template <bool EXACT> __device__ __forceinline__ float softplus(float x) {
+  return softplus2<EXACT>(both(x)).x;
+}
+
 // the sigmoids of two values
 __device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
-  float a, b;
-  unpack2(add2(ex2x2(mul2(x, both(-kLog2e))), both(1.f)), &a, &b);
-  return pack2(rcp(a), rcp(b));
+  const f32x2 d = add2(ex2x2(mul2(x, both(-kLog2e))), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
-__device__ __forceinline__ float softplus(float x) {
-  float y;
-  unpack2(softplus2(both(x)), &x, &y);
-  return x;
+// softplus' derivative, 1 / (1 + e^-x), as accurate as softplus2
+template <bool EXACT> __device__ __forceinline__ f32x2 softplus_slope2(f32x2 x) {
+  if (!EXACT) return sigmoid2(x);
+  const f32x2 e = exp_neg_abs2<true>(x), d = add2(e, both(1.f));
+  return mul2(make_float2(x.x < 0.f ? e.x : 1.f, x.y < 0.f ? e.y : 1.f),
+              make_float2(rcp(d.x), rcp(d.y)));
 }
 
 // V consecutive elements as they lie in memory (4, 8, 16 or 32 bytes), as words.
