@@ -112,7 +112,7 @@ __device__ __forceinline__ void reduce_states(float (&y)[4], int q, int* first) 
 // SUMS: the first of the three launches; else the scan itself, from init_state
 // (chunk 0: one run per sequence) or from w.h.
 template <typename IO, typename OUT, int NS, bool SUMS, int G>
-__global__ void __launch_bounds__(threads_of(G))
+__global__ void __launch_bounds__(threads_of(G), G == kChunkGroups ? 2 : 1)
 scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
   if (!SUMS) after_previous();
   using L = Tile<IO, NS, G>;
