@@ -451,13 +451,15 @@ cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk,
 }
 
 // The chunk length of a call, 0 for whole sequences.  In units of a block's time
-// for one token (about 0.06 us at NS = 16, one or two blocks a SM): whole
-// sequences take the longest one times the waves of blocks; chunks take 1.7
-// times the work (the extra pass) spread over all SMs, and about 100 for two more
-// launches.  A packed call's longest sequence is not known here: 2.5 times the
-// mean.  Measured, D = 2048 and NS = 16, whole against best chunk: 4 x 2048
-// tokens 122 and 187 us, 1 x 2048 121 and 58 (512), 1 x 512 33 and 21 (128),
-// three packed sequences of 20001 tokens 830 and 415 (1024).
+// for one token (about 0.05 us at NS = 16, a block a SM): whole sequences take the
+// longest one times the waves of blocks; chunks take 1.7 times the work (the
+// extra pass) spread over all SMs, and about 100 for two more launches.  A packed
+// call's longest sequence is not known here: 2.5 times the mean.  Measured, D =
+// 2048 and NS = 16, whole against best chunk: 4 x 2048 tokens 104 and 154 us, 2 x 2048
+// 103 and 87 (256), 1 x 2048 103 and 51 (256), 1 x 512 29 and 19 (64), three packed
+// sequences of 20001 tokens 708 and 350 (1024).  The length leaves about four
+// blocks a SM (two are resident): shorter ones pay for their starts (64 tokens:
+// 504 us in the last case), longer ones leave SMs idle.
 long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
   constexpr long long kSMs = 152;
   const long long tiles = ((long long)D * NS + 1023) / 1024, work = rows * tiles / kSMs;
@@ -466,7 +468,7 @@ long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
   const long long whole = (B * tiles + kSMs - 1) / kSMs * longest;
   if (work * 17 / 10 + 100 >= whole) return 0;
   long long chunk = 64;
-  while (chunk < work && chunk < 1024) chunk *= 2;
+  while (chunk * 6 < work && chunk < 1024) chunk *= 2;  // nearest power of two to work / 4
   return chunk;
 }
 
