@@ -193,28 +193,35 @@ __device__ __forceinline__ void stage(const ScanBwdArgs& a, const Chunk& k, int 
 }
 
 // Four states of a channel pair from [channel][NS] (base at the pair's first
-// channel and the lane's first state), scaled; and back.
-__device__ __forceinline__ void load_states(const float* base, int NS, bool two, float scale,
+// channel and the lane's first state), scaled; and back.  `swap` exchanges the
+// first two with the last two (see sum_channels).
+__device__ __forceinline__ void exchange(f32x2 (&v)[4]) {
+  const f32x2 x = v[0], y = v[1];
+  v[0] = v[2];
+  v[1] = v[3];
+  v[2] = x;
+  v[3] = y;
+}
+__device__ __forceinline__ void load_states(const float* base, int NS, float scale, bool swap,
                                             f32x2 (&v)[4]) {
   const float4 x = *reinterpret_cast<const float4*>(base);
-  const float4 y = two ? *reinterpret_cast<const float4*>(base + NS) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 y = *reinterpret_cast<const float4*>(base + NS);
   v[0] = pack2(x.x * scale, y.x * scale);
   v[1] = pack2(x.y * scale, y.y * scale);
   v[2] = pack2(x.z * scale, y.z * scale);
   v[3] = pack2(x.w * scale, y.w * scale);
+  if (swap) exchange(v);
 }
-__device__ __forceinline__ void store_states(float* base, int NS, const f32x2 (&v)[4]) {
-  float4 x, y;
-  unpack2(v[0], &x.x, &y.x);
-  unpack2(v[1], &x.y, &y.y);
-  unpack2(v[2], &x.z, &y.z);
-  unpack2(v[3], &x.w, &y.w);
-  *reinterpret_cast<float4*>(base) = x;
-  *reinterpret_cast<float4*>(base + NS) = y;
+__device__ __forceinline__ void store_states(float* base, int NS, bool swap, f32x2 (&v)[4]) {
+  if (swap) exchange(v);
+  *reinterpret_cast<float4*>(base) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+  *reinterpret_cast<float4*>(base + NS) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
 }
-// The lane's four values of a row of b or c, each twice.
-__device__ __forceinline__ void load_dup(const float2* row, f32x2 (&v)[4]) {
-  const float4 x = reinterpret_cast<const float4*>(row)[0], y = reinterpret_cast<const float4*>(row)[1];
+// The lane's four values of a row of b or c, each twice; lo and hi are the
+// places of its first and its last two.
+__device__ __forceinline__ void load_dup(const float2* row, int lo, int hi, f32x2 (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(row + lo);
+  const float4 y = *reinterpret_cast<const float4*>(row + hi);
   v[0] = pack2(x.x, x.y);
   v[1] = pack2(x.z, x.w);
   v[2] = pack2(y.x, y.y);
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
   f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, run[4], sum = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j) run[j] = both(1.f);
-  if (on) load_states(p.a + (long long)ch * NS + q * 4, NS, true, kLog2e, a2);
+  if (on) load_states(p.a + (long long)ch * NS + q * 4, NS, kLog2e, false, a2);
   __syncthreads();
 #pragma unroll 4
   for (int t = 0; t < kCH; ++t) {
@@ -248,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
     const float2 gg = s.g[t][pair];
     const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w), g = pack2(gg.x, gg.y);
     f32x2 b[4], c[4];
-    load_dup(&s.b[t][q * 4], b);
-    load_dup(&s.c[t][q * 4], c);
+    load_dup(s.b[t], q * 4, q * 4 + 2, b);
+    load_dup(s.c[t], q * 4, q * 4 + 2, c);
     sum = add2(sum, dl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -261,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
   }
   if (on) {
     const long long at = (slot * p.D + ch) * NS + q * 4;
-    store_states(w.h + at, NS, h);
-    store_states(w.e + at, NS, e);
+    store_states(w.h + at, NS, false, h);
+    store_states(w.e + at, NS, false, e);
     if (q == 0) {
       float2 v;
       unpack2(sum, &v.x, &v.y);
@@ -299,27 +306,44 @@ chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
   if (back && a.d_init_state) reinterpret_cast<float4*>(a.d_init_state)[(long long)s * per + in] = run;
 }
 
-// The sums of v[0 .. 8) over the lanes that differ in the bits OFF, OFF / 2 .. 1,
-// scattered: afterwards a lane holds N of them, v[0 .. N), from index *first.
-template <int OFF, int N>
-__device__ __forceinline__ void reduce_channels(float (&v)[8], int lane, int* first) {
-  if constexpr (OFF >= 1) {
-    if constexpr (N > 1) {
-      const bool up = (lane & OFF) != 0;
+// The sums over the warp's channels of two tokens' values v[token * 4 + state]
+// (of db and dc), scattered: afterwards a lane holds N = 4, 2 or 1 of them.  Lanes
+// in the upper half of the pairs hold their states exchanged, the first two
+// for the last two, so that in the first step every lane keeps its first two
+// states and gives the last two, without selecting which.  Value i of the result is token token_of(i)'s, of state
+// state_of(i) of the lane's four.
+template <int PPW> struct ChannelSums {
+  static constexpr int N = PPW == 2 ? 4 : PPW == 4 ? 2 : 1;
+  f32x2 r[4];
+  int lane;
+  __device__ __forceinline__ ChannelSums(const f32x2 (&v)[8], int lane) : lane(lane) {
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) {
-        const float give = up ? v[k] : v[k + N / 2];
-        const float keep = up ? v[k + N / 2] : v[k];
-        v[k] = keep + __shfl_xor_sync(0xffffffffu, give, OFF);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        r[t * 2 + j] = add2(v[t * 4 + j], shfl_xor2(v[t * 4 + j + 2], PPW / 2));
+    if constexpr (PPW >= 4) {
+      const bool up = (lane & (PPW / 4)) != 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const f32x2 give = up ? r[j] : r[j + 2], keep = up ? r[j + 2] : r[j];
+        r[j] = add2(keep, shfl_xor2(give, PPW / 4));
       }
-      if (up) *first += N / 2;
-      reduce_channels<OFF / 2, N / 2>(v, lane, first);
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], OFF);
-      reduce_channels<OFF / 2, 1>(v, lane, first);
     }
+    if constexpr (PPW >= 8) {
+      const bool up = (lane & (PPW / 8)) != 0;
+      const f32x2 give = up ? r[0] : r[1], keep = up ? r[1] : r[0];
+      r[0] = add2(keep, shfl_xor2(give, PPW / 8));
+    }
+    if constexpr (PPW == 16) r[0] = add2(r[0], shfl_xor2(r[0], 1));
   }
-}
+  __device__ __forceinline__ int token_of(int i) const {
+    return PPW == 2 ? i / 2 : (lane & (PPW / 4)) != 0;
+  }
+  __device__ __forceinline__ int state_of(int i) const {
+    return (PPW <= 4 ? i % 2 : (lane & (PPW / 8)) != 0) + ((lane & (PPW / 2)) != 0 ? 2 : 0);
+  }
+};
 
 // The sums of v[0 .. 4) over a channel pair's lanes (bits PPW and up),
 // scattered: a lane holds 4 / LPC of them, or one that lanes share.
@@ -356,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
   after_previous();
   using L = Roles<NS>;
   constexpr int LPC = L::LPC, PPW = L::PPW, CT = L::CT;
-  constexpr int HELD = PPW >= 8 ? 1 : 8 / PPW;   // sums over d that a lane ends up with
   constexpr int kShare = LPC > 4 ? LPC / 4 : 1;  // lanes that share a sum over n
   const ScanArgs& p = a.f;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -372,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
   const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) {  // no chunk: its partials count as zero
     if (on) {
-      const f32x2 none[4] = {};
-      store_states(w.h + at, NS, none);
+      f32x2 none[4] = {};
+      store_states(w.h + at, NS, false, none);
       if (q == 0) {
         const float2 zero = make_float2(0.f, 0.f);
         *reinterpret_cast<float2*>(w.sum + slot * p.D + ch) = zero;
@@ -382,11 +405,13 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
     }
     return;
   }
+  const bool swap = (lane & (PPW / 2)) != 0;
+  const int lo4 = q * 4 + (swap ? 2 : 0), hi4 = q * 4 + (swap ? 0 : 2);
   f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, da[4] = {};
   if (on) {
-    load_states(p.a + (long long)ch * NS + q * 4, NS, true, kLog2e, a2);
-    load_states(w.h + at, NS, true, 1.f, h);
-    load_states(w.e + at, NS, true, 1.f, e);
+    load_states(p.a + (long long)ch * NS + q * 4, NS, kLog2e, swap, a2);
+    load_states(w.h + at, NS, 1.f, swap, h);
+    load_states(w.e + at, NS, 1.f, swap, e);
   }
   stage<IO, NS>(a, k, d0, s);
   __syncthreads();
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       const float4 d = s.d[t][pair];
       const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w);
       f32x2 b[4];
-      load_dup(&s.b[t][q * 4], b);
+      load_dup(s.b[t], lo4, hi4, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         h[j] = fma2(ex2x2(mul2(dl, a2[j])), h[j], mul2(du, b[j]));
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       const float4 d = s.d[t][pair];
       const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w);
       f32x2 b[4];
-      load_dup(&s.b[t][q * 4], b);
+      load_dup(s.b[t], lo4, hi4, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ds[i][j] = ex2x2(mul2(dl, a2[j]));
@@ -442,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
 #pragma unroll
     for (int half = kSub / 4 - 1; half >= 0; --half) {
       f32x2 s1[4], s2[4], y[4];
-      float vb[8], vc[8];
+      f32x2 v[8];  // a token's and state's terms of db and dc
 #pragma unroll
       for (int x = 3; x >= 0; --x) {
         const int i = half * 4 + x, t = gr * kSub + i;
@@ -450,16 +475,13 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
         const float2 gg = s.g[t][pair];
         const f32x2 dl = pack2(d.x, d.y), du = pack2(d.z, d.w), g = pack2(gg.x, gg.y);
         f32x2 b[4], c[4];
-        load_dup(&s.b[t][q * 4], b);
-        load_dup(&s.c[t][q * 4], c);
+        load_dup(s.b[t], lo4, hi4, b);
+        load_dup(s.c[t], lo4, hi4, c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float lo, hi;
           e[j] = fma2(c[j], g, e[j]);
-          unpack2(mul2(g, hs[i + 1][j]), &lo, &hi);
-          vc[(x & 1) * 4 + j] = lo + hi;
-          unpack2(mul2(du, e[j]), &lo, &hi);
-          vb[(x & 1) * 4 + j] = lo + hi;
+          const f32x2 tb = mul2(du, e[j]), tc = mul2(g, hs[i + 1][j]);
+          v[(x & 1) * 4 + j] = make_float2(tb.x + tb.y, tc.x + tc.y);
           s1[x] = j == 0 ? mul2(e[0], b[0]) : fma2(e[j], b[j], s1[x]);
           y[x] = j == 0 ? mul2(c[0], hs[i + 1][0]) : fma2(c[j], hs[i + 1][j], y[x]);
           e[j] = mul2(e[j], ds[i][j]);
@@ -468,14 +490,13 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
           s2[x] = j == 0 ? mul2(a2[0], wj) : fma2(a2[j], wj, s2[x]);
         }
         if ((x & 1) == 0) {  // tokens i and i + 1
-          int fb = 0, fc = 0;
-          reduce_channels<PPW / 2, 8>(vb, lane, &fb);
-          reduce_channels<PPW / 2, 8>(vc, lane, &fc);
+          const ChannelSums<PPW> sums(v, lane);
           if (PPW <= 8 || (lane & 1) == 0) {
 #pragma unroll
-            for (int v = 0; v < HELD; ++v) {
-              m.red[warp][i + (fb + v) / 4][q * 4 + (fb + v) % 4] = vb[v];
-              m.red[warp][i + (fc + v) / 4][NS + q * 4 + (fc + v) % 4] = vc[v];
+            for (int n = 0; n < ChannelSums<PPW>::N; ++n) {
+              float* to = m.red[warp][i + sums.token_of(n)] + q * 4 + sums.state_of(n);
+              to[0] = sums.r[n].x;
+              to[NS] = sums.r[n].y;
             }
           }
         }
@@ -510,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
     }
     __syncthreads();
   }
-  if (on) store_states(w.h + at, NS, da);  // over the state that has been read
+  if (on) store_states(w.h + at, NS, swap, da);  // over the state that has been read
 
   // du, ddt, dz: the inputs once more (from L2), rows of adjacent channels
   const int vt = tid / L::VPT, vc = (tid % L::VPT) * kV;
