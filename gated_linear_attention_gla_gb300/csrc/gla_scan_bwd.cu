@@ -76,6 +76,18 @@ template <int NS> struct Roles {
   static constexpr int CT = kWarps * PPW * 2; // channels per block: 1024 / NS
   static constexpr int PT = CT / 2;
   static constexpr int VPT = CT / kV, STEP = kThreads / VPT;  // threads per token of a load
+  // A lane's bits: the pair's lowest, q's lowest, the pair's others, q's others.
+  // Reads by pair are then the same in lanes 2 apart and reads by q in lanes 1
+  // apart: either lets 16 bytes a lane take two cycles instead of four.
+  static __device__ __forceinline__ int pair_of(int lane) {
+    return PPW == 1 ? 0 : (lane & 1) | ((lane >> 1) & (PPW - 2));
+  }
+  static __device__ __forceinline__ int q_of(int lane) {
+    return PPW == 1 ? lane : ((lane >> 1) & 1) | (lane / PPW & ~1);
+  }
+  // The distance of lanes that differ in bit m of the pair, of q.
+  static constexpr int pair_bit(int m) { return m == 1 ? 1 : 2 * m; }
+  static constexpr int q_bit(int m) { return PPW == 1 ? m : m == 1 ? 2 : PPW * m; }
 };
 
 // A chunk's inputs in shared memory.
@@ -240,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
   const int d0 = (int)(blockIdx.x % tiles) * L::CT;
   const Chunk k = chunk_of_slot(p, slot, kCH);
   if (!k.ok) return;
-  const int lane = threadIdx.x & 31, q = lane / L::PPW;
-  const int pair = (threadIdx.x >> 5) * L::PPW + lane % L::PPW, ch = d0 + 2 * pair;
+  const int lane = threadIdx.x & 31, q = L::q_of(lane);
+  const int pair = (threadIdx.x >> 5) * L::PPW + L::pair_of(lane), ch = d0 + 2 * pair;
   const bool on = ch < p.D;  // (D is even: both channels or none)
   stage<IO, NS>(a, k, d0, s);
   f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, run[4], sum = {};
@@ -312,58 +324,62 @@ chunk_scan_kernel(ScanBwdArgs a, Space w, long long slots) {
 // for the last two, so that in the first step every lane keeps its first two
 // states and gives the last two, without selecting which.  Value i of the result is token token_of(i)'s, of state
 // state_of(i) of the lane's four.
-template <int PPW> struct ChannelSums {
+template <int NS> struct ChannelSums {
+  using L = Roles<NS>;
+  static constexpr int PPW = L::PPW;
   static constexpr int N = PPW == 2 ? 4 : PPW == 4 ? 2 : 1;
   f32x2 r[4];
-  int lane;
-  __device__ __forceinline__ ChannelSums(const f32x2 (&v)[8], int lane) : lane(lane) {
+  int p;
+  __device__ __forceinline__ ChannelSums(const f32x2 (&v)[8], int p) : p(p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        r[t * 2 + j] = add2(v[t * 4 + j], shfl_xor2(v[t * 4 + j + 2], PPW / 2));
+        r[t * 2 + j] = add2(v[t * 4 + j], shfl_xor2(v[t * 4 + j + 2], L::pair_bit(PPW / 2)));
     if constexpr (PPW >= 4) {
-      const bool up = (lane & (PPW / 4)) != 0;
+      const bool up = (p & (PPW / 4)) != 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const f32x2 give = up ? r[j] : r[j + 2], keep = up ? r[j + 2] : r[j];
-        r[j] = add2(keep, shfl_xor2(give, PPW / 4));
+        r[j] = add2(keep, shfl_xor2(give, L::pair_bit(PPW / 4)));
       }
     }
     if constexpr (PPW >= 8) {
-      const bool up = (lane & (PPW / 8)) != 0;
+      const bool up = (p & (PPW / 8)) != 0;
       const f32x2 give = up ? r[0] : r[1], keep = up ? r[1] : r[0];
-      r[0] = add2(keep, shfl_xor2(give, PPW / 8));
+      r[0] = add2(keep, shfl_xor2(give, L::pair_bit(PPW / 8)));
     }
     if constexpr (PPW == 16) r[0] = add2(r[0], shfl_xor2(r[0], 1));
   }
   __device__ __forceinline__ int token_of(int i) const {
-    return PPW == 2 ? i / 2 : (lane & (PPW / 4)) != 0;
+    return PPW == 2 ? i / 2 : (p & (PPW / 4)) != 0;
   }
   __device__ __forceinline__ int state_of(int i) const {
-    return (PPW <= 4 ? i % 2 : (lane & (PPW / 8)) != 0) + ((lane & (PPW / 2)) != 0 ? 2 : 0);
+    return (PPW <= 4 ? i % 2 : (p & (PPW / 8)) != 0) + ((p & (PPW / 2)) != 0 ? 2 : 0);
   }
 };
 
 // The sums of v[0 .. 4) over a channel pair's lanes (bits PPW and up),
 // scattered: a lane holds 4 / LPC of them, or one that lanes share.
-template <int LPC, int PPW>
+template <int NS>
 __device__ __forceinline__ void reduce_states(f32x2 (&v)[4], int q, int* first) {
+  using L = Roles<NS>;
+  constexpr int LPC = L::LPC;
   const bool up = (q & (LPC / 2)) != 0;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const f32x2 give = up ? v[k] : v[k + 2], keep = up ? v[k + 2] : v[k];
-    v[k] = add2(keep, shfl_xor2(give, PPW * LPC / 2));
+    v[k] = add2(keep, shfl_xor2(give, L::q_bit(LPC / 2)));
   }
   *first = up ? 2 : 0;
   if constexpr (LPC >= 4) {
     const bool up2 = (q & (LPC / 4)) != 0;
     const f32x2 give = up2 ? v[0] : v[1], keep = up2 ? v[1] : v[0];
-    v[0] = add2(keep, shfl_xor2(give, PPW * LPC / 4));
+    v[0] = add2(keep, shfl_xor2(give, L::q_bit(LPC / 4)));
     *first += up2 ? 1 : 0;
 #pragma unroll
     for (int off = LPC / 8; off > 0; off >>= 1)
-      v[0] = add2(v[0], shfl_xor2(v[0], PPW * off));
+      v[0] = add2(v[0], shfl_xor2(v[0], L::q_bit(off)));
   }
 }
 
@@ -386,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
   GradSmem<NS>& m = *reinterpret_cast<GradSmem<NS>*>(smem);
   Staged<NS>& s = m.in;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = lane / PPW;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = L::q_of(lane);
   const int tiles = (p.D + CT - 1) / CT, tile = (int)(blockIdx.x % tiles);
   const long long slot = blockIdx.x / tiles, rows = rows_of(p);
-  const int d0 = tile * CT, pair = warp * PPW + lane % PPW, ch = d0 + 2 * pair;
+  const int d0 = tile * CT, p_in = L::pair_of(lane), pair = warp * PPW + p_in, ch = d0 + 2 * pair;
   const bool on = ch < p.D;
   const long long at = (slot * p.D + ch) * NS + q * 4;
   const Chunk k = chunk_of_slot(p, slot, kCH);
@@ -405,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
     }
     return;
   }
-  const bool swap = (lane & (PPW / 2)) != 0;
+  const bool swap = (p_in & (PPW / 2)) != 0;
   const int lo4 = q * 4 + (swap ? 2 : 0), hi4 = q * 4 + (swap ? 0 : 2);
   f32x2 a2[4] = {}, h[4] = {}, e[4] = {}, da[4] = {};
   if (on) {
@@ -490,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
           s2[x] = j == 0 ? mul2(a2[0], wj) : fma2(a2[j], wj, s2[x]);
         }
         if ((x & 1) == 0) {  // tokens i and i + 1
-          const ChannelSums<PPW> sums(v, lane);
-          if (PPW <= 8 || (lane & 1) == 0) {
+          const ChannelSums<NS> sums(v, p_in);
+          if (PPW <= 8 || (p_in & 1) == 0) {
 #pragma unroll
-            for (int n = 0; n < ChannelSums<PPW>::N; ++n) {
+            for (int n = 0; n < ChannelSums<NS>::N; ++n) {
               float* to = m.red[warp][i + sums.token_of(n)] + q * 4 + sums.state_of(n);
               to[0] = sums.r[n].x;
               to[NS] = sums.r[n].y;
@@ -502,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
         }
       }
       int first;
-      reduce_states<LPC, PPW>(s1, q, &first);
-      reduce_states<LPC, PPW>(s2, q, &first);
-      reduce_states<LPC, PPW>(y, q, &first);
+      reduce_states<NS>(s1, q, &first);
+      reduce_states<NS>(s2, q, &first);
+      reduce_states<NS>(y, q, &first);
       __syncwarp();  // the pair's lanes have read these tokens' d and g
       if (q % kShare == 0) {
 #pragma unroll
