@@ -135,8 +135,11 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
   const int tiles_t = (int)((k.t1 - k.t0 + TT - 1) / TT);
 
   if (threadIdx.x < kCompute) {
-    const int lane = threadIdx.x & 31, q = lane / L::CPW;
-    const int lc = (threadIdx.x >> 5) * L::CPW + lane % L::CPW;
+    // lane bits: q's lowest, the channel's, q's others: reads by channel are the
+    // same in lanes 1 apart and reads by q in lanes 2 apart, and either halves the
+    // time of a read of 8 or 16 bytes a lane
+    const int lane = threadIdx.x & 31, q = LPC == 1 ? 0 : (lane & 1) | (lane / L::CPW & ~1);
+    const int lc = (threadIdx.x >> 5) * L::CPW + (LPC == 1 ? lane : lane / 2 % L::CPW);
     const int ch = min(d0 + lc, p.D - 1);
     auto load8 = [&](const float* from, f32x2 (&v)[4], float scale) {
       const float4* r = reinterpret_cast<const float4*>(from + (long long)ch * NS) + q * 2;
