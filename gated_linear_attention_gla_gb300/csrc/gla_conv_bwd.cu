@@ -152,121 +152,162 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
   const long long r0 = ((long long)blockIdx.x * kGroups + group) * run;
   const long long r1 = min(r0 + run, rows), stop = min(r1 + K, rows);  // rows own, rows read
   if (on && r0 < r1) {
+    // Rows are counted from r0 in what follows.
+    const int own = (int)(r1 - r0), read = (int)(stop - r0);
     const IO* px = x + r0 * a.x_stride;
     const IO* pd = dy + r0 * a.D;
-    long long ahead = r0;
-    int put = 0, get = 0;
+    int ahead = 0, put = 0, get = 0;
     auto copy_group = [&]() {
+      if (ahead + kGroup <= read) {
 #pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
-        if (ahead < stop) {
+        for (int u = 0; u < kGroup; ++u) {
           cp_async<kBytes>(&ring[put][u][0][tid], px);
           cp_async<kBytes>(&ring[put][u][1][tid], pd);
+          px += a.x_stride;
+          pd += a.D;
         }
-        ++ahead;
-        px += a.x_stride;
-        pd += a.D;
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kGroup && ahead + u < read; ++u) {
+          cp_async<kBytes>(&ring[put][u][0][tid], px);
+          cp_async<kBytes>(&ring[put][u][1][tid], pd);
+          px += a.x_stride;
+          pd += a.D;
+        }
       }
+      ahead += kGroup;
       cp_commit();
       put = put + 1 == kRing ? 0 : put + 1;
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) copy_group();
 
-    f32x2 win[K][P], dpw[K][P];  // the K rows before the current one
+    // The last four rows of x and of dp: row i of a group in place i, so that the
+    // windows of a group's rows turn through fixed registers.
+    static_assert(K < kGroup, "the rows before the current one and itself");
+    f32x2 xr[kGroup][P], dpr[kGroup][P];
     int s = seq_of_row(a.cu_seqlens, a.B, a.T, r0);
-    long long lo = 0, hi = 0, first = r0;  // the sequence's rows; the first of them in this run
-    auto enter = [&](long long r) {        // false: malformed offsets
+    long long lo = 0, hi = 0;
+    int first = 0, end = 0;  // the sequence's rows in this run, and those read behind it
+    auto enter = [&](int r, int u) {  // row r, the u-th of its group; false: malformed offsets
       seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
-      if (lo > r || hi > rows) return false;
+      if (lo > r0 + r || hi > rows) return false;
       first = r;
+      end = (int)min(hi - r0, (long long)read);
       float w0[K][kV];
-      load_window<IO, K>(a, s, lo, r, c, w0);
+      load_window<IO, K>(a, s, lo, r0 + r, c, w0);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int x = 0; x < kGroup; ++x)
+        if (x == u)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          win[k][i] = pack2(w0[k][2 * i], w0[k][2 * i + 1]);
-          dpw[k][i] = f32x2{};
-        }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              xr[(x + kGroup - K + k) % kGroup][i] = pack2(w0[k][2 * i], w0[k][2 * i + 1]);
+              dpr[(x + kGroup - K + k) % kGroup][i] = f32x2{};
+            }
       return true;
     };
-    // dx of row q = (row of dp) - K from the K dp before and dp itself
-    auto emit = [&](long long q, const f32x2 (&dp)[P]) {
-      f32x2 d[P];
+    // dx of the row K before the u-th of its group, whose dp is in dpr[u]
+    auto sum_dp = [&](int u, f32x2 (&d)[P]) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        d[i] = mul2(w2[i][0], dp[i]);
+        d[i] = mul2(w2[i][0], dpr[u][i]);
 #pragma unroll
-        for (int k = 0; k < K; ++k) d[i] = fma2(w2[i][K - k], dpw[k][i], d[i]);
-#pragma unroll
-        for (int k = 0; k + 1 < K; ++k) dpw[k][i] = dpw[k + 1][i];
-        dpw[K - 1][i] = dp[i];
+        for (int k = 0; k < K; ++k)
+          d[i] = fma2(w2[i][K - k], dpr[(u + kGroup - K + k) % kGroup][i], d[i]);
       }
-      if (q < first || q >= r1) return;
-      if (a.d_final_state && q >= hi - K) {
-        f32x2 f[P];
-        unpack_pairs<float, kV>(
-            load_raw<float, kV>(a.d_final_state + ((long long)s * K + q - (hi - K)) * a.D + c), f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) d[i] = add2(d[i], f[i]);
-      }
+    };
+    OUT* const out = (OUT*)a.dx + r0 * a.D + c;
+    auto put_dx = [&](OUT* to, const f32x2 (&d)[P]) {
       float o[kV];
 #pragma unroll
       for (int i = 0; i < P; ++i) unpack2(d[i], &o[2 * i], &o[2 * i + 1]);
-      store4<OUT>((OUT*)a.dx + q * a.D + c, o);
+      store4<OUT>(to, o);
     };
-    // the last rows before `row`, which no dp follows
-    auto flush = [&](long long row) {
-      const f32x2 none[P] = {};
-#pragma unroll 1
-      for (int k = 0; k < K; ++k) emit(row + k - K, none);
+    // ... where that row is of this sequence and run
+    auto emit = [&](int u, int q) {
+      f32x2 d[P];
+      sum_dp(u, d);
+      if (q < first || q >= own) return;
+      const long long from_end = r0 + q - (hi - K);
+      if (a.d_final_state && from_end >= 0) {
+        f32x2 f[P];
+        unpack_pairs<float, kV>(
+            load_raw<float, kV>(a.d_final_state + ((long long)s * K + from_end) * a.D + c), f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = add2(d[i], f[i]);
+      }
+      put_dx(out + (long long)q * a.D, d);
+    };
+    auto clear = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dpr[u][i] = f32x2{};
+    };
+    // The u-th row of a group: dp, and its terms of the weight's gradient.
+    auto take = [&](int u, bool count) {
+      f32x2 dv[P];
+      unpack_pairs<IO, kV>(ring[get][u][0][tid], xr[u]);
+      unpack_pairs<IO, kV>(ring[get][u][1][tid], dv);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        f32x2 p = bias2[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          p = fma2(w2[i][k], xr[(u + kGroup - K + k) % kGroup][i], p);
+        dpr[u][i] = d_pre<SILU>(dv[i], p);
+      }
+      if (count) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          db[i] = add2(db[i], dpr[u][i]);
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            dw[i][k] = fma2(dpr[u][i], xr[(u + kGroup - K + k) % kGroup][i], dw[i][k]);
+        }
+      }
     };
 
-    bool ok = enter(r0), more = ok;
-    long long row = r0;
+    bool ok = enter(0, 0), more = ok;
+    int row = 0;
+    OUT* to = out - (long long)K * a.D;  // dx of row - K
     while (more) {
       copy_group();
       cp_wait<kAhead>();
+      if (row >= first + K && row + kGroup <= min(end, own)) {
+        // inside a sequence and the run: no checks, no moves
 #pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
-        while (more && row >= hi) {  // the sequence ends here
-          flush(row);
-          ++s;
-          more = hi < r1;
-          ok = !more || s < a.B;
-          if (more) more = ok = ok && enter(row);
+        for (int u = 0; u < kGroup; ++u) {
+          take(u, true);
+          f32x2 d[P];
+          sum_dp(u, d);
+          put_dx(to, d);
+          to += a.D;
         }
-        more = more && row < stop;
-        if (more) {
-          f32x2 xv[P], dv[P], dp[P];
-          unpack_pairs<IO, kV>(ring[get][u][0][tid], xv);
-          unpack_pairs<IO, kV>(ring[get][u][1][tid], dv);
+        row += kGroup;
+      } else {
+        to += (long long)kGroup * a.D;
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            f32x2 p = bias2[i];
+        for (int u = 0; u < kGroup; ++u) {
+          while (more && r0 + row >= hi) {  // the sequence ends here
+            // the K rows before this one, which no dp follows: turn the places on
+            // and back again
 #pragma unroll
-            for (int k = 0; k < K; ++k) p = fma2(w2[i][k], win[k][i], p);
-            p = fma2(w2[i][K], xv[i], p);
-            dp[i] = d_pre<SILU>(dv[i], p);
-          }
-          if (row < r1) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-              db[i] = add2(db[i], dp[i]);
-#pragma unroll
-              for (int k = 0; k < K; ++k) dw[i][k] = fma2(dp[i], win[k][i], dw[i][k]);
-              dw[i][K] = fma2(dp[i], xv[i], dw[i][K]);
+            for (int k = 0; k < K; ++k) {
+              clear((u + k) % kGroup);
+              emit((u + k) % kGroup, row + k - K);
             }
+            ++s;
+            more = hi < r1;
+            ok = !more || s < a.B;
+            if (more) more = ok = ok && enter(row, u);
           }
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-#pragma unroll
-            for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
-            win[K - 1][i] = xv[i];
+          more = more && row < read;
+          if (more) {
+            take(u, row < own);
+            emit(u, row - K);
+            ++row;
           }
-          emit(row - K, dp);
-          ++row;
         }
       }
       get = get + 1 == kRing ? 0 : get + 1;
