@@ -64,16 +64,24 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
   constexpr int P = V / 2;
   __shared__ __align__(16) uint4 ring[kRing][kGroup][128];
   const long long r0 = (long long)blockIdx.x * run, r1 = min(r0 + run, rows);
+  const int own = (int)(r1 - r0);      // rows are counted from r0 in what follows
   const IO* px = x + r0 * a.x_stride;  // the next row to copy
-  long long ahead = r0;
-  int put = 0;
+  int ahead = 0, put = 0;
   auto copy_group = [&]() {
+    if (ahead + kGroup <= own) {
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u) {
-      if (ahead < r1) cp_async16(&ring[put][u][threadIdx.x], px);
-      ++ahead;
-      px += a.x_stride;
+      for (int u = 0; u < kGroup; ++u) {
+        cp_async16(&ring[put][u][threadIdx.x], px);
+        px += a.x_stride;
+      }
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kGroup && ahead + u < own; ++u) {
+        cp_async16(&ring[put][u][threadIdx.x], px);
+        px += a.x_stride;
+      }
     }
+    ahead += kGroup;
     cp_commit();
     put = put + 1 == kRing ? 0 : put + 1;
   };
@@ -81,7 +89,10 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
   for (int i = 0; i < kAhead; ++i) copy_group();
   // (behind the first copies, which take longest)
   // two adjacent channels a register pair
-  f32x2 w[P][W], bias[P], win[K][P];
+  // the last four rows of x: row i of a group in place i, so that the windows of
+  // a group's rows turn through fixed registers
+  static_assert(kGroup == 4 && K < kGroup, "the rows before the current one and itself");
+  f32x2 w[P][W], bias[P], xr[kGroup][P];
   {
     float f[V][W], b[V];
     load_filters<W, V>(a.weight + (long long)c * W, f);
@@ -102,53 +113,60 @@ conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
   // the sequence of row r0, and its window there
   int s = seq_of_row(a.cu_seqlens, a.B, a.T, r0);
   long long lo = 0, hi = 0;
-  auto enter = [&](long long r) {  // false: malformed offsets
+  int end = 0;  // the sequence's rows in this run
+  auto enter = [&](int r, int u) {  // row r, the u-th of its group; false: malformed offsets
     seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
-    if (lo > r || hi > rows) return false;
+    if (lo > r0 + r || hi > rows) return false;
+    end = (int)max(min(hi - r0, (long long)own), 0ll);
+    Raw<IO, V> v[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const long long t = r - K + i;
-      Raw<IO, V> v = zero_raw<IO, V>();
-      if (t >= lo) v = load_raw<IO, V>(x + t * a.x_stride);
-      else if (init) v = load_raw<IO, V>(init + ((long long)s * K + K - (lo - t)) * a.D + c);
-      unpack_pairs<IO, V>(v, win[i]);
+      const long long t = r0 + r - K + i;
+      v[i] = zero_raw<IO, V>();
+      if (t >= lo) v[i] = load_raw<IO, V>(x + t * a.x_stride);
+      else if (init) v[i] = load_raw<IO, V>(init + ((long long)s * K + K - (lo - t)) * a.D + c);
     }
+#pragma unroll
+    for (int p = 0; p < kGroup; ++p)
+      if (p == u)
+#pragma unroll
+        for (int i = 0; i < K; ++i) unpack_pairs<IO, V>(v[i], xr[(p + kGroup - K + i) % kGroup]);
     return true;
   };
-  bool ok = enter(r0);
   int get = 0;
-  for (long long r = r0; r < r1 && ok; r += kGroup) {
+  auto take = [&](int u) {  // the u-th row of a group
+    unpack_pairs<IO, V>(
+        load_raw<IO, V>(reinterpret_cast<const IO*>(&ring[get][u][threadIdx.x])), xr[u]);
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f32x2 p = bias[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) p = fma2(w[i][k], xr[(u + kGroup - K + k) % kGroup][i], p);
+      if (SILU) p = mul2(p, sigmoid2(p));
+      unpack2(p, &y[2 * i], &y[2 * i + 1]);
+    }
+    store_raw<OUT, V>(out, pack_as<OUT, V>(y));
+    out += a.D;
+  };
+  bool ok = enter(0, 0);
+  for (int row = 0; row < own && ok; row += kGroup) {
     copy_group();
     cp_wait<kAhead>();
+    if (row + kGroup <= end) {  // inside a sequence
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u) {
-      const long long row = r + u;
-      if (row < r1 && ok) {
-        while (row >= hi && ok) {  // the next sequence that has a row (empty ones have none)
-          ++s;
-          ok = s < a.B && enter(row);
-        }
-        if (ok) {
-          f32x2 xv[P];
-          unpack_pairs<IO, V>(load_raw<IO, V>(reinterpret_cast<const IO*>(
-                                  &ring[get][u][threadIdx.x])), xv);
-          float y[V];
+      for (int u = 0; u < kGroup; ++u) take(u);
+    } else {
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            f32x2 p = bias[i];
-#pragma unroll
-            for (int k = 0; k < K; ++k) p = fma2(w[i][k], win[k][i], p);
-            p = fma2(w[i][K], xv[i], p);
-            if (SILU) p = mul2(p, sigmoid2(p));
-            unpack2(p, &y[2 * i], &y[2 * i + 1]);
-#pragma unroll
-            for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
-            win[K - 1][i] = xv[i];
+      for (int u = 0; u < kGroup; ++u) {
+        if (row + u < own && ok) {
+          while (r0 + row + u >= hi && ok) {  // the next sequence that has a row
+            ++s;
+            ok = s < a.B && enter(row + u, u);
           }
-          store_raw<OUT, V>(out, pack_as<OUT, V>(y));
+          if (ok) take(u);
         }
       }
-      out += a.D;
     }
     get = get + 1 == kRing ? 0 : get + 1;
   }

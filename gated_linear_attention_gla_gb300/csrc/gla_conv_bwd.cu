@@ -193,7 +193,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
       seq_rows(a.cu_seqlens, s, a.T, &lo, &hi);
       if (lo > r0 + r || hi > rows) return false;
       first = r;
-      end = (int)min(hi - r0, (long long)read);
+      end = (int)max(min(hi - r0, (long long)read), 0ll);
       float w0[K][kV];
       load_window<IO, K>(a, s, lo, r0 + r, c, w0);
 #pragma unroll
