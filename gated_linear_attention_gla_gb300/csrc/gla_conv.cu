@@ -25,7 +25,7 @@ constexpr int kRing = kAhead + 1;
 template <typename IO> constexpr int conv_vec() { return 16 / (int)sizeof(IO); }
 
 template <typename IO, typename OUT, int W, bool SILU>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 5)
 conv_fwd_kernel(ConvArgs a, int run, long long row_blocks) {
   constexpr int V = conv_vec<IO>();
   constexpr int K = W - 1;
@@ -236,11 +236,13 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
   const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
   const unsigned gy = (unsigned)((vecs + threads - 1) / threads);
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
-  // one wave of blocks (five a SM by registers), so that filters and windows are
-  // loaded once: 65536 x 2048 bf16 rows in runs of 64 111 us, this rule 94 us; at least
-  // 8 rows a run (its first W - 1 rows are read twice)
+  // Runs of at most 32 rows, so that SMs that are ahead take more of them: 65536 x 2048
+  // bf16 rows in one wave of five blocks a SM 100 us, in runs of 57 88 us, of 32 85 us, of
+  // 19 87 us.  Shorter ones for one wave where the rows are fewer: 8192 rows in one
+  // wave 15.7 us, in two 17.8 us.  At least 8 rows (a run's first W - 1 rows are read
+  // twice).
   const long long share = (rows * gy + 5 * 152 - 1) / (5 * 152);
-  const int run = share < 8 ? 8 : (int)((share + kGroup - 1) / kGroup * kGroup);
+  const int run = share < 8 ? 8 : share > 32 ? 32 : (int)((share + kGroup - 1) / kGroup * kGroup);
   const long long blocks = (rows + run - 1) / run;
   const long long states = a.final_state ? a.B : 0;
   // an in-place state is written by a launch of its own: its initial rows are
