@@ -12,7 +12,8 @@
 // rows come through a ring of the thread's own in shared memory, eight rows
 // ahead.  The weight's gradient is summed in registers over the run, in shared
 // memory over a block's 8 runs, and written as one fp32 partial per block; a
-// second launch sums the partials in block order.  No atomics: the same inputs
+// second launch sums the partials in block order and forms the initial states'
+// gradients.  No atomics: the same inputs
 // give the same bits.  Bound: HBM (6 bytes an element in bf16).
 #include "gla_ssm.cuh"
 
@@ -64,7 +65,8 @@ template <bool SILU> __device__ __forceinline__ f32x2 d_pre(f32x2 dy, f32x2 p) {
 
 template <typename IO, typename OUT, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, 2)
-conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
+conv_bwd_kernel(ConvBwdArgs a, float* partial, int run) {
+  start_next();
   constexpr int K = W - 1;
   const int lane = threadIdx.x, group = threadIdx.y;
   const int c = ((int)blockIdx.y * 32 + lane) * kV;
@@ -80,56 +82,6 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + c));
       bias[0] = v.x; bias[1] = v.y; bias[2] = v.z; bias[3] = v.w;
     }
-  }
-
-  if ((long long)blockIdx.x >= row_blocks) {
-    // the initial state's gradient, one sequence per group
-    const long long s = ((long long)blockIdx.x - row_blocks) * kGroups + group;
-    if (s >= a.B || !on) return;
-    long long lo, hi;
-    seq_rows(a.cu_seqlens, (int)s, a.T, &lo, &hi);
-    if (lo < 0 || hi < lo || hi > rows) {
-      if (lane == 0) atomicOr(a.status, kDevBadSeqlens);
-      return;
-    }
-    float win[K][kV], g[K][kV];
-    load_window<IO, K>(a, (int)s, lo, lo, c, win);
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-#pragma unroll
-      for (int e = 0; e < kV; ++e) g[i][e] = 0.f;
-      // a sequence shorter than the filter leaves rows of its initial state in the final one
-      if (a.d_final_state && i >= hi - lo)
-        unpack_as<float, kV>(load_raw<float, kV>(
-                                 a.d_final_state + (s * K + i - (hi - lo)) * a.D + c),
-                             g[i]);
-    }
-#pragma unroll
-    for (int t = 0; t < K; ++t) {
-      if (lo + t < hi) {
-        float xv[kV], dv[kV];
-        unpack_as<IO, kV>(load_raw<IO, kV>(x + (lo + t) * a.x_stride), xv);
-        unpack_as<IO, kV>(load_raw<IO, kV>(dy + (lo + t) * a.D), dv);
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-          float p = bias[e];
-#pragma unroll
-          for (int k = 0; k < K; ++k) p = fmaf(w[e][k], win[k][e], p);
-          p = fmaf(w[e][K], xv[e], p);
-          const float dp = dv[e] * d_act<SILU>(p);
-          // row i of the state is t + K - i tokens before token t
-#pragma unroll
-          for (int i = 0; i < K; ++i)
-            if (i >= t) g[i][e] = fmaf(w[e][i - t], dp, g[i][e]);
-#pragma unroll
-          for (int k = 0; k + 1 < K; ++k) win[k][e] = win[k + 1][e];
-          win[K - 1][e] = xv[e];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < K; ++i) store4<float>(a.d_init_state + (s * K + i) * a.D + c, g[i]);
-    return;
   }
 
   constexpr int P = kV / 2;  // two adjacent channels a register pair
@@ -343,10 +295,80 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run, long long row_blocks) {
   }
 }
 
-// d_weight[d][k] and d_bias[d] from the blocks' partials.
-__global__ void __launch_bounds__(256)
-conv_bwd_sum_kernel(const float* partial, long long blocks, int D, int W, float* dw, float* db) {
+// The initial state's gradient of sequence s, four channels a thread.
+template <typename IO, int W, bool SILU>
+__device__ __forceinline__ void d_init_rows(const ConvBwdArgs& a, long long s, int c, bool first) {
+  constexpr int K = W - 1;
+  const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
+  const IO* x = (const IO*)a.x + c;
+  const IO* dy = (const IO*)a.d_out + c;
+  float w[kV][W], bias[kV] = {};
+  load_filters<W, kV>(a.weight + (long long)c * W, w);
+  if (a.bias) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + c));
+    bias[0] = v.x; bias[1] = v.y; bias[2] = v.z; bias[3] = v.w;
+  }
+  long long lo, hi;
+  seq_rows(a.cu_seqlens, (int)s, a.T, &lo, &hi);
+  if (lo < 0 || hi < lo || hi > rows) {
+    if (first) atomicOr(a.status, kDevBadSeqlens);
+    return;
+  }
+  float win[K][kV], g[K][kV];
+  load_window<IO, K>(a, (int)s, lo, lo, c, win);
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+#pragma unroll
+    for (int e = 0; e < kV; ++e) g[i][e] = 0.f;
+    // a sequence shorter than the filter leaves rows of its initial state in the final one
+    if (a.d_final_state && i >= hi - lo)
+      unpack_as<float, kV>(load_raw<float, kV>(
+                               a.d_final_state + (s * K + i - (hi - lo)) * a.D + c),
+                           g[i]);
+  }
+#pragma unroll
+  for (int t = 0; t < K; ++t) {
+    if (lo + t < hi) {
+      float xv[kV], dv[kV];
+      unpack_as<IO, kV>(load_raw<IO, kV>(x + (lo + t) * a.x_stride), xv);
+      unpack_as<IO, kV>(load_raw<IO, kV>(dy + (lo + t) * a.D), dv);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        float p = bias[e];
+#pragma unroll
+        for (int k = 0; k < K; ++k) p = fmaf(w[e][k], win[k][e], p);
+        p = fmaf(w[e][K], xv[e], p);
+        const float dp = dv[e] * d_act<SILU>(p);
+        // row i of the state is t + K - i tokens before token t
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (i >= t) g[i][e] = fmaf(w[e][i - t], dp, g[i][e]);
+#pragma unroll
+        for (int k = 0; k + 1 < K; ++k) win[k][e] = win[k + 1][e];
+        win[K - 1][e] = xv[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i) store4<float>(a.d_init_state + (s * K + i) * a.D + c, g[i]);
+}
+
+// d_weight[d][k] and d_bias[d] from the blocks' partials; in the blocks behind those, the
+// initial states' gradients, which need nothing of the launch before (it has started,
+// so all that precedes it is complete) and run beside it.
+template <typename IO, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads)
+conv_bwd_sum_kernel(ConvBwdArgs a, const float* partial, long long blocks, unsigned sum_blocks) {
+  if (blockIdx.x >= sum_blocks) {
+    const int tiles = (a.D + 32 * kV - 1) / (32 * kV);
+    if (blocks == 0) after_previous();  // there was no launch before
+    const long long n = (long long)(blockIdx.x - sum_blocks) * kGroups + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, c = ((int)(n % tiles) * 32 + lane) * kV;
+    if (n / tiles < a.B && c < a.D) d_init_rows<IO, W, SILU>(a, n / tiles, c, lane == 0);
+    return;
+  }
   after_previous();
+  const int D = a.D;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= (long long)(W + 1) * D) return;
   const int k = (int)(i / D), d = (int)(i % D);
@@ -360,8 +382,8 @@ conv_bwd_sum_kernel(const float* partial, long long blocks, int D, int W, float*
   for (int u = 0; u < 8; ++u)
     if (b + u < blocks) s[u] += partial[(b + u) * step + i];
   const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-  if (k < W) dw[(long long)d * W + k] = sum;
-  else if (db) db[d] = sum;
+  if (k < W) a.d_weight[(long long)d * W + k] = sum;
+  else if (a.d_bias) a.d_bias[d] = sum;
 }
 
 // Rows per run: one wave of blocks (two a SM), at least 8 (W - 1 more are read).
@@ -379,7 +401,6 @@ template <typename IO, typename OUT, int W, bool SILU>
 cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream) {
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
   const long long blocks = bwd_blocks(rows, a.D);
-  const long long states = a.d_init_state ? ((long long)a.B + kGroups - 1) / kGroups : 0;
   constexpr int rings = kRing * kGroup * 2 * kThreads * kV * (int)sizeof(IO);
   constexpr int sums = kGroups * (W + 1) * 32 * kV * 4;
   constexpr int smem = rings > sums ? rings : sums;
@@ -387,14 +408,16 @@ cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream)
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_shared(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  if (blocks + states > 0)
-    kernel<<<dim3((unsigned)(blocks + states), (unsigned)((a.D + 32 * kV - 1) / (32 * kV))),
-             dim3(32, kGroups), smem, stream>>>(a, partial, bwd_run(rows, a.D), blocks);
-  const long long n = (long long)(W + 1) * a.D;
+  const int tiles = (a.D + 32 * kV - 1) / (32 * kV);
+  if (blocks > 0)
+    kernel<<<dim3((unsigned)blocks, (unsigned)tiles), dim3(32, kGroups), smem, stream>>>(
+        a, partial, bwd_run(rows, a.D));
   const cudaError_t main = cudaGetLastError();
   if (main != cudaSuccess) return main;
-  return launch_after(conv_bwd_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
-                      partial, blocks, a.D, W, a.d_weight, a.d_bias);
+  const long long sum_blocks = ((long long)(W + 1) * a.D + kThreads - 1) / kThreads;
+  const long long states = a.d_init_state ? ((long long)a.B * tiles + kGroups - 1) / kGroups : 0;
+  return launch_after(conv_bwd_sum_kernel<IO, W, SILU>, dim3((unsigned)(sum_blocks + states)),
+                      dim3(kThreads), 0, stream, a, partial, blocks, (unsigned)sum_blocks);
 }
 
 template <typename IO, typename OUT>

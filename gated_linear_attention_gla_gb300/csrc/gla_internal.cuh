@@ -330,7 +330,8 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 // Lets the next launch of such a chain start (its blocks then wait for this
-// launch's end): for kernels of one block, which leave the GPU empty.
+// launch's end): for kernels of one block or one wave, which leave SMs empty at
+// their end.
 __device__ __forceinline__ void start_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
