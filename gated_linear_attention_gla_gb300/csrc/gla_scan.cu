@@ -190,7 +190,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
       fetch(0, r[0]);
       fetch(1, r[1]);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) e[m] = ex2x2(mul2(both(r[0].d.x), a[m]));
+      for (int m = 0; m < 4; ++m) e[m] = decay2<sizeof(IO) == 4>(mul2(both(r[0].d.x), a[m]));
 #pragma unroll 1
       for (int t4 = 0; t4 < TT; t4 += 4) {
         float y[4];
@@ -202,7 +202,7 @@ scan_fwd_kernel(ScanArgs p, FwdSpace w, long long chunk) {
           f32x2 ys = {};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const f32x2 en = ex2x2(mul2(dl, a[m]));
+            const f32x2 en = decay2<sizeof(IO) == 4>(mul2(dl, a[m]));
             h[m] = fma2(e[m], h[m], mul2(du, cur.b[m]));
             if (!SUMS) ys = m == 0 ? mul2(cur.c[0], h[0]) : fma2(cur.c[m], h[m], ys);
             e[m] = en;

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_sums_kernel(ScanBwdArgs a, 
     sum = add2(sum, dl);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const f32x2 decay = ex2x2(mul2(dl, a2[j]));
+      const f32x2 decay = decay2<sizeof(IO) == 4>(mul2(dl, a2[j]));
       h[j] = fma2(decay, h[j], mul2(du, b[j]));
       run[j] = mul2(run[j], decay);
       e[j] = fma2(mul2(run[j], c[j]), g, e[j]);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       load_dup(s.b[t], lo4, hi4, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        h[j] = fma2(ex2x2(mul2(dl, a2[j])), h[j], mul2(du, b[j]));
+        h[j] = fma2(decay2<sizeof(IO) == 4>(mul2(dl, a2[j])), h[j], mul2(du, b[j]));
     }
   }
   // backwards
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_grads_kernel(ScanBwdArgs a,
       load_dup(s.b[t], lo4, hi4, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        ds[i][j] = ex2x2(mul2(dl, a2[j]));
+        ds[i][j] = decay2<sizeof(IO) == 4>(mul2(dl, a2[j]));
         hs[i + 1][j] = fma2(ds[i][j], hs[i][j], mul2(du, b[j]));
       }
     }

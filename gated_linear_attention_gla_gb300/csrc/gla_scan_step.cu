@@ -158,10 +158,12 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStepArgs p) {
         const float4 b = *reinterpret_cast<const float4*>(&s.bc[buf][i][0][q * 4]);
         const float4 c = *reinterpret_cast<const float4*>(&s.bc[buf][i][1][q * 4]);
         float4 x;
-        x.x = fmaf(ex2(ei * a.x), h.x, wi * b.x);
-        x.y = fmaf(ex2(ei * a.y), h.y, wi * b.y);
-        x.z = fmaf(ex2(ei * a.z), h.z, wi * b.z);
-        x.w = fmaf(ex2(ei * a.w), h.w, wi * b.w);
+        const f32x2 d0 = decay2<sizeof(IO) == 4>(pack2(ei * a.x, ei * a.y));
+        const f32x2 d1 = decay2<sizeof(IO) == 4>(pack2(ei * a.z, ei * a.w));
+        x.x = fmaf(d0.x, h.x, wi * b.x);
+        x.y = fmaf(d0.y, h.y, wi * b.y);
+        x.z = fmaf(d1.x, h.z, wi * b.z);
+        x.w = fmaf(d1.y, h.w, wi * b.w);
         if (on) __stcs(reinterpret_cast<float4*>(state + to * page), x);
         y[i] = fmaf(c.x, x.x, fmaf(c.y, x.y, fmaf(c.z, x.z, c.w * x.w)));
       }
