@@ -12,7 +12,10 @@
 // registers, so that a row is read once but for the W - 1 rows in front of a
 // run.  Its rows come through a ring of its own in shared memory, eight rows
 // ahead: the bytes in flight that HBM needs (about 45 KB a SM) without registers
-// or barriers.  65536 x 2048 bf16 rows: four rows ahead in registers 170 us.
+// or barriers.  65536 x 2048 bf16 rows: four rows ahead in registers 170 us, through
+// the ring with windows that move a register a row 95 us, with windows that turn
+// through the places of a group's four rows 92 us, in shorter runs 85 us: 93 % of copy
+// bandwidth.
 #include "gla_ssm.cuh"
 
 namespace gla {

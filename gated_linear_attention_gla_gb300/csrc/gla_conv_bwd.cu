@@ -13,8 +13,12 @@
 // ahead.  The weight's gradient is summed in registers over the run, in shared
 // memory over a block's 8 runs, and written as one fp32 partial per block; a
 // second launch sums the partials in block order and forms the initial states'
-// gradients.  No atomics: the same inputs
-// give the same bits.  Bound: HBM (6 bytes an element in bf16).
+// gradients.  No atomics: the same inputs give the same bits.
+//
+// Bound: HBM (6 bytes an element in bf16) for many rows, 65536 x 2048 in 140 us (85 % of
+// copy bandwidth); 8192 x 2048 take 28 us, of which 12 are the start of the runs, the
+// block sums and the second launch.  Rows loaded as they are needed 55 us, through the
+// ring 38 us, without checks and moves inside a sequence 31 us.
 #include "gla_ssm.cuh"
 
 namespace gla {
@@ -386,7 +390,9 @@ conv_bwd_sum_kernel(ConvBwdArgs a, const float* partial, long long blocks, unsig
   else if (a.d_bias) a.d_bias[d] = sum;
 }
 
-// Rows per run: one wave of blocks (two a SM), at least 8 (W - 1 more are read).
+// Rows per run: one wave of blocks (two a SM), at least 8 (W - 1 more are read).  A block's
+// start and sums cost more than waves of runs would even out: 16384 x 2048 rows in
+// one wave 46 us, in runs of at most 64 57 us, of 32 64 us.
 int bwd_run(long long rows, int D) {
   const long long tiles = (D + 32 * kV - 1) / (32 * kV);
   const long long run = (rows * tiles + 2 * 152 * kGroups - 1) / (2 * 152 * kGroups);

@@ -16,10 +16,16 @@
 // (dt, u) of a tile of 1024 (token, channel) pairs into (delta, delta u) in shared
 // memory, and finishes and stores the outputs of its tile before, so that the
 // recurrence does not wait for loads, the softplus or the gate; named barriers
-// hand the stages over.  Lanes that differ in the state sit in different
-// quarters of a warp, so that the reads of b and c are broadcasts within a quarter
-// (2 cycles instead of 4 for 16 bytes a lane); the sums over n go through
-// shared memory, up to two terms per pair, and the helpers add them.
+// hand the stages over.  The sums over n go through shared memory, up to two terms
+// per pair, and the helpers add them.
+//
+// 8192 bf16 rows (four sequences) x 2048 channels x 16 states: 103 us, where the
+// tensors' bytes at copy bandwidth are 20 us and the exponentials 36 us of the
+// exponential unit.  What bounds it now: 128 blocks of 64 channels, one a SM, each with
+// one compute warp a scheduler, whose ~50 instructions a token issue at 55 % together
+// with the helpers'.  A warp that owns channel pairs instead of state pairs 132 us
+// (against 122 then), step sizes stored twice 130 us, tiles fetched across their border
+// 120 us (against 114).
 //
 // One run is a whole sequence, or, where sequences times channel tiles leave
 // SMs idle, a chunk of it (three launches): what every chunk adds to the state
@@ -37,8 +43,8 @@ constexpr int kHelp = 128;     // threads of a helper group; group g of G serves
 constexpr int threads_of(int groups) { return kCompute + groups * kHelp; }
 // A whole sequence a block leaves one or two blocks a SM: a third helper group
 // keeps the recurrence fed (8192 x 2048 x 16: 117 us with two, 109 with three, 114 with
-// four).  Chunks fill the SMs: two groups leave room for more blocks (20001 packed
-// tokens: 398 us with two, 409 with three).
+// four, before the lanes' present order).  Chunks fill the SMs: two groups leave room
+// for two blocks a SM (20001 packed tokens: one block 396 us, two 350).
 // (Three groups' stages of fp32 rows do not fit at NS = 64.)
 constexpr int kChunkGroups = 2;
 template <typename IO, int NS> constexpr int whole_groups() {
@@ -458,7 +464,7 @@ cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk,
 // longest one times the waves of blocks; chunks take 1.7 times the work (the
 // extra pass) spread over all SMs, and about 100 for two more launches.  A packed
 // call's longest sequence is not known here: 2.5 times the mean.  Measured, D =
-// 2048 and NS = 16, whole against best chunk: 4 x 2048 tokens 104 and 154 us, 2 x 2048
+// 2048 and NS = 16, whole against best chunk: 4 x 2048 tokens 103 and 154 us, 2 x 2048
 // 103 and 87 (256), 1 x 2048 103 and 51 (256), 1 x 512 29 and 19 (64), three packed
 // sequences of 20001 tokens 708 and 350 (1024).  The length leaves about four
 // blocks a SM (two are resident): shorter ones pay for their starts (64 tokens:
