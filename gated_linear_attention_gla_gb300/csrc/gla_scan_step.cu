@@ -188,10 +188,13 @@ template <typename IO, typename OUT, int NS>
 cudaError_t launch_typed(const ScanStepArgs& a, cudaStream_t stream) {
   constexpr int CT = StepSmem<IO, NS>::CT, smem = (int)sizeof(StepSmem<IO, NS>);
   const int tiles = (a.D + CT - 1) / CT;
-  // one wave of blocks, no more than there are groups of sequences
+  // one wave of blocks, or two where each still walks eight groups (1280 sequences of
+  // 2048 x 16: bf16 61.9 and 61.1 us, fp32 rows 67.8 and 64.0; 256 sequences 15.6 and
+  // 17.8); no more than there are groups of sequences
   const long long quads = ((long long)a.N + kSeqs - 1) / kSeqs;
   long long groups = 3 * 152 / tiles;
   if (groups < 1) groups = 1;
+  if (quads >= 16 * groups) groups *= 2;
   if (groups * kMostGroups < quads) groups = (quads + kMostGroups - 1) / kMostGroups;
   if (groups > quads) groups = quads;
   auto kernel = scan_step_kernel<IO, OUT, NS>;
