@@ -9,10 +9,10 @@ errors scale with:
       and its product: below 5 * 2^-24 + 2^-21 + 16 * 2^-24 + 4 * 2^-24 < 2^-18.
   scan: a decay is off by 2^-22 (hardware exponential) and 2^-24 times its
       exponent (|delta a| < 4 here: below 2^-21 together), each step adds one
-      rounding, and the step size is off by a few 2^-24, also in every exponent:
-      below 2^-20 per step, over the steps that a state remembers, at most
-      min(T, 1 / (1 - slowest decay)); 2^-17 covers the products, the sums over
-      n and the gate around them.  Gradients run two such recurrences.
+      rounding, and the step size is off by a few 2^-24 (bf16 rows:
+      and by |dt + bias| 2^-24), also in every exponent: below 2^-20 per step, over
+      the steps that a state remembers, at most min(T, 1 / (1 - slowest decay));
+      2^-17 covers the products, the sums over n and the gate around them.  Gradients run two such recurrences.
 bf16 results are required to be the fp32 results rounded once (half a step).
 """
 import pytest
@@ -128,6 +128,31 @@ def test_conv(gla, lens, packed, io, D, W, act, bias, init):
         check_bf16_rounding(grads[DT[io]][0], dx)
         assert all(torch.equal(p, q) for p, q in zip(grads[DT[io]][1:], grads[torch.float32][1:])
                    if p is not None)
+    gla.status_sync()
+
+
+@pytest.mark.parametrize("io,W,act", [("bf16", 4, "silu"), ("fp32", 3, None), ("bf16", 2, "silu")])
+def test_conv_long_runs(gla, io, W, act):
+    """Enough rows that a thread's run is tens of rows and holds whole groups inside
+    sequences, their starts and ends at every place of a group, and empty ones."""
+    lens = [1, 0, 2, 3, 4, 0, 0, 5, 6, 7, 8, 9, 10, 11, 700, 13, 37, 1, 1, 1, 1500, 2, 0, 41, 1023, 3, 0]
+    D = 2048
+    x, cu = conv_inputs(lens, D, W, io, 6)
+    ref = ssm_ref.conv(x["x"], x["w"], x["bias"], x["init"], cu, act, x["dy"], x["df"])
+    size = ssm_ref.conv(x["x"], x["w"], x["bias"], x["init"], cu, act, x["dy"], x["df"], absolute=True)
+    args = (strided(x["x"]), gpu(x["w"]))
+    kw = dict(init_state=gpu(x["init"]), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(),
+              activation=act)
+    y, fin = gla.conv_fwd(*args, gpu(x["bias"]), **kw, out_dtype=torch.float32)
+    near(y, ref["y"], size["y"], 2 ** -18, "y")
+    assert torch.equal(fin.double().cpu(), ref["final"])
+    dx, dw, db, di = gla.conv_bwd(*args, gpu(x["dy"]), gpu(x["bias"]), **kw,
+                                  d_final_state=gpu(x["df"]), grad_dtype=torch.float32)
+    R = sum(lens)
+    near(dx, ref["dx"], size["dx"], 2 ** -17, "dx")
+    near(di, ref["d_init"], size["d_init"], 2 ** -17, "d_init")
+    near(dw, ref["dw"], size["dw"], 2 ** -17 + R * 2 ** -24, "dw")
+    near(db, ref["db"], size["db"], 2 ** -17 + R * 2 ** -24, "db")
     gla.status_sync()
 
 
