@@ -459,26 +459,58 @@ cudaError_t launch_kernel(const ScanArgs& a, const FwdSpace& w, long long chunk,
   return cudaGetLastError();
 }
 
+// About the time of a launch of `full` blocks of `len` tokens and `part` blocks of
+// `rest` tokens at two blocks a SM, in tokens; a block that has a SM to itself takes
+// two thirds, a start costs as much as 24 tokens.
+long long span(long long full, long long len, long long part, long long rest) {
+  constexpr long long kSlots = 2 * 152;
+  len += 24;
+  rest += 24;
+  const long long waves = full / kSlots, over = full % kSlots, left = kSlots - over;
+  const bool room = over + part <= kSlots / 2;
+  if (over == 0) return waves * len + (part == 0 ? 0 : room ? rest * 2 / 3 : rest);
+  const long long last = room ? len * 2 / 3 : len;  // the last wave's whole chunks
+  if (part == 0) return waves * len + last;
+  const long long beside = (part + left - 1) / left * rest;  // short ones in the slots left
+  return waves * len + (beside < last ? last : beside < last + rest ? beside : last + rest);
+}
+
 // The chunk length of a call, 0 for whole sequences.  In units of a block's time
 // for one token (about 0.05 us at NS = 16, a block a SM): whole sequences take the
 // longest one times the waves of blocks; chunks take 1.7 times the work (the
 // extra pass) spread over all SMs, and about 100 for two more launches.  A packed
 // call's longest sequence is not known here: 2.5 times the mean.  Measured, D =
 // 2048 and NS = 16, whole against best chunk: 4 x 2048 tokens 103 and 154 us, 2 x 2048
-// 103 and 87 (256), 1 x 2048 103 and 51 (256), 1 x 512 29 and 19 (64), three packed
-// sequences of 20001 tokens 708 and 350 (1024).  The length leaves about four
-// blocks a SM (two are resident): shorter ones pay for their starts (64 tokens:
-// 504 us in the last case), longer ones leave SMs idle.
+// 103 and 87, 1 x 2048 103 and 45, 1 x 512 29 and 19, three packed sequences of 20001
+// tokens 708 and 347.
+//
+// Equal sequences: the length whose blocks fill their waves best.  1 x 2048 tokens: 224 45
+// us, 256 50, 208 52, 320 60; 1 x 8192: 896 152 us, 576 153, 1024 171, 768 193.  Packed
+// ones: about four blocks a SM (two are resident); the last case in 1024 347 us, in 512
+// 357, in 64 504, in 2048 397.
 long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
   constexpr long long kSMs = 152;
   const long long tiles = ((long long)D * NS + 1023) / 1024, work = rows * tiles / kSMs;
   long long longest = (rows + B - 1) / B;
-  if (packed) longest = longest * 5 / 2 < rows ? longest * 5 / 2 : rows;
+  if (packed && B > 1) longest = longest * 5 / 2 < rows ? longest * 5 / 2 : rows;
   const long long whole = (B * tiles + kSMs - 1) / kSMs * longest;
   if (work * 17 / 10 + 100 >= whole) return 0;
   long long chunk = 64;
-  while (chunk * 6 < work && chunk < 1024) chunk *= 2;  // nearest power of two to work / 4
-  return chunk;
+  if (packed && B > 1) {
+    while (chunk * 6 < work && chunk < 1024) chunk *= 2;  // nearest power of two to work / 4
+    return chunk;
+  }
+  long long least = 0;
+  for (long long c = 64; c <= 1024; c += 16) {
+    const long long n = longest / c, rest = longest % c, blocks = B * tiles;
+    const long long t = span(n * blocks, c, rest ? blocks : 0, rest) +
+                        span((rest ? n : n - 1) * blocks, c, 0, 0) * 2 / 3;
+    if (c == 64 || t < least) {
+      least = t;
+      chunk = c;
+    }
+  }
+  return least * 2 + 140 >= whole ? 0 : chunk;  // (1 x 300: 16.4 us whole, 17.8 in chunks)
 }
 
 template <typename IO, typename OUT, int NS>
