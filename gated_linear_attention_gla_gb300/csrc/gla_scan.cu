@@ -510,7 +510,7 @@ long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
       chunk = c;
     }
   }
-  return least * 2 + 140 >= whole ? 0 : chunk;  // (1 x 300: 16.4 us whole, 17.8 in chunks)
+  return least * 2 + 40 >= whole ? 0 : chunk;  // (1 x 256 tokens: 15.8 us whole, 14.4 in chunks)
 }
 
 template <typename IO, typename OUT, int NS>
