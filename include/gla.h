@@ -459,7 +459,10 @@ gla_status gla_conv_step(const void *x, int64_t x_stride, const float *weight, c
  *     out[t][d]  = (sum_n c[t][n] h[t][d][n] + skip[d] u[t][d]) z / (1 + exp(-z))
  *
  *   u, dt        [rows, D]; b, c [rows, N]: bf16, or fp32 with GLA_FLAG_FP32_IO
- *   a            [D, N], finite; N = 8, 16, 32 or 64 (16-byte aligned)
+ *   a            [D, N], finite; N = 8, 16, 32 or 64 (16-byte aligned).  Either
+ *                sign, as delta without GLA_FLAG_SOFTPLUS: decays may exceed 1.
+ *                Where their product over a stretch of a sequence leaves fp32's
+ *                range, what follows from it is infinite or NaN.
  *   skip, dt_bias  [D] or NULL (zero)
  *   z            [rows, D] or NULL (no gate); z_stride is then ignored
  *   init_state   fp32 [B, D, N] or NULL (zeros); final_state likewise or NULL
