@@ -314,7 +314,7 @@ __device__ __forceinline__ void d_init_rows(const ConvBwdArgs& a, long long s, i
   }
   long long lo, hi;
   seq_rows(a.cu_seqlens, (int)s, a.T, &lo, &hi);
-  if (lo < 0 || hi < lo || hi > rows) {
+  if (!bounds_ok(lo, hi, rows)) {
     if (first) atomicOr(a.status, kDevBadSeqlens);
     return;
   }
@@ -371,9 +371,12 @@ conv_bwd_sum_kernel(ConvBwdArgs a, const float* partial, long long blocks, unsig
     if (n / tiles < a.B && c < a.D) d_init_rows<IO, W, SILU>(a, n / tiles, c, lane == 0);
     return;
   }
-  after_previous();
   const int D = a.D;
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (blocks == 0) after_previous();
+  if (a.cu_seqlens)  // (an input, as above)
+    check_offsets(a.cu_seqlens, a.B, a.T, i, (long long)sum_blocks * blockDim.x, a.status);
+  after_previous();
   if (i >= (long long)(W + 1) * D) return;
   const int k = (int)(i / D), d = (int)(i % D);
   const long long step = (long long)(W + 1) * D;

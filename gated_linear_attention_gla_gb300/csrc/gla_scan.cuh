@@ -38,7 +38,7 @@ __device__ __forceinline__ Chunk chunk_of_slot(const ScanArgs& p, long long slot
   const long long c = slot - first_slot(p, lo, chunk);
   Chunk k;
   k.s = lo;
-  k.ok = a >= 0 && b >= a && b <= rows_of(p) && c >= 0 && a + c * chunk < b;
+  k.ok = bounds_ok(a, b, rows_of(p)) && c >= 0 && a + c * chunk < b;
   k.t0 = a + c * chunk;
   k.t1 = min(k.t0 + chunk, b);
   k.last = k.t1 == b;
@@ -50,7 +50,7 @@ __device__ __forceinline__ bool seq_ok(const ScanArgs& p, int s, bool report, lo
                                        long long* hi) {
   seq_rows(p.cu_seqlens, s, p.T, lo, hi);
   const long long rows = rows_of(p);
-  const bool ok = *lo >= 0 && *hi >= *lo && *hi <= rows &&
+  const bool ok = bounds_ok(*lo, *hi, rows) &&
                   (!p.cu_seqlens ||
                    (__ldg(p.cu_seqlens) == 0 && __ldg(p.cu_seqlens + p.B) == rows));
   if (!ok && report) atomicOr(p.status, kDevBadSeqlens);

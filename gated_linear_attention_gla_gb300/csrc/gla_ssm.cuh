@@ -244,15 +244,34 @@ __device__ __forceinline__ void load_filters(const float* weight, float (&w)[V][
   }
 }
 
-// Bounds [a, b) of sequence s in packed rows (dense batches: s * T ..).
+// Bounds [a, b) of sequence s in packed rows (dense batches: s * T ..).  A negative
+// offset, which is malformed, comes out above every row (as unsigned), so that a
+// comparison with a row from above is enough to refuse it.
 __device__ __forceinline__ void seq_rows(const int32_t* cu, int s, int T, long long* a,
                                          long long* b) {
   if (cu == nullptr) {
     *a = (long long)s * T;
     *b = *a + T;
   } else {
-    *a = __ldg(cu + s);
-    *b = __ldg(cu + s + 1);
+    *a = static_cast<unsigned>(__ldg(cu + s));
+    *b = static_cast<unsigned>(__ldg(cu + s + 1));
+  }
+}
+
+// Whether sequence bounds of seq_rows lie in rows [0, rows).
+__device__ __forceinline__ bool bounds_ok(long long lo, long long hi, long long rows) {
+  return hi >= lo && hi <= rows;
+}
+
+// Reports malformed offsets, whatever the call computes from them: thread i of n
+// looks at every n-th sequence.
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int B, long long rows,
+                                              long long i, long long n, unsigned* status) {
+  for (long long s = i; s < B; s += n) {
+    long long lo, hi;
+    seq_rows(cu, (int)s, 0, &lo, &hi);
+    if (!bounds_ok(lo, hi, rows) || (s == 0 && lo != 0) || (s == B - 1 && hi != rows))
+      atomicOr(status, kDevBadSeqlens);
   }
 }
 

@@ -108,3 +108,35 @@ def test_decays_around_one_in_fp32_rows(gla):  # noqa: F811
     want = torch.exp(e.double())
     err = (state.double().cpu().flatten() - want).abs() / want
     assert bool((err <= 2 ** -22 + 2 ** -24 + 3 * 2 ** -24 * e.double().abs()).all()), float(err.max())
+
+
+# ---------------------------------------------------------------------------
+# Malformed offsets are reported whatever else is asked for.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [8, 64, 2048])
+@pytest.mark.parametrize("states", [False, True])
+def test_malformed_offsets_of_convolutions(gla, D, states):  # noqa: F811
+    """A start before or behind the first row, an end outside, decreasing ones next to a run's border
+    and far down a long table; also without the outputs that belong to sequences, which
+    have blocks of their own."""
+    R = 64
+    x = torch.randn(R, D, device="cuda").to(torch.bfloat16)
+    w = torch.ones(D, 4, device="cuda")
+    many = [min(i // 4, R) for i in range(301)]     # 300 sequences, most of one row or none
+    many[-1] = R
+    calls = (lambda c: gla.conv_fwd(x, w, cu_seqlens=c, output_final_state=states),
+             lambda c: gla.conv_bwd(x, w, x, cu_seqlens=c, need_d_init=states))
+    bad = [[0, 70, 64], [3, 20, 64], [0, 20, 60], [0, 40, 20, 64], [0, -5, 64], [0, -5, 70], [-1, 64], [-3, 0, 64],
+           [0, 33, 32, 64], [0, 0, -1, 0, 64], [0, 2 ** 31 - 1, 64], [0, -2 ** 31, 64],
+           many[:250] + [many[250] - 2] + many[251:], many[:-2] + [R + 1, R], [-1] + many[1:]]
+    for cu in bad:
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for call in calls:
+            call(c)
+            with pytest.raises(gla.GlaError) as e:
+                gla.status_sync()
+            assert e.value.status == 1, cu
+    for cu in ([0, 64], [0, 0, 64, 64], many):
+        for call in calls:
+            call(torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    gla.status_sync()
