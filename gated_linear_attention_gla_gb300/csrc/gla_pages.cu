@@ -261,14 +261,13 @@ cudaError_t copy_pages(const PagePool* list, int count, const int32_t* src, cons
 cudaError_t launch_pages_copy(const PagePool* pools, int count, int S, const int32_t* src,
                               const int32_t* dst, int32_t* plan, int n, unsigned* status,
                               cudaStream_t stream) {
-  const int smem = 3 * ((S + 31) / 32) * 4;
-  if (smem > 48 * 1024) {  // (as many bytes as the call needs: set every time)
-    const cudaError_t e = cudaFuncSetAttribute(
-        copy_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  copy_plan_kernel<<<1, kPlan, smem, stream>>>(src, dst, n, S, plan, status);
-  const cudaError_t e = cudaGetLastError();
+  // the limit for the largest pool, once: set to a call's own size, it would take from
+  // another thread's call between that one's setting and its launch
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(copy_plan_kernel, 3 * (kMaxPages / 32) * 4, done);
+  if (e != cudaSuccess) return e;
+  copy_plan_kernel<<<1, kPlan, 3 * ((S + 31) / 32) * 4, stream>>>(src, dst, n, S, plan, status);
+  e = cudaGetLastError();
   return e != cudaSuccess ? e : copy_pages(pools, count, src, plan, n, stream);
 }
 

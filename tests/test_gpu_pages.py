@@ -1,5 +1,7 @@
 """The page operators on the GPU against a plain implementation with Python lists."""
+import ctypes
 import random
+import threading
 
 import pytest
 import torch
@@ -222,3 +224,40 @@ def test_serving_round_captured(gla):
     gla.status_sync()
     assert all(torch.equal(a, b) for a, b in zip((pool, tail, used), after))
     assert all(torch.equal(a[:3], b[:3]) for a, b in zip(held, eager))
+
+
+def test_copies_from_several_threads(gla):
+    """Host threads copy in pools of different sizes at the same time; the plans of large pools need
+    more shared memory than a kernel has without asking for it.  A captured copy replays behind them."""
+    sizes, turns = [524_288, 140_000, 200_000], 20_000
+    pools = [torch.arange(S, dtype=torch.int32, device="cuda")[:, None].repeat(1, 4) for S in sizes]
+    src, dst = [i32([S - 1, 7]) for S in sizes], [i32([3, S - 2]) for S in sizes]
+    gla.copy_pages([pools[0]], src[0], dst[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = gla.copy_pages([pools[0]], src[0], dst[0])
+    streams, copied = [torch.cuda.Stream() for _ in sizes], [torch.empty_like(s) for s in src]
+    torch.cuda.synchronize()
+    results, gate = [set() for _ in sizes], threading.Barrier(len(sizes))
+
+    def work(i):
+        pool = gla._binding.PagePool(pools[i].data_ptr(), 16)
+        call = (ctypes.byref(pool), 1, sizes[i], src[i].data_ptr(), dst[i].data_ptr(),
+                copied[i].data_ptr(), 2, streams[i].cuda_stream)
+        copy = gla.lib().gla_pages_copy
+        gate.wait()
+        for _ in range(turns):
+            results[i].add(copy(*call))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert results == [{0}] * len(sizes)
+    graph.replay()
+    synced(gla, False)
+    assert held.tolist() == dst[0].tolist()
+    for S, p in zip(sizes, pools):
+        assert p[3].tolist() == [S - 1] * 4 and p[S - 2].tolist() == [7] * 4 and p[4].tolist() == [4] * 4
