@@ -73,7 +73,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run) {
   start_next();
   constexpr int K = W - 1;
   const int lane = threadIdx.x, group = threadIdx.y;
-  const int c = ((int)blockIdx.y * 32 + lane) * kV;
+  const int c = ((int)blockIdx.x * 32 + lane) * kV;
   const bool on = c < a.D;
   const long long rows = a.cu_seqlens ? (long long)a.T : (long long)a.B * a.T;
   const IO* x = (const IO*)a.x + c;
@@ -105,7 +105,7 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run) {
   constexpr int kBytes = kV * (int)sizeof(IO);
   auto ring = reinterpret_cast<R (*)[kGroup][2][kThreads]>(smem);  // [kRing]: x, dy
   const int tid = group * 32 + lane;
-  const long long r0 = ((long long)blockIdx.x * kGroups + group) * run;
+  const long long r0 = ((long long)blockIdx.y * kGroups + group) * run;
   const long long r1 = min(r0 + run, rows), stop = min(r1 + K, rows);  // rows own, rows read
   if (on && r0 < r1) {
     // Rows are counted from r0 in what follows.
@@ -290,12 +290,12 @@ conv_bwd_kernel(ConvBwdArgs a, float* partial, int run) {
   __syncthreads();
   for (int i = tid; i < (W + 1) * 32 * kV; i += 32 * kGroups) {
     const int k = i / (32 * kV), ch = i % (32 * kV);
-    const int d = (int)blockIdx.y * 32 * kV + ch;
+    const int d = (int)blockIdx.x * 32 * kV + ch;
     if (d >= a.D) continue;
     float sum = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) sum += red[g][k][ch];
-    partial[((long long)blockIdx.x * (W + 1) + k) * a.D + d] = sum;
+    partial[((long long)blockIdx.y * (W + 1) + k) * a.D + d] = sum;
   }
 }
 
@@ -418,8 +418,10 @@ cudaError_t bwd_typed(const ConvBwdArgs& a, float* partial, cudaStream_t stream)
   const cudaError_t e = allow_shared(kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int tiles = (a.D + 32 * kV - 1) / (32 * kV);
+  // (the tiles of 2^24 channels are too many for a grid's second dimension, the blocks
+  // of a tile's rows are at most about two a SM)
   if (blocks > 0)
-    kernel<<<dim3((unsigned)blocks, (unsigned)tiles), dim3(32, kGroups), smem, stream>>>(
+    kernel<<<dim3((unsigned)tiles, (unsigned)blocks), dim3(32, kGroups), smem, stream>>>(
         a, partial, bwd_run(rows, a.D));
   const cudaError_t main = cudaGetLastError();
   if (main != cudaSuccess) return main;

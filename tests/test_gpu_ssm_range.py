@@ -140,3 +140,36 @@ def test_malformed_offsets_of_convolutions(gla, D, states):  # noqa: F811
         for call in calls:
             call(torch.tensor(cu, dtype=torch.int32, device="cuda"))
     gla.status_sync()
+
+
+# ---------------------------------------------------------------------------
+# Very many channels
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io,D", [("bf16", 65535 * 128 + 8), ("bf16", 2 ** 24), ("fp32", 2 ** 24)])
+def test_conv_of_very_many_channels(gla, io, D):  # noqa: F811
+    """Up to the documented 2^24, forwards and backwards: more tiles of channels than a grid
+    dimension holds.  All channels against the formula in 64 bits, on the GPU."""
+    T, W = 3, 2
+    g = torch.Generator(device="cuda").manual_seed(44)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy, w, bias = r(1, T, D).to(DT[io]), r(1, T, D).to(DT[io]), r(D, W), r(D)
+    y, fin = gla.conv_fwd(x, w, bias, out_dtype=torch.float32)
+    dx, dw, db, di = gla.conv_bwd(x, w, dy, bias, grad_dtype=torch.float32)
+    gla.status_sync()
+    x, dy, w = x[0].double(), dy[0].double(), w.double()
+    back = torch.cat([torch.zeros_like(x[:1]), x[:-1]])
+    after = torch.cat([dy[1:], torch.zeros_like(dy[:1])])
+    zero = torch.zeros_like(x[0])
+
+    def same(got, terms):
+        """W + 1 products and sums at most: below 2^-18 of their absolute values."""
+        size = sum(t.abs() for t in terms)
+        assert bool(((got.double() - sum(terms)).abs() <= 2 ** -18 * size).all())
+
+    same(y[0], [w[:, 1] * x, w[:, 0] * back, bias.double().expand_as(x)])
+    assert torch.equal(fin[0, 0].double(), x[-1])
+    same(dx[0], [w[:, 1] * dy, w[:, 0] * after])
+    same(di[0, 0], [w[:, 0] * dy[0], zero])
+    same(dw[:, 1], list(dy * x))
+    same(dw[:, 0], list(dy * back))
+    same(db, list(dy))
