@@ -1,5 +1,7 @@
 """The selective scan and the causal convolution over the rest of their documented range,
-against the plain 64-bit implementations.
+against the plain 64-bit implementations: decays above 1, long sequences and many rows,
+infinities and NaN, tensors of more than 2^31 elements, malformed offsets, very many
+channels.
 
 Tolerances as in test_gpu_ssm, per element, as parts of the same sum over the
 absolute values of its terms (its decays as they are, so that growth is in it).
@@ -111,6 +113,255 @@ def test_decays_around_one_in_fp32_rows(gla):  # noqa: F811
 
 
 # ---------------------------------------------------------------------------
+# Long sequences, long chunks, many rows: every stage of the pipelines is passed.
+# ---------------------------------------------------------------------------
+def some(x, sel):
+    """The inputs of the channels ``sel``, which are independent of the others."""
+    by_row = ("u", "dt", "z", "dy")
+    return {k: None if v is None else v[:, sel] if k in by_row + ("init", "df") else
+            v[sel] if k in ("a", "skip", "bias") else v for k, v in x.items()}
+
+
+# chunks of 224 tokens; of 80 and of 336 (no multiples of a tile's 64 tokens); packed, of 128;
+# whole sequences of many tiles; 33 and 47 chunks of 64, the last one partial
+@pytest.mark.parametrize("io,D,N,lens,packed", [
+    ("bf16", 2048, 16, [2048], False), ("bf16", 512, 64, [700], False), ("fp32", 1024, 64, [1500], False),
+    ("bf16", 2048, 16, [1100, 0, 1300], True), ("fp32", 2048, 16, [600] * 4, False),
+    ("bf16", 264, 8, [2100], False), ("fp32", 40, 32, [5, 3000, 64], True)])
+def test_scan_long(gla, io, D, N, lens, packed):  # noqa: F811
+    x, cu = scan_inputs(lens, D, N, io, 33)
+    sel = torch.cat([torch.arange(0, D, max(1, D // 12)), torch.arange(D - 4, D)]).unique()
+    part = some(x, sel)
+    ref = ssm_ref.scan(*[part[k] for k in ORDER], True, part["init"], cu)
+    size = ssm_ref.scan(*[part[k] for k in ORDER], True, part["init"], cu, absolute=True)
+    L = lambda t: strided(lead(t, lens, packed))  # noqa: E731
+    args = (L(x["u"]), L(x["dt"]), gpu(x["a"]), L(x["b"]), L(x["c"]))
+    kw = dict(skip=gpu(x["skip"]), z=L(x["z"]), dt_bias=gpu(x["bias"]), init_state=gpu(x["init"]),
+              cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda() if packed else None)
+    f = scan_factor(x, cu, True)
+    y, fin = gla.scan_fwd(*args, **kw, out_dtype=torch.float32)
+    near(y.reshape(-1, D)[:, sel], ref["y"], size["y"], f, "y")
+    near(fin[:, sel], ref["final"], size["final"], f, "final")
+    if io == "bf16":
+        y16, fin16 = gla.scan_fwd(*args, **kw)
+        check_bf16_rounding(y16, y)
+        assert torch.equal(fin16, fin)
+    gla.status_sync()
+
+
+# 33 chunks; 18 and 47 chunks beside an empty sequence; every channel, since db and dc sum over them
+@pytest.mark.parametrize("io,D,N,lens,packed", [
+    ("fp32", 40, 8, [2100], False), ("bf16", 72, 16, [1100, 0, 3000, 1], True), ("bf16", 24, 64, [1200, 1200], False),
+    ("fp32", 136, 32, [1500], False)])
+def test_scan_gradients_long(gla, io, D, N, lens, packed):  # noqa: F811
+    x, cu = scan_inputs(lens, D, N, io, 34)
+    more = (True, x["init"], cu, x["dy"], x["df"])
+    ref = ssm_ref.scan(*[x[k] for k in ORDER], *more)
+    size = ssm_ref.scan(*[x[k] for k in ORDER], *more, absolute=True)
+    L = lambda t: strided(lead(t, lens, packed))  # noqa: E731
+    got = gla.scan_bwd(L(x["u"]), L(x["dt"]), gpu(x["a"]), L(x["b"]), L(x["c"]),
+                       gpu(lead(x["dy"], lens, packed)), skip=gpu(x["skip"]), z=L(x["z"]),
+                       dt_bias=gpu(x["bias"]), init_state=gpu(x["init"]), d_final_state=gpu(x["df"]),
+                       cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda() if packed else None,
+                       grad_dtype=torch.float32)
+    f = scan_factor(x, cu, True, gradients=True) + sum(lens) * 2 ** -24
+    for k, v in zip(GRADS, got):
+        near(v.reshape(ref[k].shape), ref[k], size[k], f, k)
+    gla.status_sync()
+
+
+def step_check(gla, x, R, io, slots, outs, pool):  # noqa: F811
+    """One scan step over a pool against the formula in 64 bits, on the GPU (some inputs are large)."""
+    before = pool.clone()
+    out = torch.full((R, x["u"].shape[1]), 7.0, device="cuda")
+    gla.scan_step(x["u"], x["dt"], x["a"], x["b"], x["c"], pool, skip=x["skip"], z=x["z"],
+                  dt_bias=x["bias"], slots=slots, out_slots=outs, out=out)
+    gla.status_sync()
+    live = (slots >= 0) & (outs >= 0)
+    assert bool((out[~live] == 7.0).all())
+    untouched = torch.ones(pool.shape[0], dtype=torch.bool, device="cuda")
+    untouched[outs[live].long()] = False
+    assert torch.equal(pool[untouched], before[untouched])
+    D64 = {k: v.double() for k, v in x.items()}
+    delta = torch.nn.functional.softplus(D64["dt"] + D64["bias"], threshold=60)[live]
+    u, z = D64["u"][live], D64["z"][live]
+    old, b, c = before[slots[live].long()].double(), D64["b"][live][:, None], D64["c"][live][:, None]
+    del before
+    kept, drive = torch.exp(delta[..., None] * D64["a"]) * old, (delta * u)[..., None] * b
+    gate = z * torch.sigmoid(z)
+    h, h_size = kept + drive, kept.abs() + drive.abs()
+    y = ((h * c).sum(-1) + D64["skip"] * u) * gate
+    y_size = ((h_size * c.abs()).sum(-1) + (D64["skip"] * u).abs()) * gate.abs()
+    f = 2 ** -20 + 2 ** -17
+    assert bool(((pool[outs[live].long()].double() - h).abs() <= f * h_size + 1e-30).all())
+    assert bool(((out[live].double() - y).abs() <= f * y_size + 1e-30).all())
+
+
+@pytest.mark.parametrize("io,R,D,N", [
+    ("bf16", 573, 2048, 8), ("fp32", 291, 2048, 16), ("bf16", 71, 2432, 64), ("fp32", 67, 2424, 64),
+    ("bf16", 1001, 1032, 32)])
+def test_scan_step_of_many_rows(gla, io, R, D, N):  # noqa: F811
+    """Blocks that walk five groups of rows and more, the last one partial, rows without a page among them."""
+    x, _ = scan_inputs([1] * R, D, N, io, 35)
+    x = {k: gpu(v) for k, v in x.items() if k not in ("init", "dy", "df")}
+    g = torch.Generator().manual_seed(36)
+    order = torch.randperm(2 * R + 1, generator=g).to(torch.int32)
+    slots, outs = gpu(order[:R].clone()), gpu(order[R:2 * R].clone())
+    slots[[0, 5, R // 2, R - 1]] = -1
+    outs[[6, R // 3]] = -1
+    pool = torch.randn(2 * R + 1, D, N, generator=torch.Generator(device="cuda").manual_seed(37), device="cuda")
+    step_check(gla, x, R, io, slots, outs, pool)
+
+
+def test_scan_step_of_more_rows_than_tables_hold(gla):  # noqa: F811
+    """More blocks than two waves, because a block's table of pages holds 1024 rows."""
+    R, D, N = 940_003, 8, 8
+    x, _ = scan_inputs([1] * R, D, N, "bf16", 38)
+    x = {k: gpu(v) for k, v in x.items() if k not in ("init", "dy", "df")}
+    slots = torch.arange(R, dtype=torch.int32, device="cuda")
+    slots[::1000] = -1
+    pool = torch.randn(R, D, N, generator=torch.Generator(device="cuda").manual_seed(39), device="cuda")
+    step_check(gla, x, R, "bf16", slots, slots.clone(), pool)
+
+
+# ---------------------------------------------------------------------------
+# Infinities and NaN stay in their sequence, rows and channels.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_other_sequences_of_a_poisoned_one(gla, io, bad):  # noqa: F811
+    """A packed sequence full of ``bad`` changes no bit of its neighbours' results."""
+    lens, D, N, W = [37, 0, 70, 1, 129, 33], 136, 16, 4
+    x, cu = scan_inputs(lens, D, N, io, 40)
+    x = {k: gpu(v) for k, v in x.items()}
+    w, wb = torch.randn(D, W, device="cuda"), torch.randn(D, device="cuda")
+    ci = torch.randn(len(lens), W - 1, D, device="cuda").to(DT[io])
+    cu_gpu = torch.tensor(cu, dtype=torch.int32).cuda()
+
+    def everything():
+        y, f = gla.conv_fwd(x["u"], w, wb, init_state=ci, cu_seqlens=cu_gpu, activation="silu")
+        dx, _, _, di = gla.conv_bwd(x["u"], w, x["dy"], wb, init_state=ci, d_final_state=ci.float(),
+                                    cu_seqlens=cu_gpu, activation="silu")
+        args = (x["u"], x["dt"], x["a"], x["b"], x["c"])
+        kw = dict(skip=x["skip"], z=x["z"], dt_bias=x["bias"], init_state=x["init"], cu_seqlens=cu_gpu)
+        o, h = gla.scan_fwd(*args, **kw)
+        du, ddt, _, db, dc, _, dz, _, dh = gla.scan_bwd(*args, x["dy"], **kw, d_final_state=x["df"])
+        return [y, dx, o, du, ddt, db, dc, dz], [f, di, h, dh]
+
+    rows, states = everything()
+    s = 2
+    for k in ("u", "dt", "b", "c", "z", "dy"):
+        x[k][cu[s]:cu[s + 1]] = bad
+    x["init"][s], x["df"][s], ci[s] = bad, bad, bad
+    rows2, states2 = everything()
+    gla.status_sync()
+    keep = torch.ones(cu[-1], dtype=torch.bool)
+    keep[cu[s]:cu[s + 1]] = False
+    others = [i for i in range(len(lens)) if i != s]
+    for p, q in zip(rows, rows2):
+        assert torch.equal(p[keep.cuda()], q[keep.cuda()])
+    for p, q in zip(states, states2):
+        assert torch.equal(p[others], q[others])
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_other_rows_of_a_poisoned_one_in_steps(gla, io):  # noqa: F811
+    R, D, N, W = 9, 136, 16, 4
+    x, _ = scan_inputs([1] * R, D, N, io, 41)
+    x = {k: gpu(v) for k, v in x.items()}
+    w, cs = torch.randn(D, W, device="cuda"), torch.randn(R, W - 1, D, device="cuda").to(DT[io])
+
+    def everything():
+        h, c = x["init"].clone(), cs.clone()
+        y = gla.scan_step(x["u"], x["dt"], x["a"], x["b"], x["c"], h, skip=x["skip"], z=x["z"], dt_bias=x["bias"])
+        return [y, h, gla.conv_step(x["u"], w, c, activation="silu"), c]
+
+    first = everything()
+    for k in ("u", "dt", "b", "c", "z"):
+        x[k][3] = float("nan")
+    others = [i for i in range(R) if i != 3]
+    assert all(torch.equal(p[others], q[others]) for p, q in zip(first, everything()))
+
+
+# ---------------------------------------------------------------------------
+# More than 2^31 elements
+# ---------------------------------------------------------------------------
+def test_prompts_of_more_than_31_bits(gla):  # noqa: F811
+    """Packed bf16 rows of 2^31 and some elements: the last sequences, which start behind
+    element 2^31, are those of a call on them alone (convolution: bit for bit) and the
+    definition's (scan: some channels)."""
+    D, N, W, tail = 2048, 16, 4, [70, 0, 1, 33]
+    head = 2 ** 31 // D + 7
+    g = torch.Generator(device="cuda").manual_seed(42)
+    lens = [head] + tail
+    R, B, T = sum(lens), len(lens), sum(tail)
+    cu = torch.tensor(cu_of(lens), dtype=torch.int32, device="cuda")
+    cu_tail = torch.tensor(cu_of([0] + tail), dtype=torch.int32, device="cuda")
+    x = torch.empty(R, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.randn(D, W, generator=g, device="cuda")
+    init = torch.randn(B, W - 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    y, f = gla.conv_fwd(x, w, init_state=init, cu_seqlens=cu, activation="silu")
+    y2, f2 = gla.conv_fwd(x[head:], w, init_state=init, cu_seqlens=cu_tail, activation="silu")
+    assert torch.equal(y[head:], y2) and torch.equal(f[1:], f2[1:])
+    dx, _, _, di = gla.conv_bwd(x, w, y, init_state=init, cu_seqlens=cu, activation="silu")
+    dx2, _, _, di2 = gla.conv_bwd(x[head:], w, y2, init_state=init, cu_seqlens=cu_tail, activation="silu")
+    assert torch.equal(dx[head:], dx2) and torch.equal(di[1:], di2[1:])
+    gla.status_sync()
+    del dx
+    a = -torch.arange(1, N + 1, device="cuda").float() * torch.rand(D, 1, generator=g, device="cuda").add(0.5)
+    dt = torch.empty(R, D, dtype=torch.bfloat16, device="cuda").normal_(-3, 0.5, generator=g)
+    bc = torch.randn(R, 2 * N, generator=g, device="cuda").to(torch.bfloat16)
+    b, c = bc[:, :N], bc[:, N:]
+    o, h = gla.scan_fwd(y, dt, a, b, c, z=x, cu_seqlens=cu, out_dtype=torch.float32)
+    sel = torch.tensor([0, 1, 1000, 2047], device="cuda")
+    cl = cu_of([0] + tail)
+    ins = (y[head:][:, sel], dt[head:][:, sel], a[sel], b[head:], c[head:], None, x[head:][:, sel], None, True, None, cl)
+    names = dict(zip(ORDER, ins))
+    factor = scan_factor({k: None if v is None else v.cpu() for k, v in names.items()}, cl, True)
+    ref, size = ssm_ref.scan(*ins), ssm_ref.scan(*ins, absolute=True)
+    near(o[head:][:, sel], ref["y"], size["y"], factor, "y")
+    near(h[1:, sel], ref["final"][1:], size["final"][1:], factor, "final")
+    gla.status_sync()
+    del o
+    dy = x
+    got = gla.scan_bwd(y, dt, a, b, c, dy, z=x, cu_seqlens=cu)
+    alone = gla.scan_bwd(y[head:], dt[head:], a, b[head:], c[head:], dy[head:], z=x[head:], cu_seqlens=cu_tail)
+    for k, p, q in zip(GRADS, got, alone):
+        if p is not None and p.shape[0] == R:
+            assert torch.equal(p[head:], q) and q.shape[0] == T, k
+    assert torch.equal(got[8][1:], alone[8][1:])
+    gla.status_sync()
+
+
+def test_pools_of_more_than_31_bits(gla):  # noqa: F811
+    """Pages behind element 2^31 of a pool step as pages of a small one."""
+    D, N, W, R = 2048, 16, 4, 3
+    P = 2 ** 31 // (D * N) + 9
+    x, _ = scan_inputs([1] * R, D, N, "bf16", 43)
+    x = {k: gpu(v) for k, v in x.items()}
+    slots = torch.tensor([P - 1, P - 3, 5], dtype=torch.int32, device="cuda")
+    outs = torch.tensor([P - 1, P - 2, P - 5], dtype=torch.int32, device="cuda")
+    pool = torch.zeros(P, D, N, device="cuda")
+    pool[slots.long()] = x["init"]
+    state = x["init"].clone()
+    args = (x["u"], x["dt"], x["a"], x["b"], x["c"])
+    y = gla.scan_step(*args, pool, dt_bias=x["bias"], slots=slots, out_slots=outs)
+    assert torch.equal(y, gla.scan_step(*args, state, dt_bias=x["bias"]))
+    assert torch.equal(pool[outs.long()], state)
+    del pool
+    P = 2 ** 31 // (D * (W - 1)) + 9
+    w, cs = torch.randn(D, W, device="cuda"), torch.randn(R, W - 1, D, device="cuda").to(torch.bfloat16)
+    pool = torch.zeros(P, W - 1, D, dtype=torch.bfloat16, device="cuda")
+    slots, outs = slots.clone(), outs.clone()
+    slots[:2], outs[:] = torch.tensor([P - 1, P - 3]), torch.tensor([P - 1, P - 2, P - 5])
+    pool[slots.long()] = cs
+    y = gla.conv_step(x["u"], w, pool, slots=slots, out_slots=outs)
+    assert torch.equal(y, gla.conv_step(x["u"], w, cs))
+    assert torch.equal(pool[outs.long()], cs)
+    gla.status_sync()
+
+
+# ---------------------------------------------------------------------------
 # Malformed offsets are reported whatever else is asked for.
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("D", [8, 64, 2048])
@@ -173,3 +424,56 @@ def test_conv_of_very_many_channels(gla, io, D):  # noqa: F811
     same(dw[:, 1], list(dy * x))
     same(dw[:, 0], list(dy * back))
     same(db, list(dy))
+
+
+def test_scan_of_very_many_channels(gla):  # noqa: F811
+    """2^24 channels of two tokens, prompt, gradients and step, against the formula in 64 bits on the GPU."""
+    D, N = 2 ** 24, 8
+    g = torch.Generator(device="cuda").manual_seed(45)
+    r = lambda *s, std=1.0: torch.randn(*s, generator=g, device="cuda") * std  # noqa: E731
+    u, dt, dy = (r(1, 2, D, std=s).to(torch.bfloat16) for s in (1.0, 0.5, 1.0))
+    b, c = r(1, 2, N).to(torch.bfloat16), r(1, 2, N).to(torch.bfloat16)
+    a = -torch.rand(D, N, generator=g, device="cuda") - 0.1
+    init = r(1, D, N)
+    y, fin = gla.scan_fwd(u, dt, a, b, c, init_state=init, out_dtype=torch.float32)
+    got = gla.scan_bwd(u, dt, a, b, c, dy, init_state=init, grad_dtype=torch.float32)
+    state = init.clone()
+    y0 = gla.scan_step(u[:, 0], dt[:, 0], a, b[:, 0], c[:, 0], state, out_dtype=torch.float32)
+    gla.status_sync()
+    for lo in range(0, D, 2 ** 22):                             # (64-bit states of 2^22 channels are 256 MB)
+        at = slice(lo, lo + 2 ** 22)
+        U, X, G, A, H = u[0, :, at].double(), dt[0, :, at].double(), dy[0, :, at].double(), a[at].double(), \
+            init[0, at].double()
+        B, C = b[0].double(), c[0].double()
+        delta = torch.nn.functional.softplus(X, threshold=60)
+        decay = torch.exp(delta[..., None] * A)
+        h = [H]
+        size = H.abs()
+        sizes = []
+        for t in range(2):
+            drive = (delta[t] * U[t])[:, None] * B[t]
+            h.append(decay[t] * h[-1] + drive)
+            size = decay[t] * size + drive.abs()
+            sizes.append(size)
+        f = 2 ** -17 + 2 * 2 ** -20
+        ok = lambda p, q, s, f=f: bool(((p.double() - q).abs() <= f * s + 1e-30).all())  # noqa: E731
+        for t in range(2):
+            assert ok(y[0, t, at], (h[t + 1] * C[t]).sum(-1), (sizes[t] * C[t].abs()).sum(-1))
+        assert ok(fin[0, at], h[2], sizes[1])
+        assert ok(state[0, at], h[1], sizes[0]) and ok(y0[0, at], (h[1] * C[0]).sum(-1), (sizes[0] * C[0].abs()).sum(-1))
+        e1 = G[1][:, None] * C[1]
+        e0 = G[0][:, None] * C[0] + decay[1] * e1
+        e0s = (G[0][:, None] * C[0]).abs() + decay[1] * e1.abs()
+        du, ddt, da, _, _, _, _, _, di = got
+        assert ok(di[0, at], decay[0] * e0, decay[0] * e0s, 2 * f)
+        for t, (e, es) in enumerate(((e0, e0s), (e1, e1.abs()))):
+            s1, s1s = (e * B[t]).sum(-1), (es * B[t].abs()).sum(-1)
+            before, bs = (h[t], H.abs() if t == 0 else sizes[0])
+            w, ws = e * decay[t] * before, es * decay[t] * bs
+            slope = torch.sigmoid(X[t])
+            assert ok(du[0, t, at], delta[t] * s1, delta[t] * s1s, 2 * f)
+            assert ok(ddt[0, t, at], ((w * A).sum(-1) + U[t] * s1) * slope,
+                      ((ws * A.abs()).sum(-1) + U[t].abs() * s1s) * slope, 2 * f)
+            part, part_s = (w * delta[t][:, None], ws * delta[t][:, None]) if t == 0 else \
+                (part + w * delta[t][:, None], part_s + ws * delta[t][:, None])
+        assert ok(da[at], part, part_s, 2 * f)
