@@ -477,3 +477,71 @@ def test_scan_of_very_many_channels(gla):  # noqa: F811
             part, part_s = (w * delta[t][:, None], ws * delta[t][:, None]) if t == 0 else \
                 (part + w * delta[t][:, None], part_s + ws * delta[t][:, None])
         assert ok(da[at], part, part_s, 2 * f)
+
+
+# ---------------------------------------------------------------------------
+# Every built variant of the convolutions over hundreds of ends of sequences, again and again
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("io,out", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+def test_convolution_variants_at_sequence_ends(gla, io, out, act, W):  # noqa: F811
+    """A build of an earlier kernel, right by its source, let the address of the next sequence's offset into
+    the registers of a sequence's last row before they were stored, in some blocks of some
+    runs.  So every variant runs over many ends with the GPU full, six times, to the same
+    bits, and all rows are compared with the formula in fp32 (each side within 2^-18 of the
+    terms, gradients 2^-17, as in test_gpu_ssm; then one rounding of the result)."""
+    D, K = 2048, W - 1
+    g = torch.Generator(device="cuda").manual_seed(46)
+    lens = torch.randint(0, 120, (300,), generator=torch.Generator().manual_seed(47)).tolist()
+    cu, R, B = cu_of(lens), sum(lens), len(lens)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dy = r(R, D).to(DT[io]), r(R, D).to(DT[io])
+    w, bias, init = r(D, W) * 0.5, r(D), r(B, K, D).to(DT[io])
+    df = r(B, K, D)
+    cu_gpu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kw = dict(init_state=init, cu_seqlens=cu_gpu, activation=act)
+
+    def everything():
+        y, fin = gla.conv_fwd(x, w, bias, **kw, out_dtype=DT[out])
+        return [y, fin, *gla.conv_bwd(x, w, dy, bias, **kw, d_final_state=df, grad_dtype=DT[out])]
+
+    first = everything()
+    for _ in range(5):
+        assert all(torch.equal(p, q) for p, q in zip(first, everything()))
+    gla.status_sync()
+    # rows of the initial states in front of them all; row i of a window lies K - i rows back
+    rows = torch.cat([init.reshape(B * K, D), x]).float()
+    seq = torch.arange(B, device="cuda").repeat_interleave(torch.tensor(lens, device="cuda"))
+    at = torch.arange(R, device="cuda")
+    start = cu_gpu.long()
+    pos, left = at - start[seq], start[seq + 1] - at
+
+    def back(j):
+        return torch.where(pos >= j, B * K + at - j, seq * K + K + pos - j)
+
+    p, size = bias.expand(R, D).clone(), bias.abs().expand(R, D).clone()
+    for j in range(W):
+        t = rows[back(j)] * w[:, K - j]
+        p += t
+        size += t.abs()
+    s = torch.sigmoid(p)
+    y = p * s if act else p
+    half = torch.finfo(DT[out]).eps / 2
+    err = (first[0].float() - y).abs()
+    assert bool((err <= 2 * 2 ** -18 * size + half * y.abs()).all())
+    dp = dy.float() * (s * (1 + p * (1 - s)) if act else 1)
+    # silu' moves with p by at most a half
+    dp_size = dy.float().abs() * (((s * (1 + p * (1 - s))).abs() + size) if act else 1)
+    del p, s, y, err, size
+    dx, dx_size = torch.zeros(R, D, device="cuda"), torch.zeros(R, D, device="cuda")
+    for j in range(W):
+        ok = (left > j)[:, None]
+        src = torch.where(left > j, at + j, at)
+        dx += torch.where(ok, dp[src] * w[:, K - j], 0.0)
+        dx_size += torch.where(ok, dp_size[src] * w[:, K - j].abs(), 0.0)
+    last = left <= K
+    extra = torch.where(last[:, None], df[seq, (K - left).clamp(min=0)], 0.0)
+    dx += extra
+    dx_size += extra.abs()
+    assert bool(((first[2].float() - dx).abs() <= 2 * 2 ** -17 * dx_size + half * dx.abs()).all())
