@@ -307,7 +307,7 @@ gla_status chunk_bwd_impl(const void* q, const void* k, const void* v, const flo
   const size_t st_b = (size_t)(st_elems * 4);
   const void* in_p[] = {q, k, v, g, d_out, init_state, d_final_state, cu_seqlens};
   const size_t in_b[] = {qk_b, qk_b, v_b, g_b, v_b, st_b, st_b,
-                         cu_seqlens ? (size_t)(B + 1) * 4 : 0};
+                         cu_seqlens ? ((size_t)B + 1) * 4 : 0};
   // the tensor-core path runs when it covers the call and the workspace is large enough
   const size_t ws_need = gla::chunk_bwd_tc_supported(dk, dv, fp32, vec)
                              ? gla::chunk_bwd_tc_workspace(B, H, rows, dk, dv, vec)

@@ -74,7 +74,7 @@ gla_status gla_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
   const long long esz = fp32 ? 4 : 2, osz = f32out ? 4 : 2;
   const long long rows = cu_seqlens ? (long long)T : (long long)B * T;
   if (stride_bad(x_stride, D) || rows * x_stride > kMaxElems ||
-      (long long)B * (W - 1) * D > kMaxElems || rows / 8 + B > kMaxGrid)
+      (long long)B * (W - 1) * D > kMaxElems || (rows + 7) / 8 + B > kMaxGrid)
     return GLA_ERR_INVALID_ARG;
   if (!weight || (rows > 0 && (!x || !out))) return GLA_ERR_INVALID_ARG;
   if (rows == 0 && !final_state) return GLA_OK;
@@ -87,7 +87,7 @@ gla_status gla_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
                       {weight, (size_t)D * W * 4},
                       {bias, (size_t)D * 4},
                       {init_state == final_state ? nullptr : init_state, st},
-                      {cu_seqlens, (size_t)(B + 1) * 4}};
+                      {cu_seqlens, ((size_t)B + 1) * 4}};
   const Range outs[] = {{out, (size_t)(rows * D * osz)}, {final_state, st}};
   if (!disjoint(in, outs)) return GLA_ERR_INVALID_ARG;
   cudaError_t err;
@@ -122,7 +122,7 @@ gla_status gla_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
   const long long esz = fp32 ? 4 : 2, osz = f32out ? 4 : 2;
   const long long rows = cu_seqlens ? (long long)T : (long long)B * T;
   if (stride_bad(x_stride, D) || rows * x_stride > kMaxElems ||
-      (long long)B * (W - 1) * D > kMaxElems || rows / 8 + B > kMaxGrid)
+      (long long)B * (W - 1) * D > kMaxElems || (rows + 7) / 8 + B > kMaxGrid)
     return GLA_ERR_INVALID_ARG;
   if (!weight || !d_weight || (rows > 0 && (!x || !d_out || !dx || B == 0)))
     return GLA_ERR_INVALID_ARG;
@@ -141,7 +141,7 @@ gla_status gla_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
                       {init_state, (size_t)(st * esz)},
                       {d_out, (size_t)(rows * D * esz)},
                       {d_final_state, (size_t)st * 4},
-                      {cu_seqlens, (size_t)(B + 1) * 4}};
+                      {cu_seqlens, ((size_t)B + 1) * 4}};
   const Range outs[] = {{dx, (size_t)(rows * D * osz)},
                         {d_weight, (size_t)D * W * 4},
                         {d_bias, (size_t)D * 4},
@@ -246,7 +246,7 @@ gla_status scan_args(const void* u, int64_t u_stride, const void* dt, int64_t dt
       {s.b, span(rows, s.b_stride, s.NS, esz)}, {s.c, span(rows, s.c_stride, s.NS, esz)},    \
       {s.z, s.z ? span(rows, s.z_stride, s.D, esz) : 0}, {s.a, (size_t)s.D * s.NS * 4},      \
       {s.skip, (size_t)s.D * 4}, {s.dt_bias, (size_t)s.D * 4},                               \
-      {s.cu_seqlens, (size_t)(s.B + 1) * 4}
+      {s.cu_seqlens, ((size_t)s.B + 1) * 4}
 
 constexpr unsigned kScanFlags = GLA_FLAG_FP32_IO | GLA_FLAG_FP32_OUT | GLA_FLAG_SOFTPLUS;
 

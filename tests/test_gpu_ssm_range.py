@@ -545,3 +545,57 @@ def test_convolution_variants_at_sequence_ends(gla, io, out, act, W):  # noqa: F
     dx += extra
     dx_size += extra.abs()
     assert bool(((first[2].float() - dx).abs() <= 2 * 2 ** -17 * dx_size + half * dx.abs()).all())
+
+
+# ---------------------------------------------------------------------------
+# Nothing to do, and as many sequences as can be counted
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_sequences_without_tokens(gla, io, packed):  # noqa: F811
+    """Three sequences of no tokens: final states are the initial ones (or zero), the initial states'
+    gradients the final ones', parameters' gradients zero, in place and onto used memory."""
+    D, N, W, B = 136, 16, 4, 3
+    ty = DT[io]
+    g = torch.Generator(device="cuda").manual_seed(48)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    none = lambda n: torch.empty(*((0, n) if packed else (B, 0, n)), dtype=ty, device="cuda")  # noqa: E731
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda") if packed else None
+    w, bias, ci, df = r(D, W), r(D), r(B, W - 1, D).to(ty), r(B, W - 1, D)
+    a, h, dh, p = -r(D, N).abs(), r(B, D, N), r(B, D, N), r(D)
+    for init in (ci, None):
+        y, f = gla.conv_fwd(none(D), w, bias, init_state=init, cu_seqlens=cu)
+        assert y.numel() == 0 and torch.equal(f, ci if init is not None else torch.zeros_like(ci))
+    state = ci.clone()
+    gla.conv_fwd(none(D), w, bias, init_state=state, final_state=state, cu_seqlens=cu)
+    assert torch.equal(state, ci)
+    dx, dw, db, di = gla.conv_bwd(none(D), w, none(D), bias, init_state=ci, d_final_state=df, cu_seqlens=cu)
+    assert torch.equal(di, df) and not dw.any() and not db.any() and dx.shape == none(D).shape
+    args = (none(D), none(D), a, none(N), none(N))
+    for init in (h, None):
+        y, f = gla.scan_fwd(*args, init_state=init, cu_seqlens=cu)
+        assert y.numel() == 0 and torch.equal(f, h if init is not None else torch.zeros_like(h))
+    got = dict(zip(GRADS, gla.scan_bwd(*args, none(D), skip=p, z=none(D), dt_bias=p, init_state=h,
+                                       d_final_state=dh, cu_seqlens=cu)))
+    assert torch.equal(got["d_init"], dh) and not got["da"].any() and not got["dskip"].any() and \
+        not got["dbias"].any() and got["db"].numel() == 0
+    if not packed:  # and no sequences at all
+        x = torch.empty(0, 5, D, dtype=ty, device="cuda")
+        bc = torch.empty(0, 5, N, dtype=ty, device="cuda")
+        assert gla.conv_fwd(x, w)[0].shape == x.shape and gla.scan_fwd(x, x, a, bc, bc)[1].shape == (0, D, N)
+        assert not gla.conv_bwd(x, w, x)[1].any() and not gla.scan_bwd(x, x, a, bc, bc, x)[2].any()
+    gla.status_sync()
+
+
+def test_most_sequences(gla):  # noqa: F811
+    """2^31 - 2 sequences, all empty but the last, which has one token: a block each, and one for the row."""
+    B, D = 2 ** 31 - 2, 8
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[B] = 1
+    x = torch.arange(D, device="cuda").to(torch.bfloat16)[None] + 1
+    final = torch.full((B, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    y, _ = gla.conv_fwd(x, torch.ones(D, 2, device="cuda"), cu_seqlens=cu, final_state=final)
+    gla.status_sync()
+    assert torch.equal(y, x) and torch.equal(final[B - 1], x)
+    for lo in range(0, B - 1, 2 ** 28):
+        assert not final[lo:min(lo + 2 ** 28, B - 1)].any()

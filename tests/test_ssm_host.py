@@ -60,6 +60,12 @@ def test_conv_fwd_rejects_before_launch(L, kw, status):
     assert conv_fwd(L, **kw) == status
 
 
+def test_conv_fwd_rejects_more_blocks_than_a_grid_has(L):
+    """A block for every sequence's final state and one for the rows: 2^31 - 1 and one."""
+    many = dict(B=2 ** 31 - 1, D=8, xs=8, W=2, cu=1 << 40, fin=1 << 42, init=None)
+    assert conv_fwd(L, T=1, **many) == E.GLA_ERR_INVALID_ARG
+
+
 def test_conv_empty_calls_do_nothing(L):
     assert conv_fwd(L, B=0) == E.GLA_OK and conv_fwd(L, D=0) == E.GLA_OK
     assert conv_fwd(L, T=0, fin=None, x=None, out=None) == E.GLA_OK
