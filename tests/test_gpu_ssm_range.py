@@ -6,6 +6,8 @@ channels.
 Tolerances as in test_gpu_ssm, per element, as parts of the same sum over the
 absolute values of its terms (its decays as they are, so that growth is in it).
 """
+import threading
+
 import pytest
 import torch
 
@@ -599,3 +601,90 @@ def test_most_sequences(gla):  # noqa: F811
     assert torch.equal(y, x) and torch.equal(final[B - 1], x)
     for lo in range(0, B - 1, 2 ** 28):
         assert not final[lo:min(lo + 2 ** 28, B - 1)].any()
+
+
+# ---------------------------------------------------------------------------
+# Chains of launches captured, and calls at the same time
+# ---------------------------------------------------------------------------
+def chain_inputs(seed, R=3001, D=1032, N=16, W=4, n=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std)  # noqa: E731
+    bf = torch.bfloat16
+    cut = sorted(torch.randint(0, R, (n - 1,), generator=torch.Generator().manual_seed(seed)).tolist())
+    return dict(x=r(R, D).to(bf), dt=(r(R, D, std=0.5) - 3).to(bf), bc=r(R, 2 * N).to(bf), z=r(R, D).to(bf),
+                dy=r(R, D).to(bf), a=-r(D, N).abs() - 0.1, h=r(n, D, N), w=r(D, W), ci=r(n, W - 1, D).to(bf),
+                skip=r(D), cu=torch.tensor([0] + cut + [R], dtype=torch.int32, device="cuda"),
+                parents=torch.randint(0, 8, (n,), generator=g, device="cuda").to(torch.int32),
+                used=(torch.arange(24, device="cuda") < 8).to(torch.int32), pool=r(24, D, N), tail=r(24, W - 1, D).to(bf))
+
+
+def chain(gla, t, stream=None):  # noqa: F811
+    """Every operator that takes more than one launch, the pools' pages and the steps on them."""
+    N, kw = t["a"].shape[1], dict(cu_seqlens=t["cu"], stream=stream)
+    u, cf = gla.conv_fwd(t["x"], t["w"], init_state=t["ci"], activation="silu", **kw)
+    args = (u, t["dt"], t["a"], t["bc"][:, :N], t["bc"][:, N:])
+    y, h = gla.scan_fwd(*args, skip=t["skip"], z=t["z"], init_state=t["h"], **kw)
+    g = gla.scan_bwd(*args, t["dy"], skip=t["skip"], z=t["z"], init_state=t["h"], d_final_state=t["h"], **kw)
+    dx = gla.conv_bwd(t["x"], t["w"], g[0], init_state=t["ci"], activation="silu", **kw)
+    pools = [t["pool"], t["tail"]]
+    kids, used = gla.fork_pages(pools, t["used"], t["parents"], used_out=torch.empty_like(t["used"]), stream=stream)
+    n = kids.shape[0]
+    v = gla.conv_step(t["x"][:n], t["w"], t["tail"], activation="silu", slots=kids, stream=stream)
+    o = gla.scan_step(v, *(q[:n] for q in args[1:2]), t["a"], args[3][:n], args[4][:n], t["pool"], slots=kids, stream=stream)
+    slots, left, moved = gla.compact_pages(pools, used, kids, used_out=torch.empty_like(used), stream=stream)
+    return [p for p in (u, cf, y, h, *g, *dx, kids, used, v, o, slots, left, moved) if p is not None]
+
+
+def test_chains_captured_and_replayed(gla):  # noqa: F811
+    """Chunked scans, gradients, forks, steps and compaction as one graph, replayed on new inputs (the pools
+    go back to what they were between runs)."""
+    t, other = chain_inputs(49), chain_inputs(50)
+    keep = {k: t[k].clone() for k in ("pool", "tail")}
+    warm = chain(gla, t)
+    torch.cuda.synchronize()
+    for k, v in keep.items():
+        t[k].copy_(v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = chain(gla, t)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(warm, held))
+    for k in t:
+        t[k].copy_(other[k])
+    graph.replay()
+    fresh = chain(gla, other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(held, fresh))
+    assert torch.equal(t["pool"], other["pool"]) and torch.equal(t["tail"], other["tail"])
+    gla.status_sync()
+
+
+def test_calls_at_the_same_time(gla):  # noqa: F811
+    """The same chains from three threads on three streams, over and over, against each alone."""
+    inputs = [chain_inputs(s) for s in (51, 52, 53)]
+    saved = [{k: t[k].clone() for k in ("pool", "tail")} for t in inputs]
+    alone = [chain(gla, t) for t in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            stream, t = torch.cuda.Stream(), inputs[i]
+            with torch.cuda.stream(stream):
+                for _ in range(8):
+                    for k, v in saved[i].items():
+                        t[k].copy_(v)
+                    got = chain(gla, t, stream if i else None)
+                    if not all(torch.equal(p, q) for p, q in zip(got, alone[i])):
+                        wrong.append(i)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    gla.status_sync()
+    assert not wrong
