@@ -481,13 +481,14 @@ long long span(long long full, long long len, long long part, long long rest) {
 // extra pass) spread over all SMs, and about 100 for two more launches.  A packed
 // call's longest sequence is not known here: 2.5 times the mean.  Measured, D =
 // 2048 and NS = 16, whole against best chunk: 4 x 2048 tokens 103 and 154 us, 2 x 2048
-// 103 and 87, 1 x 2048 103 and 45, 1 x 512 29 and 19, three packed sequences of 20001
+// 103 and 84, 1 x 2048 103 and 45, 1 x 512 29 and 19, three packed sequences of 20001
 // tokens 708 and 347.
 //
 // Equal sequences: the length whose blocks fill their waves best.  1 x 2048 tokens: 224 45
-// us, 256 50, 208 52, 320 60; 1 x 8192: 896 152 us, 576 153, 1024 171, 768 193.  Packed
-// ones: about four blocks a SM (two are resident); the last case in 1024 347 us, in 512
-// 357, in 64 504, in 2048 397.
+// us, 256 50, 208 52, 320 60; 1 x 8192: 864 147 us, 896 152, 576 153, 1024 171, 768
+// 193.  Packed ones: about four blocks a SM (two are resident); the last case in 1024 347 us,
+// in 512 357, in 64 504, in 2048 397.  The constants are those of 16 states: with 64 the
+// rule errs where it is close (1 x 5000 tokens of 1024 channels: 287 us, whole 254).
 long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
   constexpr long long kSMs = 152;
   const long long tiles = ((long long)D * NS + 1023) / 1024, work = rows * tiles / kSMs;
@@ -510,7 +511,7 @@ long long chunk_rule(int B, long long rows, int D, int NS, bool packed) {
       chunk = c;
     }
   }
-  return least * 2 + 40 >= whole ? 0 : chunk;  // (1 x 256 tokens: 15.8 us whole, 14.4 in chunks)
+  return least * 2 + 40 >= whole ? 0 : chunk;  // (1 x 256 tokens: 15.8 us whole, 14.3 in chunks)
 }
 
 template <typename IO, typename OUT, int NS>

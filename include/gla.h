@@ -56,7 +56,8 @@
  *     an error has launched nothing and written nothing.
  *   - Layouts are dense, row-major, token-major ("[B, T, H, d]": d fastest).
  *   - bf16 is IEEE-style bfloat16 (1-8-7); outputs are rounded to nearest even
- *     from fp32.  States are always fp32.  Accumulation is fp32.
+ *     from fp32.  States are fp32 (the convolution's, which hold inputs, in the
+ *     inputs' dtype).  Accumulation is fp32.
  *   - Errors detected on the device (a malformed cu_seqlens, an internal wait
  *     that ran out) set bits in the status word; the affected (sequence, head)
  *     writes nothing.  gla_status_sync() reports and clears them.
