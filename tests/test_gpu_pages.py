@@ -261,3 +261,47 @@ def test_copies_from_several_threads(gla):
     assert held.tolist() == dst[0].tolist()
     for S, p in zip(sizes, pools):
         assert p[3].tolist() == [S - 1] * 4 and p[S - 2].tolist() == [7] * 4 and p[4].tolist() == [4] * 4
+
+
+def test_largest_tables(gla):
+    """As many pages as a pool may have: fork, free, compact and copy against the plain implementation."""
+    S = gla._binding.GLA_MAX_PAGES
+    g = torch.Generator().manual_seed(55)
+    used = (torch.rand(S, generator=g) < 0.6).int().tolist()
+    pool = torch.arange(S, dtype=torch.int32, device="cuda")[:, None].repeat(1, 4)
+    live = [p for p in range(S) if used[p]]
+    pick = torch.randint(0, len(live), (150_000,), generator=g).tolist()
+    parents = [-2 if i % 5 == 0 else -1 if i % 7 == 0 else live[p] for i, p in enumerate(pick)]
+    children, used2, bad = fork_ref(used, parents)
+    assert not bad
+    want = list(range(S))
+    for p, q in zip(parents, children):
+        if q >= 0:
+            want[q] = 0 if p == -2 else p
+    table = i32(used)
+    got, _ = gla.fork_pages([pool], table, i32(parents))
+    synced(gla, False)
+    assert got.tolist() == children and table.tolist() == used2
+    assert torch.equal(pool, i32(want)[:, None].expand(S, 4))
+    done = live[::3]
+    gla.free_pages(table, i32(done))
+    for p in done:
+        used2[p] = 0
+    assert table.tolist() == used2
+    forward, used3 = compact_ref(used2)
+    slots = [p for p in range(S) if used2[p]][::-1]
+    moved, _, fwd = gla.compact_pages([pool], table, i32(slots))
+    synced(gla, False)
+    for p, q in enumerate(forward):
+        if q >= 0 and q != p:
+            want[q] = want[p]
+    assert fwd.tolist() == forward and table.tolist() == used3
+    assert moved.tolist() == [forward[p] for p in slots]
+    assert torch.equal(pool, i32(want)[:, None].expand(S, 4))
+    order = torch.randperm(S, generator=g).int()
+    src, dst = order[:S // 2].tolist(), order[S // 2:].tolist()
+    assert gla.copy_pages([pool], i32(src), i32(dst)).tolist() == dst
+    synced(gla, False)
+    for p, q in zip(src, dst):
+        want[q] = want[p]
+    assert torch.equal(pool, i32(want)[:, None].expand(S, 4))

@@ -226,6 +226,30 @@ def test_scan_step_of_more_rows_than_tables_hold(gla):  # noqa: F811
     step_check(gla, x, R, "bf16", slots, slots.clone(), pool)
 
 
+def test_conv_step_of_many_rows(gla):  # noqa: F811
+    """More rows than one grid dimension is given, some without a page, against the formula in 64 bits."""
+    R, D, W = 100_003, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(54)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, w, bias, pool = r(R, D), r(D, W), r(D), r(2 * R, W - 1, D)
+    order = torch.randperm(2 * R, generator=g, device="cuda").to(torch.int32)
+    slots, outs = order[:R].clone(), order[R:].clone()
+    slots[::777] = -1
+    outs[5::1000] = -1
+    before, out = pool.clone(), torch.full((R, D), 7.0, device="cuda")
+    gla.conv_step(x, w, pool, bias, slots=slots, out_slots=outs, out=out)
+    gla.status_sync()
+    live = (slots >= 0) & (outs >= 0)
+    window = torch.cat([before[slots[live].long()], x[live][:, None]], 1)
+    terms = window.double() * w.double().t()
+    size = terms.abs().sum(1) + bias.abs()
+    assert bool(((out[live].double() - terms.sum(1) - bias).abs() <= 2 ** -18 * size).all())
+    assert bool((out[~live] == 7.0).all())
+    want = before
+    want[outs[live].long()] = window[:, 1:]
+    assert torch.equal(pool, want)
+
+
 # ---------------------------------------------------------------------------
 # Infinities and NaN stay in their sequence, rows and channels.
 # ---------------------------------------------------------------------------
