@@ -10,6 +10,9 @@ library's CUDA kernels, and a missing library is an error, never a fallback.
 
     y, state = conv_fwd(x, weight, activation="silu")            # a selective-scan layer
     y, state = scan_fwd(u, dt, a, b, c, z=z)                     # (conv_bwd, scan_bwd; conv_step, scan_step)
+    y, state = recur_fwd(x, f, decay, i=i, z=z)                  # a gated linear recurrence
+    res, u = block_norm_fwd(res, y, weight=w)                    # between two blocks
+    h = glu_fwd(u, w_gate, w_up)                                 # gated feed-forward projections
     children, used = fork_pages(pools, used, parents)            # pages of the state pools
 
 The recurrence (the "i14 Laplace 3B on AWS Trainium2" page, paragraph "GLA
@@ -29,6 +32,8 @@ __all__ = ["chunk_fwd", "chunk_bwd", "decode_step", "status_sync", "set_wait_lim
            "lib", "version",
            "GLA_FLAG_FP32_IO", "GLA_FLAG_FP32_OUT", "GLA_FLAG_VECTOR_GATE",
            "conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step",
+           "recur_fwd", "recur_bwd", "recur_step", "block_norm_fwd", "block_norm_bwd",
+           "glu_fwd", "glu_bwd",
            "copy_pages", "fork_pages", "compact_pages", "free_pages", "PAGE_NEW"]
 
 
@@ -304,6 +309,9 @@ def status_sync(stream=None) -> int:
     return rc
 
 
-# The selective-scan layer and the state pools' pages live in files of their own.
+# The selective-scan layer, the rest of a recurrent block and the state pools' pages live
+# in files of their own.
+from .block import (block_norm_bwd, block_norm_fwd, glu_bwd, glu_fwd, recur_bwd,  # noqa: E402
+                    recur_fwd, recur_step)
 from .pages import PAGE_NEW, compact_pages, copy_pages, fork_pages, free_pages  # noqa: E402
 from .ssm import conv_bwd, conv_fwd, conv_step, scan_bwd, scan_fwd, scan_step  # noqa: E402

@@ -25,6 +25,9 @@ GLA_FLAG_VECTOR_GATE = 1 << 1
 GLA_FLAG_FP32_OUT = 1 << 2
 GLA_FLAG_SILU = 1 << 3
 GLA_FLAG_SOFTPLUS = 1 << 4
+GLA_FLAG_UNIT_VARIANCE = 1 << 5
+GLA_FLAG_LAYER_NORM = 1 << 6
+GLA_FLAG_FP32_RESIDUAL = 1 << 7
 
 GLA_PAGE_NEW = -2
 GLA_MAX_PAGES = 524288
@@ -118,6 +121,30 @@ def lib() -> ctypes.CDLL:
             L.gla_scan_bwd_workspace_size.restype = sz
             L.gla_scan_step.argtypes = rows + [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, un]
             L.gla_scan_step.restype = _i
+            rows = [_vp, _i64] * 4 + [_vp]
+            L.gla_recur_fwd.argtypes = rows + [_vp] * 4 + [_i] * 3 + [_vp, un]
+            L.gla_recur_fwd.restype = _i
+            L.gla_recur_bwd.argtypes = rows + [_vp] * 10 + [_i] * 3 + [_vp, sz, _vp, un]
+            L.gla_recur_bwd.restype = _i
+            L.gla_recur_bwd_workspace_size.argtypes = [_i] * 4
+            L.gla_recur_bwd_workspace_size.restype = sz
+            L.gla_recur_step.argtypes = rows + [_vp, _i, _vp, _vp, _vp, _i, _i, _vp, un]
+            L.gla_recur_step.restype = _i
+            fl = ctypes.c_float
+            rows = [_vp, _vp, _i64, _vp, _i64]
+            L.gla_block_norm_fwd.argtypes = rows + [_vp] * 5 + [fl, _vp, _vp, _i, _i, _vp, un]
+            L.gla_block_norm_fwd.restype = _i
+            L.gla_block_norm_bwd.argtypes = rows + [_vp] * 4 + [fl] + [_vp] * 10 + \
+                [_i, _i, _vp, sz, _vp, un]
+            L.gla_block_norm_bwd.restype = _i
+            L.gla_block_norm_bwd_workspace_size.argtypes = [_i] * 2
+            L.gla_block_norm_bwd_workspace_size.restype = sz
+            L.gla_glu_fwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _i, _i, _i, _vp, un]
+            L.gla_glu_fwd.restype = _i
+            L.gla_glu_bwd.argtypes = [_vp, _i64] + [_vp] * 6 + [_i] * 3 + [_vp, sz, _vp, un]
+            L.gla_glu_bwd.restype = _i
+            L.gla_glu_bwd_workspace_size.argtypes = [_i] * 3
+            L.gla_glu_bwd_workspace_size.restype = sz
             L.gla_pages_copy.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _i, _vp]
             L.gla_pages_copy.restype = _i
             L.gla_pages_fork.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp]

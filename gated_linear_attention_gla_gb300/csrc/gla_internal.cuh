@@ -200,6 +200,91 @@ struct ScanStepArgs {
   unsigned* status;
 };
 
+// The norms, the gate and the residual sum between two blocks (gla_block_norm_*):
+// y, z [rows, D] with row strides, res [rows, D]; the parameters [D] fp32.
+struct NormArgs {
+  const void* res;
+  const void* y;             // or null: s = res
+  const void* z;             // or null
+  long long y_stride, z_stride;
+  const float* post_weight;  // or null: no norm of y
+  const float* post_bias;    // or null
+  const float* scale;        // or null
+  const float* weight;
+  const float* bias;         // or null
+  float eps, inv_d;          // inv_d = 1 / D
+  void* res_out;             // or null; may be res
+  void* out;                 // or null: no norm of s
+  int rows, D;
+  bool layer, fp32_io, fp32_res, fp32_out;
+};
+
+struct NormBwdArgs {
+  NormArgs f;                // the forward's inputs (res_out, out, bias unused)
+  const void* d_out;         // [rows, D] or null: zero
+  const void* d_res_out;     // [rows, D] or null: zero
+  void *d_res, *dy, *dz;     // dy, dz null without y, z
+  // [D] each, or null: not computed
+  float *d_post_weight, *d_post_bias, *d_scale, *d_weight, *d_bias;
+};
+
+// The gated linear recurrence (gla_recur_*): x, f, i, z [rows, D] with row
+// strides; states [B, D] fp32.
+struct RecurArgs {
+  const void *x, *f, *i, *z;  // i and z may be null
+  long long x_stride, f_stride, i_stride, z_stride;
+  const float* decay;         // [D] or null
+  const float* init_state;    // or null
+  void* out;
+  float* final_state;
+  const int32_t* cu_seqlens;
+  int B, T, D;
+  bool unit, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+struct RecurBwdArgs {
+  RecurArgs f;                 // the forward's inputs (out and final_state unused)
+  const void* d_out;           // [rows, D]
+  const float* d_final_state;  // [B, D] or null
+  void *dx, *df, *di, *dz;     // di, dz null without i, z
+  float* d_decay;              // or null without decay
+  float* d_init_state;         // or null
+};
+
+struct RecurStepArgs {
+  const void *x, *f, *i, *z;
+  long long x_stride, f_stride, i_stride, z_stride;
+  const float* decay;
+  float* state;
+  int num_slots;
+  const int32_t* slots;
+  const int32_t* out_slots;
+  void* out;
+  int N, D;
+  bool unit, fp32_io, fp32_out;
+  unsigned* status;
+};
+
+// The gated feed-forward projections (gla_glu_*), bf16: x [rows, D] with
+// x_stride elements between rows, weights [F, D].
+struct GluArgs {
+  const void* x;
+  long long x_stride;
+  const void* w_gate;
+  const void* w_up;
+  void* out;             // [rows, F]
+  int rows, D, F;
+  bool fp32_out;
+  unsigned* status;
+};
+
+struct GluBwdArgs {
+  GluArgs f;             // the forward's inputs (out unused)
+  const void* d_out;     // [rows, F]
+  void *dx, *dw_gate, *dw_up;
+};
+
 // One pool of state pages: page i at base + i * page_bytes.
 struct PagePool {
   void* base;
@@ -258,6 +343,17 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, void* workspace, cudaStream_t str
 size_t scan_bwd_workspace(int B, long long rows, int D, int NS);
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
+constexpr int kNormMaxD = 8192;
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
+size_t norm_bwd_workspace(int rows, int D);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_recur_fwd(const RecurArgs& a, cudaStream_t stream);
+size_t recur_bwd_workspace(int B, long long rows, int D, bool packed);
+cudaError_t launch_recur_bwd(const RecurBwdArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_recur_step(const RecurStepArgs& a, cudaStream_t stream);
+cudaError_t launch_glu_fwd(const GluArgs& a, cudaStream_t stream);
+size_t glu_bwd_workspace(int rows, int D, int F);
+cudaError_t launch_glu_bwd(const GluBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool* pools, int count, int S, const int32_t* src,
                               const int32_t* dst, int32_t* plan, int n, unsigned* status,
                               cudaStream_t stream);

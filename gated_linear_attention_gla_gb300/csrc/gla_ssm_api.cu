@@ -6,55 +6,17 @@
 #include <cstdint>
 
 #include "gla.h"
+#include "gla_checks.h"
 #include "gla_internal.cuh"
 
-namespace {
+using namespace gla::checks;
 
-constexpr long long kMaxElems = 1ll << 40;  // per tensor; keeps index arithmetic exact
-constexpr long long kMaxGrid = 0x7fffffffll;
+namespace {
 
 static_assert(GLA_PAGE_NEW == gla::kPageNew && GLA_MAX_PAGES == gla::kMaxPages,
               "the header states the kernels' constants");
 
-bool aligned(const void* p, uintptr_t bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
-}
-
-// A byte range of a call's arguments.
-struct Range {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.n && y < x + a.n;
-}
-// every output apart from every input and from the other outputs
-template <int I, int O> bool disjoint(const Range (&in)[I], const Range (&out)[O]) {
-  for (int o = 0; o < O; ++o) {
-    for (int i = 0; i < I; ++i)
-      if (overlap(out[o], in[i])) return false;
-    for (int o2 = o + 1; o2 < O; ++o2)
-      if (overlap(out[o], out[o2])) return false;
-  }
-  return true;
-}
-
-// Bytes spanned by `rows` rows of `cols` elements, `stride` elements apart.
-size_t span(long long rows, long long stride, long long cols, long long esz) {
-  return rows > 0 ? (size_t)(((rows - 1) * stride + cols) * esz) : 0;
-}
-
-gla_status finish(cudaError_t e) { return static_cast<gla_status>(gla::cuda_result(e)); }
-
 bool ns_ok(int n) { return n == 8 || n == 16 || n == 32 || n == 64; }
-bool channels_ok(int D) { return D % 8 == 0 && D <= 1 << 24; }
-
-// Rows, channel count and row strides shared by the entry points below.
-// stride rows must hold the columns and keep every row 16-byte aligned.
-bool stride_bad(long long stride, int cols) { return stride < cols || stride > kMaxElems; }
-bool stride_misaligned(long long stride, long long esz) { return stride * esz % 16 != 0; }
 
 }  // namespace
 

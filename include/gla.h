@@ -40,6 +40,13 @@
  *   gla_scan_fwd, gla_scan_bwd, gla_scan_step
  *                    the selective state space scan, whose decay differs for
  *                    every channel, state and token: likewise.
+ *   gla_recur_fwd, gla_recur_bwd, gla_recur_step
+ *                    a gated linear recurrence with one state per channel:
+ *                    prompts, gradients, one token over a pool of states.
+ *   gla_block_norm_fwd, gla_block_norm_bwd
+ *                    between two blocks: norm, gate, residual sum, norm.
+ *   gla_glu_fwd, gla_glu_bwd
+ *                    the gated feed-forward projections and their product.
  *   gla_pages_copy, gla_pages_fork, gla_pages_compact, gla_pages_free
  *                    the pages of state pools, managed on the device.
  *   gla_status_sync, gla_status_string, gla_last_error_string, gla_version,
@@ -96,6 +103,11 @@ typedef enum gla_status {
 #define GLA_FLAG_SILU (1u << 3)        /* gla_conv_*: silu after the convolution */
 #define GLA_FLAG_SOFTPLUS (1u << 4)    /* gla_scan_*: the step size is softplus(dt + dt_bias)
                                           (default dt + dt_bias) */
+#define GLA_FLAG_UNIT_VARIANCE (1u << 5) /* gla_recur_*: the drive's factor is sqrt(1 - a^2)
+                                          (default 1 - a) */
+#define GLA_FLAG_LAYER_NORM (1u << 6)  /* gla_block_norm_*: norms subtract the mean (default RMS) */
+#define GLA_FLAG_FP32_RESIDUAL (1u << 7) /* gla_block_norm_*: the residual rows are fp32 while the
+                                          others stay bf16 */
 
 /*
  * gla_chunk_fwd -- chunked prefill over a batch of sequences.
@@ -508,6 +520,137 @@ gla_status gla_scan_step(const void *u, int64_t u_stride, const void *dt, int64_
                          const float *dt_bias, float *state, int num_slots,
                          const int32_t *slots, const int32_t *out_slots, void *out, int rows,
                          int D, int N, gla_stream_t stream, unsigned flags);
+
+/*
+ * The gated linear recurrence: one state per channel, whose decay comes from a gate of
+ * the token's own.  With s(v) = 1 / (1 + exp(-v)), for every sequence and channel d
+ *     log a = decay[d] s(f[t][d]);  without decay: log s(f[t][d])
+ *     m     = sqrt(1 - a^2) with GLA_FLAG_UNIT_VARIANCE, else 1 - a
+ *     h[t]  = a h[t-1] + m s(i[t][d]) x[t][d]            (without i: m x)
+ *     out   = h[t] z s(z)                                  (without z: h[t])
+ * The pages the library's recurrence comes from have no counterpart; these entry
+ * points stand beside it and the scan for layers without a state matrix.
+ *
+ *   x, f, i, z   [rows, D]: bf16, or fp32 with GLA_FLAG_FP32_IO; row strides as for
+ *                the scan; i and z may be NULL (their strides are then ignored)
+ *   decay        fp32 [D], finite and <= 0 (a value above 0 acts as 0), or NULL.
+ *                Where a rounds to 1, m and its share of the gradients are 0.
+ *   init_state   fp32 [B, D] or NULL (zeros); final_state likewise or NULL (not
+ *                written), may be init_state itself
+ *   out          [rows, D], x's dtype (fp32 with GLA_FLAG_FP32_OUT)
+ *   D            as for the scan; rows dense or packed (cu_seqlens) as for the scan
+ * Nothing of one sequence reaches another, infinities and NaN included.  Inside
+ * a sequence an infinite state stays infinite until the product of the decays
+ * behind it underflows, and is NaN from then on.
+ */
+gla_status gla_recur_fwd(const void *x, int64_t x_stride, const void *f, int64_t f_stride,
+                         const void *i, int64_t i_stride, const void *z, int64_t z_stride,
+                         const float *decay, const float *init_state, void *out,
+                         float *final_state, const int32_t *cu_seqlens, int B, int T, int D,
+                         gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_recur_bwd -- the gradient of gla_recur_fwd, from its inputs alone.  d_out
+ * [rows, D] in x's dtype; d_final_state, d_init_state fp32 [B, D] or NULL; dx, df,
+ * di, dz [rows, D] in x's dtype (fp32 with GLA_FLAG_FP32_OUT), di and dz NULL
+ * exactly without i and z; d_decay fp32 [D] or NULL.  workspace:
+ * gla_recur_bwd_workspace_size(...) bytes, 256-byte aligned.  Sums run in a
+ * fixed order (the same inputs give the same bits).
+ */
+gla_status gla_recur_bwd(const void *x, int64_t x_stride, const void *f, int64_t f_stride,
+                         const void *i, int64_t i_stride, const void *z, int64_t z_stride,
+                         const float *decay, const float *init_state, const void *d_out,
+                         const float *d_final_state, void *dx, void *df, void *di, void *dz,
+                         float *d_decay, float *d_init_state, const int32_t *cu_seqlens, int B,
+                         int T, int D, void *workspace, size_t workspace_bytes,
+                         gla_stream_t stream, unsigned flags);
+size_t gla_recur_bwd_workspace_size(int B, int T, int D, int packed);
+
+/*
+ * gla_recur_step -- one token for each of N sequences: x, f, i, z, out [N, D];
+ * state fp32 [N, D] updated in place, or a pool with slots and out_slots as for
+ * gla_conv_step.
+ */
+gla_status gla_recur_step(const void *x, int64_t x_stride, const void *f, int64_t f_stride,
+                          const void *i, int64_t i_stride, const void *z, int64_t z_stride,
+                          const float *decay, float *state, int num_slots, const int32_t *slots,
+                          const int32_t *out_slots, void *out, int N, int D,
+                          gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_block_norm_fwd -- what stands between two blocks, for every row
+ *     p = norm(y) post_weight + post_bias          (post_weight NULL: p = y)
+ *     s = res + scale p z / (1 + exp(-z))          (scale, z NULL: 1; y NULL: s = res)
+ *     out = norm(s) weight + bias
+ * norm(v) = v / sqrt(mean(v^2) + eps), with GLA_FLAG_LAYER_NORM of v - mean(v).
+ *
+ *   res          [rows, D], contiguous: the residual stream, in y's dtype, or fp32
+ *                with GLA_FLAG_FP32_RESIDUAL
+ *   y            [rows, D] with y_stride, the block's output, bf16 (fp32 with
+ *                GLA_FLAG_FP32_IO, and then everything is), or NULL; z [rows, D]
+ *                with z_stride, y's dtype, or NULL.  Strides as for the scan.
+ *   post_weight, post_bias, scale, weight, bias   fp32 [D], 16-byte aligned;
+ *                each may be NULL (weight exactly without out; the others: left out)
+ *   eps          >= 0
+ *   res_out      [rows, D] in res's dtype: s, or NULL (not written; NULL without
+ *                y).  May be res itself.
+ *   out          [rows, D] in y's dtype (fp32 with GLA_FLAG_FP32_OUT), from the
+ *                unrounded s, or NULL
+ *   D            a multiple of 8, at most 8192
+ * Alignment: every pointer 16 bytes.  Outputs must not overlap anything else.
+ */
+gla_status gla_block_norm_fwd(const void *res, const void *y, int64_t y_stride, const void *z,
+                              int64_t z_stride, const float *post_weight, const float *post_bias,
+                              const float *scale, const float *weight, const float *bias,
+                              float eps, void *res_out, void *out, int rows, int D,
+                              gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_block_norm_bwd -- the gradient of gla_block_norm_fwd, from its inputs alone.
+ * d_out [rows, D] in y's dtype and d_res_out [rows, D] in res's dtype, contiguous,
+ * or NULL (zero; weight is needed exactly with d_out, and d_weight, d_bias only then).
+ * d_res [rows, D] in res's dtype, dy and dz [rows, D] in y's (all fp32 with
+ * GLA_FLAG_FP32_OUT); dy NULL exactly without y, dz without z.  d_post_weight,
+ * d_post_bias, d_scale, d_weight, d_bias fp32 [D], each or NULL (not computed).
+ * workspace: gla_block_norm_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * Sums over rows run in a fixed order.
+ */
+gla_status gla_block_norm_bwd(const void *res, const void *y, int64_t y_stride, const void *z,
+                              int64_t z_stride, const float *post_weight, const float *post_bias,
+                              const float *scale, const float *weight, float eps,
+                              const void *d_out, const void *d_res_out, void *d_res, void *dy,
+                              void *dz, float *d_post_weight, float *d_post_bias, float *d_scale,
+                              float *d_weight, float *d_bias, int rows, int D, void *workspace,
+                              size_t workspace_bytes, gla_stream_t stream, unsigned flags);
+size_t gla_block_norm_bwd_workspace_size(int rows, int D);
+
+/*
+ * gla_glu_fwd -- the gated feed-forward projections: g = x w_gate^T, u = x w_up^T,
+ *     out = g u / (1 + exp(-g))
+ *
+ *   x            [rows, D] bf16 with x_stride (rows start on 16 bytes)
+ *   w_gate, w_up [F, D] bf16, contiguous
+ *   out          [rows, F] bf16 (fp32 with GLA_FLAG_FP32_OUT)
+ *   D, F         multiples of 8, at most 2^20; any number of rows
+ * g and u are fp32 sums that stay on the chip.  fp32 inputs (GLA_FLAG_FP32_IO)
+ * return GLA_ERR_UNSUPPORTED.  Alignment: every pointer 16 bytes.
+ */
+gla_status gla_glu_fwd(const void *x, int64_t x_stride, const void *w_gate, const void *w_up,
+                       void *out, int rows, int D, int F, gla_stream_t stream, unsigned flags);
+
+/*
+ * gla_glu_bwd -- the gradient of gla_glu_fwd, from its inputs alone: with s = 1 / (1 + exp(-g))
+ *     dg = d_out u s (1 + g (1 - s)),  du = d_out g s        (rounded to bf16)
+ *     dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * d_out [rows, F] bf16; dx [rows, D], dw_gate and dw_up [F, D], all bf16 (fp32 with
+ * GLA_FLAG_FP32_OUT, of the same rounded dg and du).  workspace:
+ * gla_glu_bwd_workspace_size(...) bytes, 256-byte aligned (dg and du).
+ */
+gla_status gla_glu_bwd(const void *x, int64_t x_stride, const void *w_gate, const void *w_up,
+                       const void *d_out, void *dx, void *dw_gate, void *dw_up, int rows, int D,
+                       int F, void *workspace, size_t workspace_bytes, gla_stream_t stream,
+                       unsigned flags);
+size_t gla_glu_bwd_workspace_size(int rows, int D, int F);
 
 /*
  * The pages of state pools.  A sequence's state is page i of every pool (one
