@@ -22,7 +22,7 @@ static gla_status norm_args(const void* res, const void* y, int64_t y_stride, co
   if (D % 8 != 0 || D > gla::kNormMaxD) return GLA_ERR_UNSUPPORTED;
   const bool fp32 = (flags & GLA_FLAG_FP32_IO) != 0;
   const long long esz = fp32 ? 4 : 2;
-  if (!y && (z || post_weight || scale)) return GLA_ERR_INVALID_ARG;
+  if (rows > 0 && !y && (z || post_weight || scale)) return GLA_ERR_INVALID_ARG;
   if (!post_weight && post_bias) return GLA_ERR_INVALID_ARG;
   if (D > 0 && ((y && (stride_bad(y_stride, D) || rows * y_stride > kMaxElems)) ||
                 (z && (stride_bad(z_stride, D) || rows * z_stride > kMaxElems))))
@@ -50,9 +50,9 @@ gla_status gla_block_norm_fwd(const void* res, const void* y, int64_t y_stride, 
   const gla_status bad = norm_args(res, y, y_stride, z, z_stride, post_weight, post_bias, scale,
                                    weight, eps, rows, D, flags, &a);
   if (bad != GLA_OK) return bad;
+  if (rows == 0 || D == 0) return GLA_OK;  // (pointers of empty tensors are null)
   if ((!y && res_out) || (out && !weight) || (!out && (weight || bias)))
     return GLA_ERR_INVALID_ARG;
-  if (rows == 0 || D == 0) return GLA_OK;
   if (!res_out && !out) return GLA_ERR_INVALID_ARG;
   if (!aligned(bias, 16) || !aligned(res_out, 16) || !aligned(out, 16)) return GLA_ERR_MISALIGNED;
   const long long esz = a.fp32_io ? 4 : 2, rsz = a.fp32_res ? 4 : 2, osz = a.fp32_out ? 4 : 2;
