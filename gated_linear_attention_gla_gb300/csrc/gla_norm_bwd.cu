@@ -7,9 +7,11 @@
 //     dq = d scale silu(z),  d_post_weight = sum dq p,  d_post_bias = sum dq
 //     dy = r_y (dp - mean(dp) - p mean(dp p)),       dp = dq post_weight
 // One pass: a group of threads owns a row as in the forward (whose values it
-// computes again) and walks over rows; the sums over rows stay with the thread that owns the
+// computes again) and walks over rows.  Of the sums over rows four suffice, A = sum d silu(z) p,
+// B = sum d silu(z), d_weight and d_bias: d_post_weight = scale A, d_post_bias = scale B,
+// d_scale = post_weight A + post_bias B.  They stay with the thread that owns the
 // column (in registers; in shared memory where a thread holds two vectors, whose
-// eighty sums would not fit), are summed over a block's groups and written as one partial a
+// sums would not fit), are summed over a block's groups and written as one partial a
 // block, which a second launch sums in block order.  No atomics: the same inputs
 // give the same bits.
 // Bound: HBM.
@@ -20,13 +22,12 @@ namespace {
 
 using namespace norm;
 
-constexpr int kSums = 5;  // d_post_weight, d_post_bias, d_scale, d_weight, d_bias
-constexpr int kThreads = 256;
+constexpr int kSums = 4;  // A, B, d_weight, d_bias
 
 // The sums of a thread's columns over the rows.
-template <int K, bool SHARED> struct Sums {
-  float v[SHARED ? 1 : kSums][SHARED ? 1 : K][SHARED ? 1 : kV];
-  float* s;  // SHARED: element (i, k, j) at ((i K + k) kV + j) threads + thread
+template <int K> struct Sums {
+  float v[K == 1 ? kSums : 1][K == 1 ? kV : 1];
+  float* s;  // K = 2: element (i, k, j) at ((i K + k) kV + j) threads + thread
   __device__ void init(float* shared) {
     s = shared + threadIdx.x;
 #pragma unroll
@@ -35,121 +36,122 @@ template <int K, bool SHARED> struct Sums {
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-          if constexpr (SHARED) s[((i * K + k) * kV + j) * blockDim.x] = 0.f;
-          else v[i][k][j] = 0.f;
+          if constexpr (K == 1) v[i][j] = 0.f;
+          else s[((i * K + k) * kV + j) * blockDim.x] = 0.f;
         }
   }
   __device__ __forceinline__ void add(int i, int k, int j, float x, float y) {
-    if constexpr (SHARED) {
+    if constexpr (K == 1) {
+      v[i][j] = fmaf(x, y, v[i][j]);
+    } else {
       float& t = s[((i * K + k) * kV + j) * blockDim.x];
       t = fmaf(x, y, t);
-    } else {
-      v[i][k][j] = fmaf(x, y, v[i][k][j]);
     }
   }
   __device__ __forceinline__ float get(int i, int k, int j) const {
-    if constexpr (SHARED) return s[((i * K + k) * kV + j) * blockDim.x];
-    else return v[i][k][j];
+    if constexpr (K == 1) return v[i][j];
+    else return s[((i * K + k) * kV + j) * blockDim.x];
   }
 };
 
-template <typename T, typename RT, typename GT, typename GRT, int K>
-__global__ void __launch_bounds__(K == 1 ? 512 : 512)
-norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr) {
+// BIAS: layer norm's biases (post_bias, d_post_bias, d_bias)
+template <typename T, typename RT, typename GT, typename GRT, int K, bool BIAS>
+__global__ void __launch_bounds__(512, 1)
+norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   start_next();
-  extern __shared__ float shared[];
-  constexpr bool kShared = K > 1;
+  extern __shared__ __align__(16) unsigned char shared[];
   const NormArgs& a = b.f;
-  const Group g(tpr, shared);
-  Sums<K, kShared> sums;
-  sums.init(shared + g.count * kRedFloats);
-  for (long long row = (long long)blockIdx.x * g.count + g.index; row < a.rows;
-       row += (long long)gridDim.x * g.count) {
+  const Group g(tpr, (float*)shared);
+  // pieces of a row: res, ds, y, z, du
+  constexpr int kDs = kPieces<RT>, kY = 2 * kDs, kZ = kY + kPieces<T>, kDu = kZ + kPieces<T>;
+  Ring<K> ring(shared + g.count * kRedFloats * 4, kDu + kPieces<T>, stages);
+  Sums<K> sums;
+  sums.init((float*)(shared + g.count * kRedFloats * 4));  // (K = 2, which has no ring)
+  Param<K> post, post_b, scale, weight;
+  post.init(g, a.D, a.post_weight, 1.f);
+  if (BIAS) post_b.init(g, a.D, a.post_bias, 0.f);
+  scale.init(g, a.D, a.scale, 1.f);
+  weight.init(g, a.D, a.weight, 1.f);
+  const long long hop = (long long)gridDim.x * g.count;
+  auto fetch = [&](long long row, int slot) {
+    if constexpr (K == 1) {
+      const int c = g.column(0);
+      if (row < a.rows && c < a.D) {
+        ring.copy(slot, 0, (const RT*)a.res + row * a.D + c);
+        if (b.d_res_out) ring.copy(slot, kDs, (const RT*)b.d_res_out + row * a.D + c);
+        if (a.y) ring.copy(slot, kY, (const T*)a.y + row * a.y_stride + c);
+        if (a.z) ring.copy(slot, kZ, (const T*)a.z + row * a.z_stride + c);
+        if (b.d_out) ring.copy(slot, kDu, (const T*)b.d_out + row * a.D + c);
+      }
+      cp_commit();
+    }
+  };
+  long long row = (long long)blockIdx.x * g.count + g.index;
+  for (int i = 0; i < stages - 1; ++i) fetch(row + i * hop, i);
+  for (; row < a.rows; row += hop, ring.next()) {
+    fetch(row + (stages - 1) * hop, ring.ahead());
+    ring.wait();
+    const long long at = row * a.D;
+    const T* zr = (const T*)a.z + row * a.z_stride;
     float s[K][kV], p[K][kV];
-    Raw<T, kV> z[K], du[K];
-    Raw<RT, kV> ds[K];
     float ry = 1.f;
-    each<K>(g, a.D, [&](int k, int c) {
-      load_f32<RT>((const RT*)a.res + row * a.D + c, s[k]);
-    }, s);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = g.column(k);
-      z[k] = a.z && c < a.D ? load_raw<T, kV>((const T*)a.z + row * a.z_stride + c)
-                            : zero_raw<T, kV>();
-      du[k] = b.d_out && c < a.D ? load_raw<T, kV>((const T*)b.d_out + row * a.D + c)
-                                 : zero_raw<T, kV>();
-      ds[k] = b.d_res_out && c < a.D ? load_raw<RT, kV>((const RT*)b.d_res_out + row * a.D + c)
-                                     : zero_raw<RT, kV>();
-    }
-    if (a.y) {
-      each<K>(g, a.D, [&](int k, int c) {
-        load_f32<T>((const T*)a.y + row * a.y_stride + c, p[k]);
-      }, p);
-      if (a.post_weight) {
-        ry = normalise<K>(g, a, p);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int j = 0; j < kV; ++j) p[k][j] *= ry;
+      fill(s[k], 0.f);
+      fill(p[k], 0.f);
+      if (g.column(k) < a.D) {
+        ring.read(0, (const RT*)a.res + at + g.column(k), s[k]);
+        if (a.y) ring.read(kY, (const T*)a.y + row * a.y_stride + g.column(k), p[k]);
       }
-    } else {
+    }
+    if (a.post_weight) {
+      ry = normalise<K>(g, a, p);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < kV; ++j) p[k][j] = 0.f;
+        for (int j = 0; j < kV; ++j) p[k][j] *= ry;
     }
-    // q = p post_weight + post_bias, computed twice (again below) rather than held
+    // q = p post_weight + post_bias, formed twice (again below) rather than held
     auto affine = [&](int k, float (&q)[kV]) {
-      const int c = g.column(k);
+      float w[kV], o[kV];
+      post.at(g.column(k), w);
+      if (BIAS) post_b.at(g.column(k), o);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) q[j] = p[k][j];
-      if (a.post_weight) {
-        float w[kV], o[kV] = {};
-        load_vec(a.post_weight + c, w);
-        if (a.post_bias) load_vec(a.post_bias + c, o);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) q[j] = fmaf(q[j], w[j], o[j]);
-      }
+      for (int j = 0; j < kV; ++j) q[j] = BIAS ? fmaf(p[k][j], w[j], o[j]) : p[k][j] * w[j];
     };
-    auto scales = [&](int k, float (&w)[kV]) {
-#pragma unroll
-      for (int j = 0; j < kV; ++j) w[j] = 1.f;
-      if (a.scale) load_vec(a.scale + g.column(k), w);
-    };
-    if (a.y && b.d_out) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (g.column(k) >= a.D) continue;
-        float q[kV], w[kV];
-        affine(k, q);
-        scales(k, w);
-        if (a.z) {
-          float zf[kV];
-          unpack_as<T, kV>(z[k], zf);
-#pragma unroll
-          for (int j = 0; j < kV; ++j) q[j] *= silu(zf[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kV; ++j) s[k][j] = fmaf(w[j], q[j], s[k][j]);
-      }
-    }
     // s becomes d = dL/ds
     if (b.d_out) {
+      if (a.y) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (g.column(k) >= a.D) continue;
+          float q[kV], w[kV];
+          affine(k, q);
+          scale.at(g.column(k), w);
+          if (a.z) {
+            float z[kV];
+            ring.read(kZ, zr + g.column(k), z);
+#pragma unroll
+            for (int j = 0; j < kV; ++j) w[j] *= silu(z[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kV; ++j) s[k][j] = fmaf(w[j], q[j], s[k][j]);
+        }
+      }
       const float r = normalise<K>(g, a, s);
       float2 m = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (g.column(k) >= a.D) continue;
         float d[kV], w[kV];
-        unpack_as<T, kV>(du[k], d);
-        load_vec(a.weight + g.column(k), w);
+        ring.read(kDu, (const T*)b.d_out + at + g.column(k), d);
+        weight.at(g.column(k), w);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           const float n = s[k][j] * r;
           s[k][j] = n;
-          sums.add(3, k, j, d[j], n);
-          sums.add(4, k, j, d[j], 1.f);
+          sums.add(2, k, j, d[j], n);
+          if (BIAS) sums.add(3, k, j, d[j], 1.f);
           const float dn = d[j] * w[j];
           m.x = fmaf(dn, n, m.x);
           m.y += dn;
@@ -162,16 +164,21 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr) {
       for (int k = 0; k < K; ++k) {
         if (g.column(k) >= a.D) continue;
         float d[kV], w[kV], e[kV];
-        unpack_as<T, kV>(du[k], d);
-        unpack_as<RT, kV>(ds[k], e);
-        load_vec(a.weight + g.column(k), w);
+        ring.read(kDu, (const T*)b.d_out + at + g.column(k), d);
+        fill(e, 0.f);
+        if (b.d_res_out) ring.read(kDs, (const RT*)b.d_res_out + at + g.column(k), e);
+        weight.at(g.column(k), w);
 #pragma unroll
         for (int j = 0; j < kV; ++j)
           s[k][j] = fmaf(r, fmaf(-s[k][j], m.x, fmaf(d[j], w[j], -m.y)), e[j]);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) unpack_as<RT, kV>(ds[k], s[k]);
+      for (int k = 0; k < K; ++k) {
+        fill(s[k], 0.f);
+        if (b.d_res_out && g.column(k) < a.D) 
+          ring.read(kDs, (const RT*)b.d_res_out + at + g.column(k), s[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -184,28 +191,31 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr) {
     for (int k = 0; k < K; ++k) {
       const int c = g.column(k);
       if (c >= a.D) continue;
-      float q[kV], w[kV], zf[kV];
-      affine(k, q);
-      scales(k, w);
-      unpack_as<T, kV>(z[k], zf);
-      float dz[kV];
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        const float sig = a.z ? sigmoid(zf[j]) : 1.f;
-        const float gate = a.z ? zf[j] * sig : 1.f;
-        sums.add(2, k, j, s[k][j], q[j] * gate);
-        const float d = s[k][j] * w[j];
-        dz[j] = d * q[j] * fmaf(gate, 1.f - sig, sig);
-        s[k][j] = d * gate;
-      }
-      if (a.z) store_raw<GT, kV>((GT*)b.dz + row * a.D + c, pack_as<GT, kV>(dz));
-      if (a.post_weight) {
-        float pw[kV];
-        load_vec(a.post_weight + c, pw);
+      float w[kV];
+      scale.at(c, w);
+      if (a.z) {
+        float z[kV], q[kV];
+        affine(k, q);
+        ring.read(kZ, zr + c, z);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-          sums.add(0, k, j, s[k][j], p[k][j]);
-          sums.add(1, k, j, s[k][j], 1.f);
+          const float sig = sigmoid(z[j]), gate = z[j] * sig, d = s[k][j] * gate;
+          q[j] *= s[k][j] * w[j] * fmaf(gate, 1.f - sig, sig);  // dz
+          s[k][j] = d;
+        }
+        store_raw<GT, kV>((GT*)b.dz + row * a.D + c, pack_as<GT, kV>(q));
+      }
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        sums.add(0, k, j, s[k][j], p[k][j]);
+        if (BIAS) sums.add(1, k, j, s[k][j], 1.f);
+        s[k][j] *= w[j];
+      }
+      if (a.post_weight) {
+        float pw[kV];
+        post.at(c, pw);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
           s[k][j] *= pw[j];
           m.x = fmaf(s[k][j], p[k][j], m.x);
           m.y += s[k][j];
@@ -226,11 +236,11 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr) {
       if (g.column(k) < a.D)
         store_raw<GT, kV>((GT*)b.dy + row * a.D + g.column(k), pack_as<GT, kV>(s[k]));
   }
+  cp_wait<0>();
   // the groups' sums in group order (one group: the threads' own)
-  float* dst[kSums] = {b.d_post_weight, b.d_post_bias, b.d_scale, b.d_weight, b.d_bias};
 #pragma unroll
   for (int i = 0; i < kSums; ++i) {
-    if (!dst[i]) continue;
+    if (!BIAS && i % 2 == 1) continue;
     float* to = partial + ((long long)blockIdx.x * kSums + i) * a.D;
     if (g.count == 1) {
 #pragma unroll
@@ -238,76 +248,89 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr) {
 #pragma unroll
         for (int j = 0; j < kV; ++j)
           if (g.column(k) + j < a.D) to[g.column(k) + j] = sums.get(i, k, j);
-    } else {  // K = 1
+    } else {  // K = 1; the ring is free
+      float* all = (float*)(shared + g.count * kRedFloats * 4);
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kV; ++j) shared[j * blockDim.x + threadIdx.x] = sums.get(i, 0, j);
+      for (int j = 0; j < kV; ++j) all[j * blockDim.x + threadIdx.x] = sums.get(i, 0, j);
       __syncthreads();
       for (int e = threadIdx.x; e < tpr * kV; e += blockDim.x) {
         const int j = e / tpr, lane = e % tpr;
         float t = 0.f;
-        for (int q = 0; q < g.count; ++q) t += shared[j * blockDim.x + q * tpr + lane];
+        for (int q = 0; q < g.count; ++q) t += all[j * blockDim.x + q * tpr + lane];
         if (lane * kV + j < a.D) to[lane * kV + j] = t;
       }
     }
   }
 }
 
-// Sums the blocks' partials in block order: 32 columns of one sum a block.
+// Sums the blocks' partials in block order, 32 columns of a pair of sums a block: A and B
+// (blockIdx.y 0), or d_weight and d_bias.
 __global__ void __launch_bounds__(1024)
-norm_bwd_sum_kernel(NormBwdArgs b, const float* partial, int blocks) {
+norm_bwd_sum_kernel(NormBwdArgs b, const float* partial, int blocks, int bias) {
   after_previous();
-  __shared__ float part[32][33];
-  float* dst[kSums] = {b.d_post_weight, b.d_post_bias, b.d_scale, b.d_weight, b.d_bias};
-  float* to = dst[0];
-#pragma unroll
-  for (int i = 1; i < kSums; ++i)
-    if (i == (int)blockIdx.y) to = dst[i];
-  if (!to) return;
+  __shared__ float2 part[32][33];
   const int D = b.f.D, c = blockIdx.x * 32 + threadIdx.x;
-  float t = 0.f;
+  float2 t = make_float2(0.f, 0.f);
   if (c < D)
-    for (int k = threadIdx.y; k < blocks; k += 32)
-      t += partial[((long long)k * kSums + blockIdx.y) * D + c];
+    for (int k = threadIdx.y; k < blocks; k += 32) {
+      const float* from = partial + ((long long)k * kSums + 2 * blockIdx.y) * D + c;
+      t.x += from[0];
+      if (bias) t.y += from[D];
+    }
   part[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
-  if (threadIdx.y == 0 && c < D) {
-    for (int k = 1; k < 32; ++k) t += part[k][threadIdx.x];
-    to[c] = t;
+  if (threadIdx.y != 0 || c >= D) return;
+  for (int k = 1; k < 32; ++k) t = add2(t, part[k][threadIdx.x]);
+  if (blockIdx.y == 1) {
+    if (b.d_weight) b.d_weight[c] = t.x;
+    if (b.d_bias) b.d_bias[c] = t.y;
+    return;
   }
+  const float sc = b.f.scale ? b.f.scale[c] : 1.f;
+  const float w = b.f.post_weight ? b.f.post_weight[c] : 1.f;
+  const float o = b.f.post_bias ? b.f.post_bias[c] : 0.f;
+  if (b.d_post_weight) b.d_post_weight[c] = sc * t.x;
+  if (b.d_post_bias) b.d_post_bias[c] = sc * t.y;
+  if (b.d_scale) b.d_scale[c] = fmaf(w, t.x, o * t.y);
 }
 
 // Blocks of the first launch: as many as the GPU holds at once.
 int bwd_blocks(int rows, int D) {
-  const Shape s = bwd_shape(D);
+  const Shape s = shape_of(D);
   const long long need = ((long long)rows + s.groups - 1) / s.groups;
-  const int hold = 152 * (s.tpr * s.groups <= kThreads ? 2 : 1);
+  const int hold = 152 * (s.tpr * s.groups <= 256 ? 2 : 1);
   return (int)(need < hold ? need : hold);
 }
 
 template <typename T, typename RT, typename GT, typename GRT>
 cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
-  const Shape s = bwd_shape(b.f.D);
+  const Shape s = shape_of(b.f.D);
   const int threads = s.tpr * s.groups, blocks = bwd_blocks(b.f.rows, b.f.D);
-  int smem = s.groups * kRedFloats * 4;
-  if (s.groups > 1 && smem < threads * kV * 4) smem = threads * kV * 4;
-  if (s.k > 1) smem += kSums * s.k * kV * threads * 4;
+  const bool bias = b.f.post_bias || b.d_bias;
+  const int pieces = 2 * kPieces<RT> + 3 * kPieces<T>, other = s.groups * kRedFloats * 4;
+  const int stages = s.k == 1 ? ring_stages(pieces, threads, other, threads <= 256 ? 2 : 1) : 1;
+  int room = s.k == 1 ? stages * pieces * 16 * threads : kSums * s.k * kV * threads * 4;
+  if (room < threads * kV * 4) room = threads * kV * 4;  // the groups' sums at the end
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
-    cudaError_t e = allow_shared(kernel, smem, done);
+    const cudaError_t e = allow_shared(kernel, 227 * 1024, done);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, threads, smem, stream>>>(b, partial, s.tpr);
+    kernel<<<blocks, threads, other + room, stream>>>(b, partial, s.tpr, stages);
     return cudaGetLastError();
   };
   if (blocks > 0) {
-    static std::atomic<uint64_t> done1{0}, done2{0};
-    const cudaError_t e = s.k == 1 ? go(norm_bwd_kernel<T, RT, GT, GRT, 1>, done1)
-                                   : go(norm_bwd_kernel<T, RT, GT, GRT, 2>, done2);
+    static std::atomic<uint64_t> d0{0}, d1{0}, d2{0}, d3{0};
+    const cudaError_t e =
+        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, true>, d0)
+                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, false>, d1))
+                 : (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 2, true>, d2)
+                         : go(norm_bwd_kernel<T, RT, GT, GRT, 2, false>, d3));
     if (e != cudaSuccess) return e;
   }
   if (!b.d_post_weight && !b.d_post_bias && !b.d_scale && !b.d_weight && !b.d_bias)
     return cudaSuccess;
-  return launch_after(norm_bwd_sum_kernel, dim3((b.f.D + 31) / 32, kSums), dim3(32, 32), 0, stream,
-                      b, (const float*)partial, blocks);
+  return launch_after(norm_bwd_sum_kernel, dim3((b.f.D + 31) / 32, 2), dim3(32, 32), 0, stream, b,
+                      (const float*)partial, blocks, (int)bias);
 }
 
 }  // namespace

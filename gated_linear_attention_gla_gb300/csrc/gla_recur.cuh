@@ -19,67 +19,78 @@ namespace gla {
 namespace recur {
 
 constexpr int kChans = 64;     // channels of a block: two a lane
-constexpr int kMaxWarps = 16;  // runs of a block
+constexpr int kMaxWarps = 15;  // runs of a block
 constexpr int kMaxCluster = 8;
 
 // ---------------------------------------------------------------- the gates
 // A token's values for a pair of channels.
 struct Gate {
   f32x2 sf, nf;  // sigmoid(f), 1 - sigmoid(f)
-  f32x2 si, ni;  // sigmoid(i), 1 - sigmoid(i)  (1, 0 without i)
+  f32x2 si, ni;  // sigmoid(i), 1 - sigmoid(i)  (with i only)
   f32x2 l;       // log2 of the decay (with `decay` only)
   f32x2 a, m;    // decay, factor of the drive
   f32x2 k;       // -dm / d(log a)
 };
 
-// e / (1 + e) and 1 / (1 + e), whichever is which for the sign of v
-__device__ __forceinline__ f32x2 pick(f32x2 v, f32x2 x, f32x2 y) {
-  return make_float2(v.x < 0.f ? y.x : x.x, v.y < 0.f ? y.y : x.y);
+// Sigmoids of a pair and, where `n` is asked for, 1 - sigmoid without cancellation.
+// Four special-function instructions a pair: one reciprocal of the product of several
+// denominators saves two of them but costs ten others, and it is issue slots
+// that bound these kernels (8192 x 2048 with three gates 68 -> 37 us together with
+// the square root below and the cheaper maps).
+// 1 - s = e s with e = exp(-v); where e is infinite s is 0 and the product NaN,
+// which the minimum turns into 1 (a NaN of v stays one in s, and n only ever
+// multiplies values that s is in).
+// EXACT (fp32 rows): from e = exp(-|v|) with its argument's rounding taken back.
+template <bool EXACT>
+__device__ __forceinline__ void sigmoids(f32x2 v, f32x2* s, f32x2* n) {
+  if (EXACT) {
+    const f32x2 e = exp_neg_abs2<true>(v), d = add2(e, both(1.f));
+    const f32x2 q = make_float2(rcp(d.x), rcp(d.y)), p = mul2(e, q);
+    *s = make_float2(v.x < 0.f ? p.x : q.x, v.y < 0.f ? p.y : q.y);
+    if (n) *n = make_float2(v.x < 0.f ? q.x : p.x, v.y < 0.f ? q.y : p.y);
+  } else {
+    const f32x2 e = ex2x2(mul2(v, both(-kLog2e))), d = add2(e, both(1.f));
+    *s = make_float2(rcp(d.x), rcp(d.y));
+    if (n) {
+      const f32x2 p = mul2(e, *s);
+      *n = make_float2(fminf(p.x, 1.f), fminf(p.y, 1.f));
+    }
+  }
 }
 
-// Sigmoids of a pair (or of two pairs) from e = exp(-|v|) <= 1: the denominators
-// lie in [1, 2], so one reciprocal of their product serves all of them (the special-function unit
-// is as busy as HBM here: it does a quarter of an instruction's lanes a clock).
-template <bool EXACT>
-__device__ __forceinline__ void sigmoids2(f32x2 v, f32x2* s, f32x2* n) {
-  const f32x2 e = exp_neg_abs2<EXACT>(v), d = add2(e, both(1.f));
-  const float r = rcp(d.x * d.y);
-  const f32x2 q = make_float2(r * d.y, r * d.x), p = mul2(e, q);
-  *s = pick(v, q, p);
-  *n = pick(v, p, q);
-}
-template <bool EXACT>
-__device__ __forceinline__ void sigmoids4(f32x2 v, f32x2 w, f32x2* s, f32x2* n, f32x2* t,
-                                          f32x2* o) {
-  const f32x2 e = exp_neg_abs2<EXACT>(v), g = exp_neg_abs2<EXACT>(w);
-  const f32x2 d = add2(e, both(1.f)), c = add2(g, both(1.f)), dc = mul2(d, c);
-  const float r = rcp(dc.x * dc.y);
-  const f32x2 rr = make_float2(r * dc.y, r * dc.x);  // 1 / dc
-  const f32x2 q = mul2(rr, c), u = mul2(rr, d), p = mul2(e, q), x = mul2(g, u);
-  *s = pick(v, q, p);
-  *n = pick(v, p, q);
-  *t = pick(w, u, x);
-  *o = pick(w, x, u);
-}
-
-// 2^l - 1 and 2^l of l in [-126, 0] without the special-function unit and without
-// cancellation near l = 0: l = k + r with |r| <= 1/2, 2^r - 1 by its Taylor
-// polynomial (degree 7: off by 5e-9), 2^k in the exponent.  1 - a^2 = -(a - 1)(2 + (a - 1))
+// 2^l and 1 - 2^l of l in [-126, 0] without the special-function unit and without
+// cancellation near l = 0: l = k + r with |r| <= 1/2, (2^r - 1) / r by a
+// polynomial of degree 5 (least maximal relative error there, by exchange of its
+// extrema: 1.1e-8), 2^k in the exponent.  1 - a^2 = (1 - a)(2 - (1 - a))
 // then keeps its relative accuracy for decays of 0.9999.
 __device__ __forceinline__ void exp2m1(f32x2 l, f32x2* a, f32x2* u) {
   const f32x2 t = add2(l, both(12582912.f));  // its low bits: k
   const f32x2 r = fma2(add2(t, both(-12582912.f)), both(-1.f), l);
-  f32x2 p = fma2(both(1.5252734e-5f), r, both(1.5403530e-4f));
-  p = fma2(p, r, both(1.3333558e-3f));
-  p = fma2(p, r, both(9.6181291e-3f));
-  p = fma2(p, r, both(5.5504109e-2f));
-  p = fma2(p, r, both(0.24022651f));
-  p = fma2(p, r, both(kLn2));
+  f32x2 p = fma2(both(1.54035122e-4f), r, both(1.33907353e-3f));
+  p = fma2(p, r, both(9.61823761e-3f));
+  p = fma2(p, r, both(5.55035733e-2f));
+  p = fma2(p, r, both(0.240226492f));
+  p = fma2(p, r, both(0.693147182f));
   p = mul2(p, r);
   const f32x2 s = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
                               __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
-  *a = fma2(s, p, s);
-  *u = fma2(s, p, add2(s, both(-1.f)));
+  const f32x2 q = mul2(s, p);
+  *a = add2(s, q);
+  *u = fma2(q, both(-1.f), fma2(s, both(-1.f), both(1.f)));
+}
+
+// The same for l in [-2, 0] (kNear) without taking k apart: a polynomial of degree 6 over
+// that range, off by 2.2e-8 of 2^l - 1.  A third of the instructions.
+constexpr float kNear = -2.f;
+__device__ __forceinline__ void exp2m1_near(f32x2 l, f32x2* a, f32x2* u) {
+  f32x2 p = fma2(both(-8.35481114e-6f), l, both(-1.36740666e-4f));
+  p = fma2(p, l, both(-1.3104945e-3f));
+  p = fma2(p, l, both(-9.60214809e-3f));
+  p = fma2(p, l, both(-5.54986782e-2f));
+  p = fma2(p, l, both(-0.240225807f));
+  p = fma2(p, l, both(-0.693147182f));
+  *u = mul2(p, l);
+  *a = fma2(*u, both(-1.f), both(1.f));
 }
 
 __device__ __forceinline__ float rsqrt_or_0(float v) {  // 0 where v is 0
@@ -87,35 +98,47 @@ __device__ __forceinline__ float rsqrt_or_0(float v) {  // 0 where v is 0
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return v < 1e-37f ? 0.f : r;
 }
+__device__ __forceinline__ float sqrt_of(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {  // a NaN stays one
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
 
-// `c`: decay log2(e) of the pair (DECAY)
-template <bool EXACT, bool DECAY, bool BWD>
-__device__ __forceinline__ Gate gates(f32x2 f, f32x2 i, f32x2 c, bool has_i, bool unit) {
+// `c`: decay log2(e) of the pair (DECAY); NEAR: it is at least kNear
+template <bool EXACT, bool DECAY, bool GATE, bool BWD, bool NEAR>
+__device__ __forceinline__ Gate gates(f32x2 f, f32x2 i, f32x2 c, bool unit) {
   Gate g;
-  if (has_i) {
-    sigmoids4<EXACT>(f, i, &g.sf, &g.nf, &g.si, &g.ni);
-  } else {
-    sigmoids2<EXACT>(f, &g.sf, &g.nf);
-    g.si = both(1.f);
-    g.ni = both(0.f);
-  }
-  f32x2 u;  // a - 1
+  sigmoids<EXACT>(f, &g.sf, BWD || !DECAY ? &g.nf : nullptr);
+  if (GATE) sigmoids<EXACT>(i, &g.si, BWD ? &g.ni : nullptr);
+  f32x2 u;  // 1 - a
   if (DECAY) {
     g.l = mul2(c, g.sf);
-    g.l = make_float2(g.l.x < -126.f ? -126.f : g.l.x, g.l.y < -126.f ? -126.f : g.l.y);
-    exp2m1(g.l, &g.a, &u);
+    if (NEAR) {
+      exp2m1_near(g.l, &g.a, &u);
+    } else {
+      g.l = make_float2(max_nan(g.l.x, -126.f), max_nan(g.l.y, -126.f));
+      exp2m1(g.l, &g.a, &u);
+    }
   } else {
     g.a = g.sf;
-    u = mul2(g.nf, both(-1.f));
+    u = g.nf;
   }
-  if (unit) {
-    const f32x2 v = mul2(mul2(u, both(-1.f)), add2(u, both(2.f)));
+  // 1 - a^2 = u (2 - u).  Both factors are computed: a branch would part the tokens of a
+  // run, whose latencies hide one another.
+  if (BWD) {
+    const f32x2 v = mul2(u, fma2(u, both(-1.f), both(2.f)));
     const f32x2 rs = make_float2(rsqrt_or_0(v.x), rsqrt_or_0(v.y));
-    g.m = mul2(v, rs);
-    if (BWD) g.k = mul2(mul2(g.a, g.a), rs);
+    const f32x2 m = mul2(v, rs), k = mul2(mul2(g.a, g.a), rs);
+    g.m = make_float2(unit ? m.x : u.x, unit ? m.y : u.y);
+    g.k = make_float2(unit ? k.x : g.a.x, unit ? k.y : g.a.y);
   } else {
-    g.m = mul2(u, both(-1.f));
-    if (BWD) g.k = g.a;
+    const f32x2 v = mul2(u, fma2(u, both(-1.f), both(2.f)));
+    g.m = make_float2(unit ? sqrt_of(v.x) : u.x, unit ? sqrt_of(v.y) : u.y);
   }
   return g;
 }
@@ -134,19 +157,42 @@ __device__ __forceinline__ f32x2 pair_at<__nv_bfloat16>(const __nv_bfloat16* row
   return widen(reinterpret_cast<const uint32_t*>(row)[lane]);
 }
 
-// Asynchronous copy of n <= L rows of a block's channels, by one warp.
-template <typename T, int L>
-__device__ __forceinline__ void copy_rows(T* dst, const void* src, long long stride,
-                                          long long row, int n, int c0, int D, int lane) {
-  constexpr int E = 16 / (int)sizeof(T), PER = kChans / E, ROWS = 32 / PER;
-  const int at = lane % PER * E;
-#pragma unroll
-  for (int k = 0; k < L; k += ROWS) {
-    const int t = k + lane / PER;
-    if (t < n && c0 + at < D)
-      cp_async16(dst + t * kChans + at, (const T*)src + (row + t) * stride + c0 + at);
+// A warp's asynchronous copies of runs of L rows of one stream: the lane's place in the
+// first row, moved on from run to run (address arithmetic is a sixth of the work
+// otherwise).
+template <typename T, int L> struct Stream {
+  static constexpr int kE = 16 / (int)sizeof(T), kPer = kChans / kE, kRows = 32 / kPer;
+  const T* at;
+  long long hop;   // elements between the lane's rows
+  long long step;  // elements between the warp's runs
+  int place;       // the lane's element of the tile
+  bool on;         // the lane's channels exist
+  __device__ __forceinline__ void init(const void* src, long long stride, long long row,
+                                       long long rows_step, int c0, int D, int lane) {
+    const int c = lane % kPer * kE;
+    on = c0 + c < D;
+    at = (const T*)src + (row + lane / kPer) * stride + c0 + c;
+    hop = stride * kRows;
+    step = stride * rows_step;
+    place = lane / kPer * kChans + c;
   }
-}
+  // Rows [FROM, TO) of n at the current place.
+  template <int FROM = 0, int TO = L>
+  __device__ __forceinline__ void copy(T* tile, int n, int lane) const {
+    static_assert(FROM % kRows == 0 && TO % kRows == 0, "whole groups of rows");
+    const T* p = at + FROM / kRows * hop;
+    if (!on) return;
+    if (n >= TO) {
+#pragma unroll
+      for (int k = FROM; k < TO; k += kRows, p += hop) cp_async16(tile + place + k * kChans, p);
+    } else {
+#pragma unroll
+      for (int k = FROM; k < TO; k += kRows, p += hop)
+        if (k + lane / kPer < n) cp_async16(tile + place + k * kChans, p);
+    }
+  }
+  __device__ __forceinline__ void next() { at += step; }
+};
 
 template <typename OT>
 __device__ __forceinline__ void store_pair(OT* p, f32x2 v) {
@@ -155,75 +201,146 @@ __device__ __forceinline__ void store_pair(OT* p, f32x2 v) {
 }
 
 // ---------------------------------------------------------------- composition
-// A run's map of a lane's two channels; P < 0: it starts anew (a sequence begins inside),
-// so that nothing in front of it is multiplied, infinities included.
-__device__ __forceinline__ f32x2 apply(float4 map, f32x2 h) {
-  return make_float2(map.x < 0.f ? map.z : fmaf(map.x, h.x, map.z),
-                     map.y < 0.f ? map.w : fmaf(map.y, h.y, map.w));
+// A run's map of a lane's two channels (P, P, H, H).  STARTS: sequences may begin inside;
+// P < 0 says that one does, so that nothing in front of it is multiplied,
+// infinities included.
+template <bool STARTS> __device__ __forceinline__ f32x2 apply(float4 map, f32x2 h) {
+  const f32x2 v = fma2(make_float2(map.x, map.y), h, make_float2(map.z, map.w));
+  if (!STARTS) return v;
+  return make_float2(map.x < 0.f ? map.z : v.x, map.x < 0.f ? map.w : v.y);
 }
 // `next` after `map`
-__device__ __forceinline__ float4 compose(float4 map, float4 next) {
-  float4 r;
-  r.x = next.x < 0.f || map.x < 0.f ? -1.f : map.x * next.x;
-  r.y = next.y < 0.f || map.y < 0.f ? -1.f : map.y * next.y;
-  r.z = next.x < 0.f ? next.z : fmaf(next.x, map.z, next.z);
-  r.w = next.y < 0.f ? next.w : fmaf(next.y, map.w, next.w);
-  return r;
+template <bool STARTS> __device__ __forceinline__ float4 compose(float4 map, float4 next) {
+  f32x2 p = mul2(make_float2(map.x, map.y), make_float2(next.x, next.y));
+  const f32x2 h = apply<STARTS>(next, make_float2(map.z, map.w));
+  if (STARTS && (next.x < 0.f || map.x < 0.f)) p = both(-1.f);
+  return make_float4(p.x, p.y, h.x, h.y);
 }
 
-__device__ __forceinline__ void store_remote(const void* local, uint32_t rank, float4 v) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;"
-      : "=r"(at)
-      : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(local))), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
+// What a block's warps exchange, for two steps in turn: their maps, the maps of the
+// cluster's blocks, and the state in front of each warp's run.  The block has a warp
+// for the exchange beside the `warps` that compute: those hand a run's map over and
+// work on their next run before they need the state in front of the one before, so that the
+// latency of the exchange (a microsecond across a cluster) is not theirs.
+struct Maps {
+  float4 warp[2][kMaxWarps][32];
+  float4 block[2][kMaxCluster][32];
+  f32x2 front[2][kMaxWarps][32];
+  uint64_t given[2];  // the warps' maps of a step are there
+  uint64_t full[2];   // counts the bytes of block[turn]
+  uint64_t ready[2];  // front[turn] is there
+};
+
+__device__ __forceinline__ uint32_t shared_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-
-// The maps of one step: of the block's warps and of the cluster's blocks, two
-// buffers in turn (a block writes one again only after the barrier behind the
-// step in which everyone has read it).
-struct Maps {
-  float4 warp[2][kMaxWarps][32];
-  float4 block[2][kMaxCluster][32];
-};
-
-// One exchange: `mine` is the warp's map (warp `w` of `warps`, block `rank` of
-// `cluster`); returns the state in front of the warp's run and moves *state, the one in front of the
-// step, behind it.  Every thread of the cluster calls it.
-__device__ __forceinline__ f32x2 exchange(Maps& s, int turn, float4 mine, int w, int warps,
-                                          int rank, int cluster, int lane, f32x2* state) {
-  s.warp[turn][w][lane] = mine;
-  __syncthreads();
-  f32x2 h = *state;
-  if (cluster == 1) {
-    f32x2 front = h;
-    for (int k = 0; k < warps; ++k) {
-      if (k == w) front = h;
-      h = apply(s.warp[turn][k][lane], h);
+__device__ __forceinline__ void arrive(const uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(shared_at(bar)) : "memory");
+}
+// Before the first step; every thread of the cluster calls it.
+__device__ __forceinline__ void maps_init(Maps& s, int warps, int cluster) {
+  if (threadIdx.x == 0) {
+    auto init = [](const uint64_t* bar, int count) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(count)
+                   : "memory");
+    };
+    for (int i = 0; i < 2; ++i) {
+      init(&s.given[i], warps);
+      init(&s.full[i], 1);
+      init(&s.ready[i], 1);
     }
-    *state = h;
-    return front;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (w == 0) {
-    float4 all = s.warp[turn][0][lane];
-    for (int k = 1; k < warps; ++k) all = compose(all, s.warp[turn][k][lane]);
-    for (int k = 0; k < cluster; ++k) store_remote(&s.block[turn][rank][lane], k, all);
+  if (cluster > 1) cluster_sync();
+  else __syncthreads();
+}
+// 16 bytes into block `rank`'s copy of a variable, counted on its barrier.
+__device__ __forceinline__ void send(const void* to, const uint64_t* bar, uint32_t rank, float4 v) {
+  uint32_t at, b;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_at(to)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(shared_at(bar)), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+      "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+      "r"(__float_as_uint(v.w)), "r"(b)
+      : "memory");
+}
+// Waits for a phase of a barrier, for a bounded number of tests (each may hold the
+// warp for a time the hardware defines; a peer's bytes come within microseconds).
+// Then the status word says so and the call's results are undefined.  (Counted,
+// because reading the time in the loop slowed it.)
+__device__ __forceinline__ void await(const uint64_t* bar, uint32_t parity, unsigned* status) {
+  for (uint32_t i = 0; i < 1u << 24; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(shared_at(bar)), "r"(parity)
+        : "memory");
+    if (done) return;
   }
-  cluster_sync();
-  f32x2 front = h;
-  for (int k = 0; k < cluster; ++k) {
-    if (k == rank) front = h;
-    h = apply(s.block[turn][k][lane], h);
+  atomicOr(status, kDevTimeout);
+}
+
+// A computing warp's map of step `step`.
+__device__ __forceinline__ void give(Maps& s, int step, int w, int lane, float4 mine) {
+  s.warp[step & 1][w][lane] = mine;
+  __syncwarp();
+  if (lane == 0) arrive(&s.given[step & 1]);
+}
+// The state in front of its run of that step.
+__device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane, unsigned* status) {
+  await(&s.ready[step & 1], (step >> 1) & 1, status);
+  return s.front[step & 1][w][lane];
+}
+
+// The exchange warp of block `rank` of `cluster`: `steps` exchanges from the state in front of
+// the first one; returns the one behind the last.
+//
+// Every block sends its map to all blocks of the cluster, where the bytes' arrival
+// completes a barrier: no cluster barrier and no fence.  Buffers are written again
+// safely: a warp gives step k + 2 after it took step k; a front of step k + 2
+// is written after all gave k + 2; and a block sends step k + 2 after it has received all of
+// k + 1, which every block sends after it has read all of step k.
+template <bool STARTS>
+__device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, int rank,
+                                          int cluster, int lane, f32x2 state, unsigned* status) {
+  for (long long step = 0; step < steps; ++step) {
+    const int turn = (int)step & 1;
+    const uint32_t parity = (uint32_t)(step >> 1) & 1;
+    if (cluster > 1 && lane == 0)
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                       shared_at(&s.full[turn])),
+                   "r"(cluster * 512)
+                   : "memory");
+    await(&s.given[turn], parity, status);
+    f32x2 front = state;
+    if (cluster > 1) {
+      float4 all = s.warp[turn][0][lane];
+      for (int k = 1; k < warps; ++k) all = compose<STARTS>(all, s.warp[turn][k][lane]);
+      for (int k = 0; k < cluster; ++k)
+        send(&s.block[turn][rank][lane], &s.full[turn], (rank + k) % cluster, all);
+      await(&s.full[turn], parity, status);
+      for (int k = 0; k < cluster; ++k) {
+        if (k == rank) front = state;
+        state = apply<STARTS>(s.block[turn][k][lane], state);
+      }
+    }
+    for (int k = 0; k < warps; ++k) {
+      s.front[turn][k][lane] = front;
+      front = apply<STARTS>(s.warp[turn][k][lane], front);
+    }
+    if (cluster == 1) state = front;
+    __syncwarp();
+    if (lane == 0) arrive(&s.ready[turn]);
   }
-  for (int k = 0; k < w; ++k) front = apply(s.warp[turn][k][lane], front);
-  *state = h;
-  return front;
+  return state;
 }
 
 // ---------------------------------------------------------------- the split
@@ -266,12 +383,22 @@ struct Seqs {
 };
 
 constexpr int kKeep = 4;  // tokens between two states kept for the backward pass
+constexpr int kBwdWarps = 15, kBwdBlocks = 1;  // that compute in the backward kernel's blocks
 
-// How a call of these sizes is split; `run`: tokens of a run, `most`: warps of a block.
-Split split(int B, int T, int D, bool packed, int run, int most);
-// The state in front of every kKeep rows of every group: kept [groups][kept_rows][D].
-cudaError_t launch_keep(const RecurArgs& a, const Split& p, float* kept, long long kept_rows,
-                        cudaStream_t stream);
+// How a call of these sizes is split; `run`: tokens of a run, `most`: warps of a block,
+// `blocks`: blocks an SM holds.
+Split split(int B, int T, int D, bool packed, int run, int most, int blocks);
+
+// The launchers, by the rows' type: prompts; the state in front of every kKeep rows of
+// every group, kept [groups][kept_rows][D]; gradients.
+cudaError_t fwd_bf16(const RecurArgs& a, cudaStream_t stream);
+cudaError_t fwd_f32(const RecurArgs& a, cudaStream_t stream);
+cudaError_t keep_bf16(const RecurArgs& a, float* kept, long long kept_rows, cudaStream_t stream);
+cudaError_t keep_f32(const RecurArgs& a, float* kept, long long kept_rows, cudaStream_t stream);
+cudaError_t bwd_bf16(const RecurBwdArgs& b, const Split& p, const float* kept,
+                     long long kept_rows, float* partial, cudaStream_t stream);
+cudaError_t bwd_f32(const RecurBwdArgs& b, const Split& p, const float* kept,
+                    long long kept_rows, float* partial, cudaStream_t stream);
 
 }  // namespace recur
 }  // namespace gla
