@@ -10,9 +10,10 @@
 // registers, so nothing cancels.
 //
 // A group of threads owns a row, eight adjacent channels a thread and vector, and walks
-// over rows with its parameters in registers and the next two rows on their way into
-// shared memory; the sums over the row are shuffles and one exchange through shared
-// memory.  Bound: HBM.
+// over rows, two at a time where there are many, with its parameters in registers and
+// the next rows on their way into shared memory; the sums over the rows are shuffles
+// and one exchange through shared memory.
+// Bound: HBM and issue slots.
 #include "gla_norm.cuh"
 
 namespace gla {
@@ -20,83 +21,104 @@ namespace {
 
 using namespace norm;
 
-template <typename T, typename RT, typename OT, int K>
+// R: rows at a time; BIAS: with post_bias or bias
+template <typename T, typename RT, typename OT, int K, int R, bool BIAS>
 __global__ void __launch_bounds__(512, 1)
 norm_fwd_kernel(NormArgs a, int tpr, int stages) {
   extern __shared__ __align__(16) unsigned char shared[];
   const Group g(tpr, (float*)shared);
   constexpr int kY = kPieces<RT>, kZ = kY + kPieces<T>;  // pieces behind res
-  Ring<K> ring(shared + g.count * kRedFloats * 4, kZ + kPieces<T>, stages);
+  Ring<K> ring(shared + g.count * kRedFloats * 4, R, kZ + kPieces<T>, stages);
   Param<K> post, post_b, scale, weight, bias;
   post.init(g, a.D, a.post_weight, 1.f);
-  post_b.init(g, a.D, a.post_bias, 0.f);
   scale.init(g, a.D, a.scale, 1.f);
   weight.init(g, a.D, a.weight, 1.f);
-  bias.init(g, a.D, a.bias, 0.f);
-  const long long hop = (long long)gridDim.x * g.count;
+  if (BIAS) {
+    post_b.init(g, a.D, a.post_bias, 0.f);
+    bias.init(g, a.D, a.bias, 0.f);
+  }
+  const long long hop = (long long)gridDim.x * g.count * R;
   auto fetch = [&](long long row, int slot) {
     if constexpr (K == 1) {
       const int c = g.column(0);
-      if (row < a.rows && c < a.D) {
-        ring.copy(slot, 0, (const RT*)a.res + row * a.D + c);
-        if (a.y) ring.copy(slot, kY, (const T*)a.y + row * a.y_stride + c);
-        if (a.z) ring.copy(slot, kZ, (const T*)a.z + row * a.z_stride + c);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (row + i < a.rows && c < a.D) {
+          ring.copy(slot, i, 0, (const RT*)a.res + (row + i) * a.D + c);
+          if (a.y) ring.copy(slot, i, kY, (const T*)a.y + (row + i) * a.y_stride + c);
+          if (a.z) ring.copy(slot, i, kZ, (const T*)a.z + (row + i) * a.z_stride + c);
+        }
       }
       cp_commit();
     }
   };
-  long long row = (long long)blockIdx.x * g.count + g.index;
+  long long row = ((long long)blockIdx.x * g.count + g.index) * R;
   for (int i = 0; i < stages - 1; ++i) fetch(row + i * hop, i);
   for (; row < a.rows; row += hop, ring.next()) {
     fetch(row + (stages - 1) * hop, ring.ahead());
     ring.wait();
-    const RT* res = (const RT*)a.res + row * a.D;
-    float s[K][kV];
+    Vec s[R][K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (g.column(k) < a.D) ring.read(0, res + g.column(k), s[k]);
-      else fill(s[k], 0.f);
-    }
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        s[i][k] = g.column(k) < a.D && row + i < a.rows
+                      ? ring.read(i, 0, (const RT*)a.res + (row + i) * a.D + g.column(k))
+                      : vec_of(0.f);
     if (a.y) {
-      const T* yr = (const T*)a.y + row * a.y_stride;
-      float y[K][kV];
+      Vec y[R][K];
+      float r[R];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (g.column(k) < a.D) ring.read(kY, yr + g.column(k), y[k]);
-        else fill(y[k], 0.f);
+      for (int i = 0; i < R; ++i) {
+        r[i] = 1.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          y[i][k] = g.column(k) < a.D && row + i < a.rows
+                        ? ring.read(i, kY, (const T*)a.y + (row + i) * a.y_stride + g.column(k))
+                        : vec_of(0.f);
       }
-      const float r = a.post_weight ? normalise<K>(g, a, y) : 1.f;
+      if (a.post_weight) normalise<K, R>(g, a, y, r);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = g.column(k);
-        if (c >= a.D) continue;
-        float w[kV], b[kV], sc[kV];
-        post.at(c, w);
-        post_b.at(c, b);
-        scale.at(c, sc);
-        if (a.z) {
-          float z[kV];
-          ring.read(kZ, (const T*)a.z + row * a.z_stride + c, z);
+      for (int i = 0; i < R; ++i) {
 #pragma unroll
-          for (int j = 0; j < kV; ++j) sc[j] *= silu(z[j]);
+        for (int k = 0; k < K; ++k) {
+          const int c = g.column(k);
+          if (c >= a.D || row + i >= a.rows) continue;
+          const Vec w = post.at(c), o = BIAS ? post_b.at(c) : w;
+          Vec sc = scale.at(c);
+          if (a.z) {
+            const Vec z = ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + c);
+#pragma unroll
+            GLA_PAIRS sc.v[j] = mul2(sc.v[j], mul2(z.v[j], sigmoid2(z.v[j])));
+          }
+#pragma unroll
+          GLA_PAIRS {
+            const f32x2 n = mul2(y[i][k].v[j], both(r[i]));
+            const f32x2 p = BIAS ? fma2(n, w.v[j], o.v[j]) : mul2(n, w.v[j]);
+            s[i][k].v[j] = fma2(sc.v[j], p, s[i][k].v[j]);
+          }
+          if (a.res_out) store_vec((RT*)a.res_out + (row + i) * a.D + c, s[i][k]);
         }
-#pragma unroll
-        for (int j = 0; j < kV; ++j) s[k][j] = fmaf(sc[j], fmaf(y[k][j] * r, w[j], b[j]), s[k][j]);
-        if (a.res_out) store_raw<RT, kV>((RT*)a.res_out + row * a.D + c, pack_as<RT, kV>(s[k]));
       }
     }
     if (a.out) {
-      const float r = normalise<K>(g, a, s);
+      float r[R];
+      normalise<K, R>(g, a, s, r);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = g.column(k);
-        if (c >= a.D) continue;
-        float w[kV], b[kV];
-        weight.at(c, w);
-        bias.at(c, b);
+      for (int i = 0; i < R; ++i) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) w[j] = fmaf(s[k][j] * r, w[j], b[j]);
-        store_raw<OT, kV>((OT*)a.out + row * a.D + c, pack_as<OT, kV>(w));
+        for (int k = 0; k < K; ++k) {
+          const int c = g.column(k);
+          if (c >= a.D || row + i >= a.rows) continue;
+          const Vec w = weight.at(c), o = BIAS ? bias.at(c) : w;
+          Vec u;
+#pragma unroll
+          GLA_PAIRS {
+            const f32x2 n = mul2(s[i][k].v[j], both(r[i]));
+            u.v[j] = BIAS ? fma2(n, w.v[j], o.v[j]) : mul2(n, w.v[j]);
+          }
+          store_vec((OT*)a.out + (row + i) * a.D + c, u);
+        }
       }
     }
   }
@@ -108,18 +130,29 @@ cudaError_t run_fwd(const NormArgs& a, cudaStream_t stream) {
   const Shape s = shape_of(a.D);
   const int threads = s.tpr * s.groups;
   const int blocks = threads <= 256 ? 2 : 1;  // an SM
-  const int pieces = kPieces<RT> + 2 * kPieces<T>, other = s.groups * kRedFloats * 4;
-  const int stages = s.k == 1 ? ring_stages(pieces, threads, other, blocks) : 1;
-  const int smem = other + (s.k == 1 ? stages * pieces * 16 * threads : 0);
-  const long long need = (a.rows + s.groups - 1) / s.groups, hold = 152ll * blocks;
-  auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+  const int other = s.groups * kRedFloats * 4;
+  const long long hold = 152ll * blocks;
+  auto go = [&](auto kernel, int R, std::atomic<uint64_t>& done) {
+    const int pieces = R * (kPieces<RT> + 2 * kPieces<T>);
+    const int stages = s.k == 1 ? ring_stages(pieces, threads, other, blocks) : 1;
+    const int smem = other + (s.k == 1 ? stages * pieces * 16 * threads : 0);
+    const long long need = (a.rows + s.groups * R - 1) / (s.groups * R);
     const cudaError_t e = allow_shared(kernel, 227 * 1024, done);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(need < hold ? need : hold), threads, smem, stream>>>(a, s.tpr, stages);
     return cudaGetLastError();
   };
-  static std::atomic<uint64_t> d1{0}, d2{0};
-  return s.k == 1 ? go(norm_fwd_kernel<T, RT, OT, 1>, d1) : go(norm_fwd_kernel<T, RT, OT, 2>, d2);
+  static std::atomic<uint64_t> d[6];
+  const bool bias = a.post_bias || a.bias;
+  if (s.k == 2)
+    return bias ? go(norm_fwd_kernel<T, RT, OT, 2, 1, true>, 1, d[0])
+                : go(norm_fwd_kernel<T, RT, OT, 2, 1, false>, 1, d[1]);
+  // one row at a time where that fills no more than the GPU once
+  if (a.rows <= hold * s.groups)
+    return bias ? go(norm_fwd_kernel<T, RT, OT, 1, 1, true>, 1, d[2])
+                : go(norm_fwd_kernel<T, RT, OT, 1, 1, false>, 1, d[3]);
+  return bias ? go(norm_fwd_kernel<T, RT, OT, 1, 2, true>, 2, d[4])
+              : go(norm_fwd_kernel<T, RT, OT, 1, 2, false>, 2, d[5]);
 }
 
 }  // namespace

@@ -9,7 +9,8 @@ namespace norm {
 
 constexpr int kV = 8;             // channels a thread and vector
 constexpr int kMaxThreads = 512;  // of a row
-constexpr int kRedFloats = 2 * 2 * 32;  // two buffers of up to 32 warps' pairs of sums, per group
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kRedFloats = 2 * 4 * kMaxWarps;  // two buffers of up to four sums of every warp, per group
 static_assert(kNormMaxD == kMaxThreads * 2 * kV, "two vectors a thread at most");
 
 // Threads of a row (whole warps), vectors of each, rows of a block.
@@ -24,129 +25,155 @@ inline Shape shape_of(int D) {
   return {tpr, k, tpr >= 256 ? 1 : 256 / tpr};
 }
 
-// The threads that own one row: `tpr` of them, `count` groups a block.
+// The threads that own a row (or a few rows at a time): `tpr` of them, `count` groups a block.
 struct Group {
   int index, count, lane, tpr;
   float* red;
   mutable int turn = 0;
   __device__ Group(int tpr_, float* shared)
       : index(threadIdx.x / tpr_), count(blockDim.x / tpr_), lane(threadIdx.x % tpr_), tpr(tpr_),
-        red(shared + (threadIdx.x / tpr_) * kRedFloats) {}
+        red(shared + (threadIdx.x / tpr_) * kRedFloats) {
+    for (int i = lane; i < kRedFloats; i += tpr) red[i] = 0.f;  // (of warps that are not there)
+    __syncthreads();
+  }
   __device__ __forceinline__ int column(int k) const { return (k * tpr + lane) * kV; }
 
-  // Sums over the group's threads, the same bits in each of them.  The two buffers
-  // take turns: a thread writes one again only after a barrier behind its last reads.
-  __device__ __forceinline__ float2 sum(float2 v) const {
+  // N sums (1, 2 or 4) over the group's threads, the same bits in each of them.  Inside a
+  // warp the lanes' halves hand each other the sums they give up, so that two sums
+  // cost the shuffles of one and four cost one more.  The two buffers take turns: a
+  // thread writes one again only after a barrier behind its last reads.
+  template <int N> __device__ __forceinline__ void sum(float (&v)[N]) const {
+    static_assert(N == 1 || N == 2 || N == 4, "sums at a time");
+    const int l = lane & 31;
+    float x;
+    if constexpr (N == 1) {
+      x = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+    } else {
+      const bool up = l & 16;
+      float w[N / 2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = add2(v, shfl_xor2(v, o));
-    if (tpr == 32) return v;
-    float2* buf = exchange();
-    if ((lane & 31) == 0) buf[lane >> 5] = v;
-    wait();
-    v = buf[0];
-    for (int w = 1; w < tpr / 32; ++w) v = add2(v, buf[w]);
-    return v;
-  }
-  __device__ __forceinline__ float sum(float v) const {
+      for (int i = 0; i < N / 2; ++i)
+        w[i] = (up ? v[N / 2 + i] : v[i]) +
+               __shfl_xor_sync(0xffffffffu, up ? v[i] : v[N / 2 + i], 16);
+      if constexpr (N == 2) {
+        x = w[0] + __shfl_xor_sync(0xffffffffu, w[0], 8);
+      } else {
+        const bool second = l & 8;
+        x = (second ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, second ? w[0] : w[1], 8);
+      }
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (tpr == 32) return v;
-    float* buf = reinterpret_cast<float*>(exchange());
-    if ((lane & 31) == 0) buf[lane >> 5] = v;
-    wait();
-    v = buf[0];
-    for (int w = 1; w < tpr / 32; ++w) v += buf[w];
-    return v;
-  }
-
- private:
-  __device__ __forceinline__ float2* exchange() const {
-    float2* buf = reinterpret_cast<float2*>(red) + turn * 32;
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    // sum i is in the lanes from i 32 / N on
+    if (tpr == 32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xffffffffu, x, i * (32 / N));
+      return;
+    }
+    float* buf = red + turn * 4 * kMaxWarps;
     turn ^= 1;
-    return buf;
-  }
-  __device__ __forceinline__ void wait() const {
+    if (l % (32 / N) == 0) buf[l / (32 / N) * kMaxWarps + (lane >> 5)] = x;
     asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(tpr) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4* from = reinterpret_cast<const float4*>(buf + i * kMaxWarps);
+      f32x2 t = both(0.f);
+      for (int w = 0; w < tpr; w += 128) {
+        const float4 q = from[w / 128];
+        t = add2(t, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+      }
+      v[i] = t.x + t.y;
+    }
   }
 };
 
-__device__ __forceinline__ void load_vec(const float* p, float (&x)[kV]) {
+// A thread's vector, as pairs: one instruction works on two channels.
+struct Vec {
+  f32x2 v[kV / 2];
+};
+__device__ __forceinline__ Vec vec_of(float x) {
+  Vec r;
+#pragma unroll
+  for (int j = 0; j < kV / 2; ++j) r.v[j] = both(x);
+  return r;
+}
+__device__ __forceinline__ Vec load_vec(const float* p) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  Vec r;
+  r.v[0] = make_float2(a.x, a.y); r.v[1] = make_float2(a.z, a.w);
+  r.v[2] = make_float2(b.x, b.y); r.v[3] = make_float2(b.z, b.w);
+  return r;
 }
-__device__ __forceinline__ void fill(float (&x)[kV], float v) {
+template <typename T> __device__ __forceinline__ void store_vec(T* p, const Vec& x) {
+  float t[kV];
 #pragma unroll
-  for (int j = 0; j < kV; ++j) x[j] = v;
+  for (int j = 0; j < kV / 2; ++j) unpack2(x.v[j], &t[2 * j], &t[2 * j + 1]);
+  store_raw<T, kV>(p, pack_as<T, kV>(t));
 }
+#define GLA_PAIRS for (int j = 0; j < kV / 2; ++j)
 // A parameter at the thread's columns: held over the rows (one vector a thread), or loaded
 // where it is used (two, whose registers would not do).
 template <int K> struct Param {
-  float v[K == 1 ? kV : 1];
+  Vec v;
   const float* p;
   float none;
   __device__ __forceinline__ void init(const Group& g, int D, const float* from, float otherwise) {
     p = from;
     none = otherwise;
-    if constexpr (K == 1) {
-      if (from && g.column(0) < D) load_vec(from + g.column(0), v);
-      else fill(v, otherwise);
-    }
+    if constexpr (K == 1) v = from && g.column(0) < D ? load_vec(from + g.column(0)) : vec_of(otherwise);
   }
-  __device__ __forceinline__ void at(int column, float (&x)[kV]) const {
-    if constexpr (K == 1) {
-#pragma unroll
-      for (int j = 0; j < kV; ++j) x[j] = v[j];
-    } else if (p) {
-      load_vec(p + column, x);
-    } else {
-      fill(x, none);
-    }
+  __device__ __forceinline__ Vec at(int column) const {
+    if constexpr (K == 1) return v;
+    else return p ? load_vec(p + column) : vec_of(none);
   }
 };
 
 // A thread's vectors of the next rows in shared memory: its own copies, its own reads, no
-// barrier.  Sixteen-byte pieces of all threads lie side by side, `pieces` a row.  With two
+// barrier.  Sixteen-byte pieces of all threads lie side by side, `per` a row.  With two
 // vectors a thread (whose rows would not fit) the reads go to memory themselves.
 constexpr int kMaxStages = 3;
 template <typename T> constexpr int kPieces = kV * (int)sizeof(T) / 16;  // of a vector
 template <int K> struct Ring {
   unsigned char* at;  // the thread's piece 0 of stage 0
   int hop;            // bytes between pieces
-  int pieces, stages, stage = 0;
-  __device__ Ring(void* shared, int pieces_, int stages_)
-      : at((unsigned char*)shared + threadIdx.x * 16), hop(blockDim.x * 16), pieces(pieces_),
-        stages(stages_) {}
+  int per, pieces, stages, stage = 0;  // pieces of a row, of a stage (which is R rows)
+  __device__ Ring(void* shared, int R, int per_, int stages_)
+      : at((unsigned char*)shared + threadIdx.x * 16), hop(blockDim.x * 16), per(per_),
+        pieces(R * per_), stages(stages_) {}
   template <typename T>
-  __device__ __forceinline__ void copy(int slot, int first, const T* from) const {
+  __device__ __forceinline__ void copy(int slot, int row, int first, const T* from) const {
 #pragma unroll
     for (int i = 0; i < kPieces<T>; ++i)
-      cp_async16(at + (slot * pieces + first + i) * hop, (const unsigned char*)from + 16 * i);
+      cp_async16(at + (slot * pieces + row * per + first + i) * hop,
+                 (const unsigned char*)from + 16 * i);
   }
-  // The slot of the row that is stages - 1 rows ahead.
+  // The slot of the rows that are stages - 1 turns ahead.
   __device__ __forceinline__ int ahead() const { return stage == 0 ? stages - 1 : stage - 1; }
   __device__ __forceinline__ void next() { stage = stage == stages - 1 ? 0 : stage + 1; }
-  // The current row's copies have landed (of one group a row).
+  // The current rows' copies have landed (of one group a turn).
   __device__ __forceinline__ void wait() const {
     if (stages == 3) cp_wait<2>();
     else if (stages == 2) cp_wait<1>();
     else cp_wait<0>();
   }
-  // A vector of the current row: piece `first` on, or from memory.
+  // A vector of a current row: piece `first` on, or from memory.
   template <typename T>
-  __device__ __forceinline__ void read(int first, const T* from, float (&x)[kV]) const {
+  __device__ __forceinline__ Vec read(int row, int first, const T* from) const {
     Raw<T, kV> r;
     if constexpr (K == 1) {
 #pragma unroll
       for (int i = 0; i < kPieces<T>; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4*>(at + (stage * pieces + first + i) * hop);
+        const uint4 v = *reinterpret_cast<const uint4*>(at + (stage * pieces + row * per + first + i) * hop);
         r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
       }
     } else {
       r = load_raw<T, kV>(from);
     }
-    unpack_as<T, kV>(r, x);
+    Vec x;
+    unpack_pairs<T, kV>(r, x.v);
+    return x;
   }
 };
 // Stages that fit beside `other` bytes, for `blocks` blocks an SM.
@@ -155,28 +182,43 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
   return n < 1 ? 1 : n > kMaxStages ? kMaxStages : n;
 }
 
-// Centres the row (layer norm) and returns 1 / sqrt(mean of squares + eps).
-template <int K>
-__device__ __forceinline__ float normalise(const Group& g, const NormArgs& a, float (&x)[K][kV]) {
+// Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r.
+template <int K, int R>
+__device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec (&x)[R][K],
+                                          float (&r)[R]) {
   if (a.layer) {
-    float m = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int i = 0; i < R; ++i) {
+      f32x2 m = both(0.f);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) m += x[k][j];
-    m = g.sum(m) * a.inv_d;
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (g.column(k) < a.D)
+        GLA_PAIRS m = add2(m, x[i][k].v[j]);
+      r[i] = m.x + m.y;
+    }
+    g.sum(r);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) x[k][j] -= m;
+    for (int i = 0; i < R; ++i) {
+      const f32x2 m = both(-r[i] * a.inv_d);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (g.column(k) < a.D)
+#pragma unroll
+          GLA_PAIRS x[i][k].v[j] = add2(x[i][k].v[j], m);
+    }
   }
-  float q = 0.f;
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int i = 0; i < R; ++i) {
+    f32x2 q = both(0.f);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) q = fmaf(x[k][j], x[k][j], q);
-  return 1.f / sqrtf(g.sum(q) * a.inv_d + a.eps);
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      GLA_PAIRS q = fma2(x[i][k].v[j], x[i][k].v[j], q);
+    r[i] = q.x + q.y;
+  }
+  g.sum(r);
+#pragma unroll
+  for (int i = 0; i < R; ++i) r[i] = rsqrtf(fmaf(r[i], a.inv_d, a.eps));
 }
 
 }  // namespace norm

@@ -23,39 +23,39 @@ namespace {
 using namespace norm;
 
 constexpr int kSums = 4;  // A, B, d_weight, d_bias
+constexpr int kRows = 2;  // rows of a group at a time (one with two vectors a thread)
 
 // The sums of a thread's columns over the rows.
 template <int K> struct Sums {
-  float v[K == 1 ? kSums : 1][K == 1 ? kV : 1];
-  float* s;  // K = 2: element (i, k, j) at ((i K + k) kV + j) threads + thread
-  __device__ void init(float* shared) {
-    s = shared + threadIdx.x;
+  Vec v[K == 1 ? kSums : 1];
+  f32x2* s;  // K = 2: pair (i, k, j) at ((i K + k) kV / 2 + j) threads + thread
+  __device__ void init(void* shared) {
+    s = (f32x2*)shared + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < kSums; ++i)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          if constexpr (K == 1) v[i][j] = 0.f;
-          else s[((i * K + k) * kV + j) * blockDim.x] = 0.f;
-        }
-  }
-  __device__ __forceinline__ void add(int i, int k, int j, float x, float y) {
-    if constexpr (K == 1) {
-      v[i][j] = fmaf(x, y, v[i][j]);
-    } else {
-      float& t = s[((i * K + k) * kV + j) * blockDim.x];
-      t = fmaf(x, y, t);
+    for (int i = 0; i < kSums; ++i) {
+      if constexpr (K == 1) {
+        v[i] = vec_of(0.f);
+      } else {
+        for (int e = 0; e < K * kV / 2; ++e) s[(i * K * kV / 2 + e) * blockDim.x] = both(0.f);
+      }
     }
   }
-  __device__ __forceinline__ float get(int i, int k, int j) const {
-    if constexpr (K == 1) return v[i][j];
-    else return s[((i * K + k) * kV + j) * blockDim.x];
+  __device__ __forceinline__ void add(int i, int k, int j, f32x2 x, f32x2 y) {
+    if constexpr (K == 1) {
+      v[i].v[j] = fma2(x, y, v[i].v[j]);
+    } else {
+      f32x2& t = s[((i * K + k) * kV / 2 + j) * blockDim.x];
+      t = fma2(x, y, t);
+    }
+  }
+  __device__ __forceinline__ f32x2 get(int i, int k, int j) const {
+    if constexpr (K == 1) return v[i].v[j];
+    else return s[((i * K + k) * kV / 2 + j) * blockDim.x];
   }
 };
 
-// BIAS: layer norm's biases (post_bias, d_post_bias, d_bias)
-template <typename T, typename RT, typename GT, typename GRT, int K, bool BIAS>
+// R: rows at a time; BIAS: layer norm's biases (post_bias, d_post_bias, d_bias)
+template <typename T, typename RT, typename GT, typename GRT, int K, int R, bool BIAS>
 __global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   start_next();
@@ -64,177 +64,206 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   const Group g(tpr, (float*)shared);
   // pieces of a row: res, ds, y, z, du
   constexpr int kDs = kPieces<RT>, kY = 2 * kDs, kZ = kY + kPieces<T>, kDu = kZ + kPieces<T>;
-  Ring<K> ring(shared + g.count * kRedFloats * 4, kDu + kPieces<T>, stages);
+  Ring<K> ring(shared + g.count * kRedFloats * 4, R, kDu + kPieces<T>, stages);
   Sums<K> sums;
-  sums.init((float*)(shared + g.count * kRedFloats * 4));  // (K = 2, which has no ring)
+  sums.init(shared + g.count * kRedFloats * 4);  // (K = 2, which has no ring)
   Param<K> post, post_b, scale, weight;
   post.init(g, a.D, a.post_weight, 1.f);
   if (BIAS) post_b.init(g, a.D, a.post_bias, 0.f);
   scale.init(g, a.D, a.scale, 1.f);
   weight.init(g, a.D, a.weight, 1.f);
-  const long long hop = (long long)gridDim.x * g.count;
+  const long long hop = (long long)gridDim.x * g.count * R;
   auto fetch = [&](long long row, int slot) {
     if constexpr (K == 1) {
       const int c = g.column(0);
-      if (row < a.rows && c < a.D) {
-        ring.copy(slot, 0, (const RT*)a.res + row * a.D + c);
-        if (b.d_res_out) ring.copy(slot, kDs, (const RT*)b.d_res_out + row * a.D + c);
-        if (a.y) ring.copy(slot, kY, (const T*)a.y + row * a.y_stride + c);
-        if (a.z) ring.copy(slot, kZ, (const T*)a.z + row * a.z_stride + c);
-        if (b.d_out) ring.copy(slot, kDu, (const T*)b.d_out + row * a.D + c);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (row + i < a.rows && c < a.D) {
+          const long long at = (row + i) * a.D + c;
+          ring.copy(slot, i, 0, (const RT*)a.res + at);
+          if (b.d_res_out) ring.copy(slot, i, kDs, (const RT*)b.d_res_out + at);
+          if (a.y) ring.copy(slot, i, kY, (const T*)a.y + (row + i) * a.y_stride + c);
+          if (a.z) ring.copy(slot, i, kZ, (const T*)a.z + (row + i) * a.z_stride + c);
+          if (b.d_out) ring.copy(slot, i, kDu, (const T*)b.d_out + at);
+        }
       }
       cp_commit();
     }
   };
-  long long row = (long long)blockIdx.x * g.count + g.index;
+  long long row = ((long long)blockIdx.x * g.count + g.index) * R;
   for (int i = 0; i < stages - 1; ++i) fetch(row + i * hop, i);
   for (; row < a.rows; row += hop, ring.next()) {
     fetch(row + (stages - 1) * hop, ring.ahead());
     ring.wait();
-    const long long at = row * a.D;
-    const T* zr = (const T*)a.z + row * a.z_stride;
-    float s[K][kV], p[K][kV];
-    float ry = 1.f;
+    // whether the thread has channels of row i
+    auto has = [&](int i, int k) { return g.column(k) < a.D && row + i < a.rows; };
+    auto at = [&](int i, int k) { return (row + i) * a.D + g.column(k); };
+    auto z_of = [&](int i, int k) {
+      return ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k));
+    };
+    auto du_of = [&](int i, int k) { return ring.read(i, kDu, (const T*)b.d_out + at(i, k)); };
+    auto ds_of = [&](int i, int k) {
+      return b.d_res_out ? ring.read(i, kDs, (const RT*)b.d_res_out + at(i, k)) : vec_of(0.f);
+    };
+    Vec s[R][K], p[R][K];
+    float ry[R];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      fill(s[k], 0.f);
-      fill(p[k], 0.f);
-      if (g.column(k) < a.D) {
-        ring.read(0, (const RT*)a.res + at + g.column(k), s[k]);
-        if (a.y) ring.read(kY, (const T*)a.y + row * a.y_stride + g.column(k), p[k]);
+    for (int i = 0; i < R; ++i) {
+      ry[i] = 1.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        s[i][k] = has(i, k) ? ring.read(i, 0, (const RT*)a.res + at(i, k)) : vec_of(0.f);
+        p[i][k] = a.y && has(i, k)
+                      ? ring.read(i, kY, (const T*)a.y + (row + i) * a.y_stride + g.column(k))
+                      : vec_of(0.f);
       }
     }
     if (a.post_weight) {
-      ry = normalise<K>(g, a, p);
+      normalise<K, R>(g, a, p, ry);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < kV; ++j) p[k][j] *= ry;
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          GLA_PAIRS p[i][k].v[j] = mul2(p[i][k].v[j], both(ry[i]));
     }
     // q = p post_weight + post_bias, formed twice (again below) rather than held
-    auto affine = [&](int k, float (&q)[kV]) {
-      float w[kV], o[kV];
-      post.at(g.column(k), w);
-      if (BIAS) post_b.at(g.column(k), o);
+    auto affine = [&](int i, int k) {
+      const Vec w = post.at(g.column(k)), o = BIAS ? post_b.at(g.column(k)) : w;
+      Vec q;
 #pragma unroll
-      for (int j = 0; j < kV; ++j) q[j] = BIAS ? fmaf(p[k][j], w[j], o[j]) : p[k][j] * w[j];
+      GLA_PAIRS q.v[j] = BIAS ? fma2(p[i][k].v[j], w.v[j], o.v[j]) : mul2(p[i][k].v[j], w.v[j]);
+      return q;
     };
     // s becomes d = dL/ds
     if (b.d_out) {
       if (a.y) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (g.column(k) >= a.D) continue;
-          float q[kV], w[kV];
-          affine(k, q);
-          scale.at(g.column(k), w);
-          if (a.z) {
-            float z[kV];
-            ring.read(kZ, zr + g.column(k), z);
+        for (int i = 0; i < R; ++i) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) w[j] *= silu(z[j]);
+          for (int k = 0; k < K; ++k) {
+            if (!has(i, k)) continue;
+            const Vec q = affine(i, k);
+            Vec w = scale.at(g.column(k));
+            if (a.z) {
+              const Vec z = z_of(i, k);
+#pragma unroll
+              GLA_PAIRS w.v[j] = mul2(w.v[j], mul2(z.v[j], sigmoid2(z.v[j])));
+            }
+#pragma unroll
+            GLA_PAIRS s[i][k].v[j] = fma2(w.v[j], q.v[j], s[i][k].v[j]);
           }
-#pragma unroll
-          for (int j = 0; j < kV; ++j) s[k][j] = fmaf(w[j], q[j], s[k][j]);
         }
       }
-      const float r = normalise<K>(g, a, s);
-      float2 m = make_float2(0.f, 0.f);
+      float r[R], m[2 * R];
+      normalise<K, R>(g, a, s, r);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (g.column(k) >= a.D) continue;
-        float d[kV], w[kV];
-        ring.read(kDu, (const T*)b.d_out + at + g.column(k), d);
-        weight.at(g.column(k), w);
+      for (int i = 0; i < R; ++i) {
+        f32x2 mx = both(0.f), my = both(0.f);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          const float n = s[k][j] * r;
-          s[k][j] = n;
-          sums.add(2, k, j, d[j], n);
-          if (BIAS) sums.add(3, k, j, d[j], 1.f);
-          const float dn = d[j] * w[j];
-          m.x = fmaf(dn, n, m.x);
-          m.y += dn;
+        for (int k = 0; k < K; ++k) {
+          if (!has(i, k)) continue;
+          const Vec d = du_of(i, k), w = weight.at(g.column(k));
+#pragma unroll
+          GLA_PAIRS {
+            const f32x2 n = mul2(s[i][k].v[j], both(r[i]));
+            s[i][k].v[j] = n;
+            sums.add(2, k, j, d.v[j], n);
+            if (BIAS) sums.add(3, k, j, d.v[j], both(1.f));
+            const f32x2 dn = mul2(d.v[j], w.v[j]);
+            mx = fma2(dn, n, mx);
+            my = add2(my, dn);
+          }
         }
+        m[2 * i] = mx.x + mx.y;
+        m[2 * i + 1] = my.x + my.y;
       }
-      m = g.sum(m);
-      m.x *= a.inv_d;
-      m.y = a.layer ? m.y * a.inv_d : 0.f;
+      g.sum(m);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (g.column(k) >= a.D) continue;
-        float d[kV], w[kV], e[kV];
-        ring.read(kDu, (const T*)b.d_out + at + g.column(k), d);
-        fill(e, 0.f);
-        if (b.d_res_out) ring.read(kDs, (const RT*)b.d_res_out + at + g.column(k), e);
-        weight.at(g.column(k), w);
+      for (int i = 0; i < R; ++i) {
+        const f32x2 mx = both(-m[2 * i] * a.inv_d);
+        const f32x2 my = both(a.layer ? -m[2 * i + 1] * a.inv_d : 0.f);
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-          s[k][j] = fmaf(r, fmaf(-s[k][j], m.x, fmaf(d[j], w[j], -m.y)), e[j]);
+        for (int k = 0; k < K; ++k) {
+          if (!has(i, k)) continue;
+          const Vec d = du_of(i, k), e = ds_of(i, k), w = weight.at(g.column(k));
+#pragma unroll
+          GLA_PAIRS s[i][k].v[j] = fma2(
+              both(r[i]), fma2(s[i][k].v[j], mx, fma2(d.v[j], w.v[j], my)), e.v[j]);
+        }
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        fill(s[k], 0.f);
-        if (b.d_res_out && g.column(k) < a.D) 
-          ring.read(kDs, (const RT*)b.d_res_out + at + g.column(k), s[k]);
-      }
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[i][k] = has(i, k) ? ds_of(i, k) : vec_of(0.f);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (g.column(k) < a.D)
-        store_raw<GRT, kV>((GRT*)b.d_res + row * a.D + g.column(k), pack_as<GRT, kV>(s[k]));
-    if (!a.y) continue;
-    // s becomes dp, then dy
-    float2 m = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = g.column(k);
-      if (c >= a.D) continue;
-      float w[kV];
-      scale.at(c, w);
-      if (a.z) {
-        float z[kV], q[kV];
-        affine(k, q);
-        ring.read(kZ, zr + c, z);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          const float sig = sigmoid(z[j]), gate = z[j] * sig, d = s[k][j] * gate;
-          q[j] *= s[k][j] * w[j] * fmaf(gate, 1.f - sig, sig);  // dz
-          s[k][j] = d;
-        }
-        store_raw<GT, kV>((GT*)b.dz + row * a.D + c, pack_as<GT, kV>(q));
-      }
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        sums.add(0, k, j, s[k][j], p[k][j]);
-        if (BIAS) sums.add(1, k, j, s[k][j], 1.f);
-        s[k][j] *= w[j];
-      }
-      if (a.post_weight) {
-        float pw[kV];
-        post.at(c, pw);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          s[k][j] *= pw[j];
-          m.x = fmaf(s[k][j], p[k][j], m.x);
-          m.y += s[k][j];
-        }
-      }
-    }
-    if (a.post_weight) {
-      m = g.sum(m);
-      m.x *= a.inv_d;
-      m.y = a.layer ? m.y * a.inv_d : 0.f;
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int k = 0; k < K; ++k)
+        if (has(i, k)) store_vec((GRT*)b.d_res + at(i, k), s[i][k]);
+    if (!a.y) continue;
+    // s becomes dp, then dy
+    float m[2 * R];
 #pragma unroll
-        for (int j = 0; j < kV; ++j) s[k][j] = ry * fmaf(-p[k][j], m.x, s[k][j] - m.y);
+    for (int i = 0; i < R; ++i) {
+      f32x2 mx = both(0.f), my = both(0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!has(i, k)) continue;
+        const int c = g.column(k);
+        const Vec w = scale.at(c);
+        if (a.z) {
+          const Vec z = z_of(i, k);
+          Vec q = affine(i, k);
+#pragma unroll
+          GLA_PAIRS {
+            const f32x2 sig = sigmoid2(z.v[j]), gate = mul2(z.v[j], sig);
+            // silu' = sig + gate (1 - sig)
+            const f32x2 slope = fma2(gate, fma2(sig, both(-1.f), both(1.f)), sig);
+            q.v[j] = mul2(q.v[j], mul2(mul2(s[i][k].v[j], w.v[j]), slope));  // dz
+            s[i][k].v[j] = mul2(s[i][k].v[j], gate);
+          }
+          store_vec((GT*)b.dz + at(i, k), q);
+        }
+#pragma unroll
+        GLA_PAIRS {
+          sums.add(0, k, j, s[i][k].v[j], p[i][k].v[j]);
+          if (BIAS) sums.add(1, k, j, s[i][k].v[j], both(1.f));
+          s[i][k].v[j] = mul2(s[i][k].v[j], w.v[j]);
+        }
+        if (a.post_weight) {
+          const Vec pw = post.at(c);
+#pragma unroll
+          GLA_PAIRS {
+            s[i][k].v[j] = mul2(s[i][k].v[j], pw.v[j]);
+            mx = fma2(s[i][k].v[j], p[i][k].v[j], mx);
+            my = add2(my, s[i][k].v[j]);
+          }
+        }
+      }
+      m[2 * i] = mx.x + mx.y;
+      m[2 * i + 1] = my.x + my.y;
+    }
+    if (a.post_weight) {
+      g.sum(m);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const f32x2 mx = both(-m[2 * i] * a.inv_d);
+        const f32x2 my = both(a.layer ? -m[2 * i + 1] * a.inv_d : 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          GLA_PAIRS s[i][k].v[j] =
+              mul2(both(ry[i]), fma2(p[i][k].v[j], mx, add2(s[i][k].v[j], my)));
+      }
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (g.column(k) < a.D)
-        store_raw<GT, kV>((GT*)b.dy + row * a.D + g.column(k), pack_as<GT, kV>(s[k]));
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (has(i, k)) store_vec((GT*)b.dy + at(i, k), s[i][k]);
   }
   cp_wait<0>();
   // the groups' sums in group order (one group: the threads' own)
@@ -246,13 +275,17 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (g.column(k) + j < a.D) to[g.column(k) + j] = sums.get(i, k, j);
+        GLA_PAIRS if (g.column(k) < a.D)
+          *reinterpret_cast<float2*>(to + g.column(k) + 2 * j) = sums.get(i, k, j);
     } else {  // K = 1; the ring is free
       float* all = (float*)(shared + g.count * kRedFloats * 4);
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kV; ++j) all[j * blockDim.x + threadIdx.x] = sums.get(i, 0, j);
+      GLA_PAIRS {
+        const f32x2 t = sums.get(i, 0, j);
+        all[2 * j * blockDim.x + threadIdx.x] = t.x;
+        all[(2 * j + 1) * blockDim.x + threadIdx.x] = t.y;
+      }
       __syncthreads();
       for (int e = threadIdx.x; e < tpr * kV; e += blockDim.x) {
         const int j = e / tpr, lane = e % tpr;
@@ -298,7 +331,8 @@ norm_bwd_sum_kernel(NormBwdArgs b, const float* partial, int blocks, int bias) {
 // Blocks of the first launch: as many as the GPU holds at once.
 int bwd_blocks(int rows, int D) {
   const Shape s = shape_of(D);
-  const long long need = ((long long)rows + s.groups - 1) / s.groups;
+  const int at_once = s.groups * (s.k == 1 ? kRows : 1);
+  const long long need = ((long long)rows + at_once - 1) / at_once;
   const int hold = 152 * (s.tpr * s.groups <= 256 ? 2 : 1);
   return (int)(need < hold ? need : hold);
 }
@@ -308,7 +342,7 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
   const Shape s = shape_of(b.f.D);
   const int threads = s.tpr * s.groups, blocks = bwd_blocks(b.f.rows, b.f.D);
   const bool bias = b.f.post_bias || b.d_bias;
-  const int pieces = 2 * kPieces<RT> + 3 * kPieces<T>, other = s.groups * kRedFloats * 4;
+  const int pieces = kRows * (2 * kPieces<RT> + 3 * kPieces<T>), other = s.groups * kRedFloats * 4;
   const int stages = s.k == 1 ? ring_stages(pieces, threads, other, threads <= 256 ? 2 : 1) : 1;
   int room = s.k == 1 ? stages * pieces * 16 * threads : kSums * s.k * kV * threads * 4;
   if (room < threads * kV * 4) room = threads * kV * 4;  // the groups' sums at the end
@@ -321,10 +355,10 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
   if (blocks > 0) {
     static std::atomic<uint64_t> d0{0}, d1{0}, d2{0}, d3{0};
     const cudaError_t e =
-        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, true>, d0)
-                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, false>, d1))
-                 : (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 2, true>, d2)
-                         : go(norm_bwd_kernel<T, RT, GT, GRT, 2, false>, d3));
+        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows, true>, d0)
+                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows, false>, d1))
+                 : (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, true>, d2)
+                         : go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, false>, d3));
     if (e != cudaSuccess) return e;
   }
   if (!b.d_post_weight && !b.d_post_bias && !b.d_scale && !b.d_weight && !b.d_bias)
