@@ -57,12 +57,14 @@ norm_fwd_kernel(NormArgs a, int tpr, int stages) {
   for (; row < a.rows; row += hop, ring.next()) {
     fetch(row + (stages - 1) * hop, ring.ahead());
     ring.wait();
+    const int rows = R == 1 || row + 1 >= a.rows ? 1 : 2;
+    auto has = [&](int i, int k) { return g.column(k) < a.D && i < rows; };
     Vec s[R][K];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        s[i][k] = g.column(k) < a.D && row + i < a.rows
+        s[i][k] = has(i, k)
                       ? ring.read(i, 0, (const RT*)a.res + (row + i) * a.D + g.column(k))
                       : vec_of(0.f);
     if (a.y) {
@@ -73,21 +75,22 @@ norm_fwd_kernel(NormArgs a, int tpr, int stages) {
         r[i] = 1.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          y[i][k] = g.column(k) < a.D && row + i < a.rows
+          y[i][k] = has(i, k)
                         ? ring.read(i, kY, (const T*)a.y + (row + i) * a.y_stride + g.column(k))
                         : vec_of(0.f);
       }
-      if (a.post_weight) normalise<K, R>(g, a, y, r);
+      if (a.post_weight) normalise<K, R>(g, a, y, r, rows);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           const int c = g.column(k);
-          if (c >= a.D || row + i >= a.rows) continue;
+          if (K > 1 && c >= a.D) continue;
           const Vec w = post.at(c), o = BIAS ? post_b.at(c) : w;
           Vec sc = scale.at(c);
           if (a.z) {
-            const Vec z = ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + c);
+            const Vec z = has(i, k) ? ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + c)
+                                    : vec_of(0.f);
 #pragma unroll
             GLA_PAIRS sc.v[j] = mul2(sc.v[j], mul2(z.v[j], sigmoid2(z.v[j])));
           }
@@ -97,19 +100,19 @@ norm_fwd_kernel(NormArgs a, int tpr, int stages) {
             const f32x2 p = BIAS ? fma2(n, w.v[j], o.v[j]) : mul2(n, w.v[j]);
             s[i][k].v[j] = fma2(sc.v[j], p, s[i][k].v[j]);
           }
-          if (a.res_out) store_vec((RT*)a.res_out + (row + i) * a.D + c, s[i][k]);
+          if (a.res_out && has(i, k)) store_vec((RT*)a.res_out + (row + i) * a.D + c, s[i][k]);
         }
       }
     }
     if (a.out) {
       float r[R];
-      normalise<K, R>(g, a, s, r);
+      normalise<K, R>(g, a, s, r, rows);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           const int c = g.column(k);
-          if (c >= a.D || row + i >= a.rows) continue;
+          if (K > 1 && c >= a.D) continue;
           const Vec w = weight.at(c), o = BIAS ? bias.at(c) : w;
           Vec u;
 #pragma unroll
@@ -117,7 +120,7 @@ norm_fwd_kernel(NormArgs a, int tpr, int stages) {
             const f32x2 n = mul2(s[i][k].v[j], both(r[i]));
             u.v[j] = BIAS ? fma2(n, w.v[j], o.v[j]) : mul2(n, w.v[j]);
           }
-          store_vec((OT*)a.out + (row + i) * a.D + c, u);
+          if (has(i, k)) store_vec((OT*)a.out + (row + i) * a.D + c, u);
         }
       }
     }

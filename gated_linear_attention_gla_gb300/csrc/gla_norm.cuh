@@ -75,13 +75,22 @@ struct Group {
     turn ^= 1;
     if (l % (32 / N) == 0) buf[l / (32 / N) * kMaxWarps + (lane >> 5)] = x;
     asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(tpr) : "memory");
+    if (tpr <= 128) gather<1>(buf, v);
+    else if (tpr <= 256) gather<2>(buf, v);
+    else gather<4>(buf, v);
+  }
+
+ private:
+  template <int Q, int N>
+  static __device__ __forceinline__ void gather(const float* buf, float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float4* from = reinterpret_cast<const float4*>(buf + i * kMaxWarps);
       f32x2 t = both(0.f);
-      for (int w = 0; w < tpr; w += 128) {
-        const float4 q = from[w / 128];
-        t = add2(t, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const float4 x = reinterpret_cast<const float4*>(buf + i * kMaxWarps)[q];
+        const f32x2 y = add2(make_float2(x.x, x.y), make_float2(x.z, x.w));
+        t = q ? add2(t, y) : y;
       }
       v[i] = t.x + t.y;
     }
@@ -113,19 +122,19 @@ template <typename T> __device__ __forceinline__ void store_vec(T* p, const Vec&
   store_raw<T, kV>(p, pack_as<T, kV>(t));
 }
 #define GLA_PAIRS for (int j = 0; j < kV / 2; ++j)
-// A parameter at the thread's columns: held over the rows (one vector a thread), or loaded
-// where it is used (two, whose registers would not do).
-template <int K> struct Param {
+// A parameter at the thread's columns: HELD over the rows, or loaded where it is used (where
+// registers would not do: of two vectors a thread, of some in the backward kernel).
+template <int K, bool HELD = K == 1> struct Param {
   Vec v;
   const float* p;
   float none;
   __device__ __forceinline__ void init(const Group& g, int D, const float* from, float otherwise) {
     p = from;
     none = otherwise;
-    if constexpr (K == 1) v = from && g.column(0) < D ? load_vec(from + g.column(0)) : vec_of(otherwise);
+    if constexpr (HELD) v = from && g.column(0) < D ? load_vec(from + g.column(0)) : vec_of(otherwise);
   }
   __device__ __forceinline__ Vec at(int column) const {
-    if constexpr (K == 1) return v;
+    if constexpr (HELD) return v;
     else return p ? load_vec(p + column) : vec_of(none);
   }
 };
@@ -182,10 +191,11 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
   return n < 1 ? 1 : n > kMaxStages ? kMaxStages : n;
 }
 
-// Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r.
+// Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r; 0
+// for a row behind the last (of zeros), so that it adds nothing to sums over rows.
 template <int K, int R>
 __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec (&x)[R][K],
-                                          float (&r)[R]) {
+                                          float (&r)[R], int rows) {
   if (a.layer) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -218,7 +228,7 @@ __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec
   }
   g.sum(r);
 #pragma unroll
-  for (int i = 0; i < R; ++i) r[i] = rsqrtf(fmaf(r[i], a.inv_d, a.eps));
+  for (int i = 0; i < R; ++i) r[i] = i < rows ? rsqrtf(fmaf(r[i], a.inv_d, a.eps)) : 0.f;
 }
 
 }  // namespace norm

@@ -67,7 +67,9 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   Ring<K> ring(shared + g.count * kRedFloats * 4, R, kDu + kPieces<T>, stages);
   Sums<K> sums;
   sums.init(shared + g.count * kRedFloats * 4);  // (K = 2, which has no ring)
-  Param<K> post, post_b, scale, weight;
+  // (with biases 24 registers more are held: two parameters less)
+  Param<K> post, weight;
+  Param<K, K == 1 && !BIAS> scale, post_b;
   post.init(g, a.D, a.post_weight, 1.f);
   if (BIAS) post_b.init(g, a.D, a.post_bias, 0.f);
   scale.init(g, a.D, a.scale, 1.f);
@@ -96,14 +98,22 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
     fetch(row + (stages - 1) * hop, ring.ahead());
     ring.wait();
     // whether the thread has channels of row i
-    auto has = [&](int i, int k) { return g.column(k) < a.D && row + i < a.rows; };
+    const int rows = R == 1 || row + 1 >= a.rows ? 1 : 2;
+    auto has = [&](int i, int k) { return g.column(k) < a.D && i < rows; };
+    // (columns and rows that do not exist are zeros, without branches between the rows;
+    // columns whose parameters are not held are skipped)
+    auto skip = [&](int k) { return (K > 1 || BIAS) && g.column(k) >= a.D; };
     auto at = [&](int i, int k) { return (row + i) * a.D + g.column(k); };
     auto z_of = [&](int i, int k) {
-      return ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k));
+      return has(i, k) ? ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k))
+                       : vec_of(0.f);
     };
-    auto du_of = [&](int i, int k) { return ring.read(i, kDu, (const T*)b.d_out + at(i, k)); };
+    auto du_of = [&](int i, int k) {
+      return has(i, k) ? ring.read(i, kDu, (const T*)b.d_out + at(i, k)) : vec_of(0.f);
+    };
     auto ds_of = [&](int i, int k) {
-      return b.d_res_out ? ring.read(i, kDs, (const RT*)b.d_res_out + at(i, k)) : vec_of(0.f);
+      return b.d_res_out && has(i, k) ? ring.read(i, kDs, (const RT*)b.d_res_out + at(i, k))
+                                      : vec_of(0.f);
     };
     Vec s[R][K], p[R][K];
     float ry[R];
@@ -119,7 +129,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
       }
     }
     if (a.post_weight) {
-      normalise<K, R>(g, a, p, ry);
+      normalise<K, R>(g, a, p, ry, rows);
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -142,7 +152,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         for (int i = 0; i < R; ++i) {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!has(i, k)) continue;
+            if (skip(k)) continue;
             const Vec q = affine(i, k);
             Vec w = scale.at(g.column(k));
             if (a.z) {
@@ -156,13 +166,13 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         }
       }
       float r[R], m[2 * R];
-      normalise<K, R>(g, a, s, r);
+      normalise<K, R>(g, a, s, r, rows);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         f32x2 mx = both(0.f), my = both(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!has(i, k)) continue;
+          if (skip(k)) continue;
           const Vec d = du_of(i, k), w = weight.at(g.column(k));
 #pragma unroll
           GLA_PAIRS {
@@ -185,7 +195,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         const f32x2 my = both(a.layer ? -m[2 * i + 1] * a.inv_d : 0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!has(i, k)) continue;
+          if (skip(k)) continue;
           const Vec d = du_of(i, k), e = ds_of(i, k), w = weight.at(g.column(k));
 #pragma unroll
           GLA_PAIRS s[i][k].v[j] = fma2(
@@ -196,7 +206,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int k = 0; k < K; ++k) s[i][k] = has(i, k) ? ds_of(i, k) : vec_of(0.f);
+        for (int k = 0; k < K; ++k) s[i][k] = ds_of(i, k);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -211,7 +221,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
       f32x2 mx = both(0.f), my = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!has(i, k)) continue;
+        if (skip(k)) continue;
         const int c = g.column(k);
         const Vec w = scale.at(c);
         if (a.z) {
@@ -225,7 +235,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
             q.v[j] = mul2(q.v[j], mul2(mul2(s[i][k].v[j], w.v[j]), slope));  // dz
             s[i][k].v[j] = mul2(s[i][k].v[j], gate);
           }
-          store_vec((GT*)b.dz + at(i, k), q);
+          if (has(i, k)) store_vec((GT*)b.dz + at(i, k), q);
         }
 #pragma unroll
         GLA_PAIRS {
