@@ -24,21 +24,15 @@
 // product.  Persistent: every pair takes each 76th tile.
 // Every wait is bounded in wall time (gla_set_wait_limit_ns); one that runs out
 // flags the status word, and the kernel lets its copies and products land and ends.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "gla_ssm.cuh"
-#include "gla_sm100.cuh"
+#include "gla_glu.cuh"
 
 namespace gla {
 namespace {
 
-using namespace sm100;
+using namespace glu;
 
 constexpr int kTile = 256;           // rows and columns of a pair's tile
 constexpr int kHalf = 128;           // of one SM
-constexpr int kK = 64;               // along K per stage (128 bytes of bf16)
 constexpr int kStages = 6;
 constexpr uint32_t kOperand = kHalf * kK * 2;          // 16 KB
 constexpr uint32_t kStage = 2 * kOperand;
@@ -67,15 +61,6 @@ struct GluParams {
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // The address of the pair's first SM's copy of a shared variable.
 __device__ __forceinline__ uint32_t first_sm(const void* p) {
   uint32_t r;
@@ -196,21 +181,9 @@ glu_kernel(const __grid_constant__ GluParams p) {
   const uint32_t tmem = *tmem_at;
   after_previous();
 
-  // false: the wait ran out (or another role's has)
   auto wait = [&](int bar, uint32_t parity) {
-    if (mbar_try_wait(&bars[bar], parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&bars[bar], parity)) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > p.wait_ns) {
-        *abort_flag = 1;
-        atomicOr(p.status, kDevTimeout);
-        return false;
-      }
-    }
-    return true;
+    return wait_for(&bars[bar], parity, p.wait_ns, abort_flag, p.status);
   };
-
   auto wait_warp = [&](int bar, uint32_t parity) {  // the whole warp's answer
     return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
@@ -378,38 +351,6 @@ glu_kernel(const __grid_constant__ GluParams p) {
   }
 }
 
-// ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// bf16 [rows][cols], `stride` elements between rows; boxes of 64 columns x box_rows.
-bool make_map(CUtensorMap* map, const void* base, long long cols, long long rows,
-              long long stride, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int tiles_of(long long n, int by) { return (int)((n + by - 1) / by); }
-
 template <bool BWD2, bool GRAD, typename OT>
 cudaError_t launch(const GluParams& p, cudaStream_t stream, bool dependent) {
   static std::atomic<uint64_t> done{0};
@@ -445,6 +386,7 @@ bool up_params(const GluArgs& a, GluParams* p) {
 }  // namespace
 
 cudaError_t launch_glu_fwd(const GluArgs& a, cudaStream_t stream) {
+  if (a.rows <= kFewRows) return launch_few(a, stream);
   GluParams p{};
   if (!up_params(a, &p)) return cudaErrorInvalidValue;
   p.out = a.out;
