@@ -18,8 +18,8 @@
 // The backward is a kUp launch (dg, du rounded to bf16 into the workspace) and one
 // launch of all kDx and kDw tiles.
 //
-// Roles (6 warps): 0..3 epilogue (thread = accumulator row), 4 producer (TMA into a
-// ring of 6 stages of 64 along K), 5 issuer (the first SM's alone).  The accumulators
+// Roles (10 warps): 0..7 epilogue (thread = half of an accumulator row), 8 producer (TMA into a
+// ring of 6 stages of 64 along K), 9 issuer (the first SM's alone).  The accumulators
 // are two of 256 columns in tensor memory: a tile's epilogue overlaps the next tile's
 // product.  Persistent: every pair takes each 76th tile.
 // Every wait is bounded in wall time (gla_set_wait_limit_ns); one that runs out
@@ -38,7 +38,8 @@ constexpr uint32_t kOperand = kHalf * kK * 2;          // 16 KB
 constexpr uint32_t kStage = 2 * kOperand;
 constexpr uint32_t kOffBar = kStages * kStage;
 constexpr uint32_t kSmem = kOffBar + 256 + 1024;       // 1024: the window's alignment
-constexpr int kThreads = 192;
+constexpr int kEpilogue = 8;         // warps: two a lane quadrant, half of the columns each
+constexpr int kThreads = 32 * (kEpilogue + 2);
 constexpr uint32_t kCols = 512;                        // tensor memory: two accumulators
 
 enum Bar { kFull = 0, kEmpty = kFull + kStages, kAccFull = kEmpty + kStages,
@@ -56,7 +57,8 @@ struct GluParams {
   int R, D, F;
   int tiles, dx_tiles;        // of the launch; the first dx_tiles are kDx
   int tiles_m, tiles_n;       // kUp
-  int dx_m, dx_n, dw_m, dw_n; // tiles along the axes of kDx, kDw (dw_m: of one weight)
+  int dx_m, dx_width, dw_m, dw_n;  // tiles along the axes of kDx, kDw (dw_m: of one weight)
+  int ahead;                  // kDw tiles that are as long as a kDx tile
   unsigned* status;
   uint64_t wait_ns;
 };
@@ -102,31 +104,59 @@ enum Kind { kUp = 0, kDx = 1, kDw = 2 };
 struct TileAt {
   int kind, m, n, seg;  // first row and column of the tile; seg: dg's or du's (kDw)
   int blocks;           // of kK along K
+  int width;            // columns of the accumulator: 256, or 128 (kDx of few tiles)
 };
 
-template <bool BWD2> __device__ __forceinline__ TileAt tile_at(const GluParams& p, int t) {
-  TileAt a;
-  a.seg = 0;
+// The i-th tile of a pair; false: it has no more.  The backward's second launch has two
+// kinds of different length: the kDx tiles go around the pairs first; then the pairs that got one less
+// take as many kDw tiles as one kDx tile is long, and the rest go around (4096 rows x
+// 2048 x 8192: 862 steps of K a pair at best, 896 so, 960 without).
+template <bool BWD2>
+__device__ __forceinline__ bool tile_at(const GluParams& p, int pair, int pairs, int i, TileAt* a) {
+  a->seg = 0;
+  a->width = kTile;
   if (!BWD2) {
-    a.kind = kUp;
-    a.m = t % p.tiles_m * kTile;
-    a.n = t / p.tiles_m * kHalf;
-    a.blocks = (p.D + kK - 1) / kK;
-  } else if (t < p.dx_tiles) {
-    a.kind = kDx;
-    a.m = t % p.dx_m * kTile;
-    a.n = t / p.dx_m * kTile;
-    a.blocks = 2 * ((p.F + kK - 1) / kK);
-  } else {
-    t -= p.dx_tiles;
-    a.kind = kDw;
-    a.n = t % p.dw_n * kTile;
-    t /= p.dw_n;
-    a.seg = t / p.dw_m;
-    a.m = t % p.dw_m * kTile;
-    a.blocks = (p.R + kK - 1) / kK;
+    const int t = pair + i * pairs;
+    if (t >= p.tiles) return false;
+    a->kind = kUp;
+    a->m = t % p.tiles_m * kTile;
+    a->n = t / p.tiles_m * kHalf;
+    a->blocks = (p.D + kK - 1) / kK;
+    return true;
   }
-  return a;
+  const int dx = p.dx_tiles / pairs, more = p.dx_tiles % pairs;
+  const int mine = dx + (pair < more);
+  if (i < mine) {
+    const int t = pair + i * pairs;
+    a->kind = kDx;
+    a->m = t % p.dx_m * kTile;
+    a->n = t / p.dx_m * p.dx_width;
+    a->width = p.dx_width;
+    a->blocks = 2 * ((p.F + kK - 1) / kK);
+    return true;
+  }
+  i -= mine;
+  const int light = more ? pairs - more : 0, all = p.tiles - p.dx_tiles;
+  int first = light * p.ahead;  // tiles that go to the light pairs
+  if (first > all) first = all;
+  int t = -1;
+  if (light && pair >= more) {
+    if (i < p.ahead) {
+      t = (pair - more) + i * light;
+      if (t >= first) return false;
+    } else {
+      i -= p.ahead;
+    }
+  }
+  if (t < 0) t = first + pair + i * pairs;
+  if (t >= all) return false;
+  a->kind = kDw;
+  a->n = t % p.dw_n * kTile;
+  t /= p.dw_n;
+  a->seg = t / p.dw_m;
+  a->m = t % p.dw_m * kTile;
+  a->blocks = (p.R + kK - 1) / kK;
+  return true;
 }
 
 // Columns [c, c + 32) of an output row, from fp32.
@@ -161,13 +191,13 @@ glu_kernel(const __grid_constant__ GluParams p) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[kAccFull + i], 1);
-      mbar_init(&bars[kAccEmpty + i], 8);  // four epilogue warps of either SM
+      mbar_init(&bars[kAccEmpty + i], 2 * kEpilogue);  // of either SM
     }
     mbar_init(&bars[kDrain], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kEpilogue + 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_at)),
                  "r"(kCols)
@@ -188,16 +218,17 @@ glu_kernel(const __grid_constant__ GluParams p) {
     return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
 
-  if (warp == 4 && lane == 0) {
+  if (warp == kEpilogue && lane == 0) {
     // ------------------------------------------------------------ producer
     uint32_t it = 0;
     bool ok = true;
-    for (int t = pair; ok && t < p.tiles; t += pairs) {
-      const TileAt a = tile_at<BWD2>(p, t);
+    TileAt a;
+    for (int i = 0; ok && tile_at<BWD2>(p, pair, pairs, i, &a); ++i) {
       for (int kb = 0; kb < a.blocks; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !wait(kEmpty + s, (it / kStages - 1) & 1)) { ok = false; break; }
-        if (rank == 0) mbar_arrive_expect_tx(&bars[kFull + s], 2 * kStage);
+        if (rank == 0)
+          mbar_arrive_expect_tx(&bars[kFull + s], a.width == kTile ? 2 * kStage : kStage + kOperand);
         const uint32_t bar = first_sm(&bars[kFull + s]);
         unsigned char* sa = smem + s * kStage;
         unsigned char* sb = sa + kOperand;
@@ -208,8 +239,8 @@ glu_kernel(const __grid_constant__ GluParams p) {
           const int half = a.blocks / 2, seg = kb >= half, k = (kb - seg * half) * kK;
           load_box(sa, seg ? &p.du : &p.dg, bar, k, a.m + rank * kHalf);
           const CUtensorMap* w = seg ? &p.wum : &p.wgm;
-          load_box(sb, w, bar, a.n + rank * kHalf, k);
-          load_box(sb + kOperand / 2, w, bar, a.n + rank * kHalf + 64, k);
+          load_box(sb, w, bar, a.n + rank * (a.width / 2), k);
+          if (a.width == kTile) load_box(sb + kOperand / 2, w, bar, a.n + rank * kHalf + 64, k);
         } else {
           const CUtensorMap* d = a.seg ? &p.dum : &p.dgm;
           load_box(sa, d, bar, a.m + rank * kHalf, kb * kK);
@@ -225,14 +256,14 @@ glu_kernel(const __grid_constant__ GluParams p) {
         (void)mbar_wait_bounded(&bars[kFull + i % kStages], (i / kStages) & 1,
                                 kDefaultWaitLimitNs);
     }
-  } else if (warp == 5 && rank == 0) {
+  } else if (warp == kEpilogue + 1 && rank == 0) {
     // ------------------------------------------------------------ issuer
     uint32_t it = 0, n = 0;
     bool ok = true;
-    for (int t = pair; ok && t < p.tiles; t += pairs, ++n) {
-      const TileAt a = tile_at<BWD2>(p, t);
+    TileAt a;
+    for (; ok && tile_at<BWD2>(p, pair, pairs, n, &a); ++n) {
       const bool a_mn = a.kind == kDw, b_mn = a.kind != kUp;
-      const uint32_t idesc = idesc_bf16(kTile, kTile, false, false) | (a_mn ? 1u << 15 : 0u) |
+      const uint32_t idesc = idesc_bf16(kTile, a.width, false, false) | (a_mn ? 1u << 15 : 0u) |
                              (b_mn ? 1u << 16 : 0u);
       // along K per 16: 32 bytes of a 128-byte row, or 16 rows of 128 bytes
       const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
@@ -266,32 +297,37 @@ glu_kernel(const __grid_constant__ GluParams p) {
     }
     __syncwarp();
     (void)mbar_wait_bounded(&bars[kDrain], 0u, kDefaultWaitLimitNs);
-  } else if (warp < 4) {
+  } else if (warp < kEpilogue) {
     // ------------------------------------------------------------ epilogue
     uint32_t n = 0;
-    for (int t = pair; t < p.tiles; t += pairs, ++n) {
-      const TileAt a = tile_at<BWD2>(p, t);
-      const uint32_t acc = tmem + (n & 1) * kTile + ((uint32_t)warp << 21);
-      const int row = a.m + rank * kHalf + warp * 32 + lane;
-      if (!wait_warp(kAccFull + (n & 1), (n / 2) & 1)) break;
-      tc_fence_after();
+    TileAt a;
+    const int quad = warp & 3, half = warp >> 2;
+    for (; tile_at<BWD2>(p, pair, pairs, n, &a); ++n) {
+      const uint32_t acc = tmem + (n & 1) * kTile + ((uint32_t)quad << 21);
+      const int row = a.m + rank * kHalf + quad * 32 + lane;
       if constexpr (!BWD2) {
         const bool on = row < p.R;
-#pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        const long long at = (long long)row * p.F;
+        // dout a chunk ahead: the first one comes while the product runs
+        Raw<__nv_bfloat16, 8> h[4];
+        auto fetch = [&](int c) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[j] = on && c + 8 * j < p.F ? load_raw<__nv_bfloat16, 8>(p.d_out + at + c + 8 * j)
+                                         : zero_raw<__nv_bfloat16, 8>();
+        };
+        const int c0 = half * (kHalf / 2);
+        if (GRAD) fetch(a.n + c0);
+        if (!wait_warp(kAccFull + (n & 1), (n / 2) & 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = c0; c < c0 + kHalf / 2; c += 32) {
           uint32_t gr[32], ur[32];
           tmem_ld_32x32b_x32(acc + c, gr);
           tmem_ld_32x32b_x32(acc + kHalf + c, ur);
-          const long long at = (long long)row * p.F;
+          tmem_ld_wait_x32(gr);
+          tmem_ld_wait_x32(ur);
           if constexpr (GRAD) {
-            Raw<__nv_bfloat16, 8> h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              h[j] = on && a.n + c + 8 * j < p.F
-                         ? load_raw<__nv_bfloat16, 8>(p.d_out + at + a.n + c + 8 * j)
-                         : zero_raw<__nv_bfloat16, 8>();
-            tmem_ld_wait_x32(gr);
-            tmem_ld_wait_x32(ur);
             float dg[32], du[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -302,13 +338,12 @@ glu_kernel(const __grid_constant__ GluParams p) {
               du[j] = dh * gs;
               dg[j] = dh * u * fmaf(gs, 1.f - s, s);
             }
+            if (c == c0) fetch(a.n + c + 32);
             if (on) {
               store32(p.dg_out + at, a.n + c, p.F, dg);
               store32(p.du_out + at, a.n + c, p.F, du);
             }
           } else {
-            tmem_ld_wait_x32(gr);
-            tmem_ld_wait_x32(ur);
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -318,11 +353,14 @@ glu_kernel(const __grid_constant__ GluParams p) {
           __syncwarp();  // the next loads are the whole warp's
         }
       } else {
+        if (!wait_warp(kAccFull + (n & 1), (n / 2) & 1)) break;
+        tc_fence_after();
         const int rows = a.kind == kDx ? p.R : p.F;
         OT* out = (OT*)(a.kind == kDx ? p.dx : a.seg ? p.dwu : p.dwg) + (long long)row * p.D;
         const bool on = row < rows;
+        const int c0 = half * (a.width / 2);
 #pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
+        for (int c = c0; c < c0 + a.width / 2; c += 32) {
           uint32_t r[32];
           tmem_ld_32x32b_x32(acc + c, r);
           tmem_ld_wait_x32(r);
@@ -344,7 +382,7 @@ glu_kernel(const __grid_constant__ GluParams p) {
   __syncthreads();
   start_next();
   cluster_barrier();
-  if (warp == 5) {
+  if (warp == kEpilogue + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)
                  : "memory");
@@ -421,10 +459,16 @@ cudaError_t launch_glu_bwd(const GluBwdArgs& b, void* workspace, cudaStream_t st
       !make_map(&p.wgm, a.w_gate, a.D, a.F, a.D, kK) ||
       !make_map(&p.wum, a.w_up, a.D, a.F, a.D, kK))
     return cudaErrorInvalidValue;
-  p.dx_m = tiles_of(a.rows, kTile); p.dx_n = tiles_of(a.D, kTile);
-  p.dw_m = tiles_of(a.F, kTile); p.dw_n = p.dx_n;
-  p.dx_tiles = p.dx_m * p.dx_n;
-  p.tiles = p.dx_tiles + 2 * p.dw_m * p.dw_n;
+  p.dx_m = tiles_of(a.rows, kTile);
+  p.dw_m = tiles_of(a.F, kTile); p.dw_n = tiles_of(a.D, kTile);
+  const int dw_tiles = 2 * p.dw_m * p.dw_n;
+  // kDx tiles are the long ones: of half the width where there are pairs for them (777 rows x
+  // 520 x 1352: ...)
+  p.dx_width = p.dx_m * tiles_of(a.D, kHalf) + dw_tiles <= 76 ? kHalf : kTile;
+  p.dx_tiles = p.dx_m * tiles_of(a.D, p.dx_width);
+  p.tiles = p.dx_tiles + dw_tiles;
+  const int dx_blocks = 2 * tiles_of(a.F, kK) * p.dx_width / kTile, dw_blocks = tiles_of(a.rows, kK);
+  p.ahead = dx_blocks / dw_blocks;
   return a.fp32_out ? launch<true, false, float>(p, stream, true)
                     : launch<true, false, __nv_bfloat16>(p, stream, true);
 }
