@@ -193,42 +193,55 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
 
 // Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r; 0
 // for a row behind the last (of zeros), so that it adds nothing to sums over rows.
+// Layer norm takes the sums of x and x^2 in one exchange, which loses (mean^2 / variance) 2^-23 of
+// the variance to cancellation; rows where that would be over 2^-19 take the squares of
+// the centred values in a second one.
 template <int K, int R>
 __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec (&x)[R][K],
                                           float (&r)[R], int rows) {
-  if (a.layer) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      f32x2 m = both(0.f);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        GLA_PAIRS m = add2(m, x[i][k].v[j]);
-      r[i] = m.x + m.y;
-    }
-    g.sum(r);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const f32x2 m = both(-r[i] * a.inv_d);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (g.column(k) < a.D)
-#pragma unroll
-          GLA_PAIRS x[i][k].v[j] = add2(x[i][k].v[j], m);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
+  auto squares = [&](int i) {
     f32x2 q = both(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       GLA_PAIRS q = fma2(x[i][k].v[j], x[i][k].v[j], q);
-    r[i] = q.x + q.y;
-  }
-  g.sum(r);
+    return q.x + q.y;
+  };
+  bool far = !a.layer;  // the squares are (again) to be taken
+  if (a.layer) {
+    float m[2 * R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) r[i] = i < rows ? rsqrtf(fmaf(r[i], a.inv_d, a.eps)) : 0.f;
+    for (int i = 0; i < R; ++i) {
+      f32x2 t = both(0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        GLA_PAIRS t = add2(t, x[i][k].v[j]);
+      m[2 * i] = t.x + t.y;
+      m[2 * i + 1] = squares(i);
+    }
+    g.sum(m);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float mean = m[2 * i] * a.inv_d, var = fmaf(-mean, mean, m[2 * i + 1] * a.inv_d);
+      far |= !(mean * mean <= 16.f * var) && i < rows;
+      r[i] = var;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (g.column(k) < a.D)
+#pragma unroll
+          GLA_PAIRS x[i][k].v[j] = add2(x[i][k].v[j], both(-mean));
+    }
+  }
+  if (far) {  // (the same in all of the group's threads)
+#pragma unroll
+    for (int i = 0; i < R; ++i) r[i] = squares(i);
+    g.sum(r);
+#pragma unroll
+    for (int i = 0; i < R; ++i) r[i] *= a.inv_d;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) r[i] = i < rows ? rsqrtf(r[i] + a.eps) : 0.f;
 }
 
 }  // namespace norm

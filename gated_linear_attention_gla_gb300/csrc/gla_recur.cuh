@@ -320,10 +320,19 @@ __device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, i
                    "r"(cluster * 512)
                    : "memory");
     await(&s.given[turn], parity, status);
+    // the warps' maps in batches: the loads of one do not wait for the stores of another
+    constexpr int kBatch = 5;
     f32x2 front = state;
     if (cluster > 1) {
-      float4 all = s.warp[turn][0][lane];
-      for (int k = 1; k < warps; ++k) all = compose<STARTS>(all, s.warp[turn][k][lane]);
+      float4 all = make_float4(1.f, 1.f, 0.f, 0.f);
+      for (int k = 0; k < warps; k += kBatch) {
+        float4 m[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) m[i] = s.warp[turn][k + i < warps ? k + i : k][lane];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (k + i < warps) all = compose<STARTS>(all, m[i]);
+      }
       for (int k = 0; k < cluster; ++k)
         send(&s.block[turn][rank][lane], &s.full[turn], (rank + k) % cluster, all);
       await(&s.full[turn], parity, status);
@@ -332,9 +341,17 @@ __device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, i
         state = apply<STARTS>(s.block[turn][k][lane], state);
       }
     }
-    for (int k = 0; k < warps; ++k) {
-      s.front[turn][k][lane] = front;
-      front = apply<STARTS>(s.warp[turn][k][lane], front);
+    for (int k = 0; k < warps; k += kBatch) {
+      float4 m[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) m[i] = s.warp[turn][k + i < warps ? k + i : k][lane];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (k + i < warps) {
+          s.front[turn][k + i][lane] = front;
+          front = apply<STARTS>(m[i], front);
+        }
+      }
     }
     if (cluster == 1) state = front;
     __syncwarp();

@@ -21,7 +21,7 @@ namespace recur {
 namespace {
 
 constexpr int kWarps = 15;   // that compute, of a block (with the exchange's 16 warps of 128
-constexpr int kBlocks = 1;   // registers a thread)
+constexpr int kBlocks = 1;   // registers a thread; more warps with fewer were slower)
 template <typename T> constexpr int kRun = sizeof(T) == 4 ? 4 : 8;  // tokens of a run
 constexpr int kStages = 2;   // runs whose rows are in flight or in use, per warp
 
@@ -52,10 +52,13 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
   auto finish = [&](long long s, f32x2 h) {
     if (on) *reinterpret_cast<float2*>(a.final_state + s * a.D + c) = h;
   };
+  // The initial state has been read by every block of the cluster before the first exchange, behind
+  // which one of them may write the final state in its place (the store waits for the load).
+  if (!STARTS && w == warps) maps.front[0][0][lane] = init_of(g);
   maps_init(maps, warps, p.cluster);
 
   if (w == warps) {
-    f32x2 state = STARTS ? both(0.f) : init_of(g);
+    f32x2 state = STARTS ? both(0.f) : maps.front[0][0][lane];
     state = exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a.status);
     if (!KEEP && !STARTS && a.final_state && rank == 0) finish(g, state);
   } else {

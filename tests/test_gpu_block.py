@@ -450,9 +450,31 @@ def test_block_norm_without_some_gradients(gla):
     assert s.shape == u.shape == (0, D)
 
 
+@pytest.mark.parametrize("D", [264, 2048])
+def test_block_norm_far_means(gla, D):
+    """Layer norm of rows whose mean is 1000 deviations, or that are constant.  The mean is off by
+    2^-24 times the row's size for each of some four roundings, relative to the deviation 1."""
+    R = 37
+    g = torch.Generator().manual_seed(24)
+    x = rnd(g, R, D) + 1000.0
+    x[::3] = 500.0
+    w = torch.ones(D)
+    ref = block_ref.block_norm_all(x, None, None, None, None, None, w, None, True, 1e-5)
+    _, u = gla.block_norm_fwd(gpu(x), weight=gpu(w), kind="layer")
+    # eps = 1e-6 against 1e-5 in ref matters in no row but the constant ones, which are 0 in both
+    assert not u[::3].any()
+    other = [r for r in range(R) if r % 3]
+    err = (u.double().cpu() - ref["u"][0])[other].abs()
+    assert float(err.max()) <= 8 * 2 ** -24 * 1000 + 2 ** -17 * 5
+
+
 # ---------------------------------------------------------------- feed-forward
 GLU = [(1, 8, 8), (3, 64, 128), (8, 2048, 264), (129, 72, 136), (256, 256, 128), (257, 520, 392),
-       (300, 64, 1352), (777, 136, 264), (1000, 328, 72), (64, 1352, 520)]
+       (300, 64, 1352), (777, 136, 264), (1000, 328, 72), (64, 1352, 520),
+       # few rows: tiles of 56 features, two blocks an SM, whole and shared K, 128 and 129 rows
+       (5, 64, 8192), (9, 72, 12288), (128, 1032, 136), (16, 4104, 72),
+       # more tiles than pairs of SMs, tiles of both kinds dealt out unevenly
+       (2600, 72, 1352), (20500, 264, 72), (300, 520, 2600), (600, 520, 2600)]
 
 
 @pytest.mark.parametrize("R,D,F", GLU)
@@ -536,6 +558,120 @@ def test_glu_wait_that_runs_out(gla):
     finally:
         gla.set_wait_limit_ns(0)
     assert torch.equal(gla.glu_fwd(x, wg, wu), want)
+    gla.status_sync()
+
+
+# ---------------------------------------------------------------- all of them
+def test_offsets_beyond_32_bits(gla):
+    """Column slices of a projection of more than 2^31 elements: the last rows and columns."""
+    R, wide, D = 70001, 32768, 136
+    big = torch.empty(R, wide, dtype=torch.bfloat16, device="cuda")
+    cols = [big[:, wide - (k + 1) * D:wide - k * D] for k in range(4)]
+    g = torch.Generator(device="cuda").manual_seed(25)
+    for c in cols:
+        c.normal_(generator=g)
+    tight = [c.contiguous() for c in cols]
+    dec = -torch.rand(D, generator=g, device="cuda")
+    w = torch.ones(D, device="cuda")
+    cu = torch.tensor([0, 3, 60000, R], dtype=torch.int32).cuda()
+    wg, wu = (torch.randn(72, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    dh = torch.randn(R, 72, generator=g, device="cuda").bfloat16()
+
+    def every(x, f, i, z):
+        kw = dict(decay=dec, i=i, z=z, cu_seqlens=cu)
+        return [*gla.recur_fwd(x, f, **kw), *gla.recur_bwd(x, f, tight[0], **kw),
+                *gla.block_norm_fwd(tight[1], x, z, post_weight=w, weight=w),
+                *gla.block_norm_bwd(tight[1], tight[2], tight[0], x, z, post_weight=w, weight=w),
+                gla.glu_fwd(x, wg, wu), *gla.glu_bwd(x, wg, wu, dh)]
+
+    for a, b in zip(every(*cols), every(*tight)):
+        assert (a is None and b is None) or torch.equal(a, b)
+    n = 300
+    slots = torch.arange(n, dtype=torch.int32).cuda()
+    pools = [torch.zeros(n, D, device="cuda") for _ in range(2)]
+    y = [gla.recur_step(c[0][R - n:], c[1][R - n:], p, dec, i=c[2][R - n:], slots=slots)
+         for c, p in zip((cols, tight), pools)]
+    assert torch.equal(*y) and torch.equal(*pools)
+    gla.status_sync()
+
+
+def test_given_buffers(gla):
+    """Outputs, states and workspaces that the caller keeps."""
+    x = rnd(torch.Generator().manual_seed(26), 2, 300, 136, dtype=torch.bfloat16).cuda()
+    w = torch.ones(136).cuda()
+    wg = rnd(torch.Generator().manual_seed(27), 264, 136, dtype=torch.bfloat16).cuda()
+    y, fin = gla.recur_fwd(x, x, i=x)
+    out, state = torch.empty_like(y), torch.empty_like(fin)
+    got = gla.recur_fwd(x, x, i=x, out=out, final_state=state)
+    assert got[0] is out and got[1] is state and torch.equal(out, y) and torch.equal(state, fin)
+    assert gla.recur_fwd(x, x, i=x, output_final_state=False)[1] is None
+    ws = torch.empty(64 << 20, dtype=torch.uint8).cuda()
+    for call in (lambda **k: gla.recur_bwd(x, x, x, i=x, **k),
+                 lambda **k: gla.block_norm_bwd(x, x, x, x, post_weight=w, weight=w, **k),
+                 lambda **k: gla.glu_bwd(x, wg, wg, torch.ones(2, 300, 264).bfloat16().cuda(), **k)):
+        want = call()
+        ws.fill_(255)  # NaN: whatever is read has been written before
+        for a, b in zip(call(workspace=ws), want):
+            assert (a is None and b is None) or torch.equal(a, b)
+    h = gla.glu_fwd(x, wg, wg)
+    buf = torch.empty_like(h)
+    assert gla.glu_fwd(x, wg, wg, out=buf) is buf and torch.equal(buf, h)
+    s, u = gla.block_norm_fwd(x, x, weight=w)
+    s2, u2 = torch.empty_like(s), torch.empty_like(u)
+    gla.block_norm_fwd(x, x, weight=w, res_out=s2, out=u2)
+    assert torch.equal(s, s2) and torch.equal(u, u2)
+    gla.status_sync()
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 5000, 64), (2, 1000, 136), (1, 17, 8), (3, 260, 72)])
+def test_recur_state_in_place_again(gla, B, T, D):
+    """The final state written over the initial one, over several blocks of a cluster, repeated."""
+    g = torch.Generator().manual_seed(28)
+    x, f = rnd(g, B, T, D).cuda(), rnd(g, B, T, D, mean=3.0).cuda()
+    init = rnd(g, B, D, std=5.0).cuda()
+    want = gla.recur_fwd(x, f, init_state=init)
+    for _ in range(20):
+        state = init.clone()
+        y, fin = gla.recur_fwd(x, f, init_state=state, final_state=state)
+        assert torch.equal(y, want[0]) and torch.equal(fin, want[1])
+
+
+def test_recur_many_short_sequences(gla):
+    """A hundred thousand sequences of one to three tokens, packed, and of one token, dense."""
+    g = torch.Generator().manual_seed(29)
+    D = 64
+    lens = torch.randint(0, 4, (100003,), generator=g)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)])
+    R = int(cu[-1])
+    x, f, dy = (rnd(g, R, D).cuda() for _ in range(3))
+    init, df = rnd(g, 100003, D).cuda(), rnd(g, 100003, D).cuda()
+    cug = cu.to(torch.int32).cuda()
+    dec = -torch.rand(D, generator=g).cuda()
+    y, fin = gla.recur_fwd(x, f, dec, init_state=init, cu_seqlens=cug)
+    gr = gla.recur_bwd(x, f, dy, dec, init_state=init, d_final_state=df, cu_seqlens=cug)
+    # token by token, over all sequences at once, in 64 bits
+    d64 = lambda t: t.double()  # noqa: E731
+    _, a, m, _, _ = block_ref.decays(d64(f), d64(dec), True)
+    h, e = d64(init), d64(df)
+    start = cu[:-1].cuda()
+    ln = lens.cuda()
+    for t in range(3):
+        on = ln > t
+        rows = start[on] + t
+        h[on] = a[rows] * h[on] + m[rows] * d64(x[rows])
+        near(y[rows], (h[on].cpu(), (h[on].abs() + 1).cpu()), 2 ** -17, f"y {t}")
+    near(fin, (h.cpu(), (h.abs() + 1).cpu()), 2 ** -17, "final")
+    for t in (2, 1, 0):
+        on = ln > t
+        rows = start[on] + t
+        e[on] = e[on] + d64(dy[rows])
+        near(gr[0][rows], ((e[on] * m[rows]).cpu(), (e[on].abs() + 1).cpu()), 2 ** -17, f"dx {t}")
+        e[on] = a[rows] * e[on]
+    near(gr[5], (e.cpu(), (e.abs() + 1).cpu()), 2 ** -17, "d_init")
+    dense = gla.recur_fwd(x[:, None], f[:, None], dec)
+    step = torch.zeros(R, D).cuda()
+    out = gla.recur_step(x, f, step, dec)
+    assert torch.allclose(dense[0][:, 0], out, rtol=2 ** -19, atol=1e-6) and torch.equal(out, step)
     gla.status_sync()
 
 
