@@ -23,7 +23,9 @@ namespace {
 using namespace norm;
 
 constexpr int kSums = 4;  // A, B, d_weight, d_bias
-constexpr int kRows = 2;  // rows of a group at a time (one with two vectors a thread)
+// rows of a group at a time (one with two vectors a thread, whose sums lie in shared memory, or
+// with biases, which hold 24 registers more: 8192 x 2048 with them 93 us two at a time, 81 us one)
+template <bool BIAS> constexpr int kRows = BIAS ? 1 : 2;
 
 // The sums of a thread's columns over the rows.
 template <int K> struct Sums {
@@ -67,9 +69,7 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   Ring<K> ring(shared + g.count * kRedFloats * 4, R, kDu + kPieces<T>, stages);
   Sums<K> sums;
   sums.init(shared + g.count * kRedFloats * 4);  // (K = 2, which has no ring)
-  // (with biases 24 registers more are held: two parameters less)
-  Param<K> post, weight;
-  Param<K, K == 1 && !BIAS> scale, post_b;
+  Param<K> post, post_b, scale, weight;
   post.init(g, a.D, a.post_weight, 1.f);
   if (BIAS) post_b.init(g, a.D, a.post_bias, 0.f);
   scale.init(g, a.D, a.scale, 1.f);
@@ -101,8 +101,8 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
     const int rows = R == 1 || row + 1 >= a.rows ? 1 : 2;
     auto has = [&](int i, int k) { return g.column(k) < a.D && i < rows; };
     // (columns and rows that do not exist are zeros, without branches between the rows;
-    // columns whose parameters are not held are skipped)
-    auto skip = [&](int k) { return (K > 1 || BIAS) && g.column(k) >= a.D; };
+    // of two vectors a thread those are skipped, whose parameters are not held)
+    auto skip = [&](int k) { return K > 1 && g.column(k) >= a.D; };
     auto at = [&](int i, int k) { return (row + i) * a.D + g.column(k); };
     auto z_of = [&](int i, int k) {
       return has(i, k) ? ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k))
@@ -338,11 +338,10 @@ norm_bwd_sum_kernel(NormBwdArgs b, const float* partial, int blocks, int bias) {
   if (b.d_scale) b.d_scale[c] = fmaf(w, t.x, o * t.y);
 }
 
-// Blocks of the first launch: as many as the GPU holds at once.
+// Blocks of the first launch: as many as the GPU holds at once (and no more than rows).
 int bwd_blocks(int rows, int D) {
   const Shape s = shape_of(D);
-  const int at_once = s.groups * (s.k == 1 ? kRows : 1);
-  const long long need = ((long long)rows + at_once - 1) / at_once;
+  const long long need = ((long long)rows + s.groups - 1) / s.groups;
   const int hold = 152 * (s.tpr * s.groups <= 256 ? 2 : 1);
   return (int)(need < hold ? need : hold);
 }
@@ -352,7 +351,8 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
   const Shape s = shape_of(b.f.D);
   const int threads = s.tpr * s.groups, blocks = bwd_blocks(b.f.rows, b.f.D);
   const bool bias = b.f.post_bias || b.d_bias;
-  const int pieces = kRows * (2 * kPieces<RT> + 3 * kPieces<T>), other = s.groups * kRedFloats * 4;
+  const int pieces = (bias ? kRows<true> : kRows<false>) * (2 * kPieces<RT> + 3 * kPieces<T>);
+  const int other = s.groups * kRedFloats * 4;
   const int stages = s.k == 1 ? ring_stages(pieces, threads, other, threads <= 256 ? 2 : 1) : 1;
   int room = s.k == 1 ? stages * pieces * 16 * threads : kSums * s.k * kV * threads * 4;
   if (room < threads * kV * 4) room = threads * kV * 4;  // the groups' sums at the end
@@ -365,8 +365,8 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
   if (blocks > 0) {
     static std::atomic<uint64_t> d0{0}, d1{0}, d2{0}, d3{0};
     const cudaError_t e =
-        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows, true>, d0)
-                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows, false>, d1))
+        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows<true>, true>, d0)
+                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows<false>, false>, d1))
                  : (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, true>, d2)
                          : go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, false>, d3));
     if (e != cudaSuccess) return e;
