@@ -19,7 +19,7 @@ namespace gla {
 namespace recur {
 
 constexpr int kChans = 64;     // channels of a block: two a lane
-constexpr int kMaxWarps = 15;  // runs of a block
+constexpr int kMaxWarps = 19;  // runs of a block
 constexpr int kMaxCluster = 8;
 
 // ---------------------------------------------------------------- the gates

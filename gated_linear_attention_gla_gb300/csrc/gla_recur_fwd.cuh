@@ -20,20 +20,28 @@ namespace gla {
 namespace recur {
 namespace {
 
-constexpr int kWarps = 15;   // that compute, of a block (with the exchange's 16 warps of 128
-constexpr int kBlocks = 1;   // registers a thread; more warps with fewer were slower)
-template <typename T> constexpr int kRun = sizeof(T) == 4 ? 4 : 8;  // tokens of a run
-constexpr int kStages = 2;   // runs whose rows are in flight or in use, per warp
+// A block's shape: tokens of a run, warps that compute (the exchange's comes on top), runs of
+// a warp whose rows are in flight or in use.
+template <int RUN, int WARPS, int STAGES> struct Tile {
+  static constexpr int kRun = RUN, kWarps = WARPS, kStages = STAGES;
+};
+// Long runs spread the exchange of a cluster over more tokens and cost registers (16 warps of 128);
+// where a block walks its sequence alone short ones with more warps are faster: 8192 x 2048
+// 45 us by runs of 8, 40 us by runs of 4; 20001 packed rows in clusters of 4 92 and 134 us.
+using LongRuns = Tile<8, 15, 2>;
+using ShortRuns = Tile<4, 19, 3>;
+using WideRuns = Tile<4, 15, 2>;  // fp32 rows
+constexpr int kBlocks = 1;        // an SM
 
 // DECAY, GATE, OUT: with decay, i, z.  STARTS: a group holds several sequences.  KEEP: see above.
-template <typename T, bool DECAY, bool GATE, bool OUT, bool STARTS, bool KEEP>
-__global__ void __launch_bounds__(32 * (kWarps + 1), kBlocks)
+template <typename T, typename TILE, bool DECAY, bool GATE, bool OUT, bool STARTS, bool KEEP>
+__global__ void __launch_bounds__(32 * (TILE::kWarps + 1), kBlocks)
 recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
   start_next();
   extern __shared__ __align__(16) unsigned char shared[];
   Maps& maps = *reinterpret_cast<Maps*>(shared);
   constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int kL = kRun<T>;
+  constexpr int kL = TILE::kRun, kStages = TILE::kStages;
   constexpr int kTile = kL * kChans;  // elements of a stream
   constexpr int kStreams = 2 + GATE + OUT;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = p.warps;
@@ -246,31 +254,45 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
   if (p.cluster > 1) cluster_sync();  // (no block ends while another may still send to it)
 }
 
+template <typename T, typename TILE, bool DECAY, bool GATE, bool OUT, bool STARTS, bool KEEP>
+cudaError_t run_tile(const RecurArgs& a, const Split& p, float* kept, long long kept_rows,
+                     cudaStream_t stream) {
+  constexpr int kWarpBytes =
+      TILE::kStages * (2 + GATE + OUT) * TILE::kRun * kChans * (int)sizeof(T);
+  auto kernel = recur_kernel<T, TILE, DECAY, GATE, OUT, STARTS, KEEP>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e =
+      allow_shared(kernel, (int)sizeof(Maps) + TILE::kWarps * kWarpBytes, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)p.cols * p.groups * p.cluster));
+  cfg.blockDim = dim3(32 * (p.warps + 1));
+  cfg.dynamicSmemBytes = (int)sizeof(Maps) + p.warps * kWarpBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, p, kept, kept_rows);
+}
+
 template <typename T, bool DECAY, bool GATE, bool OUT, bool KEEP>
 cudaError_t run(const RecurArgs& a, float* kept, long long kept_rows, cudaStream_t stream) {
-  constexpr int kL = kRun<T>;
-  const Split p = split(a.B, a.T, a.D, a.cu_seqlens != nullptr, kL, kWarps, kBlocks);
-  constexpr int kWarpBytes = kStages * (2 + GATE + OUT) * kL * kChans * (int)sizeof(T);
-  const long long blocks = (long long)p.cols * p.groups * p.cluster;
-  auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
-    cudaError_t e = allow_shared(kernel, (int)sizeof(Maps) + kWarps * kWarpBytes, done);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(32 * (p.warps + 1));
-    cfg.dynamicSmemBytes = (int)sizeof(Maps) + p.warps * kWarpBytes;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, p, kept, kept_rows);
+  const bool packed = a.cu_seqlens != nullptr;
+  auto of = [&](auto tile) {
+    using TILE = decltype(tile);
+    return split(a.B, a.T, a.D, packed, TILE::kRun, TILE::kWarps, kBlocks);
   };
-  static std::atomic<uint64_t> d0{0}, d1{0};
-  return p.spg == 1 ? go(recur_kernel<T, DECAY, GATE, OUT, false, KEEP>, d0)
-                    : go(recur_kernel<T, DECAY, GATE, OUT, true, KEEP>, d1);
+  using Usual = std::conditional_t<sizeof(T) == 4, WideRuns, LongRuns>;
+  const Split p = of(Usual());
+  if (p.spg != 1) return run_tile<T, Usual, DECAY, GATE, OUT, true, KEEP>(a, p, kept, kept_rows, stream);
+  if constexpr (sizeof(T) == 2)
+    if (p.cluster == 1)
+      return run_tile<T, ShortRuns, DECAY, GATE, OUT, false, KEEP>(a, of(ShortRuns()), kept,
+                                                                   kept_rows, stream);
+  return run_tile<T, Usual, DECAY, GATE, OUT, false, KEEP>(a, p, kept, kept_rows, stream);
 }
 
 template <typename T>
