@@ -3,7 +3,7 @@
 // gla_api.cu every check runs on the host before anything is enqueued; device
 // arrays (cu_seqlens, slots) are checked by the kernels.
 #include "gla.h"
-#include "gla_checks.h"
+#include "gla_checks.cuh"
 #include "gla_internal.cuh"
 
 using namespace gla::checks;
@@ -85,7 +85,7 @@ gla_status gla_block_norm_bwd(const void* res, const void* y, int64_t y_stride, 
                                    weight, eps, rows, D, flags, &b.f);
   if (bad != GLA_OK) return bad;
   if (D == 0) return GLA_OK;
-  if ((!weight && (d_out || d_weight || d_bias)) || (d_out && !weight) ||
+  if ((!weight && (d_out || d_weight || d_bias)) ||
       (!post_weight && (d_post_weight || d_post_bias)) || (!post_bias && d_post_bias) ||
       (!scale && d_scale) || (!y && dy) || (!z && dz) ||
       (rows > 0 && (!d_res || (y && !dy) || (z && !dz))))

@@ -1,4 +1,4 @@
-// gla_checks.h -- the argument checks shared by the entry points (host code).
+// gla_checks.cuh -- the argument checks shared by the entry points (host code).
 #pragma once
 
 #include <cstddef>

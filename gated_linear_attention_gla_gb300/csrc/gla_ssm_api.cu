@@ -6,7 +6,7 @@
 #include <cstdint>
 
 #include "gla.h"
-#include "gla_checks.h"
+#include "gla_checks.cuh"
 #include "gla_internal.cuh"
 
 using namespace gla::checks;

@@ -236,3 +236,10 @@ def test_reference_glu_gradients():
     (block_ref.silu(leaves[0] @ leaves[1].t()) * (leaves[0] @ leaves[2].t()) * dh).sum().backward()
     for n, v in zip(("dx", "dwg", "dwu"), leaves):
         assert torch.allclose(got[n][0], v.grad, rtol=1e-10)
+
+
+def test_build_knows_every_source_file():
+    """A change of any file of csrc rebuilds the library."""
+    import os
+    known = {os.path.basename(p) for p in glabuild._inputs()}
+    assert set(os.listdir(glabuild.CSRC)) <= known
