@@ -21,6 +21,7 @@ __device__ __forceinline__ uint32_t cta_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -58,7 +59,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // bf16 [rows][cols], `stride` elements between rows; boxes of 64 columns x box_rows.
 inline bool make_map(CUtensorMap* map, const void* base, long long cols, long long rows,
-              long long stride, int box_rows) {
+                     long long stride, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};

@@ -51,8 +51,7 @@ __global__ void __launch_bounds__(256) recur_step_kernel(RecurStepArgs a) {
   if (a.decay) dec = __ldg(reinterpret_cast<const float4*>(a.decay + c));
   const float4 old = *reinterpret_cast<const float4*>(a.state + from * a.D + c);
   const f32x2 h0[2] = {make_float2(old.x, old.y), make_float2(old.z, old.w)};
-  const f32x2 d[2] = {make_float2(fminf(dec.x, 0.f) * kLog2e, fminf(dec.y, 0.f) * kLog2e),
-                      make_float2(fminf(dec.z, 0.f) * kLog2e, fminf(dec.w, 0.f) * kLog2e)};
+  const f32x2 d[2] = {decay_log2(make_float2(dec.x, dec.y)), decay_log2(make_float2(dec.z, dec.w))};
   f32x2 h[2];
   float y[4];
 #pragma unroll

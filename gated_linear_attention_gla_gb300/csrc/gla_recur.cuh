@@ -108,6 +108,10 @@ __device__ __forceinline__ float max_nan(float x, float y) {  // a NaN stays one
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
+// log2 of the decay at s(f) = 1 from the parameter (above 0 it counts as 0, a NaN stays one)
+__device__ __forceinline__ f32x2 decay_log2(float2 v) {
+  return make_float2((v.x > 0.f ? 0.f : v.x) * kLog2e, (v.y > 0.f ? 0.f : v.y) * kLog2e);
+}
 
 // `c`: decay log2(e) of the pair (DECAY); NEAR: it is at least kNear
 template <bool EXACT, bool DECAY, bool GATE, bool BWD, bool NEAR>
@@ -229,12 +233,14 @@ struct Maps {
   uint64_t given[2];  // the warps' maps of a step are there
   uint64_t full[2];   // counts the bytes of block[turn]
   uint64_t ready[2];  // front[turn] is there
+  int given_up;       // a wait of the block ran out
 };
 
 __device__ __forceinline__ uint32_t shared_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -253,6 +259,7 @@ __device__ __forceinline__ void maps_init(Maps& s, int warps, int cluster) {
       init(&s.full[i], 1);
       init(&s.ready[i], 1);
     }
+    s.given_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (cluster > 1) cluster_sync();
@@ -271,9 +278,10 @@ __device__ __forceinline__ void send(const void* to, const uint64_t* bar, uint32
 }
 // Waits for a phase of a barrier, for a bounded number of tests (each may hold the
 // warp for a time the hardware defines; a peer's bytes come within microseconds).
-// Then the status word says so and the call's results are undefined.  (Counted,
-// because reading the time in the loop slowed it.)
-__device__ __forceinline__ void await(const uint64_t* bar, uint32_t parity, unsigned* status) {
+// Then the status word says so, the block's other waits give up too, and the call's
+// results are undefined.  (Counted, because reading the time in the loop slowed it.)
+__device__ __forceinline__ void await(Maps& s, const uint64_t* bar, uint32_t parity,
+                                      unsigned* status) {
   for (uint32_t i = 0; i < 1u << 24; ++i) {
     uint32_t done;
     asm volatile(
@@ -284,7 +292,9 @@ __device__ __forceinline__ void await(const uint64_t* bar, uint32_t parity, unsi
         : "r"(shared_at(bar)), "r"(parity)
         : "memory");
     if (done) return;
+    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(&s.given_up)) return;
   }
+  *reinterpret_cast<volatile int*>(&s.given_up) = 1;
   atomicOr(status, kDevTimeout);
 }
 
@@ -296,7 +306,7 @@ __device__ __forceinline__ void give(Maps& s, int step, int w, int lane, float4 
 }
 // The state in front of its run of that step.
 __device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane, unsigned* status) {
-  await(&s.ready[step & 1], (step >> 1) & 1, status);
+  await(s, &s.ready[step & 1], (step >> 1) & 1, status);
   return s.front[step & 1][w][lane];
 }
 
@@ -319,7 +329,7 @@ __device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, i
                        shared_at(&s.full[turn])),
                    "r"(cluster * 512)
                    : "memory");
-    await(&s.given[turn], parity, status);
+    await(s, &s.given[turn], parity, status);
     // the warps' maps in batches: the loads of one do not wait for the stores of another
     constexpr int kBatch = 5;
     f32x2 front = state;
@@ -335,7 +345,7 @@ __device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, i
       }
       for (int k = 0; k < cluster; ++k)
         send(&s.block[turn][rank][lane], &s.full[turn], (rank + k) % cluster, all);
-      await(&s.full[turn], parity, status);
+      await(s, &s.full[turn], parity, status);
       for (int k = 0; k < cluster; ++k) {
         if (k == rank) front = state;
         state = apply<STARTS>(s.block[turn][k][lane], state);

@@ -10,6 +10,9 @@ namespace recur {
 namespace {
 
 constexpr int kL = kKeep;  // tokens of a run
+// Runs of a warp whose rows are in flight or in use (gradients of 8192 x 2048: one 107.6 us, two
+// 103.8, three 103.5 and too much shared memory for fp32).
+constexpr int kBwdStages = 2;
 
 // DECAY, GATE, OUT: with decay, i, z.  STARTS: a group holds several sequences.
 template <typename T, bool DECAY, bool GATE, bool OUT, bool STARTS>
@@ -53,10 +56,9 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
     state = exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a.status);
     if (!STARTS && rank == 0) first(g, state);
   } else {
-    // a warp's tile: its streams (x, f, dy, i, z), then the kept state
-    T* tile = reinterpret_cast<T*>(shared + sizeof(Maps) +
-                                   w * (kStreams * kTile * (int)sizeof(T) + kChans * 4));
-    float* front_h = reinterpret_cast<float*>(tile + kStreams * kTile);
+    // a warp's tiles, one for every stage: its streams (x, f, dy, i, z), then the kept state
+    constexpr int kStage = kStreams * kTile + kChans * 4 / (int)sizeof(T);
+    T* const tiles = reinterpret_cast<T*>(shared + sizeof(Maps)) + w * kBwdStages * kStage;
     long long run = runs - 1 - ((long long)rank * warps + w);  // the runs from the end
 
     Stream<T, kL> streams[kStreams];
@@ -68,7 +70,7 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
       if (GATE) streams[3].init(a.i, a.i_stride, r, back, c0, a.D, lane);
       if (OUT) streams[kStreams - 1].init(a.z, a.z_stride, r, back, c0, a.D, lane);
     }
-    auto fetch = [&](long long u) {
+    auto fetch = [&](T* tile, long long u) {
       if (u >= 0) {
         const long long left = hi - lo - u * kL;
         const int n = (int)(left < kL ? left : kL);
@@ -78,17 +80,15 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
           streams[k].next();
         }
         if (lane < 16 && c0 + 4 * lane < a.D)
-          cp_async16(front_h + 4 * lane, kept + (g * kept_rows + u) * a.D + c0 + 4 * lane);
+          cp_async16(reinterpret_cast<float*>(tile + kStreams * kTile) + 4 * lane,
+                     kept + (g * kept_rows + u) * a.D + c0 + 4 * lane);
       }
       cp_commit();
     };
-    fetch(run);
+    for (int k = 0; k < kBwdStages; ++k) fetch(tiles + k * kStage, run - k * reach);
 
     f32x2 dec = both(0.f);
-    if (DECAY && on) {
-      const float2 v = *reinterpret_cast<const float2*>(a.decay + c);
-      dec = make_float2(fminf(v.x, 0.f) * kLog2e, fminf(v.y, 0.f) * kLog2e);
-    }
+    if (DECAY && on) dec = decay_log2(*reinterpret_cast<const float2*>(a.decay + c));
     const bool near = !DECAY || __all_sync(0xffffffffu, dec.x >= kNear && dec.y >= kNear);
     Seqs seqs(a.cu_seqlens, a.B, a.T);
     if (STARTS && a.cu_seqlens != nullptr) {
@@ -115,18 +115,19 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
     };
 
     int step = 0;
+    T* tile = tiles;
     for (long long base = 0; base < runs; base += reach, run -= reach, ++step) {
       const long long r0 = lo + run * kL, at = r0 * a.D + c;
       const int n = run >= 0 ? (int)(hi - r0 < kL ? hi - r0 : kL) : 0;
       f32x2 Q[kL], K[kL], ca[kL], cx[kL], cf[kL], ci[kL], cd[kL], dz[kL];
       int seq[kL];
       unsigned starts = 0, lasts = 0;
-      cp_wait<0>();
+      cp_wait<kBwdStages - 1>();
       __syncwarp();
       f32x2 h = both(0.f);
       bool plain = n == kL;
       if (n > 0) {
-        h = pair_at(front_h, lane);
+        h = pair_at(reinterpret_cast<const float*>(tile + kStreams * kTile), lane);
         if (STARTS) {
           seqs.seek(r0);
           plain = plain && r0 != seqs.lo && r0 + kL < seqs.hi;
@@ -216,7 +217,8 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
       const float4 mine = STARTS && fresh >= 0 ? make_float4(-1.f, -1.f, e.x, e.y)
                                                : make_float4(q.x, q.y, e.x, e.y);
       give(maps, step, w, lane, mine);
-      fetch(run - reach);
+      fetch(tile, run - kBwdStages * reach);
+      tile = tile == tiles + (kBwdStages - 1) * kStage ? tiles : tile + kStage;
       if (OUT) store(b.dz, at, n, dz);
       const f32x2 behind = take(maps, step, w, lane, a.status);
       f32x2 v[kL];
@@ -254,7 +256,8 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
 template <typename T, bool DECAY, bool GATE, bool OUT>
 cudaError_t run(const RecurBwdArgs& b, const Split& p, const float* kept, long long kept_rows,
                 float* partial, cudaStream_t stream) {
-  constexpr int kWarpBytes = (3 + GATE + OUT) * kL * kChans * (int)sizeof(T) + kChans * 4;
+  constexpr int kWarpBytes =
+      kBwdStages * ((3 + GATE + OUT) * kL * kChans * (int)sizeof(T) + kChans * 4);
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
     cudaError_t e = allow_shared(kernel, (int)sizeof(Maps) + kBwdWarps * kWarpBytes, done);
     if (e != cudaSuccess) return e;

@@ -92,10 +92,7 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
     for (int k = 0; k < kStages; ++k) fetch(tiles + k * kStreams * kTile, row0 + k * reach);
 
     f32x2 dec = both(0.f);
-    if (DECAY && on) {
-      const float2 v = *reinterpret_cast<const float2*>(a.decay + c);
-      dec = make_float2(fminf(v.x, 0.f) * kLog2e, fminf(v.y, 0.f) * kLog2e);
-    }
+    if (DECAY && on) dec = decay_log2(*reinterpret_cast<const float2*>(a.decay + c));
     Seqs seqs(a.cu_seqlens, a.B, a.T);
     if (STARTS && a.cu_seqlens != nullptr) {
       if (c0 == 0)

@@ -311,6 +311,41 @@ def test_recur_closed_gates(gla):
     assert torch.equal(fin, init)
 
 
+@pytest.mark.parametrize("T,lens", [(40, None), (4000, None), (78, [17, 1, 60])])
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_recur_decay_of_nan(gla, io, T, lens):
+    """A channel whose decay is NaN is NaN from its first token on, and the other channels
+    have the bits they have beside a finite one (below -2 ln 2, so that either way the
+    warp's exponential is the one for all decays)."""
+    D = 72
+    x = recur_inputs(lens or [T], D, io, True, True, True, True, 21)
+    kw = dict(i=gpu(x["i"]), z=gpu(x["z"]), init_state=gpu(x["init"]))
+    rows = [gpu(x["x"]), gpu(x["f"]), gpu(x["dy"])]
+    if lens is None:
+        rows = [v[None] for v in rows]
+        kw["i"], kw["z"] = kw["i"][None], kw["z"][None]
+    else:
+        kw["cu_seqlens"] = torch.tensor(cu_of(lens), dtype=torch.int32).cuda()
+    decay = gpu(x["decay"]).clone()
+    decay[[3, 65]] = -4.0
+    bad = decay.clone()
+    bad[[3, 65]] = float("nan")
+    fine = [c for c in range(D) if c not in (3, 65)]
+
+    def run(d):
+        y, fin = gla.recur_fwd(rows[0], rows[1], d, **kw)
+        g = gla.recur_bwd(rows[0], rows[1], rows[2], d, d_final_state=gpu(x["df"]), **kw)
+        tok = [v.reshape(-1, D)[:1].contiguous() for v in (rows[0], rows[1], kw["i"], kw["z"])]
+        state = kw["init_state"][:1].clone()
+        out = gla.recur_step(tok[0], tok[1], state, d, tok[2], tok[3])
+        return [y, fin, *g, out, state]
+
+    for p, q in zip(run(decay), run(bad)):
+        assert torch.equal(p[..., fine], q[..., fine])
+        assert not torch.isnan(p).any() and torch.isnan(q[..., [3, 65]]).all()
+    gla.status_sync()
+
+
 def test_recur_malformed_offsets(gla):
     R, D = 64, 64
     g = torch.Generator().manual_seed(15)
