@@ -143,6 +143,12 @@ template <int K, bool HELD = K == 1> struct Param {
 // barrier.  Sixteen-byte pieces of all threads lie side by side, `per` a row.  With two
 // vectors a thread (whose rows would not fit) the reads go to memory themselves.
 constexpr int kMaxStages = 3;
+__device__ __forceinline__ void cp_async16_or_0(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
 template <typename T> constexpr int kPieces = kV * (int)sizeof(T) / 16;  // of a vector
 template <int K> struct Ring {
   unsigned char* at;  // the thread's piece 0 of stage 0
@@ -157,6 +163,16 @@ template <int K> struct Ring {
     for (int i = 0; i < kPieces<T>; ++i)
       cp_async16(at + (slot * pieces + row * per + first + i) * hop,
                  (const unsigned char*)from + 16 * i);
+  }
+  // The same, or zeros, so that the reads need not ask (gradients of 8192 x 2048 82 -> 78 us; the
+  // forward, whose time is its memory's, loses by it: 85 -> 91 us).
+  template <typename T>
+  __device__ __forceinline__ void copy_or_0(int slot, int row, int first, const T* from,
+                                            bool on) const {
+#pragma unroll
+    for (int i = 0; i < kPieces<T>; ++i)
+      cp_async16_or_0(at + (slot * pieces + row * per + first + i) * hop,
+                      (const unsigned char*)from + 16 * i, on);
   }
   // The slot of the rows that are stages - 1 turns ahead.
   __device__ __forceinline__ int ahead() const { return stage == 0 ? stages - 1 : stage - 1; }
@@ -192,11 +208,14 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
 }
 
 // Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r; 0
-// for a row behind the last (of zeros), so that it adds nothing to sums over rows.
+// for a row behind the last (of zeros), so that it adds nothing to sums over rows.  KIND: which
+// of the norms, where the caller knows.
 // Layer norm takes the sums of x and x^2 in one exchange, which loses (mean^2 / variance) 2^-23 of
 // the variance to cancellation; rows where that would be over 2^-19 take the squares of
 // the centred values in a second one.
-template <int K, int R>
+enum Kind { kRms, kEither };
+__device__ __forceinline__ bool far_mean(float mean, float var) { return !(mean * mean <= 16.f * var); }
+template <int K, int R, int KIND = kEither>
 __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec (&x)[R][K],
                                           float (&r)[R], int rows) {
   auto squares = [&](int i) {
@@ -207,8 +226,9 @@ __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec
       GLA_PAIRS q = fma2(x[i][k].v[j], x[i][k].v[j], q);
     return q.x + q.y;
   };
-  bool far = !a.layer;  // the squares are (again) to be taken
-  if (a.layer) {
+  const bool layer = KIND != kRms && a.layer;
+  bool far = !layer;  // the squares are (again) to be taken
+  if (layer) {
     float m[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -224,7 +244,7 @@ __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float mean = m[2 * i] * a.inv_d, var = fmaf(-mean, mean, m[2 * i + 1] * a.inv_d);
-      far |= !(mean * mean <= 16.f * var) && i < rows;
+      far |= far_mean(mean, var) && i < rows;
       r[i] = var;
 #pragma unroll
       for (int k = 0; k < K; ++k)

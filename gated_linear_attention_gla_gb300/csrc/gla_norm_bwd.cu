@@ -15,6 +15,8 @@
 // block, which a second launch sums in block order.  No atomics: the same inputs
 // give the same bits.
 // Bound: HBM.
+#include <type_traits>
+
 #include "gla_norm.cuh"
 
 namespace gla {
@@ -23,9 +25,10 @@ namespace {
 using namespace norm;
 
 constexpr int kSums = 4;  // A, B, d_weight, d_bias
-// rows of a group at a time (one with two vectors a thread, whose sums lie in shared memory, or
-// with biases, which hold 24 registers more: 8192 x 2048 with them 93 us two at a time, 81 us one)
-template <bool BIAS> constexpr int kRows = BIAS ? 1 : 2;
+// Rows of a group at a time: two, or one with two vectors a thread (whose sums lie in shared memory)
+// and of the kernel for layer norm and biases, which holds 24 registers more and has four sums a
+// row for one exchange (8192 x 2048, layer norm with biases: 93 us two at a time, 78 us one).
+constexpr int rows_of(int kind) { return kind == kRms ? 2 : 1; }
 
 // The sums of a thread's columns over the rows.
 template <int K> struct Sums {
@@ -56,12 +59,13 @@ template <int K> struct Sums {
   }
 };
 
-// R: rows at a time; BIAS: layer norm's biases (post_bias, d_post_bias, d_bias)
-template <typename T, typename RT, typename GT, typename GRT, int K, int R, bool BIAS>
+// R: rows at a time; KIND: kRms (without biases), or kEither of the norms with what biases there are
+template <typename T, typename RT, typename GT, typename GRT, int K, int R, int KIND>
 __global__ void __launch_bounds__(512, 1)
 norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
   start_next();
   extern __shared__ __align__(16) unsigned char shared[];
+  constexpr bool RMS = KIND == kRms, BIAS = !RMS;
   const NormArgs& a = b.f;
   const Group g(tpr, (float*)shared);
   // pieces of a row: res, ds, y, z, du
@@ -80,14 +84,15 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
       const int c = g.column(0);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (row + i < a.rows && c < a.D) {
-          const long long at = (row + i) * a.D + c;
-          ring.copy(slot, i, 0, (const RT*)a.res + at);
-          if (b.d_res_out) ring.copy(slot, i, kDs, (const RT*)b.d_res_out + at);
-          if (a.y) ring.copy(slot, i, kY, (const T*)a.y + (row + i) * a.y_stride + c);
-          if (a.z) ring.copy(slot, i, kZ, (const T*)a.z + (row + i) * a.z_stride + c);
-          if (b.d_out) ring.copy(slot, i, kDu, (const T*)b.d_out + at);
-        }
+        const bool on = row + i < a.rows && c < a.D;
+        const long long r = on ? row + i : 0;
+        const int to = on ? c : 0;
+        const long long at = r * a.D + to;
+        ring.copy_or_0(slot, i, 0, (const RT*)a.res + at, on);
+        if (b.d_res_out) ring.copy_or_0(slot, i, kDs, (const RT*)b.d_res_out + at, on);
+        if (a.y) ring.copy_or_0(slot, i, kY, (const T*)a.y + r * a.y_stride + to, on);
+        if (a.z) ring.copy_or_0(slot, i, kZ, (const T*)a.z + r * a.z_stride + to, on);
+        if (b.d_out) ring.copy_or_0(slot, i, kDu, (const T*)b.d_out + at, on);
       }
       cp_commit();
     }
@@ -100,19 +105,20 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
     // whether the thread has channels of row i
     const int rows = R == 1 || row + 1 >= a.rows ? 1 : 2;
     auto has = [&](int i, int k) { return g.column(k) < a.D && i < rows; };
+    auto there = [&](int i, int k) { return K == 1 || has(i, k); };  // to be read
     // (columns and rows that do not exist are zeros, without branches between the rows;
     // of two vectors a thread those are skipped, whose parameters are not held)
     auto skip = [&](int k) { return K > 1 && g.column(k) >= a.D; };
     auto at = [&](int i, int k) { return (row + i) * a.D + g.column(k); };
     auto z_of = [&](int i, int k) {
-      return has(i, k) ? ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k))
+      return there(i, k) ? ring.read(i, kZ, (const T*)a.z + (row + i) * a.z_stride + g.column(k))
                        : vec_of(0.f);
     };
     auto du_of = [&](int i, int k) {
-      return has(i, k) ? ring.read(i, kDu, (const T*)b.d_out + at(i, k)) : vec_of(0.f);
+      return there(i, k) ? ring.read(i, kDu, (const T*)b.d_out + at(i, k)) : vec_of(0.f);
     };
     auto ds_of = [&](int i, int k) {
-      return b.d_res_out && has(i, k) ? ring.read(i, kDs, (const RT*)b.d_res_out + at(i, k))
+      return b.d_res_out && there(i, k) ? ring.read(i, kDs, (const RT*)b.d_res_out + at(i, k))
                                       : vec_of(0.f);
     };
     Vec s[R][K], p[R][K];
@@ -122,14 +128,14 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
       ry[i] = 1.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        s[i][k] = has(i, k) ? ring.read(i, 0, (const RT*)a.res + at(i, k)) : vec_of(0.f);
-        p[i][k] = a.y && has(i, k)
+        s[i][k] = there(i, k) ? ring.read(i, 0, (const RT*)a.res + at(i, k)) : vec_of(0.f);
+        p[i][k] = a.y && there(i, k)
                       ? ring.read(i, kY, (const T*)a.y + (row + i) * a.y_stride + g.column(k))
                       : vec_of(0.f);
       }
     }
     if (a.post_weight) {
-      normalise<K, R>(g, a, p, ry, rows);
+      normalise<K, R, KIND>(g, a, p, ry, rows);
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -166,40 +172,103 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         }
       }
       float r[R], m[2 * R];
-      normalise<K, R>(g, a, s, r, rows);
+      if constexpr (RMS) {
+        // mean(dn n) = r mean(dn s): its sum goes with that of the squares
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        f32x2 mx = both(0.f), my = both(0.f);
+        for (int i = 0; i < R; ++i) {
+          f32x2 q = both(0.f), mx = both(0.f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (skip(k)) continue;
-          const Vec d = du_of(i, k), w = weight.at(g.column(k));
+          for (int k = 0; k < K; ++k) {
+            if (skip(k)) continue;
+            const Vec d = du_of(i, k), w = weight.at(g.column(k));
 #pragma unroll
-          GLA_PAIRS {
-            const f32x2 n = mul2(s[i][k].v[j], both(r[i]));
-            s[i][k].v[j] = n;
-            sums.add(2, k, j, d.v[j], n);
-            if (BIAS) sums.add(3, k, j, d.v[j], both(1.f));
-            const f32x2 dn = mul2(d.v[j], w.v[j]);
-            mx = fma2(dn, n, mx);
-            my = add2(my, dn);
+            GLA_PAIRS {
+              q = fma2(s[i][k].v[j], s[i][k].v[j], q);
+              mx = fma2(mul2(d.v[j], w.v[j]), s[i][k].v[j], mx);
+            }
+          }
+          m[2 * i] = q.x + q.y;
+          m[2 * i + 1] = mx.x + mx.y;
+        }
+        g.sum(m);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          r[i] = i < rows ? rsqrtf(fmaf(m[2 * i], a.inv_d, a.eps)) : 0.f;
+          const f32x2 mx = both(-m[2 * i + 1] * r[i] * a.inv_d);
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (skip(k)) continue;
+            const Vec d = du_of(i, k), e = ds_of(i, k), w = weight.at(g.column(k));
+#pragma unroll
+            GLA_PAIRS {
+              const f32x2 n = mul2(s[i][k].v[j], both(r[i]));
+              sums.add(2, k, j, d.v[j], n);
+              s[i][k].v[j] = fma2(both(r[i]), fma2(n, mx, mul2(d.v[j], w.v[j])), e.v[j]);
+            }
           }
         }
-        m[2 * i] = mx.x + mx.y;
-        m[2 * i + 1] = my.x + my.y;
-      }
-      g.sum(m);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const f32x2 mx = both(-m[2 * i] * a.inv_d);
-        const f32x2 my = both(a.layer ? -m[2 * i + 1] * a.inv_d : 0.f);
+      } else {
+        // the same beside the sums of layer norm, whose mean comes out of both afterwards: mean(dn n) =
+        // r (mean(dn s) - mean(s) mean(dn)), with normalise's second exchange where it has one
+        static_assert(R == 1, "four sums at a time");
+        float v[4] = {};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (skip(k)) continue;
-          const Vec d = du_of(i, k), e = ds_of(i, k), w = weight.at(g.column(k));
+          const Vec d = du_of(0, k), w = weight.at(g.column(k));
+          f32x2 t[4] = {};
 #pragma unroll
-          GLA_PAIRS s[i][k].v[j] = fma2(
-              both(r[i]), fma2(s[i][k].v[j], mx, fma2(d.v[j], w.v[j], my)), e.v[j]);
+          GLA_PAIRS {
+            const f32x2 x = s[0][k].v[j], dn = mul2(d.v[j], w.v[j]);
+            t[0] = add2(t[0], x);
+            t[1] = fma2(x, x, t[1]);
+            t[2] = add2(t[2], dn);
+            t[3] = fma2(dn, x, t[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += t[e].x + t[e].y;
+        }
+        g.sum(v);
+        const float mean = a.layer ? v[0] * a.inv_d : 0.f;
+        float var = fmaf(-mean, mean, v[1] * a.inv_d), mx1 = fmaf(-mean, v[2], v[3]);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (g.column(k) < a.D)
+#pragma unroll
+            GLA_PAIRS s[0][k].v[j] = add2(s[0][k].v[j], both(-mean));
+        if (far_mean(mean, var)) {
+          float c[2] = {};
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (skip(k)) continue;
+            const Vec d = du_of(0, k), w = weight.at(g.column(k));
+            f32x2 t[2] = {};
+#pragma unroll
+            GLA_PAIRS {
+              t[0] = fma2(s[0][k].v[j], s[0][k].v[j], t[0]);
+              t[1] = fma2(mul2(d.v[j], w.v[j]), s[0][k].v[j], t[1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) c[e] += t[e].x + t[e].y;
+          }
+          g.sum(c);
+          var = c[0] * a.inv_d;
+          mx1 = c[1];
+        }
+        r[0] = rsqrtf(var + a.eps);
+        const f32x2 mx = both(-mx1 * r[0] * a.inv_d);
+        const f32x2 my = both(a.layer ? -v[2] * a.inv_d : 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (skip(k)) continue;
+          const Vec d = du_of(0, k), e = ds_of(0, k), w = weight.at(g.column(k));
+#pragma unroll
+          GLA_PAIRS {
+            const f32x2 n = mul2(s[0][k].v[j], both(r[0]));
+            sums.add(2, k, j, d.v[j], n);
+            sums.add(3, k, j, d.v[j], both(1.f));
+            s[0][k].v[j] = fma2(both(r[0]), fma2(n, mx, fma2(d.v[j], w.v[j], my)), e.v[j]);
+          }
         }
       }
     } else {
@@ -215,7 +284,8 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         if (has(i, k)) store_vec((GRT*)b.d_res + at(i, k), s[i][k]);
     if (!a.y) continue;
     // s becomes dp, then dy
-    float m[2 * R];
+    constexpr int kMeans = RMS ? 1 : 2;
+    float m[kMeans * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       f32x2 mx = both(0.f), my = both(0.f);
@@ -253,20 +323,21 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
           }
         }
       }
-      m[2 * i] = mx.x + mx.y;
-      m[2 * i + 1] = my.x + my.y;
+      m[kMeans * i] = mx.x + mx.y;
+      if (!RMS) m[kMeans * i + kMeans - 1] = my.x + my.y;
     }
     if (a.post_weight) {
       g.sum(m);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const f32x2 mx = both(-m[2 * i] * a.inv_d);
-        const f32x2 my = both(a.layer ? -m[2 * i + 1] * a.inv_d : 0.f);
+        const f32x2 mx = both(-m[kMeans * i] * a.inv_d);
+        const f32x2 my = both(a.layer ? -m[kMeans * i + kMeans - 1] * a.inv_d : 0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
           GLA_PAIRS s[i][k].v[j] =
-              mul2(both(ry[i]), fma2(p[i][k].v[j], mx, add2(s[i][k].v[j], my)));
+              mul2(both(ry[i]),
+                   fma2(p[i][k].v[j], mx, RMS ? s[i][k].v[j] : add2(s[i][k].v[j], my)));
       }
     }
 #pragma unroll
@@ -351,7 +422,8 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
   const Shape s = shape_of(b.f.D);
   const int threads = s.tpr * s.groups, blocks = bwd_blocks(b.f.rows, b.f.D);
   const bool bias = b.f.post_bias || b.d_bias;
-  const int pieces = (bias ? kRows<true> : kRows<false>) * (2 * kPieces<RT> + 3 * kPieces<T>);
+  const int kind = bias || b.f.layer ? kEither : kRms;
+  const int pieces = rows_of(kind) * (2 * kPieces<RT> + 3 * kPieces<T>);
   const int other = s.groups * kRedFloats * 4;
   const int stages = s.k == 1 ? ring_stages(pieces, threads, other, threads <= 256 ? 2 : 1) : 1;
   int room = s.k == 1 ? stages * pieces * 16 * threads : kSums * s.k * kV * threads * 4;
@@ -363,18 +435,20 @@ cudaError_t run_bwd(const NormBwdArgs& b, float* partial, cudaStream_t stream) {
     return cudaGetLastError();
   };
   if (blocks > 0) {
-    static std::atomic<uint64_t> d0{0}, d1{0}, d2{0}, d3{0};
-    const cudaError_t e =
-        s.k == 1 ? (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows<true>, true>, d0)
-                         : go(norm_bwd_kernel<T, RT, GT, GRT, 1, kRows<false>, false>, d1))
-                 : (bias ? go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, true>, d2)
-                         : go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, false>, d3));
+    auto of = [&](auto k) {
+      constexpr int KIND = decltype(k)::value;
+      static std::atomic<uint64_t> d0{0}, d1{0};
+      return s.k == 1 ? go(norm_bwd_kernel<T, RT, GT, GRT, 1, rows_of(KIND), KIND>, d0)
+                      : go(norm_bwd_kernel<T, RT, GT, GRT, 2, 1, KIND>, d1);
+    };
+    const cudaError_t e = kind == kRms ? of(std::integral_constant<int, kRms>())
+                                       : of(std::integral_constant<int, kEither>());
     if (e != cudaSuccess) return e;
   }
   if (!b.d_post_weight && !b.d_post_bias && !b.d_scale && !b.d_weight && !b.d_bias)
     return cudaSuccess;
   return launch_after(norm_bwd_sum_kernel, dim3((b.f.D + 31) / 32, 2), dim3(32, 32), 0, stream, b,
-                      (const float*)partial, blocks, (int)bias);
+                      (const float*)partial, blocks, (int)(kind != kRms));
 }
 
 }  // namespace
