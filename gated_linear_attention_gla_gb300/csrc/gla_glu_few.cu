@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1) glu_few_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
+  after_previous();
+  start_next();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return wait_for(bar, parity, p.wait_ns, &abort_flag, p.status);
   };
@@ -194,17 +196,19 @@ cudaError_t launch_few(const GluArgs& a, cudaStream_t stream) {
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
     const cudaError_t e = allow_shared(kernel, 226 * 1024, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(tiles * split);
     c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = room + 1024;
     c.stream = stream;
-    c.attrs = &attr;
-    c.numAttrs = 1;
+    c.attrs = attr;
+    c.numAttrs = 2;
     return cudaLaunchKernelEx(&c, kernel, p, split);
   };
   static std::atomic<uint64_t> d0{0}, d1{0};

@@ -27,6 +27,8 @@ __global__ void __launch_bounds__(512, 1)
 norm_fwd_kernel(NormArgs a, int tpr, int stages) {
   extern __shared__ __align__(16) unsigned char shared[];
   const Group g(tpr, (float*)shared);
+  after_previous();
+  start_next();
   constexpr int kY = kPieces<RT>, kZ = kY + kPieces<T>;  // pieces behind res
   Ring<K> ring(shared + g.count * kRedFloats * 4, R, kZ + kPieces<T>, stages);
   Param<K> post, post_b, scale, weight, bias;
@@ -142,8 +144,8 @@ cudaError_t run_fwd(const NormArgs& a, cudaStream_t stream) {
     const long long need = (a.rows + s.groups * R - 1) / (s.groups * R);
     const cudaError_t e = allow_shared(kernel, 227 * 1024, done);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(need < hold ? need : hold), threads, smem, stream>>>(a, s.tpr, stages);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3((unsigned)(need < hold ? need : hold)), dim3(threads), smem,
+                        stream, a, s.tpr, stages);
   };
   static std::atomic<uint64_t> d[6];
   const bool bias = a.post_bias || a.bias;

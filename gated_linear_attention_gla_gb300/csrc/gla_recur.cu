@@ -27,6 +27,8 @@ namespace {
 
 template <typename T, typename OT>
 __global__ void __launch_bounds__(256) recur_step_kernel(RecurStepArgs a) {
+  after_previous();
+  start_next();
   const long long n = (long long)blockIdx.z * gridDim.y + blockIdx.y;
   const int c = ((int)blockIdx.x * (int)blockDim.x + (int)threadIdx.x) * 4;
   if (c >= a.D || n >= a.N) return;
@@ -85,10 +87,10 @@ cudaError_t launch_recur_step(const RecurStepArgs& a, cudaStream_t stream) {
   const unsigned ny = a.N < 32768 ? (unsigned)a.N : 32768u;
   const dim3 grid((unsigned)((vecs + threads - 1) / threads), ny, (unsigned)((a.N + ny - 1) / ny));
   using bf16 = __nv_bfloat16;
-  if (a.fp32_io) recur::recur_step_kernel<float, float><<<grid, threads, 0, stream>>>(a);
-  else if (a.fp32_out) recur::recur_step_kernel<bf16, float><<<grid, threads, 0, stream>>>(a);
-  else recur::recur_step_kernel<bf16, bf16><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.fp32_io    ? recur::recur_step_kernel<float, float>
+                      : a.fp32_out ? recur::recur_step_kernel<bf16, float>
+                                   : recur::recur_step_kernel<bf16, bf16>,
+                      grid, dim3(threads), 0, stream, a);
 }
 
 }  // namespace gla

@@ -37,6 +37,7 @@ constexpr int kBlocks = 1;        // an SM
 template <typename T, typename TILE, bool DECAY, bool GATE, bool OUT, bool STARTS, bool KEEP>
 __global__ void __launch_bounds__(32 * (TILE::kWarps + 1), kBlocks)
 recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
+  after_previous();
   start_next();
   extern __shared__ __align__(16) unsigned char shared[];
   Maps& maps = *reinterpret_cast<Maps*>(shared);
@@ -261,17 +262,19 @@ cudaError_t run_tile(const RecurArgs& a, const Split& p, float* kept, long long 
   const cudaError_t e =
       allow_shared(kernel, (int)sizeof(Maps) + TILE::kWarps * kWarpBytes, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)p.cols * p.groups * p.cluster));
   cfg.blockDim = dim3(32 * (p.warps + 1));
   cfg.dynamicSmemBytes = (int)sizeof(Maps) + p.warps * kWarpBytes;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, p, kept, kept_rows);
 }
 
