@@ -190,7 +190,8 @@ def block_norm_bwd(res, d_out=None, d_res_out=None, y=None, z=None, post_weight=
     ``d_out`` (the rows' dtype) and ``d_res_out`` (res's dtype) are the gradients of the
     forward's outputs, contiguous, None for zero.  d_res comes in res's dtype, dy
     and dz in y's, all fp32 with ``grad_dtype=torch.float32``; the parameters' gradients
-    are fp32; gradients of what was not given are None.
+    are fp32; gradients of what was not given are None, and without ``d_out`` those of
+    ``weight`` and ``bias`` (which are zero) too.
     """
     dtype = y.dtype if y is not None else d_out.dtype if d_out is not None else res.dtype
     check(d_out is None or weight is not None, "d_out needs weight")

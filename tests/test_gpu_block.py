@@ -346,6 +346,14 @@ def test_recur_decay_of_nan(gla, io, T, lens):
     gla.status_sync()
 
 
+@pytest.mark.parametrize("B,T,D", [(100, 20, 264), (3, 127, 72), (3, 128, 72), (400, 1, 200)])
+def test_recur_equal_sequences(gla, B, T, D):
+    """Dense sequences that share a group (three by three with a last group of one, in many) and
+    that do not."""
+    x = recur_inputs([T] * B, D, "bf16", True, True, True, True, 22)
+    recur_check(gla, x, [T] * B, False, True, "bf16")
+
+
 def test_recur_malformed_offsets(gla):
     R, D = 64, 64
     g = torch.Generator().manual_seed(15)
