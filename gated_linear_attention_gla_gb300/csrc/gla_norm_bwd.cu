@@ -14,8 +14,8 @@
 // sums would not fit), are summed over a block's groups and written as one partial a
 // block, which a second launch sums in block order.  No atomics: the same inputs
 // give the same bits.
-// Bound: issue slots (53 %; 95 instructions an element before, some 80 now) and the latency of
-// three exchanges a row.  8192 x 2048, layer norm, gate and scale 73 us, 3.7 TB/s.
+// Bound: issue slots (54 % of the cycles, 85 instructions an element) and the latency of three
+// exchanges a row.  8192 x 2048, layer norm, gate and scale 73 us, 3.7 TB/s.
 #include <type_traits>
 
 #include "gla_norm.cuh"

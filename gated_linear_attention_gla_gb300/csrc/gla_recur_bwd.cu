@@ -12,7 +12,7 @@
 // registers (each gradient is e times one number), and the map (Q_t, K_t) of e over the
 // run is composed as in the forward.  d_decay: sums in registers over a thread's tokens, partials per
 // block, summed in block order by a third launch.  No atomics.
-// Bound: issue slots (54 % of the cycles, 84 instructions an element) and the wait for the states
+// Bound: issue slots (61 % of the cycles, 88 instructions an element) and the wait for the states
 // between a run's two halves, whose factors leave no registers for another run in between.
 // 8192 x 2048 with three gates 104 us, 2.9 TB/s of what has to be moved.
 #include "gla_recur.cuh"

@@ -9,7 +9,7 @@
 // map (P_t, H_t) of every token in registers; second pass, with the state in front
 // of the run: h_t = P_t h + H_t.
 // Bound: issue slots.  8192 x 2048 with three gates 39 us (4.3 TB/s; issue 68 %, 128 of 152 SMs have a
-// block), 20001 packed rows with two 88 us (3.7 TB/s; issue 52 %, the cluster's exchange).
+// block), 20001 packed rows with two 88 us (3.7 TB/s; issue 55 %, the cluster's exchange).
 // The same kernel without its outputs (KEEP) writes the state in front of every
 // kKeep tokens for the backward pass.
 #pragma once

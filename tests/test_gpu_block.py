@@ -863,3 +863,61 @@ def test_streams(gla):
     s.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_another_stream(gla, captured):
+    """A call on what a slow kernel of another stream writes waits for it, right behind a launch
+    that lets the next one start early, eagerly and captured."""
+    g = torch.Generator().manual_seed(62)
+    R, D = 96, 128
+    src = rnd(g, R, D, dtype=torch.bfloat16).cuda()
+    w, decay = torch.ones(D).cuda(), -torch.rand(D, generator=g).cuda()
+    wg, wu = (rnd(g, D, D, std=D ** -0.5, dtype=torch.bfloat16).cuda() for _ in range(2))
+    big = rnd(g, 4096, 4096, std=4096 ** -0.5, dtype=torch.bfloat16).cuda()
+    state0 = rnd(g, R, D).cuda()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    inputs = [torch.zeros_like(src) for _ in range(4)]
+
+    def late(x):  # x holds src once the side stream has come that far
+        x.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            t = big
+            for _ in range(8):
+                t = t @ big
+            x.copy_(src)
+        main.wait_stream(side)
+
+    def run(wait):
+        state = state0.clone()
+        f = gla.glu_fwd(src, wg, wu)
+        wait(inputs[0])
+        y = gla.recur_fwd(inputs[0][None], f[None], decay)[0][0]
+        wait(inputs[1])
+        s, u = gla.block_norm_fwd(inputs[1], y, weight=w)
+        wait(inputs[2])
+        h = gla.glu_fwd(inputs[2], wg, wu)
+        wait(inputs[3])
+        t = gla.recur_step(inputs[3], h, state, decay)
+        return y, s, u, h, t, state
+
+    want = run(lambda x: x.copy_(src))
+    torch.cuda.synchronize()
+    if captured:
+        with torch.cuda.stream(main):
+            run(late)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            got = run(late)
+        for _ in range(3):
+            graph.replay()
+    else:
+        with torch.cuda.stream(main):
+            for _ in range(3):
+                got = run(late)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    gla.status_sync()
