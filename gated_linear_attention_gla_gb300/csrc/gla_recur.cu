@@ -94,7 +94,7 @@ cudaError_t launch_recur_fwd(const RecurArgs& a, cudaStream_t stream) {
 cudaError_t launch_recur_step(const RecurStepArgs& a, cudaStream_t stream) {
   const int vecs = a.D / 4;
   const int threads = vecs >= 128 ? 128 : (vecs + 31) / 32 * 32;
-  const unsigned ny = a.N < 32768 ? (unsigned)a.N : 32768u;
+  const unsigned ny = a.N < 65535 ? (unsigned)a.N : 65535u;  // (2^31 - 1 rows are 32769 times as many)
   const dim3 grid((unsigned)((vecs + threads - 1) / threads), ny, (unsigned)((a.N + ny - 1) / ny));
   using bf16 = __nv_bfloat16;
   return launch_after(a.fp32_io    ? recur::recur_step_kernel<float, float>
