@@ -14,16 +14,17 @@ Split split(int B, int T, int D, bool packed, int run, int most, int blocks) {
   p.spg = 1;
   if (T > 0 && T < 128) {
     const int groups = p.cols < 152 ? 152 / p.cols : 1;  // of one wave of blocks
-    const int most = B / groups + (B % groups != 0);
+    const int share = B / groups + (B % groups != 0);
     p.spg = (512 + T - 1) / T;
-    if (p.spg > most) p.spg = most;
+    if (p.spg > share) p.spg = share;
   }
   if (packed) p.spg = 0;
   if (p.spg > B) p.spg = B;
   p.groups = packed ? 1 : ((long long)B + p.spg - 1) / (p.spg > 0 ? p.spg : 1);
   p.rows = packed ? T : (long long)p.spg * T;
   const long long units = (long long)p.cols * p.groups;
-  // enough blocks to fill the SMs, while every block has tokens
+  // as many blocks as the SMs hold, while every block has tokens (2048 channels, 4 sequences of 256
+  // tokens 8.9 us, with twice the blocks 15.4 us)
   p.warps = most;
   p.cluster = 1;
   while (p.cluster < kMaxCluster && units * p.cluster * 2 <= blocks * 152 &&
