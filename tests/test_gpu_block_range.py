@@ -1,0 +1,143 @@
+"""The gated linear recurrence, the norms between blocks and the projections on the GPU over the
+ends of their ranges, against the plain 64-bit implementations (tests/block_ref.py).
+
+Tolerances as in test_gpu_block.py; what a test adds to them is derived in it.
+"""
+import pytest
+import torch
+
+import block_ref
+import test_gpu_block as base
+from parity import check_bf16_rounding
+from test_gpu_block import DT, F32, gla, gpu, near, recur_inputs, rnd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def bf16_values(lo, hi):
+    """Every bf16 number of [lo, hi]."""
+    v = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v[(v.float() >= lo) & (v.float() <= hi)].float().sort().values
+    return v[torch.cat([torch.ones(1, dtype=torch.bool), v[1:] != v[:-1]])]
+
+
+# ---------------------------------------------------------------- recurrence
+def gates_over(values, T, io, i, z, decay, seed):
+    """Inputs [T, D] whose gates run through the values, every channel through others."""
+    g = torch.Generator().manual_seed(seed)
+    D = (len(values) + 7) // 8 * 8
+    at = torch.arange(D) % len(values)
+    roll = lambda k: torch.stack([values[(at + (7 * t + k) % len(values)) % len(values)]  # noqa: E731
+                                  for t in range(T)]).to(DT[io])
+    return dict(x=rnd(g, T, D, dtype=DT[io]), f=roll(0), decay=-torch.rand(D, generator=g) if decay else None,
+                i=roll(3) if i else None, z=roll(5) if z else None, init=rnd(g, 1, D),
+                dy=rnd(g, T, D, dtype=DT[io]), df=rnd(g, 1, D))
+
+
+def gate_gradients(x, unit):
+    """df and di with their sizes from the formulas e (a h - k s(i) x) times the slope of log a, and
+    e m x s(i) s(-i): automatic differentiation forms 1 - a and 1 - s by subtractions that leave 0 of
+    a gate beyond 37."""
+    v = {n: None if t is None else t.double() for n, t in x.items()}
+    la, a, m, _, k = block_ref.decays(v["f"], v["decay"], unit)
+    s = lambda t: 1 / (1 + torch.exp(-t))  # noqa: E731
+    one = torch.ones_like(a)
+    si, ni = (one, one) if v["i"] is None else (s(v["i"]), s(-v["i"]))
+    gate = one if v["z"] is None else block_ref.silu(v["z"])
+    w = s(-v["f"]) * (1 if v["decay"] is None else la)
+
+    def both(sign):  # the values, or with absolute values of all terms the sizes
+        sx, dy, g, wt = si * sign(v["x"]), sign(v["dy"]), sign(gate), sign(w)
+        h, e, before = sign(v["init"][0]), sign(v["df"][0]), []
+        df, di = torch.empty_like(a), torch.empty_like(a)
+        for t in range(len(a)):
+            before.append(h)
+            h = a[t] * h + m[t] * sx[t]
+        for t in reversed(range(len(a))):
+            e = dy[t] * g[t] + e
+            kx = k[t] * sx[t]
+            df[t] = e * (a[t] * before[t] + (kx if sign is torch.abs else -kx)) * wt[t]
+            di[t] = e * m[t] * sx[t] * ni[t]
+            e = a[t] * e
+        return df, di
+
+    (df, di), (dfs, dis) = both(lambda t: t), both(torch.abs)
+    return dict(df=(df, dfs), di=(di, dis))
+
+
+def check_gates(gla, x, unit, io):
+    """Prompt, gradients and single tokens.  A gate of size v adds the rounding of its exponential's
+    argument, |v| 2^-24, to a sigmoid's error (bf16 rows): at most 100 2^-24 < 2^-17, in
+    each of the sigmoids of a product: of f twice (a and 1 - a, or log a and 1 - s(f)), of i and z."""
+    T, D = x["x"].shape
+    ref = block_ref.recur_all(x["x"], x["f"], x["decay"], x["i"], x["z"], unit, x["init"], [0, T],
+                              x["dy"], x["df"])
+    for n, pair in gate_gradients(x, unit).items():
+        ref[n] = ref[n] and pair
+    tol = 2 * (ref["memory"] * 2 ** -22 + 2 ** -18) + (4 * 2 ** -17 if io == "bf16" else 0)
+    rows = [None if x[n] is None else x[n][None].cuda() for n in ("x", "f", "i", "z")]
+    kw = dict(decay=gpu(x["decay"]), i=rows[2], z=rows[3], unit_variance=unit)
+    y, fin = gla.recur_fwd(*rows[:2], init_state=gpu(x["init"]), out_dtype=F32, **kw)
+    near(y, ref["y"], tol, "y")
+    near(fin, ref["final"], tol, "final")
+    if io == "bf16":
+        check_bf16_rounding(gla.recur_fwd(*rows[:2], init_state=gpu(x["init"]), **kw)[0], y)
+    out = gla.recur_bwd(*rows[:2], x["dy"][None].cuda(), init_state=gpu(x["init"]),
+                        d_final_state=gpu(x["df"]), grad_dtype=F32, **kw)
+    for n, t in zip(("dx", "df", "d_decay", "di", "dz", "d_init"), out):
+        assert (t is None) == (ref[n] is None), n
+        if t is not None:
+            near(t, ref[n], 3 * tol + (T * 2 ** -24 if n == "d_decay" else 0), n)
+    state = gpu(x["init"]).clone()
+    for t in range(T):
+        one = [None if r is None else r[:, t] for r in rows]
+        yt = gla.recur_step(one[0], one[1], state, kw["decay"], one[2], one[3], unit, out_dtype=F32)
+        near(yt, (ref["y"][0][t:t + 1], ref["y"][1][t:t + 1]), tol, f"step {t}")
+    near(state, ref["final"], tol, "steps' state")
+    gla.status_sync()
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("unit", [True, False])
+@pytest.mark.parametrize("i,z", [(False, False), (True, False), (False, True), (True, True)])
+def test_recur_gates_far_below_zero(gla, io, unit, i, z):
+    """The gate itself as decay, over every bf16 number from -100 to -80, where exponentials pass the largest
+    number and reciprocals the smallest: a is 0 and the drive whole."""
+    check_gates(gla, gates_over(bf16_values(-100, -80), 4, io, i, z, False, 70), unit, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("unit", [True, False])
+@pytest.mark.parametrize("decay,i,z", [(False, True, True), (True, True, True)])
+def test_recur_gates_of_every_size(gla, io, unit, decay, i, z):
+    """Every bf16 gate of size 2^-6 to 60, either sign."""
+    v = bf16_values(-60, 60)
+    check_gates(gla, gates_over(v[v.abs() >= 2 ** -6], 4, io, i, z, decay, 71), unit, io)
+
+
+@pytest.mark.parametrize("unit", [True, False])
+def test_recur_gates_at_the_infinities(gla, unit):
+    """bf16 rows, the gate itself as decay: shut it passes the drive alone, open the state alone; with
+    infinities and the largest numbers."""
+    T, D = 12, 64
+    g = torch.Generator().manual_seed(72)
+    x, dy = (rnd(g, 1, T, D, dtype=torch.bfloat16).cuda() for _ in range(2))
+    init = rnd(g, 1, D).cuda()
+    for v in (-INF, -3.3895e38, -1e30, -200.0, -89.0):
+        f = torch.full_like(x, v)
+        y, fin = gla.recur_fwd(x, f, unit_variance=unit, init_state=init)
+        assert torch.equal(y, x) and torch.equal(fin, x[:, -1].float())
+        dx, df, _, _, _, d0 = gla.recur_bwd(x, f, dy, unit_variance=unit, init_state=init)
+        assert torch.equal(dx, dy) and not df.any() and not d0.any()
+        state = init.clone()
+        assert torch.equal(gla.recur_step(x[:, 0], f[:, 0], state, unit_variance=unit), x[:, 0])
+    for v in (INF, 3.3895e38, 200.0):
+        f = torch.full_like(x, v)
+        y, fin = gla.recur_fwd(x, f, unit_variance=unit, init_state=init, out_dtype=F32)
+        assert torch.equal(fin, init) and torch.equal(y, init[:, None].expand_as(y))
+        dx, df, _, _, _, d0 = gla.recur_bwd(x, f, dy, unit_variance=unit, init_state=init)
+        assert not dx.any() and not df.any()
+        torch.testing.assert_close(d0[0], dy[0].float().sum(0), rtol=1e-5, atol=1e-5)
+    gla.status_sync()
