@@ -23,7 +23,10 @@
 // are two of 256 columns in tensor memory: a tile's epilogue overlaps the next tile's
 // product.  Persistent: every pair takes each 76th tile.
 // Every wait is bounded in wall time (gla_set_wait_limit_ns); one that runs out
-// flags the status word, and the kernel lets its copies and products land and ends.
+// flags the status word, and the pair lets its copies and products land and ends.  Where one SM's block gave up
+// the two producers may have stopped at different steps, and a barrier counts both SMs'
+// bytes: they tell each other how far they came, the one behind catches up, and the
+// first SM waits for the last steps.
 // Bound: the tensor pipe, active in 95 % of the cycles of 8192 x 2048 x 8192 (268 to 278 us,
 // 1.98 to 2.05 PFLOP/s); gradients of 4096 rows 445 to 498 us by the power the GPU is given.
 #include "gla_glu.cuh"
@@ -46,7 +49,7 @@ constexpr uint32_t kCols = 512;                        // tensor memory: two acc
 
 enum Bar { kFull = 0, kEmpty = kFull + kStages, kAccFull = kEmpty + kStages,
            kAccEmpty = kAccFull + 2, kDrain = kAccEmpty + 2, kNumBars };
-static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+static_assert(kNumBars * 8 + 16 <= 256, "barrier area");
 
 struct GluParams {
   CUtensorMap x, wg, wu;      // kUp: boxes of 64 x 128 rows
@@ -100,6 +103,15 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 __device__ __forceinline__ void arrive_first_sm(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_sm(bar))
                : "memory");
+}
+
+// Two words of the pair's other block.
+__device__ __forceinline__ void tell_other(volatile uint32_t* to, uint32_t rank, uint32_t x, uint32_t y) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(at)
+      : "r"(smem_u32(const_cast<const uint32_t*>(to))), "r"(rank));
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 
 enum Kind { kUp = 0, kDx = 1, kDw = 2 };
@@ -182,6 +194,7 @@ glu_kernel(const __grid_constant__ GluParams p) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+  volatile uint32_t* other = tmem_at + 2;  // of the other SM: its producer's steps, whether it gave up
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cta_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -220,44 +233,46 @@ glu_kernel(const __grid_constant__ GluParams p) {
     return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
 
-  if (warp == kEpilogue && lane == 0) {
+  // The producer: `it` steps of K have been issued, the next one is block kb of the pair's i-th tile.
+  const bool feeds = warp == kEpilogue && lane == 0;
+  uint32_t it = 0;
+  int tile = 0, kb = 0;
+  bool more = false;
+  TileAt at;
+  auto feed = [&] {
+    const int s = it % kStages;
+    if (rank == 0)
+      mbar_arrive_expect_tx(&bars[kFull + s], at.width == kTile ? 2 * kStage : kStage + kOperand);
+    const uint32_t bar = first_sm(&bars[kFull + s]);
+    unsigned char* sa = smem + s * kStage;
+    unsigned char* sb = sa + kOperand;
+    if (!BWD2) {
+      load_box(sa, &p.x, bar, kb * kK, at.m + rank * kHalf);
+      load_box(sb, rank ? &p.wu : &p.wg, bar, kb * kK, at.n);
+    } else if (at.kind == kDx) {
+      const int half = at.blocks / 2, seg = kb >= half, k = (kb - seg * half) * kK;
+      load_box(sa, seg ? &p.du : &p.dg, bar, k, at.m + rank * kHalf);
+      const CUtensorMap* w = seg ? &p.wum : &p.wgm;
+      load_box(sb, w, bar, at.n + rank * (at.width / 2), k);
+      if (at.width == kTile) load_box(sb + kOperand / 2, w, bar, at.n + rank * kHalf + 64, k);
+    } else {
+      const CUtensorMap* d = at.seg ? &p.dum : &p.dgm;
+      load_box(sa, d, bar, at.m + rank * kHalf, kb * kK);
+      load_box(sa + kOperand / 2, d, bar, at.m + rank * kHalf + 64, kb * kK);
+      load_box(sb, &p.xm, bar, at.n + rank * kHalf, kb * kK);
+      load_box(sb + kOperand / 2, &p.xm, bar, at.n + rank * kHalf + 64, kb * kK);
+    }
+    ++it;
+    if (++kb == at.blocks) {
+      kb = 0;
+      more = tile_at<BWD2>(p, pair, pairs, ++tile, &at);
+    }
+  };
+
+  if (feeds) {
     // ------------------------------------------------------------ producer
-    uint32_t it = 0;
-    bool ok = true;
-    TileAt a;
-    for (int i = 0; ok && tile_at<BWD2>(p, pair, pairs, i, &a); ++i) {
-      for (int kb = 0; kb < a.blocks; ++kb, ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !wait(kEmpty + s, (it / kStages - 1) & 1)) { ok = false; break; }
-        if (rank == 0)
-          mbar_arrive_expect_tx(&bars[kFull + s], a.width == kTile ? 2 * kStage : kStage + kOperand);
-        const uint32_t bar = first_sm(&bars[kFull + s]);
-        unsigned char* sa = smem + s * kStage;
-        unsigned char* sb = sa + kOperand;
-        if (!BWD2) {
-          load_box(sa, &p.x, bar, kb * kK, a.m + rank * kHalf);
-          load_box(sb, rank ? &p.wu : &p.wg, bar, kb * kK, a.n);
-        } else if (a.kind == kDx) {
-          const int half = a.blocks / 2, seg = kb >= half, k = (kb - seg * half) * kK;
-          load_box(sa, seg ? &p.du : &p.dg, bar, k, a.m + rank * kHalf);
-          const CUtensorMap* w = seg ? &p.wum : &p.wgm;
-          load_box(sb, w, bar, a.n + rank * (a.width / 2), k);
-          if (a.width == kTile) load_box(sb + kOperand / 2, w, bar, a.n + rank * kHalf + 64, k);
-        } else {
-          const CUtensorMap* d = a.seg ? &p.dum : &p.dgm;
-          load_box(sa, d, bar, a.m + rank * kHalf, kb * kK);
-          load_box(sa + kOperand / 2, d, bar, a.m + rank * kHalf + 64, kb * kK);
-          load_box(sb, &p.xm, bar, a.n + rank * kHalf, kb * kK);
-          load_box(sb + kOperand / 2, &p.xm, bar, a.n + rank * kHalf + 64, kb * kK);
-        }
-      }
-    }
-    if (rank == 0) {  // every copy of the pair lands before either SM's block ends
-      const uint32_t from = it > kStages ? it - kStages : 0;
-      for (uint32_t i = from; i < it; ++i)
-        (void)mbar_wait_bounded(&bars[kFull + i % kStages], (i / kStages) & 1,
-                                kDefaultWaitLimitNs);
-    }
+    more = tile_at<BWD2>(p, pair, pairs, 0, &at);
+    while (more && (it < kStages || wait(kEmpty + it % kStages, (it / kStages - 1) & 1))) feed();
   } else if (warp == kEpilogue + 1 && rank == 0) {
     // ------------------------------------------------------------ issuer
     uint32_t it = 0, n = 0;
@@ -378,12 +393,26 @@ glu_kernel(const __grid_constant__ GluParams p) {
       if (lane == 0) arrive_first_sm(&bars[kAccEmpty + (n & 1)]);
     }
   }
-  // everything in flight has landed in the roles above; now the blocks may end together
+  // the products issued are done, and unless a wait ran out so is every copy
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   start_next();
+  if (feeds) tell_other(other, rank ^ 1, it, *abort_flag);
   cluster_barrier();
+  if (*abort_flag || other[1]) {  // (the same in both blocks)
+    // A producer is ahead by a ring at most, of stages whose products it knows to be done: the one
+    // behind fills its half of them too, and then all copies of the ring land.
+    if (feeds) {
+      const uint32_t theirs = other[0];
+      while (more && it < theirs) feed();
+      if (rank == 0)
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+          (void)mbar_wait_bounded(&bars[kFull + i % kStages], (i / kStages) & 1,
+                                  kDefaultWaitLimitNs);
+    }
+    cluster_barrier();
+  }
   if (warp == kEpilogue + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols)

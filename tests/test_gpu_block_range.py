@@ -141,3 +141,37 @@ def test_recur_gates_at_the_infinities(gla, unit):
         assert not dx.any() and not df.any()
         torch.testing.assert_close(d0[0], dy[0].float().sum(0), rtol=1e-5, atol=1e-5)
     gla.status_sync()
+
+
+# ---------------------------------------------------------------- feed-forward
+@pytest.mark.parametrize("backward", [False, True])
+def test_glu_gives_up_again_and_again(gla, backward):
+    """Waits that run out, many times over: each call ends with GLA_ERR_TIMEOUT or right, every copy of
+    either SM of a pair lands before its block ends, and what runs behind it is right.  (The sums over K
+    take a millisecond, so that a wait is open when the limit of a nanosecond has passed.)"""
+    g = torch.Generator().manual_seed(80)
+    bf = torch.bfloat16
+    R, D, F = (1 << 18, 64, 200) if backward else (256, 1 << 18, 128)
+    x = rnd(g, R, D, dtype=bf).cuda()
+    wg, wu = (rnd(g, F, D, std=D ** -0.5, dtype=bf).cuda() for _ in range(2))
+    dh = rnd(g, R, F, dtype=bf).cuda() if backward else None
+    run = (lambda: gla.glu_bwd(x, wg, wu, dh)) if backward else (lambda: (gla.glu_fwd(x, wg, wu),))
+    want = run()
+    gla.status_sync()
+    hits = 0
+    for _ in range(30):
+        gla.set_wait_limit_ns(1)
+        try:
+            got = run()
+        finally:
+            gla.set_wait_limit_ns(0)
+        behind = run()  # on the same SMs, right behind it
+        try:
+            gla.status_sync()
+            ok = True
+        except gla.GlaError as e:
+            assert e.status == 5
+            hits, ok = hits + 1, False
+        for a, b, c in zip(got, behind, want):
+            assert torch.equal(b, c) and (not ok or torch.equal(a, c))
+    assert hits
