@@ -248,7 +248,8 @@ def glu_fwd(x, w_gate, w_up, out=None, stream=None, out_dtype=None):
 
 def glu_bwd(x, w_gate, w_up, d_out, grad_dtype=None, workspace=None, stream=None):
     """Gradient of ``glu_fwd``; returns ``(dx, dw_gate, dw_up)``.  ``d_out`` [.., F] in bf16,
-    contiguous; the gradients come in bf16, or fp32 with ``grad_dtype=torch.float32``."""
+    contiguous; the gradients come in bf16, or fp32 with ``grad_dtype=torch.float32``.  At most
+    2^26 rows."""
     R, D, F, args = _glu_rows(x, w_gate, w_up)
     dev = x.device
     grad_dtype = grad_dtype or x.dtype

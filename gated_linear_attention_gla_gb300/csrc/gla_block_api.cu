@@ -317,7 +317,7 @@ gla_status gla_glu_fwd(const void* x, int64_t x_stride, const void* w_gate, cons
 }
 
 size_t gla_glu_bwd_workspace_size(int rows, int D, int F) {
-  if (rows <= 0 || D <= 0 || F <= 0) return 0;
+  if (rows <= 0 || rows > gla::kGluBwdMaxRows || D <= 0 || F <= 0) return 0;
   return gla::glu_bwd_workspace(rows, D, F);
 }
 
@@ -328,6 +328,7 @@ gla_status gla_glu_bwd(const void* x, int64_t x_stride, const void* w_gate, cons
   gla::GluBwdArgs b{};
   const gla_status bad = glu_args(x, x_stride, w_gate, w_up, rows, D, F, flags, &b.f);
   if (bad != GLA_OK) return bad;
+  if (rows > gla::kGluBwdMaxRows) return GLA_ERR_UNSUPPORTED;
   if (D == 0) return GLA_OK;
   if (F == 0) return rows == 0 ? GLA_OK : GLA_ERR_UNSUPPORTED;
   if (!dw_gate || !dw_up || (rows > 0 && (!d_out || !dx))) return GLA_ERR_INVALID_ARG;

@@ -169,7 +169,7 @@ __device__ __forceinline__ bool tile_at(const GluParams& p, int pair, int pairs,
   t /= p.dw_n;
   a->seg = t / p.dw_m;
   a->m = t % p.dw_m * kTile;
-  a->blocks = p.R / kK + (p.R % kK != 0);  // (R may be 2^31 - 1)
+  a->blocks = (p.R + kK - 1) / kK;
   return true;
 }
 

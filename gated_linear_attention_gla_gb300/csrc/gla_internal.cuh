@@ -352,6 +352,9 @@ size_t recur_bwd_workspace(int B, long long rows, int D, bool packed);
 cudaError_t launch_recur_bwd(const RecurBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_recur_step(const RecurStepArgs& a, cudaStream_t stream);
 cudaError_t launch_glu_fwd(const GluArgs& a, cudaStream_t stream);
+// A tile of dw sums over all rows, 64 of them in 0.34 us: 2^26 take 0.36 s, a fifth of the default limit of
+// the wait for them (2^29 would end as a wait that ran out).
+constexpr int kGluBwdMaxRows = 1 << 26;
 size_t glu_bwd_workspace(int rows, int D, int F);
 cudaError_t launch_glu_bwd(const GluBwdArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagePool* pools, int count, int S, const int32_t* src,

@@ -647,6 +647,9 @@ gla_status gla_glu_fwd(const void *x, int64_t x_stride, const void *w_gate, cons
  * d_out [rows, F] bf16; dx [rows, D], dw_gate and dw_up [F, D], all bf16 (fp32 with
  * GLA_FLAG_FP32_OUT, of the same rounded dg and du).  workspace:
  * gla_glu_bwd_workspace_size(...) bytes, 256-byte aligned (dg and du).
+ * At most 2^26 rows (more return GLA_ERR_UNSUPPORTED): dw_gate and dw_up are sums over all rows
+ * in one fp32 accumulator, whose length bounds both its rounding and the time for
+ * which the kernel waits for it.
  */
 gla_status gla_glu_bwd(const void *x, int64_t x_stride, const void *w_gate, const void *w_up,
                        const void *d_out, void *dx, void *dw_gate, void *dw_up, int rows, int D,

@@ -175,3 +175,23 @@ def test_glu_gives_up_again_and_again(gla, backward):
         for a, b, c in zip(got, behind, want):
             assert torch.equal(b, c) and (not ok or torch.equal(a, c))
     assert hits
+
+
+def test_glu_gradients_of_the_most_rows(gla):
+    """2^26 rows, of numbers whose sums are exact: with w_gate = 0 and w_up the identity dg is
+    d_out x / 2 and du is 0, and dw_gate = dg^T x sums halves of whole numbers."""
+    R, D = 1 << 26, 8
+    g = torch.Generator(device="cuda").manual_seed(81)
+    bf = torch.bfloat16
+    x = torch.randint(-1, 2, (R, D), generator=g, device="cuda", dtype=torch.int8).to(bf)
+    dh = torch.randint(-1, 2, (R, D), generator=g, device="cuda", dtype=torch.int8).to(bf)
+    dh[:, 3], x[:, 3] = 1, 1  # one that only grows
+    wg, wu = torch.zeros(D, D, dtype=bf, device="cuda"), torch.eye(D, dtype=bf, device="cuda")
+    dx, dg, du = gla.glu_bwd(x, wg, wu, dh, grad_dtype=F32)
+    gla.status_sync()
+    want = torch.zeros(D, D, dtype=torch.float64, device="cuda")
+    for k in range(0, R, R // 64):
+        xs, hs = x[k:k + R // 64].double(), dh[k:k + R // 64].double()
+        want += (hs * xs / 2).t() @ xs
+    assert torch.equal(dg.double(), want) and float(want[3, 3]) == R / 2
+    assert not du.any() and not dx.any()
