@@ -258,10 +258,11 @@ norm_bwd_kernel(NormBwdArgs b, float* partial, int tpr, int stages) {
         }
         r[0] = rsqrtf(var + a.eps);
         const f32x2 mx = both(-mx1 * r[0] * a.inv_d);
-        const f32x2 my = both(a.layer ? -v[2] * a.inv_d : 0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (skip(k)) continue;
+          // (columns that do not exist stay zeros: they are in the sums of the norm of y)
+          const f32x2 my = both(a.layer && g.column(k) < a.D ? -v[2] * a.inv_d : 0.f);
           const Vec d = du_of(0, k), e = ds_of(0, k), w = weight.at(g.column(k));
 #pragma unroll
           GLA_PAIRS {

@@ -143,6 +143,69 @@ def test_recur_gates_at_the_infinities(gla, unit):
     gla.status_sync()
 
 
+# ---------------------------------------------------------------- norms
+def norm_check(gla, R, D, io, res32, layer, post, pbias, z, scale, weight, bias, y, means=None, seed=73):
+    """block_norm_fwd and block_norm_bwd with these parts; `means`: row k's mean is added to
+    res and y of the rows k, k + len, ..."""
+    g = torch.Generator().manual_seed(seed)
+    dt, rt = DT[io], F32 if res32 else DT[io]
+    add = 0.0 if means is None else torch.tensor(means)[torch.arange(R) % len(means)][:, None]
+    vec = lambda on, mean=0.0: rnd(g, D, std=0.3, mean=mean) if on else None  # noqa: E731
+    res = (rnd(g, R, D, std=2.0) + 2 * add).to(rt)
+    yy = (rnd(g, R, D) + add).to(dt) if y else None
+    zz = rnd(g, R, D, dtype=dt) if z else None
+    pw, pb, sc, w, b = vec(post, 1.0), vec(pbias), vec(scale, 0.5), vec(weight, 1.0), vec(bias)
+    du, ds = rnd(g, R, D, dtype=dt) if weight else None, rnd(g, R, D, dtype=rt)
+    eps = 1e-5
+    ref = block_ref.block_norm_all(res, yy, zz, pw, pb, sc, w, b, layer, eps, du, ds)
+    kw = dict(y=base.strided(yy), z=base.strided(zz), post_weight=gpu(pw), post_bias=gpu(pb),
+              scale=gpu(sc), weight=gpu(w), bias=gpu(b), kind="layer" if layer else "rms", eps=eps)
+    tol = 2 ** -17
+    s, u = gla.block_norm_fwd(gpu(res), **kw, out_dtype=F32)
+    if y:  # bf16: rounded once where it is stored
+        value, size = ref["s"]
+        near(s, (value, tol * size + (2 ** -8 * value.abs() if rt is not F32 else 0)), 1.001, "s")
+    if weight:
+        near(u, ref["u"], tol, "u")
+        u2 = gla.block_norm_fwd(gpu(res), **kw, out_dtype=dt)[1]
+        assert torch.equal(u2, u.to(dt))
+    got = gla.block_norm_bwd(gpu(res), gpu(du), gpu(ds), **kw, grad_dtype=F32)
+    for n, t in zip(("d_res", "dy", "dz", "d_post_weight", "d_post_bias", "d_scale", "dw", "db"), got):
+        assert (t is None) == (ref.get(n) is None), n
+        if t is not None:
+            near(t, ref[n], 2 * tol + (R * 2 ** -24 if t.dim() == 1 else 0), n)
+    gla.status_sync()
+
+
+# io, res fp32, layer, post weight, post bias, z, scale, weight, bias, y
+PARTS = [("bf16", True, False, True, False, True, True, True, False, True),
+         ("bf16", False, True, True, True, True, True, True, True, True),
+         ("fp32", True, False, True, True, True, False, True, True, True),
+         ("bf16", False, True, True, False, False, True, True, False, True),
+         ("fp32", True, True, False, False, True, True, True, True, True),
+         ("bf16", True, False, True, True, False, False, False, False, True),
+         ("fp32", True, True, False, False, False, False, True, True, False),
+         ("bf16", False, False, False, False, False, False, True, True, False)]
+
+
+@pytest.mark.parametrize("R,D", [(7301, 72), (2001, 2048), (3001, 520), (1001, 4104), (701, 8192)])
+@pytest.mark.parametrize("parts", PARTS)
+def test_block_norm_of_many_rows(gla, R, D, parts):
+    """More rows than the groups of one wave own, an odd number: rows two at a time, rows on their way
+    over several turns, sums over them; one and two vectors a thread."""
+    norm_check(gla, R, D, *parts)
+
+
+@pytest.mark.parametrize("D", [8, 72, 264, 1000, 2048, 4088, 4104])
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("post,pbias,z,scale,bias", [(True, False, False, False, False), (True, True, False, True, True),
+                                                     (True, False, False, True, True), (True, True, True, False, False),
+                                                     (False, False, False, True, True)])
+def test_block_norm_parts(gla, D, layer, post, pbias, z, scale, bias):
+    """Every part with and without its neighbours, where the last threads of a row have no columns."""
+    norm_check(gla, 21, D, "fp32", True, layer, post, pbias, z, scale, True, bias, True)
+
+
 # ---------------------------------------------------------------- feed-forward
 @pytest.mark.parametrize("backward", [False, True])
 def test_glu_gives_up_again_and_again(gla, backward):
