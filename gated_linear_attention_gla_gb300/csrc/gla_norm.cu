@@ -6,8 +6,8 @@
 //
 // norm(x) = c / sqrt(mean(c^2) + eps), c = x or x - mean(x).  Everything between
 // the loads and the two stores is fp32 (s is rounded where it is stored, u comes
-// from the unrounded s); the mean square is of the centred values, which lie in
-// registers, so nothing cancels.
+// from the unrounded s); layer norm's variance is of the centred values, which lie in registers, or of
+// rows whose mean is small enough the mean square less the mean's (gla_norm.cuh).
 //
 // A group of threads owns a row, eight adjacent channels a thread and vector, and walks
 // over rows, two at a time where there are many, with its parameters in registers and

@@ -210,11 +210,12 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
 // Centres R rows (layer norm) and leaves 1 / sqrt(mean of squares + eps) of each in r; 0
 // for a row behind the last (of zeros), so that it adds nothing to sums over rows.  KIND: which
 // of the norms, where the caller knows.
-// Layer norm takes the sums of x and x^2 in one exchange, which loses (mean^2 / variance) 2^-23 of
-// the variance to cancellation; rows where that would be over 2^-19 take the squares of
-// the centred values in a second one.
+// Layer norm takes the sums of x and x^2 in one exchange, which loses (mean^2 / variance) of the sums'
+// rounding to cancellation; rows whose mean is over half a deviation take the squares of the
+// centred values in a second one, so that the variance is never off by much more than those would be (2048
+// values: 2e-7 of it; up to four deviations in one exchange it would be 4e-6).
 enum Kind { kRms, kEither };
-__device__ __forceinline__ bool far_mean(float mean, float var) { return !(mean * mean <= 16.f * var); }
+__device__ __forceinline__ bool far_mean(float mean, float var) { return !(4.f * mean * mean <= var); }
 template <int K, int R, int KIND = kEither>
 __device__ __forceinline__ void normalise(const Group& g, const NormArgs& a, Vec (&x)[R][K],
                                           float (&r)[R], int rows) {

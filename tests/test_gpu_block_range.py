@@ -206,6 +206,34 @@ def test_block_norm_parts(gla, D, layer, post, pbias, z, scale, bias):
     norm_check(gla, 21, D, "fp32", True, layer, post, pbias, z, scale, True, bias, True)
 
 
+@pytest.mark.parametrize("R,D", [(33, 264), (1501, 2048), (401, 5120)])
+@pytest.mark.parametrize("parts", [p for p in PARTS if p[2]] + [PARTS[2]])
+def test_block_norm_of_far_and_near_means(gla, R, D, parts):
+    """Rows whose means are 0 to 1000 deviations, side by side."""
+    norm_check(gla, R, D, *parts, means=(0.0, 0.3, 0.49, 0.51, 1000.0, 1.0, -2.0, 0.0, 3.9, 4.1, -30.0))
+
+
+def test_layer_norm_keeps_the_variance(gla):
+    """The factor 1 / deviation of rows whose mean is up to four deviations, from the projection of the results on
+    the exact ones (which a wrong mean, and the rounding of 2048 elements, leave out): in units of
+    2^-24 the sum of the squares is off by 13 (four in a thread, one of a pair, five in a warp, three of
+    warps), 1.25 times that and 6.5 more where the mean, up to half a deviation, is
+    taken out of it, one for the difference; half of it in the root, four for the root, one for the product: 17."""
+    D, means = 2048, (0.0, 0.2, 0.45, 0.6, 1.0, 2.0, 3.0, 3.9)
+    R = 300 * len(means)
+    g = torch.Generator().manual_seed(74)
+    x = rnd(g, R, D) + torch.tensor(means)[torch.arange(R) % len(means)][:, None]
+    du = rnd(g, R, D)
+    one = torch.ones(D)
+    ref = block_ref.block_norm_all(x, None, None, None, None, None, one, None, True, 1e-12, du)
+    u = gla.block_norm_fwd(gpu(x), weight=gpu(one), kind="layer", eps=1e-12)[1]
+    d = gla.block_norm_bwd(gpu(x), gpu(du), weight=gpu(one), kind="layer", eps=1e-12)[0]
+    for n, t in (("u", u), ("d_res", d)):
+        want = ref[n][0]
+        off = ((t.double().cpu() * want).sum(-1) / (want * want).sum(-1) - 1).abs()
+        assert float(off.max()) <= 17 * 2 ** -24, (n, float(off.max()))
+
+
 # ---------------------------------------------------------------- feed-forward
 @pytest.mark.parametrize("backward", [False, True])
 def test_glu_gives_up_again_and_again(gla, backward):
