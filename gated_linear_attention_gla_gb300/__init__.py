@@ -294,8 +294,8 @@ def decode_step(q, k, v, g, state, scale: Optional[float] = None, out=None, stre
 
 
 def set_wait_limit_ns(nanoseconds: int) -> int:
-    """Wall-time limit of the tensor-core prefill kernels' hand-off waits
-    (process-wide; 0 restores the default, 2 s).  Returns the previous setting.
+    """Wall-time limit of the hand-off waits inside the kernels of the tensor-core prefill, the
+    projections and the gated recurrence (process-wide; 0 restores the default, 2 s).  Returns the previous setting.
     A wait that runs out ends the kernel early: the next status_sync() raises
     GlaError with GLA_ERR_TIMEOUT (5) and the call's outputs are undefined."""
     return _binding.gla_set_wait_limit_ns(nanoseconds)

@@ -139,6 +139,14 @@ static gla_status recur_rows(const void* x, int64_t x_stride, const void* f, int
   return GLA_OK;
 }
 
+// Limit of a wait inside the recurrence's kernels.  Warps look through packed offsets (all of them for
+// malformed and empty ones, runs of empty ones between two rows) while others wait for their
+// maps: at most some dependent reads a sequence.
+static uint64_t recur_wait_ns(const int32_t* cu_seqlens, int B) {
+  const uint64_t limit = gla::handoff_wait_limit_ns(), more = cu_seqlens ? 4000ull * (uint64_t)B : 0;
+  return limit + more < limit ? ~0ull : limit + more;
+}
+
 #define GLA_RECUR_INPUTS(rows, esz)                                                          \
   {x, span(rows, x_stride, D, esz)}, {f, span(rows, f_stride, D, esz)},                       \
       {i, i ? span(rows, i_stride, D, esz) : 0}, {z, z ? span(rows, z_stride, D, esz) : 0},   \
@@ -180,7 +188,7 @@ gla_status gla_recur_fwd(const void* x, int64_t x_stride, const void* f, int64_t
   a.i_stride = i_stride; a.z_stride = z_stride; a.decay = decay; a.init_state = init_state;
   a.out = out; a.final_state = final_state; a.cu_seqlens = cu_seqlens;
   a.B = B; a.T = T; a.D = D; a.unit = (flags & GLA_FLAG_UNIT_VARIANCE) != 0;
-  a.fp32_io = fp32; a.fp32_out = f32out;
+  a.fp32_io = fp32; a.fp32_out = f32out; a.wait_ns = recur_wait_ns(cu_seqlens, B);
   return finish(gla::launch_recur_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -237,6 +245,7 @@ gla_status gla_recur_bwd(const void* x, int64_t x_stride, const void* f, int64_t
   a.i_stride = i_stride; a.z_stride = z_stride; a.decay = decay; a.init_state = init_state;
   a.cu_seqlens = cu_seqlens; a.B = B; a.T = T; a.D = D;
   a.unit = (flags & GLA_FLAG_UNIT_VARIANCE) != 0; a.fp32_io = fp32; a.fp32_out = f32out;
+  a.wait_ns = recur_wait_ns(cu_seqlens, B);
   g.d_out = d_out; g.d_final_state = d_final_state; g.dx = dx; g.df = df; g.di = di; g.dz = dz;
   g.d_decay = d_decay; g.d_init_state = d_init_state;
   return finish(gla::launch_recur_bwd(g, workspace, reinterpret_cast<cudaStream_t>(stream)));

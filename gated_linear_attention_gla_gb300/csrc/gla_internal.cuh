@@ -241,6 +241,7 @@ struct RecurArgs {
   int B, T, D;
   bool unit, fp32_io, fp32_out;
   unsigned* status;
+  uint64_t wait_ns;           // limit of a wait
 };
 
 struct RecurBwdArgs {
@@ -300,9 +301,9 @@ struct PagePools {
 constexpr int kPageNew = -2;       // gla.h's GLA_PAGE_NEW
 constexpr int kMaxPages = 524288;  // pages of a pool (the copy plan keeps three bits a page)
 
-// Wall-time limit of the tensor-core prefill kernels' hand-off waits, read at
-// each launch (process-wide; set by gla_set_wait_limit_ns, default 2 s).  Their
-// teardown drains keep the default.
+// Wall-time limit of the hand-off waits of the tensor-core prefill, the projections and the gated
+// recurrence, read at each launch (process-wide; set by gla_set_wait_limit_ns, default 2 s).  Their
+// teardown drains keep limits of their own.
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
 uint64_t handoff_wait_limit_ns();
 

@@ -242,7 +242,9 @@ struct Maps {
   uint64_t full[2];   // counts the bytes of block[turn]
   uint64_t ready[2];  // front[turn] is there
   int given_up;       // a wait of the block ran out
+  uint32_t told[kMaxCluster];  // how many steps each block's exchange has sent, + kGaveUp
 };
+constexpr uint32_t kGaveUp = 0x80000000u;
 
 __device__ __forceinline__ uint32_t shared_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -284,26 +286,38 @@ __device__ __forceinline__ void send(const void* to, const uint64_t* bar, uint32
       "r"(__float_as_uint(v.w)), "r"(b)
       : "memory");
 }
-// Waits for a phase of a barrier, for a bounded number of tests (each may hold the
-// warp for a time the hardware defines; a peer's bytes come within microseconds).
-// Then the status word says so, the block's other waits give up too, and the call's
-// results are undefined.  (Counted, because reading the time in the loop slowed it.)
-__device__ __forceinline__ void await(Maps& s, const uint64_t* bar, uint32_t parity,
-                                      unsigned* status) {
-  for (uint32_t i = 0; i < 1u << 24; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(shared_at(bar)), "r"(parity)
-        : "memory");
-    if (done) return;
-    if ((i & 255) == 255 && *reinterpret_cast<volatile int*>(&s.given_up)) return;
+__device__ __forceinline__ bool completed(const uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(shared_at(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// Waits for a phase of a barrier, for at most limit_ns of wall time behind the first 256 tests (a peer's
+// bytes come within microseconds, and a test that fails takes some, so the time is read at every
+// 256th only).  false: it ran out, here or in another warp of the block; the status word says so, and the
+// call's results are undefined.
+__device__ __forceinline__ bool await(Maps& s, const uint64_t* bar, uint32_t parity,
+                                      unsigned* status, uint64_t limit_ns) {
+  uint64_t since = 0;
+  for (uint32_t i = 0; !completed(bar, parity); ++i) {
+    if ((i & 255) == 255) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (since == 0) since = now;
+      if (*reinterpret_cast<volatile int*>(&s.given_up)) return false;
+      if (now - since > limit_ns) {
+        *reinterpret_cast<volatile int*>(&s.given_up) = 1;
+        atomicOr(status, kDevTimeout);
+        return false;
+      }
+    }
   }
-  *reinterpret_cast<volatile int*>(&s.given_up) = 1;
-  atomicOr(status, kDevTimeout);
+  return true;
 }
 
 // A computing warp's map of step `step`.
@@ -312,70 +326,140 @@ __device__ __forceinline__ void give(Maps& s, int step, int w, int lane, float4 
   __syncwarp();
   if (lane == 0) arrive(&s.given[step & 1]);
 }
-// The state in front of its run of that step.
-__device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane, unsigned* status) {
-  await(s, &s.ready[step & 1], (step >> 1) & 1, status);
+// The state in front of its run of that step.  It comes from the exchange warp, whose waits have the limit in
+// time: this one ends when that warp has given up, with whatever lies there (and in any case
+// after 2^24 tests).
+__device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane) {
+  for (uint32_t i = 0; i < 1u << 24; ++i) {
+    if (completed(&s.ready[step & 1], (step >> 1) & 1)) break;
+    if ((i & 255) == 0 && *reinterpret_cast<volatile int*>(&s.given_up)) break;
+  }
   return s.front[step & 1][w][lane];
 }
 
-// The exchange warp of block `rank` of `cluster`: `steps` exchanges from the state in front of
-// the first one; returns the one behind the last.
-//
-// Every block sends its map to all blocks of the cluster, where the bytes' arrival
+// How far a lane of the exchange came: steps whose bytes are expected (lane 0) and that it has sent.
+struct Came {
+  int armed = 0, sent = 0;
+  bool ok = true;
+};
+__device__ __forceinline__ void expect(Maps& s, int turn, int cluster) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(&s.full[turn])),
+               "r"(cluster * 512)
+               : "memory");
+}
+// The states in front of the warps' runs of a step, and behind the last: in batches, in which the loads of one
+// map do not wait for the stores of another's.
+constexpr int kBatch = 5;
+template <bool STARTS>
+__device__ __forceinline__ f32x2 fronts(Maps& s, int turn, int warps, int lane, f32x2 front) {
+  for (int k = 0; k < warps; k += kBatch) {
+    float4 m[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) m[i] = s.warp[turn][k + i < warps ? k + i : k][lane];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (k + i < warps) {
+        s.front[turn][k + i][lane] = front;
+        front = apply<STARTS>(m[i], front);
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0) arrive(&s.ready[turn]);
+  return front;
+}
+
+// The exchange warp of a block: `steps` exchanges from the state in front of the first one; returns
+// the one behind the last.  Of a block alone (whether a wait ran out is looked at now and then only):
+template <bool STARTS>
+__device__ __forceinline__ f32x2 exchange_alone(Maps& s, long long steps, int warps, int lane,
+                                                f32x2 state, const RecurArgs& a) {
+  for (long long step = 0; step < steps; ++step) {
+    const int turn = (int)step & 1;
+    (void)await(s, &s.given[turn], (uint32_t)(step >> 1) & 1, a.status, a.wait_ns);
+    state = fronts<STARTS>(s, turn, warps, lane, state);
+    if ((step & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s.given_up))) break;
+  }
+  return state;
+}
+
+// Of block `rank` of `cluster`.  Every block sends its map to all blocks of the cluster, where the bytes' arrival
 // completes a barrier: no cluster barrier and no fence.  Buffers are written again
 // safely: a warp gives step k + 2 after it took step k; a front of step k + 2
 // is written after all gave k + 2; and a block sends step k + 2 after it has received all of
 // k + 1, which every block sends after it has read all of step k.
+// Where a wait ran out a lane waits and sends no more.
 template <bool STARTS>
-__device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, int rank,
-                                          int cluster, int lane, f32x2 state, unsigned* status) {
+__device__ __forceinline__ f32x2 exchange(Maps& s, long long steps, int warps, int rank, int cluster,
+                                          int lane, f32x2 state, const RecurArgs& a, Came& came) {
   for (long long step = 0; step < steps; ++step) {
     const int turn = (int)step & 1;
     const uint32_t parity = (uint32_t)(step >> 1) & 1;
-    if (cluster > 1 && lane == 0)
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                       shared_at(&s.full[turn])),
-                   "r"(cluster * 512)
-                   : "memory");
-    await(s, &s.given[turn], parity, status);
-    // the warps' maps in batches: the loads of one do not wait for the stores of another
-    constexpr int kBatch = 5;
-    f32x2 front = state;
-    if (cluster > 1) {
-      float4 all = make_float4(1.f, 1.f, 0.f, 0.f);
-      for (int k = 0; k < warps; k += kBatch) {
-        float4 m[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) m[i] = s.warp[turn][k + i < warps ? k + i : k][lane];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (k + i < warps) all = compose<STARTS>(all, m[i]);
-      }
-      for (int k = 0; k < cluster; ++k)
-        send(&s.block[turn][rank][lane], &s.full[turn], (rank + k) % cluster, all);
-      await(s, &s.full[turn], parity, status);
-      for (int k = 0; k < cluster; ++k) {
-        if (k == rank) front = state;
-        state = apply<STARTS>(s.block[turn][k][lane], state);
-      }
+    if (came.ok) {
+      if (lane == 0) expect(s, turn, cluster);
+      came.armed = (int)step + 1;
+      came.ok = await(s, &s.given[turn], parity, a.status, a.wait_ns);
     }
+    float4 all = make_float4(1.f, 1.f, 0.f, 0.f);
     for (int k = 0; k < warps; k += kBatch) {
       float4 m[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) m[i] = s.warp[turn][k + i < warps ? k + i : k][lane];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (k + i < warps) {
-          s.front[turn][k + i][lane] = front;
-          front = apply<STARTS>(m[i], front);
-        }
-      }
+      for (int i = 0; i < kBatch; ++i)
+        if (k + i < warps) all = compose<STARTS>(all, m[i]);
     }
-    if (cluster == 1) state = front;
-    __syncwarp();
-    if (lane == 0) arrive(&s.ready[turn]);
+    if (came.ok) {
+      for (int k = 0; k < cluster; ++k)
+        send(&s.block[turn][rank][lane], &s.full[turn], (rank + k) % cluster, all);
+      came.sent = (int)step + 1;
+      came.ok = await(s, &s.full[turn], parity, a.status, a.wait_ns);
+    }
+    f32x2 front = state;
+    for (int k = 0; k < cluster; ++k) {
+      if (k == rank) front = state;
+      state = apply<STARTS>(s.block[turn][k][lane], state);
+    }
+    (void)fronts<STARTS>(s, turn, warps, lane, front);
   }
   return state;
+}
+
+// The blocks of a cluster end together, none while another's maps may be on their way to it: all have
+// received those of every step, unless a wait ran out somewhere.  They tell each other how far they came.
+// A lane is one step ahead of any other at most (it sends a step when it has received all of the one
+// before), so those behind send theirs of that step too, whatever it holds, and all wait for the last bytes.
+__device__ __forceinline__ void part(Maps& s, bool exchanges, int lane, int rank, int cluster,
+                                     const Came& came) {
+  if (exchanges) {
+    const uint32_t most = __reduce_max_sync(0xffffffffu, (unsigned)came.sent);
+    const uint32_t told = most | (__all_sync(0xffffffffu, came.ok) ? 0u : kGaveUp);
+    if (lane < cluster) {
+      uint32_t at;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_at(&s.told[rank])), "r"(lane));
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(told) : "memory");
+    }
+  }
+  cluster_sync();
+  const volatile uint32_t* told = s.told;
+  uint32_t early = 0, most = 0;
+  for (int k = 0; k < cluster; ++k) {
+    early |= told[k] & kGaveUp;
+    most = max(most, told[k] & ~kGaveUp);
+  }
+  if (!early) return;  // (the same in all blocks)
+  if (exchanges) {
+    if ((uint32_t)came.sent < most) {
+      const int turn = came.sent & 1;
+      if (lane == 0 && came.armed == came.sent) expect(s, turn, cluster);
+      for (int k = 0; k < cluster; ++k)
+        send(&s.block[turn][rank][lane], &s.full[turn], k, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    for (uint32_t step = most < 2 ? 0 : most - 2; step < most; ++step)
+      for (int i = 0; i < 4096; ++i)
+        if (completed(&s.full[step & 1], step >> 1 & 1)) break;
+  }
+  cluster_sync();
 }
 
 // ---------------------------------------------------------------- the split

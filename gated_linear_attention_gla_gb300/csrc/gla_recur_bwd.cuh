@@ -51,9 +51,12 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
   };
   maps_init(maps, warps, p.cluster);
 
+  Came came;
   if (w == warps) {
     f32x2 state = STARTS ? both(0.f) : last_of(g);
-    state = exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a.status);
+    state = p.cluster == 1
+                ? exchange_alone<STARTS>(maps, steps, warps, lane, state, a)
+                : exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a, came);
     if (!STARTS && rank == 0) first(g, state);
   } else {
     // a warp's tiles, one for every stage: its streams (x, f, dy, i, z), then the kept state
@@ -220,7 +223,7 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
       fetch(tile, run - kBwdStages * reach);
       tile = tile == tiles + (kBwdStages - 1) * kStage ? tiles : tile + kStage;
       if (OUT) store(b.dz, at, n, dz);
-      const f32x2 behind = take(maps, step, w, lane, a.status);
+      const f32x2 behind = take(maps, step, w, lane);
       f32x2 v[kL];
 #pragma unroll
       for (int t = 0; t < kL; ++t) {
@@ -240,7 +243,7 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
     }
     cp_wait<0>();
   }
-  if (p.cluster > 1) cluster_sync();  // (no block ends while another may still send to it)
+  if (p.cluster > 1) part(maps, w == warps, lane, rank, p.cluster, came);
   if (DECAY && b.d_decay) {
     float2* part = reinterpret_cast<float2*>(shared + sizeof(Maps));
     __syncthreads();

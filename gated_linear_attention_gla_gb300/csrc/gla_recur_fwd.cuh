@@ -24,14 +24,16 @@ namespace {
 
 // A block's shape: tokens of a run, warps that compute (the exchange's comes on top), runs of
 // a warp whose rows are in flight or in use.
-template <int RUN, int WARPS, int STAGES> struct Tile {
+template <int RUN, int WARPS, int STAGES, bool ALONE = false> struct Tile {
   static constexpr int kRun = RUN, kWarps = WARPS, kStages = STAGES;
+  static constexpr bool kAlone = ALONE;  // for a cluster of one block
 };
 // Long runs spread the exchange of a cluster over more tokens and cost registers (16 warps of 128);
 // where a block walks its sequence alone short ones with more warps are faster: 8192 x 2048
-// 45 us by runs of 8, 40 us by runs of 4; 20001 packed rows in clusters of 4 92 and 134 us.
+// 45 us by runs of 8, 40 us by runs of 4; 20001 packed rows in clusters of 4 92 and 134 us.  (Without the
+// code for clusters 39.0 us, with it 40.4.)
 using LongRuns = Tile<8, 15, 2>;
-using ShortRuns = Tile<4, 19, 3>;
+using ShortRuns = Tile<4, 19, 3, true>;
 using WideRuns = Tile<4, 15, 2>;  // fp32 rows
 constexpr int kBlocks = 1;        // an SM
 
@@ -68,9 +70,12 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
   if (!STARTS && w == warps) maps.front[0][0][lane] = init_of(g);
   maps_init(maps, warps, p.cluster);
 
+  Came came;
   if (w == warps) {
     f32x2 state = STARTS ? both(0.f) : maps.front[0][0][lane];
-    state = exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a.status);
+    state = TILE::kAlone || p.cluster == 1
+                ? exchange_alone<STARTS>(maps, steps, warps, lane, state, a)
+                : exchange<STARTS>(maps, steps, warps, rank, p.cluster, lane, state, a, came);
     if (!KEEP && !STARTS && a.final_state && rank == 0) finish(g, state);
   } else {
     T* const tiles = reinterpret_cast<T*>(shared + sizeof(Maps)) + w * kStages * kStreams * kTile;
@@ -193,7 +198,7 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
     };
 
     auto second_pass = [&](Run& u, long long step) {
-      const f32x2 front = take(maps, (int)step, w, lane, a.status);
+      const f32x2 front = take(maps, (int)step, w, lane);
       if constexpr (KEEP) {
         // in front of tokens 0, kKeep, ... of the run
         float* to = kept + (g * kept_rows + (u.r0 - lo) / kKeep) * a.D + c;
@@ -251,7 +256,7 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
     if (steps > 0 && steps % 2 == 0) second_pass(odd, steps - 1);
     cp_wait<0>();
   }
-  if (p.cluster > 1) cluster_sync();  // (no block ends while another may still send to it)
+  if (!TILE::kAlone && p.cluster > 1) part(maps, w == warps, lane, rank, p.cluster, came);
 }
 
 template <typename T, typename TILE, bool DECAY, bool GATE, bool OUT, bool STARTS, bool KEEP>
@@ -290,10 +295,11 @@ cudaError_t run(const RecurArgs& a, float* kept, long long kept_rows, cudaStream
   using Usual = std::conditional_t<sizeof(T) == 4, WideRuns, LongRuns>;
   const Split p = of(Usual());
   if (p.spg != 1) return run_tile<T, Usual, DECAY, GATE, OUT, true, KEEP>(a, p, kept, kept_rows, stream);
-  if constexpr (sizeof(T) == 2)
-    if (p.cluster == 1)
-      return run_tile<T, ShortRuns, DECAY, GATE, OUT, false, KEEP>(a, of(ShortRuns()), kept,
-                                                                   kept_rows, stream);
+  if constexpr (sizeof(T) == 2) {
+    const Split alone = of(ShortRuns());
+    if (p.cluster == 1 && alone.cluster == 1)
+      return run_tile<T, ShortRuns, DECAY, GATE, OUT, false, KEEP>(a, alone, kept, kept_rows, stream);
+  }
   return run_tile<T, Usual, DECAY, GATE, OUT, false, KEEP>(a, p, kept, kept_rows, stream);
 }
 

@@ -742,16 +742,19 @@ const char *gla_last_error_string(void);
 /*
  * gla_set_wait_limit_ns -- the wall-time limit of the waits with which the
  * warp roles of the tensor-core prefill kernels (gla_chunk_fwd, the mixer and
- * backward calls that run them) hand chunks to one another; 0 restores the
- * default, 2 s.  Process-wide, read at each launch; returns the previous
- * setting (0 = the default).  A wait that runs out makes the kernel stop
- * issuing work, let its own copies and matrix products land (with the default
- * limit), release its tensor memory and return: gla_status_sync then reports
- * GLA_ERR_TIMEOUT and the call's outputs are undefined.  For tests of that
- * path: a limit shorter than a chunk's hand-offs (about a microsecond) makes
- * the next call fail that way, and the call after the default is restored
- * runs normally.  The pages have no counterpart (failure handling is the
- * library's own).
+ * backward calls that run them), of the projections (gla_glu_*) and of the gated
+ * recurrence's prompts and gradients (gla_recur_fwd, gla_recur_bwd) hand work to
+ * one another; 0 restores the default, 2 s.  Process-wide, read at each launch;
+ * returns the previous setting (0 = the default).  A wait that runs out makes the
+ * kernel stop issuing work, let its own copies and matrix products land (with
+ * limits of their own), release its tensor memory and return: gla_status_sync
+ * then reports GLA_ERR_TIMEOUT and the call's outputs are undefined.  For tests of
+ * that path: a limit shorter than a chunk's hand-offs (about a microsecond) makes
+ * the next prefill fail that way, and the call after the default is restored
+ * runs normally.  In the projections a wait lasts as long as one tile's sum over
+ * K (0.34 us for every 64), in the recurrence microseconds; its limit there is longer
+ * by 4 us for each packed sequence.  The pages have no counterpart (failure
+ * handling is the library's own).
  */
 uint64_t gla_set_wait_limit_ns(uint64_t nanoseconds);
 
