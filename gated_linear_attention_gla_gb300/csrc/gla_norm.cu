@@ -141,7 +141,7 @@ cudaError_t run_fwd(const NormArgs& a, cudaStream_t stream) {
     const int pieces = R * (kPieces<RT> + 2 * kPieces<T>);
     const int stages = s.k == 1 ? ring_stages(pieces, threads, other, blocks) : 1;
     const int smem = other + (s.k == 1 ? stages * pieces * 16 * threads : 0);
-    const long long need = (a.rows + s.groups * R - 1) / (s.groups * R);
+    const long long need = ((long long)a.rows + s.groups * R - 1) / (s.groups * R);
     const cudaError_t e = allow_shared(kernel, 227 * 1024, done);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3((unsigned)(need < hold ? need : hold)), dim3(threads), smem,

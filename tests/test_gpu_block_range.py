@@ -234,6 +234,44 @@ def test_layer_norm_keeps_the_variance(gla):
         assert float(off.max()) <= 17 * 2 ** -24, (n, float(off.max()))
 
 
+def room_for(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < (gigabytes + 8) << 30:
+        pytest.skip(f"needs {gigabytes} GB of free GPU memory")
+
+
+def test_block_norm_of_the_most_rows(gla):
+    """2^31 - 1 rows of eight channels: the first and the last rows, forward and gradient."""
+    R, D, n = 2 ** 31 - 1, 8, 1000
+    room_for(136)
+    g = torch.Generator().manual_seed(75)
+    ends = rnd(g, 2 * n, D, dtype=torch.bfloat16)
+    du, ds = (rnd(g, 2 * n, D, dtype=torch.bfloat16) for _ in range(2))
+    w = rnd(g, D, mean=1.0)
+    eps = 1e-6
+    ref = block_ref.block_norm_all(ends, None, None, None, None, None, w, None, False, eps, du, ds)
+
+    def long(t):
+        x = torch.zeros(R, D, dtype=torch.bfloat16, device="cuda")
+        x[:n], x[-n:] = t[:n].cuda(), t[n:].cuda()
+        return x
+
+    res = long(ends)
+    u = gla.block_norm_fwd(res, weight=gpu(w), eps=eps)[1]
+    got = torch.cat([u[:n], u[-n:]])
+    near(got, (ref["u"][0], 2 ** -17 * ref["u"][1] + 2 ** -8 * ref["u"][0].abs()), 1.001, "u")
+    assert not u[n:2 * n].any() and not u[R // 2:R // 2 + n].any()
+    del u
+    d = gla.block_norm_bwd(res, long(du), long(ds), weight=gpu(w), eps=eps)
+    got = torch.cat([d[0][:n], d[0][-n:]])
+    near(got, (ref["d_res"][0], 2 ** -16 * ref["d_res"][1] + 2 ** -8 * ref["d_res"][0].abs()), 1.001, "d_res")
+    # (of the rows between nothing is added)
+    near(d[6], ref["dw"], 2 ** -16 + 2 * n * 2 ** -24, "dw")
+    gla.status_sync()
+    del res, d
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- feed-forward
 @pytest.mark.parametrize("backward", [False, True])
 def test_glu_gives_up_again_and_again(gla, backward):
@@ -286,3 +324,22 @@ def test_glu_gradients_of_the_most_rows(gla):
         want += (hs * xs / 2).t() @ xs
     assert torch.equal(dg.double(), want) and float(want[3, 3]) == R / 2
     assert not du.any() and not dx.any()
+
+
+def test_glu_of_the_most_rows(gla):
+    """2^31 - 1 rows of eight channels and features: the first and the last rows."""
+    R, D, n = 2 ** 31 - 1, 8, 1000
+    room_for(68)
+    g = torch.Generator().manual_seed(82)
+    bf = torch.bfloat16
+    ends = rnd(g, 2 * n, D, dtype=bf)
+    wg, wu = (rnd(g, D, D, std=D ** -0.5, dtype=bf) for _ in range(2))
+    x = torch.zeros(R, D, dtype=bf, device="cuda")
+    x[:n], x[-n:] = ends[:n].cuda(), ends[n:].cuda()
+    h = gla.glu_fwd(x, gpu(wg), gpu(wu))
+    gla.status_sync()
+    value, tol = block_ref.glu_all(ends, wg, wu)["h"]
+    near(torch.cat([h[:n], h[-n:]]), (value, tol + 2 ** -8 * value.abs()), 1.001, "h")
+    assert not h[R // 2:R // 2 + n].any()
+    del x, h
+    torch.cuda.empty_cache()
