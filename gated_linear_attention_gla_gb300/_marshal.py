@@ -1,4 +1,4 @@
-"""Argument marshalling shared by ``ssm`` and ``pages``: checks, row strides,
+"""Argument marshalling shared by ``ssm``, ``block`` and ``pages``: checks, row strides,
 the device and stream a call runs on."""
 from __future__ import annotations
 
@@ -22,6 +22,14 @@ def check(cond: bool, msg: str):
     that calls which are fine do not pay for it."""
     if not cond:
         raise ValueError(msg)
+
+
+def counted(n: int, what: str) -> int:
+    """A number of rows, sequences, channels or pages as the library takes it, a C int (ctypes cuts
+    off what does not fit)."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{n} {what}: at most 2^31 - 1")
+    return n
 
 
 def ptr(t) -> int:
@@ -113,13 +121,13 @@ def batch(x, cu_seqlens, name: str):
         if x.dim() != 3:
             raise ValueError(f"a dense {name} is [B, T, D]")
         lead = x.shape[:2]
-        return lead, lead[0], lead[1]
+        return lead, counted(lead[0], "sequences"), counted(lead[1], "tokens")
     if x.dim() != 2 and not (x.dim() == 3 and x.shape[0] == 1):
         raise ValueError(f"a packed {name} is [1, R, D] or [R, D]")
     check(cu_seqlens.dtype is torch.int32 and cu_seqlens.device == x.device and
           cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
           "cu_seqlens must be contiguous int32 [B + 1] on the inputs' GPU")
-    return x.shape[:-1], cu_seqlens.numel() - 1, x.shape[-2]
+    return x.shape[:-1], counted(cu_seqlens.numel() - 1, "sequences"), counted(x.shape[-2], "rows")
 
 
 def output(out, shape, dtype, device):

@@ -18,7 +18,7 @@ import torch
 
 from ._binding import (GLA_FLAG_FP32_IO, GLA_FLAG_FP32_OUT, GLA_FLAG_FP32_RESIDUAL,
                        GLA_FLAG_LAYER_NORM, GLA_FLAG_UNIT_VARIANCE)
-from ._marshal import (batch, check, done, io_flags, launch_on, lib, output, page_tables, ptr,
+from ._marshal import (batch, check, counted, done, io_flags, launch_on, lib, output, page_tables, ptr,
                        rows, scratch, whole)
 
 _F32 = torch.float32
@@ -26,6 +26,7 @@ _F32 = torch.float32
 
 def _recur_rows(x, f, decay, i, z):
     """Checks; the row arguments shared by the recurrence's entry points."""
+    counted(x.shape[-1], "channels")
     check(x.is_cuda, "x must be a CUDA tensor")
     dev, ty, wide = x.device, x.dtype, x.shape
     pi, si = (None, 0) if i is None else rows(i, "i", wide, ty, dev)
@@ -103,8 +104,10 @@ def recur_step(x, f, state, decay=None, i=None, z=None, unit_variance: bool = Tr
     pool [num_slots, D], as for ``conv_step``."""
     check(x.dim() == 2, "x is [N, D]")
     (N, D), dev, dt = x.shape, x.device, x.dtype
+    n = counted(N, "rows")
     args = _recur_rows(x, f, decay, i, z)
-    n = N if slots is None else state.shape[0] if state.dim() else 0
+    if slots is not None:
+        n = counted(state.shape[0], "pages") if state.dim() else 0
     ps = whole(state, "state", (n, D), _F32, dev)
     pi, po = page_tables(N, dev, slots, out_slots)
     flags = io_flags(dt, out.dtype if out is not None else out_dtype or dt)
@@ -118,11 +121,11 @@ def recur_step(x, f, state, decay=None, i=None, z=None, unit_variance: bool = Tr
 
 def _norm_rows(res, y, z, post_weight, post_bias, scale, weight, bias, kind, dtype):
     """Checks; (D, rows, flags, the leading row arguments, the parameters' addresses)."""
+    check(res.dim() in (2, 3), "res is [R, D] or [B, T, D]")
+    R, D = counted(res.shape[:-1].numel(), "rows"), counted(res.shape[-1], "channels")
     check(res.is_cuda, "res must be a CUDA tensor")
     check(kind in ("rms", "layer"), 'kind is "rms" or "layer"')
     dev, wide = res.device, res.shape
-    check(res.dim() in (2, 3), "res is [R, D] or [B, T, D]")
-    D, R = wide[-1], wide[:-1].numel()
     if dtype is torch.float32:
         flags = GLA_FLAG_FP32_IO
     else:
@@ -224,12 +227,13 @@ def block_norm_bwd(res, d_out=None, d_res_out=None, y=None, z=None, post_weight=
 
 def _glu_rows(x, w_gate, w_up):
     """Checks; (R, D, F, the leading arguments)."""
+    check(x.dim() in (2, 3) and w_gate.dim() == 2, "x is [R, D] or [B, T, D], weights are [F, D]")
+    R, D = counted(x.shape[:-1].numel(), "rows"), counted(x.shape[-1], "channels")
+    F = counted(w_gate.shape[0], "features")
     check(x.is_cuda, "x must be a CUDA tensor")
     check(x.dtype is torch.bfloat16, "the projections are bf16")
-    check(x.dim() in (2, 3) and w_gate.dim() == 2, "x is [R, D] or [B, T, D], weights are [F, D]")
-    D, dev = x.shape[-1], x.device
-    F = w_gate.shape[0]
-    return x.shape[:-1].numel(), D, F, (
+    dev = x.device
+    return R, D, F, (
         *rows(x, "x", x.shape, x.dtype, dev), whole(w_gate, "w_gate", (F, D), x.dtype, dev),
         whole(w_up, "w_up", (F, D), x.dtype, dev))
 

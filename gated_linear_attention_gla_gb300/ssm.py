@@ -19,8 +19,8 @@ from typing import Optional
 import torch
 
 from ._binding import GLA_FLAG_SILU, GLA_FLAG_SOFTPLUS
-from ._marshal import (batch, check, done, io_flags, launch_on, lib, output, page_tables, ptr,
-                       rows, scratch, whole)
+from ._marshal import (batch, check, counted, done, io_flags, launch_on, lib, output, page_tables,
+                       ptr, rows, scratch, whole)
 
 _F32 = torch.float32
 
@@ -38,13 +38,13 @@ def _state(state, n, a, b, dtype, device, slots):
             (slots is None and shape[0] != n):
         raise ValueError(f"state must be contiguous {dtype} "
                          f"[{n if slots is None else 'num_slots'}, {a}, {b}] on {device}")
-    return state.data_ptr(), 0 if slots is None else shape[0]
+    return state.data_ptr(), 0 if slots is None else counted(shape[0], "pages")
 
 
 def _filter(x, weight, bias):
     """(D, W, the filter's and the bias's addresses)."""
+    D, dev = counted(x.shape[-1], "channels"), x.device
     check(x.is_cuda, "x must be a CUDA tensor")
-    D, dev = x.shape[-1], x.device
     check(weight.dim() == 2, "weight is [D, W]")
     W = weight.shape[1]
     return (D, W, whole(weight, "weight", (D, W), _F32, dev),
@@ -63,8 +63,8 @@ def conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None,
     inputs (oldest first).  ``out`` has x's dtype, or fp32
     (``out_dtype=torch.float32``); ``final_state`` may be ``init_state``.
     """
-    D, W, w, b = _filter(x, weight, bias)
     lead, B, T = batch(x, cu_seqlens, "x")
+    D, W, w, b = _filter(x, weight, bias)
     dev, dt, st = x.device, x.dtype, (B, W - 1, D)
     px, stride = rows(x, "x", x.shape, dt, dev)
     flags = io_flags(dt, out.dtype if out is not None else out_dtype or dt)
@@ -90,8 +90,8 @@ def conv_bwd(x, weight, d_out, bias=None, init_state=None, d_final_state=None, c
     ``dx`` has x's dtype, or fp32 with ``grad_dtype=torch.float32``; ``d_bias`` is
     None without a bias; ``d_init`` is fp32 (None when not requested).
     """
-    D, W, w, b = _filter(x, weight, bias)
     lead, B, T = batch(x, cu_seqlens, "x")
+    D, W, w, b = _filter(x, weight, bias)
     dev, dt, st = x.device, x.dtype, (B, W - 1, D)
     px, stride = rows(x, "x", x.shape, dt, dev)
     grad_dtype = grad_dtype or dt
@@ -122,9 +122,9 @@ def conv_step(x, weight, state, bias=None, activation: Optional[str] = None, slo
     given (the page read stays as it was).  -1 in either marks a row that does
     nothing.
     """
-    D, W, w, b = _filter(x, weight, bias)
     check(x.dim() == 2, "x is [N, D]")
-    N, dev, dt = x.shape[0], x.device, x.dtype
+    N, dev, dt = counted(x.shape[0], "rows"), x.device, x.dtype
+    D, W, w, b = _filter(x, weight, bias)
     px, stride = rows(x, "x", x.shape, dt, dev)
     ps, pages = _state(state, N, W - 1, D, dt, dev, slots)
     pi, po = page_tables(N, dev, slots, out_slots)
@@ -139,9 +139,9 @@ def conv_step(x, weight, state, bias=None, activation: Optional[str] = None, slo
 
 def _scan_common(u, dt, a, b, c, skip, z, dt_bias, lead):
     """Checks; returns (D, N, the row arguments shared by the scan's entry points)."""
-    check(u.is_cuda, "u must be a CUDA tensor")
     dev, ty, wide = u.device, u.dtype, u.shape
-    D, N = wide[-1], a.shape[-1]
+    D, N = counted(wide[-1], "channels"), a.shape[-1]
+    check(u.is_cuda, "u must be a CUDA tensor")
     narrow = (*lead, N)
     pz, sz = (None, 0) if z is None else rows(z, "z", wide, ty, dev)
     return D, N, (*rows(u, "u", wide, ty, dev), *rows(dt, "dt", wide, ty, dev),
@@ -223,7 +223,7 @@ def scan_step(u, dt, a, b, c, state, skip=None, z=None, dt_bias=None, softplus: 
     ``out`` [R, D].  ``state`` (fp32 [R, D, N]) is updated in place; with ``slots``
     and ``out_slots`` it is a pool [num_slots, D, N], as for ``conv_step``."""
     check(u.dim() == 2, "u is [R, D]")
-    R = u.shape[0]
+    R = counted(u.shape[0], "rows")
     D, N, args = _scan_common(u, dt, a, b, c, skip, z, dt_bias, (R,))
     dev = u.device
     ps, pages = _state(state, R, D, N, _F32, dev, slots)
