@@ -24,8 +24,8 @@ static gla_status norm_args(const void* res, const void* y, int64_t y_stride, co
   const long long esz = fp32 ? 4 : 2;
   if (rows > 0 && !y && (z || post_weight || scale)) return GLA_ERR_INVALID_ARG;
   if (!post_weight && post_bias) return GLA_ERR_INVALID_ARG;
-  if (D > 0 && ((y && (stride_bad(y_stride, D) || rows * y_stride > kMaxElems)) ||
-                (z && (stride_bad(z_stride, D) || rows * z_stride > kMaxElems))))
+  if (D > 0 && ((y && (stride_bad(y_stride, D) || too_many(rows, y_stride))) ||
+                (z && (stride_bad(z_stride, D) || too_many(rows, z_stride)))))
     return GLA_ERR_INVALID_ARG;
   if (rows > 0 && D > 0 && !res) return GLA_ERR_INVALID_ARG;
   if (!aligned(res, 16) || !aligned(y, 16) || !aligned(z, 16) || !aligned(post_weight, 16) ||
@@ -127,9 +127,8 @@ static gla_status recur_rows(const void* x, int64_t x_stride, const void* f, int
                              const float* decay, long long rows, int D, unsigned flags) {
   const long long esz = (flags & GLA_FLAG_FP32_IO) ? 4 : 2;
   if (stride_bad(x_stride, D) || stride_bad(f_stride, D) || (i && stride_bad(i_stride, D)) ||
-      (z && stride_bad(z_stride, D)) || rows * x_stride > kMaxElems ||
-      rows * f_stride > kMaxElems || (i && rows * i_stride > kMaxElems) ||
-      (z && rows * z_stride > kMaxElems) || (rows > 0 && (!x || !f)))
+      (z && stride_bad(z_stride, D)) || too_many(rows, x_stride) || too_many(rows, f_stride) ||
+      (i && too_many(rows, i_stride)) || (z && too_many(rows, z_stride)) || (rows > 0 && (!x || !f)))
     return GLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(f, 16) || !aligned(i, 16) || !aligned(z, 16) ||
       stride_misaligned(x_stride, esz) || stride_misaligned(f_stride, esz) ||
@@ -294,7 +293,7 @@ static gla_status glu_args(const void* x, int64_t x_stride, const void* w_gate, 
   if ((flags & GLA_FLAG_FP32_IO) || D % 8 != 0 || F % 8 != 0 || D > 1 << 20 || F > 1 << 20)
     return GLA_ERR_UNSUPPORTED;
   if (D == 0 || F == 0) return GLA_OK;
-  if (stride_bad(x_stride, D) || rows * x_stride > kMaxElems || (long long)rows * F > kMaxElems ||
+  if (stride_bad(x_stride, D) || too_many(rows, x_stride) || too_many(rows, F) ||
       !w_gate || !w_up || (rows > 0 && !x))
     return GLA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || stride_misaligned(x_stride, 2) || !aligned(w_gate, 16) ||

@@ -43,6 +43,9 @@ inline size_t span(long long rows, long long stride, long long cols, long long e
   return rows > 0 ? (size_t)(((rows - 1) * stride + cols) * esz) : 0;
 }
 
+// More than kMaxElems elements (whose number need not fit 64 bits).
+inline bool too_many(long long rows, long long stride) { return stride > 0 && rows > kMaxElems / stride; }
+
 inline gla_status finish(cudaError_t e) { return static_cast<gla_status>(gla::cuda_result(e)); }
 
 inline bool channels_ok(int D) { return D % 8 == 0 && D <= 1 << 24; }

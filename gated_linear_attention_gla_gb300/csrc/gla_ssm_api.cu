@@ -35,7 +35,7 @@ gla_status gla_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
   const long long esz = fp32 ? 4 : 2, osz = f32out ? 4 : 2;
   const long long rows = cu_seqlens ? (long long)T : (long long)B * T;
-  if (stride_bad(x_stride, D) || rows * x_stride > kMaxElems ||
+  if (stride_bad(x_stride, D) || too_many(rows, x_stride) ||
       (long long)B * (W - 1) * D > kMaxElems || (rows + 7) / 8 + B > kMaxGrid)
     return GLA_ERR_INVALID_ARG;
   if (!weight || (rows > 0 && (!x || !out))) return GLA_ERR_INVALID_ARG;
@@ -83,7 +83,7 @@ gla_status gla_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
   const long long esz = fp32 ? 4 : 2, osz = f32out ? 4 : 2;
   const long long rows = cu_seqlens ? (long long)T : (long long)B * T;
-  if (stride_bad(x_stride, D) || rows * x_stride > kMaxElems ||
+  if (stride_bad(x_stride, D) || too_many(rows, x_stride) ||
       (long long)B * (W - 1) * D > kMaxElems || (rows + 7) / 8 + B > kMaxGrid)
     return GLA_ERR_INVALID_ARG;
   if (!weight || !d_weight || (rows > 0 && (!x || !d_out || !dx || B == 0)))
@@ -136,7 +136,7 @@ gla_status gla_conv_step(const void* x, int64_t x_stride, const float* weight, c
   const bool f32out = fp32 || (flags & GLA_FLAG_FP32_OUT) != 0;
   const long long esz = fp32 ? 4 : 2, osz = f32out ? 4 : 2;
   const long long pages = slots ? num_slots : N;
-  if (stride_bad(x_stride, D) || (long long)N * x_stride > kMaxElems ||
+  if (stride_bad(x_stride, D) || too_many(N, x_stride) ||
       pages * (W - 1) * D > kMaxElems)
     return GLA_ERR_INVALID_ARG;
   if (!x || !weight || (!state && pages > 0) || !out) return GLA_ERR_INVALID_ARG;
@@ -181,7 +181,7 @@ gla_status scan_args(const void* u, int64_t u_stride, const void* dt, int64_t dt
     return GLA_ERR_INVALID_ARG;
   const long long widest = u_stride > dt_stride ? u_stride : dt_stride;
   const long long narrow = b_stride > c_stride ? b_stride : c_stride;
-  if (rows * widest > kMaxElems || rows * narrow > kMaxElems || (z && rows * z_stride > kMaxElems) ||
+  if (too_many(rows, widest) || too_many(rows, narrow) || (z && too_many(rows, z_stride)) ||
       (long long)B * D * N > kMaxElems || (rows / 64 + B) * (((long long)D * N + 1023) / 1024) > kMaxGrid ||
       rows * 2 * N / 256 > kMaxGrid)
     return GLA_ERR_INVALID_ARG;

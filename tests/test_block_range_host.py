@@ -5,6 +5,8 @@ import torch
 
 import gated_linear_attention_gla_gb300 as gla
 from gated_linear_attention_gla_gb300 import _binding as E
+import test_block_host as block
+import test_ssm_host as ssm
 from test_block_host import L, glu  # noqa: F401
 
 FAR = [k << 48 for k in range(1, 16)]  # fake, aligned, never dereferenced, far apart
@@ -48,3 +50,31 @@ def test_counts_that_no_c_int_holds(n):
     for call in calls:
         with pytest.raises(ValueError, match="at most 2.31 - 1"):
             call()
+
+
+MOST, APART = 2 ** 31 - 1, 1 << 40
+
+
+def far(*names):
+    """Tensors far apart, so that no overlap is found."""
+    return {n: (k + 1) << 54 for k, n in enumerate(names)}
+
+
+RECUR = far("x", "f", "i", "z", "decay", "init", "out", "fin", "dy", "dfin", "dx", "df", "di", "dz", "dd", "d0", "ws", "st")
+NORM = far("res", "y", "z", "pw", "pb", "sc", "w", "b", "ro", "out", "du", "ds", "dr", "dy", "dz", "dpw", "dpb", "dsc", "dw", "db", "ws")
+GLU = far("x", "wg", "wu", "out", "dx", "dwg", "dwu", "ws")
+SSM = far("x", "w", "b", "init", "out", "fin", "u", "dt", "a", "c", "skip", "z", "bias", "ws")
+
+
+@pytest.mark.parametrize("call,kw", [
+    (block.recur_fwd, dict(RECUR, B=MOST, T=MOST, i=None, z=None)), (block.recur_fwd, dict(RECUR, B=1 << 8, T=1 << 16, xs=APART)),
+    (block.recur_bwd, dict(RECUR, B=MOST, T=MOST, wb=1 << 62)), (block.recur_bwd, dict(RECUR, B=1, T=1 << 24, fs=APART, wb=1 << 62)),
+    (block.recur_step, dict(RECUR, N=1 << 24, zs=APART)), (block.recur_step, dict(RECUR, N=MOST, is_=APART)),
+    (block.norm_fwd, dict(NORM, R=MOST, ys=APART)), (block.norm_fwd, dict(NORM, R=1 << 24, zs=APART)),
+    (block.norm_bwd, dict(NORM, R=1 << 24, zs=APART, wb=1 << 62)),
+    (lambda L, **kw: glu(L, False, **kw), dict(GLU, R=1 << 24, xs=APART)),
+    (lambda L, **kw: glu(L, True, **kw), dict(GLU, R=1 << 25, xs=APART, wb=1 << 62)),
+    (ssm.conv_fwd, dict(SSM, B=1, T=1 << 24, xs=APART)), (ssm.scan_fwd, dict(SSM, B=1, T=1 << 24, us=APART, wb=1 << 62))])
+def test_more_elements_than_64_bits_count(L, call, kw):
+    """Rows times their distance beyond 2^63, which wrapped to a small or negative number of elements."""
+    assert call(L, **kw) == E.GLA_ERR_INVALID_ARG
