@@ -101,10 +101,11 @@ __device__ __forceinline__ void exp2m1_near(f32x2 l, f32x2* a, f32x2* u) {
   *a = fma2(*u, both(-1.f), both(1.f));
 }
 
-__device__ __forceinline__ float rsqrt_or_0(float v) {  // 0 where v is 0
+// 0 where v is below the smallest normal number, as the square root of such a v is in sqrt_of
+__device__ __forceinline__ float rsqrt_or_0(float v) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return v < 1e-37f ? 0.f : r;
+  return v < 1.17549435e-38f ? 0.f : r;
 }
 __device__ __forceinline__ float sqrt_of(float v) {
   float r;

@@ -143,6 +143,32 @@ def test_recur_gates_at_the_infinities(gla, unit):
     gla.status_sync()
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_recur_factor_of_nearly_open_gates(gla, io):
+    """m = sqrt(1 - a^2) of decays next to 1: right down to 1 - a^2 = 2^-126 (although a is 1 from 2^-25 on), 0 below,
+    the same in the prompt, the gradients and the step.  From f = -84 and decay = -exp(v): 1 - a^2 =
+    2 exp(v - 84) to 2^-80 of it; with x = 1 and d_out = 1 both out and dx are m.  Errors: f's
+    sigmoid 2^-21 and 84 2^-24, u's polynomial and products 2^-20, the root 2^-22, half of them in m: 2^-17."""
+    v = torch.linspace(-5.0, 6.0, 4096)
+    D = len(v)
+    decay = -torch.exp(v)
+    one = torch.ones(1, 1, D, dtype=DT[io]).cuda()
+    f = torch.full_like(one, -84.0)
+    room = -2 * decay.double() / (1 + torch.exp(torch.tensor(84.0, dtype=torch.float64)))
+    kw = dict(decay=gpu(decay))
+    y = gla.recur_fwd(one, f, out_dtype=F32, **kw)[0][0, 0]
+    dx = gla.recur_bwd(one, f, one, grad_dtype=F32, **kw)[0][0, 0]
+    state = torch.zeros(1, D, device="cuda")
+    step = gla.recur_step(one[0], f[0], state, out_dtype=F32, **kw)[0]
+    assert torch.equal(y, step) and torch.equal(y == 0, dx == 0)
+    for m in (y, dx):
+        m, want = m.double().cpu(), room.sqrt()
+        below, above = room < 2.0 ** -126 * (1 - 2 ** -16), room > 2.0 ** -126 * (1 + 2 ** -16)
+        assert below.sum() > 100 and above.sum() > 1000
+        assert not m[below].any() and (((m - want).abs() <= 2 ** -17 * want) | ~above).all()
+    gla.status_sync()
+
+
 # ---------------------------------------------------------------- norms
 def norm_check(gla, R, D, io, res32, layer, post, pbias, z, scale, weight, bias, y, means=None, seed=73):
     """block_norm_fwd and block_norm_bwd with these parts; `means`: row k's mean is added to
