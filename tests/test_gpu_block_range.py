@@ -169,6 +169,35 @@ def test_recur_factor_of_nearly_open_gates(gla, io):
     gla.status_sync()
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("decay,unit", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("lens,packed", [([5, 0, 9, 33, 1, 130], True), ([37, 37], False), ([260], False)])
+def test_recur_every_combination(gla, io, decay, unit, lens, packed):
+    """Input gate, output gate and initial states, each there and not."""
+    for k in range(8):
+        i, z, init = bool(k & 1), bool(k & 2), bool(k & 4)
+        base.recur_check(gla, recur_inputs(lens, 72, io, decay, i, z, init, 76 + k), lens, packed, unit, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("unit", [True, False])
+@pytest.mark.parametrize("most", [1.3, 1.5, 6.0])
+@pytest.mark.parametrize("lens,packed", [([5, 0, 90, 33, 1], True), ([300], False)])
+def test_recur_strong_decays(gla, io, unit, most, lens, packed):
+    """Decays on both sides of 2 ln 2, from where a warp takes the exponential of all arguments; down to
+    -6, where log a is off by 6 2^-20 < 2^-17 of a, twice the tolerance's 2^-18, which it doubles."""
+    x = recur_inputs(lens, 136, io, True, True, True, True, 77)
+    x["decay"] = x["decay"] * (most / 0.8)
+    base.recur_check(gla, x, lens, packed, unit, io)
+
+
+@pytest.mark.parametrize("T,D", [(9000, 64), (3000, 264)])
+def test_recur_long_sequence_of_few_channels(gla, T, D):
+    x = recur_inputs([T], D, "bf16", True, True, True, True, 78)
+    x["decay"] = x["decay"] * 0.02
+    base.recur_check(gla, x, [T], False, True, "bf16")
+
+
 # ---------------------------------------------------------------- norms
 def norm_check(gla, R, D, io, res32, layer, post, pbias, z, scale, weight, bias, y, means=None, seed=73):
     """block_norm_fwd and block_norm_bwd with these parts; `means`: row k's mean is added to
@@ -230,6 +259,20 @@ def test_block_norm_of_many_rows(gla, R, D, parts):
 def test_block_norm_parts(gla, D, layer, post, pbias, z, scale, bias):
     """Every part with and without its neighbours, where the last threads of a row have no columns."""
     norm_check(gla, 21, D, "fp32", True, layer, post, pbias, z, scale, True, bias, True)
+
+
+@pytest.mark.parametrize("io,res32", [("bf16", False), ("bf16", True), ("fp32", True)])
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("D", [72, 4104])
+def test_block_norm_every_combination(gla, io, res32, layer, D):
+    """Every part there and not."""
+    for post, pbias in ((False, False), (True, False), (True, True)):
+        for weight, bias in ((False, False), (True, False), (True, True)):
+            for z in (False, True):
+                for scale in (False, True):
+                    norm_check(gla, 9, D, io, res32, layer, post, pbias, z, scale, weight, bias, True)
+    for bias in (False, True):
+        norm_check(gla, 9, D, io, res32, layer, False, False, False, False, True, bias, False)
 
 
 @pytest.mark.parametrize("R,D", [(33, 264), (1501, 2048), (401, 5120)])
@@ -369,3 +412,9 @@ def test_glu_of_the_most_rows(gla):
     assert not h[R // 2:R // 2 + n].any()
     del x, h
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("R,D,F", [(129, 1032, 520), (192, 2048, 264), (255, 72, 1352), (320, 520, 392), (511, 264, 136),
+                                   (768, 136, 2056), (128, 520, 1352), (127, 2056, 72), (2, 8192, 136)])
+def test_glu_between_few_rows_and_many(gla, R, D, F):
+    base.test_glu(gla, R, D, F)
