@@ -251,6 +251,9 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
     __syncthreads();
     if (w == 0 && on) {
       for (int k = 1; k < warps; ++k) sum = add2(sum, part[32 * k + lane]);
+      // (a decay above 0 acts as 0 whatever its value)
+      const float2 d = *reinterpret_cast<const float2*>(a.decay + c);
+      sum = make_float2(d.x > 0.f ? 0.f : sum.x, d.y > 0.f ? 0.f : sum.y);
       *reinterpret_cast<float2*>(partial + (g * p.cluster + rank) * a.D + c) = sum;
     }
   }

@@ -533,8 +533,8 @@ gla_status gla_scan_step(const void *u, int64_t u_stride, const void *dt, int64_
  *
  *   x, f, i, z   [rows, D]: bf16, or fp32 with GLA_FLAG_FP32_IO; row strides as for
  *                the scan; i and z may be NULL (their strides are then ignored)
- *   decay        fp32 [D], finite and <= 0 (a value above 0 acts as 0; a channel whose
- *                decay is NaN is NaN), or NULL.
+ *   decay        fp32 [D], finite and <= 0 (a value above 0 acts as 0, and its gradient
+ *                is 0; a channel whose decay is NaN is NaN), or NULL.
  *                1 - a is computed without cancellation, so that m is right where a rounds to
  *                1; m = sqrt(1 - a^2) and its share of the gradients are 0 where 1 - a^2,
  *                or s(f) with a decay, is below 2^-126 (the smallest normal number), in

@@ -170,6 +170,32 @@ def test_recur_factor_of_nearly_open_gates(gla, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,packed", [([5, 0, 9, 33, 1, 130], True), ([300], False)])
+def test_recur_decays_above_zero(gla, io, lens, packed):
+    """They act as 0, whatever their value: their gradient is 0, the channels beside them and all other
+    gradients are those of a decay of 0 (where the formula's own slope, with 1 - a, is e (h - x))."""
+    x = recur_inputs(lens, 72, io, True, True, True, True, 79)
+    x["decay"][::3] = 0.0
+    base.recur_check(gla, x, lens, packed, False, io)
+    above = dict(x, decay=x["decay"].clone())
+    above["decay"][::3] = torch.rand(24, generator=torch.Generator().manual_seed(80)) + 0.01
+    cu = torch.tensor(base.cu_of(lens), dtype=torch.int32).cuda() if packed else None
+
+    def run(x, unit):
+        rows = [base.lead(x[n], lens, packed).cuda() for n in ("x", "f", "dy", "i", "z")]
+        kw = dict(decay=gpu(x["decay"]), i=rows[3], z=rows[4], unit_variance=unit, init_state=gpu(x["init"]), cu_seqlens=cu)
+        return [*gla.recur_fwd(*rows[:2], **kw), *gla.recur_bwd(*rows[:3], d_final_state=gpu(x["df"]), **kw)]
+
+    for unit in (False, True):
+        for n, a, b in zip(("y", "final", "dx", "df", "d_decay", "di", "dz", "d_init"), run(x, unit), run(above, unit)):
+            if n == "d_decay":
+                assert not b[::3].any() and a[::3].all()
+                a[::3] = 0
+            assert torch.equal(a, b), n
+    gla.status_sync()
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
 @pytest.mark.parametrize("decay,unit", [(True, True), (True, False), (False, True), (False, False)])
 @pytest.mark.parametrize("lens,packed", [([5, 0, 9, 33, 1, 130], True), ([37, 37], False), ([260], False)])
 def test_recur_every_combination(gla, io, decay, unit, lens, packed):
