@@ -15,8 +15,12 @@
 //        leave the chip.
 //   kDx  A = dg, then du (the sum over K runs through both), B = Wg, Wu read along N
 //   kDw  A = dg or du read along M, B = x read along N, K = the rows
-// The backward is a kUp launch (dg, du rounded to bf16 into the workspace) and one
-// launch of all kDx and kDw tiles.
+// The backward is a kUp launch (dg, du into the workspace) and one launch of all kDx and kDw tiles.
+// dg and du are rounded to bf16, once each: they are operands of the tensor cores' next products, beside x
+// and the weights, which are bf16 too.  That puts dx and dw 0.0023 off their 64-bit values where one
+// rounding of the results alone gives 0.0017, and so it is where fp32 results are asked for (their sums
+// are fp32, of the rounded factors).  The other choice, two bf16 numbers for each, doubles these products:
+// 20 R D F instead of 12.
 //
 // Roles (10 warps): 0..7 epilogue (thread = half of an accumulator row), 8 producer (TMA into a
 // ring of 6 stages of 64 along K), 9 issuer (the first SM's alone).  The accumulators
@@ -27,8 +31,9 @@
 // the two producers may have stopped at different steps, and a barrier counts both SMs'
 // bytes: they tell each other how far they came, the one behind catches up, and the
 // first SM waits for the last steps.
-// Bound: the tensor pipe, active in 95 % of the cycles of 8192 x 2048 x 8192 (268 to 278 us,
-// 1.98 to 2.05 PFLOP/s); gradients of 4096 rows 445 to 498 us by the power the GPU is given.
+// Bound: the tensor pipe, active in 96 % of the cycles of 8192 x 2048 x 8192: 267 to 284 us (2.06 to 1.94
+// PFLOP/s) in series of some milliseconds, 316 to 319 us (1.74 PFLOP/s) in longer ones, where the power
+// limit holds the clock near 1.5 GHz.  Gradients of 4096 rows likewise 470 to 510 and 515 to 520 us.
 #include "gla_glu.cuh"
 
 namespace gla {

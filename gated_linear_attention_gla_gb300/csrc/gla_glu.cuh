@@ -75,7 +75,8 @@ inline bool make_map(CUtensorMap* map, const void* base, long long cols, long lo
 inline int tiles_of(long long n, int by) { return (int)((n + by - 1) / by); }
 
 // The projections of at most kFewRows rows (gla_glu_few.cu; 128 rows x 2048 x 8192 16.0 us there and
-// 18.0 us by tiles of 256 rows, x 520 x 1352 6.6 and 8.9 us; 192 rows 19.1 and 18.0 us).
+// 18.0 us by tiles of 256 rows, x 520 x 1352 6.6 and 8.9 us; 192 rows 19.1 and 18.0 us).  Tiles of 256 rows
+// cost the same for all of 129 to 256 rows, 18.4 to 18.8 us, of 257 to 512 25.1 to 25.9.
 constexpr int kFewRows = 128;
 cudaError_t launch_few(const GluArgs& a, cudaStream_t stream);
 

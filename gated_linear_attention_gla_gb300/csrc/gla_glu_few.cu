@@ -8,8 +8,8 @@
 // shared memory, in block order.  g and u of a feature lie 64 lanes apart; the
 // accumulators go through shared memory, from where the product leaves in rows of the output.
 //
-// Bound: HBM (the weights).  8 rows x 2048 x 8192 13.5 us where kernels follow one another, 5.0 TB/s;
-// x 4096 x 12288 34.6 us, 5.8 TB/s.
+// Bound: HBM (the weights).  8 rows x 2048 x 8192 13.5 to 17.3 us by the GPU where kernels follow one
+// another, 5.0 to 3.9 TB/s; x 4096 x 12288 34.6 us, 5.8 TB/s.
 #include "gla_glu.cuh"
 
 namespace gla {

@@ -13,7 +13,7 @@
 // over rows, two at a time where there are many, with its parameters in registers and
 // the next rows on their way into shared memory; the sums over the rows are shuffles
 // and one exchange through shared memory.
-// Bound: HBM.  16384 x 2048 with fp32 residuals 85 to 87 us, 5.4 TB/s; issue 40 %.
+// Bound: HBM.  16384 x 2048 with fp32 residuals 85 to 88 us, 5.4 TB/s; issue 40 %.
 #include "gla_norm.cuh"
 
 namespace gla {

@@ -18,7 +18,10 @@ struct Shape {
   int tpr, k, groups;
 };
 // The fewest threads that hold a row with one vector each, or with two above 4096 channels; 256
-// threads a block at least.
+// threads a block at least.  With two vectors nothing is read ahead, the parameters are read for every row,
+// and an SM has one block of 288 to 512 threads: rows of 67 MB a tensor (bf16, RMS, gate and scale) take 57 us
+// at 2048 channels, 64 at 4096, 205 at 4104, 170 at 5120, 123 at 8192; gradients of half of them
+// 55, 63, 195, 163 and 124.
 inline Shape shape_of(int D) {
   const int vecs = (D + kV - 1) / kV, k = vecs <= kMaxThreads ? 1 : 2;
   const int tpr = ((vecs + k - 1) / k + 31) / 32 * 32;

@@ -14,8 +14,8 @@
 // sums would not fit), are summed over a block's groups and written as one partial a
 // block, which a second launch sums in block order.  No atomics: the same inputs
 // give the same bits.
-// Bound: issue slots (54 % of the cycles, 85 instructions an element) and the latency of three
-// exchanges a row.  8192 x 2048, layer norm, gate and scale 73 us, 3.7 TB/s.
+// What takes the time: the latency of three exchanges a row, which 16 warps an SM do not hide (issue slots
+// 54 % used, DRAM 41 %).  8192 x 2048, layer norm with biases, gate and scale 74 us, 3.6 TB/s; RMS 55 us, 4.9.
 #include <type_traits>
 
 #include "gla_norm.cuh"

@@ -8,8 +8,9 @@
 // go out as soon as the rows are in registers).  First pass: gates, and the running
 // map (P_t, H_t) of every token in registers; second pass, with the state in front
 // of the run: h_t = P_t h + H_t.
-// Bound: issue slots.  8192 x 2048 with three gates 39 us (4.3 TB/s; issue 68 %, 128 of 152 SMs have a
-// block), 20001 packed rows with two 88 us (3.7 TB/s; issue 55 %, the cluster's exchange).
+// What takes the time: latency between dependent instructions, and 24 of 152 SMs have no block.  8192 x 2048 with
+// three gates 39 us (4.3 TB/s; 68 % of the issue slots of 128 SMs), 20001 packed rows with two 86 us (3.8 TB/s;
+// issue 56 %, DRAM 41 %, the cluster's exchange); fp32 rows 8192 x 2048 56 us (5.9 TB/s).
 // The same kernel without its outputs (KEEP) writes the state in front of every
 // kKeep tokens for the backward pass.
 #pragma once
@@ -31,7 +32,8 @@ template <int RUN, int WARPS, int STAGES, bool ALONE = false> struct Tile {
 // Long runs spread the exchange of a cluster over more tokens and cost registers (16 warps of 128);
 // where a block walks its sequence alone short ones with more warps are faster: 8192 x 2048
 // 45 us by runs of 8, 40 us by runs of 4; 20001 packed rows in clusters of 4 92 and 134 us.  (Without the
-// code for clusters 39.0 us, with it 40.4.)
+// code for clusters 39.0 us, with it 40.4; 1 x 100 tokens x 512 by one block of long runs 4.4 us, by two of
+// short ones 5.3.)
 using LongRuns = Tile<8, 15, 2>;
 using ShortRuns = Tile<4, 19, 3, true>;
 using WideRuns = Tile<4, 15, 2>;  // fp32 rows
