@@ -216,7 +216,8 @@ inline int ring_stages(int pieces, int threads, int other, int blocks) {
 // Layer norm takes the sums of x and x^2 in one exchange, which loses (mean^2 / variance) of the sums'
 // rounding to cancellation; rows whose mean is over half a deviation take the squares of the
 // centred values in a second one, so that the variance is never off by much more than those would be (2048
-// values: 2e-7 of it; up to four deviations in one exchange it would be 4e-6).
+// values: 2e-7 of it; up to four deviations in one exchange it would be 4e-6).  16384 x 2048, the norm alone,
+// means of 0.4 deviations 30.8 us, of 0.6 37.0; gradients 61.4 and 75.8.
 enum Kind { kRms, kEither };
 __device__ __forceinline__ bool far_mean(float mean, float var) { return !(4.f * mean * mean <= var); }
 template <int K, int R, int KIND = kEither>

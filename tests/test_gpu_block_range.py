@@ -23,6 +23,12 @@ def bf16_values(lo, hi):
     return v[torch.cat([torch.ones(1, dtype=torch.bool), v[1:] != v[:-1]])]
 
 
+def room_for(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < (gigabytes + 8) << 30:
+        pytest.skip(f"needs {gigabytes} GB of free GPU memory")
+
+
 # ---------------------------------------------------------------- recurrence
 def gates_over(values, T, io, i, z, decay, seed):
     """Inputs [T, D] whose gates run through the values, every channel through others."""
@@ -224,6 +230,46 @@ def test_recur_long_sequence_of_few_channels(gla, T, D):
     base.recur_check(gla, x, [T], False, True, "bf16")
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("decay,i,z", [(True, False, True), (False, True, False)])
+@pytest.mark.parametrize("B,T,D", [(90, 20, 264), (400, 1, 200), (161, 127, 72)])
+def test_recur_shared_groups(gla, io, decay, i, z, B, T, D):
+    """Dense sequences that share a group, in either type."""
+    x = recur_inputs([T] * B, D, io, decay, i, z, True, 83)
+    base.recur_check(gla, x, [T] * B, False, decay, io)
+
+
+def test_recur_of_the_most_rows(gla):
+    """2^31 - 1 rows of eight channels, packed as one sequence and as single tokens: the first and the last
+    rows (between them x is 0, and the state is 0 after some hundred rows)."""
+    R, D, n = 2 ** 31 - 1, 8, 1000
+    room_for(172)
+    g = torch.Generator().manual_seed(84)
+    bf = torch.bfloat16
+    ends = rnd(g, 2 * n, D, dtype=bf)
+    x = torch.zeros(R, D, dtype=bf, device="cuda")
+    x[:n], x[-n:] = ends[:n].cuda(), ends[n:].cuda()
+    f = torch.zeros(R, D, dtype=bf, device="cuda")
+    out = torch.empty(R, D, dtype=bf, device="cuda")
+    cu = torch.tensor([0, R], dtype=torch.int32).cuda()
+    y, fin = gla.recur_fwd(x, f, cu_seqlens=cu, out=out)
+    gla.status_sync()
+    ref = block_ref.recur_all(ends, torch.zeros(2 * n, D), None, None, None, True, None, [0, n, 2 * n])
+    value, size = ref["y"]
+    tol = 2 * (ref["memory"] * 2 ** -22 + 2 ** -18)
+    near(torch.cat([y[:n], y[-n:]]), (value, tol * size + 2 ** -8 * value.abs()), 1.001, "y")
+    near(fin, (ref["final"][0][1:], ref["final"][1][1:]), tol, "final")
+    assert not y[R // 2:R // 2 + n].any()
+    state = torch.zeros(R, D, device="cuda")
+    gla.recur_step(x, f, state, out=out)
+    gla.status_sync()
+    want = 0.75 ** 0.5 * ends.double()  # a = 1/2
+    near(torch.cat([state[:n], state[-n:]]), (want, want.abs()), tol, "state")
+    assert torch.equal(out[-n:], state[-n:].to(bf)) and not state[R // 2:R // 2 + n].any()
+    del x, f, out, y, state
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- norms
 def norm_check(gla, R, D, io, res32, layer, post, pbias, z, scale, weight, bias, y, means=None, seed=73):
     """block_norm_fwd and block_norm_bwd with these parts; `means`: row k's mean is added to
@@ -329,12 +375,6 @@ def test_layer_norm_keeps_the_variance(gla):
         assert float(off.max()) <= 17 * 2 ** -24, (n, float(off.max()))
 
 
-def room_for(gigabytes):
-    torch.cuda.empty_cache()
-    if torch.cuda.mem_get_info()[0] < (gigabytes + 8) << 30:
-        pytest.skip(f"needs {gigabytes} GB of free GPU memory")
-
-
 def test_block_norm_of_the_most_rows(gla):
     """2^31 - 1 rows of eight channels: the first and the last rows, forward and gradient."""
     R, D, n = 2 ** 31 - 1, 8, 1000
@@ -438,6 +478,20 @@ def test_glu_of_the_most_rows(gla):
     assert not h[R // 2:R // 2 + n].any()
     del x, h
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("R,D,F", [(1, 520, 72), (20, 72, 200), (128, 1032, 136)])
+def test_glu_few_rows_are_apart(gla, R, D, F):
+    """Infinities and NaN of one row reach no other of the few."""
+    g = torch.Generator().manual_seed(85)
+    x = rnd(g, R, D, dtype=torch.bfloat16)
+    wg, wu = (rnd(g, F, D, std=0.1, dtype=torch.bfloat16).cuda() for _ in range(2))
+    a = gla.glu_fwd(gpu(x), wg, wu)
+    x[R // 2, 5], x[R - 1, 0] = float("nan"), INF
+    b = gla.glu_fwd(gpu(x), wg, wu)
+    fine = [r for r in range(R) if r not in (R // 2, R - 1)]
+    assert torch.equal(a[fine], b[fine]) and torch.isnan(b[R // 2]).all() and not torch.isfinite(b[R - 1]).all()
+    gla.status_sync()
 
 
 @pytest.mark.parametrize("R,D,F", [(129, 1032, 520), (192, 2048, 264), (255, 72, 1352), (320, 520, 392), (511, 264, 136),
