@@ -331,12 +331,16 @@ __device__ __forceinline__ void give(Maps& s, int step, int w, int lane, float4 
   if (lane == 0) arrive(&s.given[step & 1]);
 }
 // The state in front of its run of that step.  It comes from the exchange warp, whose waits have the limit in
-// time: this one ends when that warp has given up, with whatever lies there (and in any case
-// after 2^24 tests).
-__device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane) {
-  for (uint32_t i = 0; i < 1u << 24; ++i) {
-    if (completed(&s.ready[step & 1], (step >> 1) & 1)) break;
+// time: this one ends when that warp has given up, with whatever lies there (or itself gives up after
+// 2^28 tests, twenty minutes).
+__device__ __forceinline__ f32x2 take(Maps& s, int step, int w, int lane, unsigned* status) {
+  for (uint32_t i = 0; !completed(&s.ready[step & 1], (step >> 1) & 1); ++i) {
     if ((i & 255) == 0 && *reinterpret_cast<volatile int*>(&s.given_up)) break;
+    if (i == 1u << 28) {
+      *reinterpret_cast<volatile int*>(&s.given_up) = 1;
+      atomicOr(status, kDevTimeout);
+      break;
+    }
   }
   return s.front[step & 1][w][lane];
 }

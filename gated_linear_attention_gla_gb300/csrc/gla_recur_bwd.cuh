@@ -223,7 +223,7 @@ recur_bwd_kernel(RecurBwdArgs b, Split p, const float* kept, long long kept_rows
       fetch(tile, run - kBwdStages * reach);
       tile = tile == tiles + (kBwdStages - 1) * kStage ? tiles : tile + kStage;
       if (OUT) store(b.dz, at, n, dz);
-      const f32x2 behind = take(maps, step, w, lane);
+      const f32x2 behind = take(maps, step, w, lane, a.status);
       f32x2 v[kL];
 #pragma unroll
       for (int t = 0; t < kL; ++t) {

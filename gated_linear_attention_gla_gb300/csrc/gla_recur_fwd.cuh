@@ -200,7 +200,7 @@ recur_kernel(RecurArgs a, Split p, float* kept, long long kept_rows) {
     };
 
     auto second_pass = [&](Run& u, long long step) {
-      const f32x2 front = take(maps, (int)step, w, lane);
+      const f32x2 front = take(maps, (int)step, w, lane, a.status);
       if constexpr (KEEP) {
         // in front of tokens 0, kKeep, ... of the run
         float* to = kept + (g * kept_rows + (u.r0 - lo) / kKeep) * a.D + c;

@@ -27,7 +27,7 @@ __global__ void alone(RecurArgs a, int steps, int bad_step, float* out) {
     for (int step = 0; step < steps; ++step) {
       if (step == bad_step) break;
       give(maps, step, 0, lane, make_float4(0.5f, 0.5f, 1.f, 1.f));
-      if (take(maps, step, 0, lane).x > 2.f) break;
+      if (take(maps, step, 0, lane, a.status).x > 2.f) break;
     }
   }
 }
@@ -43,7 +43,7 @@ __global__ void __cluster_dims__(4, 1, 1) walk(RecurArgs a, int steps, int bad_r
     for (int step = 0; step < steps; ++step) {
       if (rank == bad_rank && step == bad_step) break;
       give(maps, step, 0, lane, make_float4(0.5f, 0.5f, 1.f, 1.f));
-      if (take(maps, step, 0, lane).x > 2.f) break;
+      if (take(maps, step, 0, lane, a.status).x > 2.f) break;
     }
   }
   part(maps, w == 1, lane, rank, 4, came);
